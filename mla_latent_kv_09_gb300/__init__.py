@@ -12,7 +12,11 @@ kernels); this package is its Python face:
   * `absorb_q` / `absorb_o`, the weight-absorption BMMs on either side of
     the attention (query through W_UK, output through W_UV);
   * `indexer_scores` / `topk_indices`, the sparse-attention indexer that
-    produces the top-k lists the sparse decode consumes.
+    produces the top-k lists the sparse decode consumes;
+  * `rope` / `rope_frequencies` and `cache_append`, which turn the RoPE dims
+    and put tokens into the paged latent cache;
+  * `prefix_expand` / `prefix_attend`, attention for a batch that shares a
+    long prefix: its keys and values expanded once, attended to by all.
 
 PyTorch is used only to allocate device memory and to name streams.
 """
@@ -33,6 +37,8 @@ from ._binding import (  # noqa: F401
     MLA_FLAG_BF16_PV,
     MLA_FLAG_KV_FP8,
     MLA_FLAG_OUT_FP32,
+    MLA_FLAG_ROPE_HALF,
+    MLA_FLAG_ROPE_INVERSE,
     MLA_FLAG_VALIDATE,
     MLA_OK,
     SIGNATURES,
@@ -40,7 +46,13 @@ from ._binding import (  # noqa: F401
     load,
     mla_absorb_o,
     mla_absorb_q,
+    mla_cache_append,
     mla_indexer_scores,
+    mla_prefix_attend,
+    mla_prefix_attend_workspace_size,
+    mla_prefix_expand,
+    mla_prefix_expand_workspace_size,
+    mla_rope,
     mla_topk,
     mla_combine,
     mla_decode,
@@ -250,3 +262,284 @@ def topk_indices(scores, cache_lens, topk: int, *, causal: bool = False, max_len
     mla_topk(scores, scores.stride(1), cache_lens, B, s_q, MLA_FLAG_CAUSAL if causal else 0, max_len, topk, out,
              status, stream)
     return out
+
+
+def _tensor(t, name: str, dtype, shape, device=None, contiguous: bool = True):
+    """Checks a tensor argument: its type, its device, its shape (None: any
+    size) and that it is contiguous, or with contiguous=False that its last
+    dim is."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name}: expected on {device or 'a GPU'}, got {t.device}")
+    if not (t.is_contiguous() if contiguous else t.shape[-1] == 1 or t.stride(-1) == 1):
+        raise ValueError(f"{name}: expected {'contiguous' if contiguous else 'unit stride in the last dim'}")
+
+
+def _on_device(fn):
+    """Runs fn with its first argument's device current and, where `stream` is
+    given (a torch stream, or its raw handle), with that stream current: the
+    kernels are launched there, and what the call allocates belongs to it."""
+    import functools
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        import torch
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError(f"{fn.__name__}: expected tensors on a GPU, got {dev}")
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=dev)
+            if stream.device != dev:
+                raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {dev}")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(dev):
+            return fn(first, *args, **kw)
+    return call
+
+
+def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.0, yarn: float = 1.0,
+                     original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """Frequencies of a rotation of `rope_dim` dims, for `rope` and
+    `cache_append`: (fp64 [rope_dim / 2] radians per position, the factor on
+    the turned dims).
+
+    Pair i turns by base^(-2i / rope_dim) a position.  For contexts longer
+    than the `original_len` a model was trained on: `linear` divides every
+    frequency (position interpolation); `yarn` is YaRN's stretch: pairs of
+    fewer than beta_slow turns over original_len are slowed down by it, pairs
+    of more than beta_fast turns are kept, those between are blended linearly
+    over the pair's index, and the factor is 0.1 ln(yarn) + 1.
+    """
+    import math
+
+    import torch
+    if rope_dim < 2 or rope_dim % 2 or not base > 1 or not linear >= 1 or not yarn >= 1 or not original_len > 0:
+        raise ValueError("rope_frequencies: rope_dim must be even, base > 1, linear and yarn >= 1, original_len > 0")
+    if not beta_fast > beta_slow > 0:
+        raise ValueError("rope_frequencies: beta_fast > beta_slow > 0")
+    index = torch.arange(rope_dim // 2, dtype=torch.float64)
+    inv = base ** (-2 * index / rope_dim) / linear
+    factor = 1.0
+    if yarn > 1:
+        # the (fractional) index whose pair makes `beta` turns over original_len
+        def at(beta):
+            return rope_dim * math.log(original_len / (2 * math.pi * beta)) / (2 * math.log(base))
+        low, high = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), rope_dim - 1)
+        slow = ((index - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        inv = inv / yarn * slow + inv * (1 - slow)
+        factor = 0.1 * math.log(yarn) + 1.0
+    return inv.to(device), factor
+
+
+@_on_device
+def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse: bool = False, scale: float = 1.0,
+         out=None, stream=None):
+    """Rotary positions over part of each head.
+
+    x [T, H, D] bf16 (tokens and heads may be strided), positions [T] int32,
+    inv_freq [R / 2] fp64 (see `rope_frequencies`): dims [offset, offset + R)
+    of row (t, h) are turned by positions[t] * inv_freq and multiplied by
+    `scale`, the others copied.  Pairs are (2i, 2i + 1), or (i, i + R / 2)
+    with half=True; inverse=True turns back (the gradient of the rotation, and
+    with scale 1 its inverse).  Returns `out`, by default a new [T, H, D]
+    tensor; out=x turns in place (and leaves the other dims alone).
+    """
+    import torch
+    dev = x.device
+    _tensor(x, "x", torch.bfloat16, (None, None, None), contiguous=False)
+    T, H, D = x.shape
+    _tensor(positions, "positions", torch.int32, (T,), dev)
+    _tensor(inv_freq, "inv_freq", torch.float64, (None,), dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(out, "out", torch.bfloat16, (T, H, D), dev, contiguous=False)
+    if T == 0 or H == 0:
+        return out
+    stream = torch.cuda.current_stream(dev)
+    mla_rope(x, x.stride(0), x.stride(1), positions, T, H, D, offset, 2 * inv_freq.shape[0], inv_freq, scale,
+             (MLA_FLAG_ROPE_HALF if half else 0) | (MLA_FLAG_ROPE_INVERSE if inverse else 0), out, out.stride(0),
+             out.stride(1), stream)
+    return out
+
+
+def _cache_flags(kv_cache, device) -> int:
+    import torch
+    if kv_cache.dtype == torch.uint8:
+        _tensor(kv_cache, "kv_cache", torch.uint8, (None, PAGE, 656), device)
+        return MLA_FLAG_KV_FP8
+    _tensor(kv_cache, "kv_cache", torch.bfloat16, (None, PAGE, D_QK), device)
+    return 0
+
+
+@_on_device
+def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=None, norm_weight=None,
+                 eps: float = 1e-6, inv_freq=None, half: bool = False, rope_scale: float = 1.0, status=None,
+                 stream=None):
+    """Append tokens to the paged latent cache.
+
+    latent [T, 512] and k_pe [T, 64] bf16 (rows may be strided: the two parts
+    of a [T, 576] projection output); kv_cache [num_pages, 64, 576] bf16 or
+    uint8 [num_pages, 64, 656] FP8 rows; block_table [B, W] int32; positions
+    [T] int32, token t's position in its request (negative: padding, nothing
+    is written); request_ids [T] int32, or None when the tokens are B equal
+    runs in order.  With norm_weight [512] bf16 the latent is RMS-normed with
+    `eps` first; with inv_freq [32] fp64 k_pe is turned by its position (as
+    `rope` does, with `half` and `rope_scale`).  No two tokens may name the
+    same row.  `status` (int32 device tensor, one element) receives
+    MLA_ERR_BAD_TABLE if a token's request, position or page is out of range;
+    that token is skipped.  Returns kv_cache.
+    """
+    import torch
+    dev = latent.device
+    _tensor(latent, "latent", torch.bfloat16, (None, D_V), contiguous=False)
+    T = latent.shape[0]
+    _tensor(k_pe, "k_pe", torch.bfloat16, (T, D_QK - D_V), dev, contiguous=False)
+    flags = _cache_flags(kv_cache, dev)
+    _tensor(block_table, "block_table", torch.int32, (None, None), dev, contiguous=False)
+    _tensor(positions, "positions", torch.int32, (T,), dev)
+    if request_ids is not None:
+        _tensor(request_ids, "request_ids", torch.int32, (T,), dev)
+    if norm_weight is not None:
+        _tensor(norm_weight, "norm_weight", torch.bfloat16, (D_V,), dev)
+    if inv_freq is not None:
+        _tensor(inv_freq, "inv_freq", torch.float64, ((D_QK - D_V) // 2,), dev)
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+    else:
+        _tensor(status, "status", torch.int32, (None,), dev)
+    if T == 0:
+        return kv_cache
+    B = block_table.shape[0]
+    # a single row has no next one: its stride says nothing about the table's width
+    width = block_table.stride(0) if B > 1 else block_table.shape[1]
+    if width < block_table.shape[1]:
+        raise ValueError("block_table: its rows overlap")
+    stream = torch.cuda.current_stream(dev)
+    mla_cache_append(latent, latent.stride(0) if T > 1 else D_V, k_pe, k_pe.stride(0) if T > 1 else D_QK - D_V,
+                     norm_weight, eps, inv_freq, rope_scale, positions, request_ids, T, block_table, width, B,
+                     kv_cache, kv_cache.shape[0], flags | (MLA_FLAG_ROPE_HALF if half else 0), status, stream)
+    return kv_cache
+
+
+@_on_device
+def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=None, workspace=None, status=None,
+                  stream=None):
+    """Per-head keys and values of a shared prefix, from its cached latents.
+
+    kv_cache [num_pages, 64, 576] bf16 or uint8 [num_pages, 64, 656] FP8
+    rows; block_table [W] int32, the prefix's pages in order; w_uk, w_uv
+    [H, 512, 128] bf16 (as for `absorb_q` / `absorb_o`).  Returns (k_nope
+    [H, R, 128] bf16, k_pe [R, 64] bf16, v [H, R, 128] fp16), by default new
+    with R = prefix_len; `out` may hold them with any R >= prefix_len, whose
+    further rows are left as they are.  `workspace` (uint8, for an FP8 cache
+    only, mla_prefix_expand_workspace_size bytes) is allocated if not given.
+    `status` receives MLA_ERR_BAD_TABLE for a page outside the pool and
+    MLA_ERR_VALUE_RANGE for a value that is not finite in fp16.
+    """
+    import torch
+    dev = kv_cache.device
+    flags = _cache_flags(kv_cache, dev)
+    _tensor(block_table, "block_table", torch.int32, (None,), dev)
+    if prefix_len < 0 or prefix_len > block_table.shape[0] * PAGE:
+        raise ValueError("prefix_len: outside the block table")
+    H = w_uk.shape[0]
+    _tensor(w_uk, "w_uk", torch.bfloat16, (None, D_V, 128), dev)
+    _tensor(w_uv, "w_uv", torch.bfloat16, (H, D_V, 128), dev)
+    if out is None:
+        out = (torch.empty((H, prefix_len, 128), dtype=torch.bfloat16, device=dev),
+               torch.empty((prefix_len, D_QK - D_V), dtype=torch.bfloat16, device=dev),
+               torch.empty((H, prefix_len, 128), dtype=torch.float16, device=dev))
+    k_nope, k_pe, v = out
+    _tensor(k_nope, "k_nope", torch.bfloat16, (H, None, 128), dev)
+    R = k_nope.shape[1]
+    _tensor(k_pe, "k_pe", torch.bfloat16, (R, D_QK - D_V), dev)
+    _tensor(v, "v", torch.float16, (H, R, 128), dev)
+    if R < prefix_len:
+        raise ValueError("out: fewer rows than prefix_len")
+    if prefix_len == 0:
+        return out
+    need = mla_prefix_expand_workspace_size(prefix_len, flags)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _tensor(workspace, "workspace", torch.uint8, (None,), dev)
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+    else:
+        _tensor(status, "status", torch.int32, (None,), dev)
+    stream = torch.cuda.current_stream(dev)
+    mla_prefix_expand(kv_cache, kv_cache.shape[0], block_table, prefix_len, w_uk, w_uv, H, flags, k_nope, v, R, k_pe,
+                      workspace, 0 if workspace is None else workspace.numel(), status, stream)
+    return out
+
+
+@_on_device
+def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix_len: int | None = None, visible=None,
+                  suffix_out=None, suffix_lse=None, out_fp32: bool = False, out=None, lse=None, workspace=None,
+                  status=None, stream=None):
+    """Attention of T query tokens over one shared, expanded prefix.
+
+    q_nope [T, H, 128], q_pe [T, H, 64] bf16 with one row stride (slices of a
+    [T, H, 192] projection output; q_pe already turned); k_nope [H, R, 128],
+    k_pe [R, 64], v [H, R, 128] as `prefix_expand` returns them, of which the
+    first prefix_len (default R) rows count; every value of them finite.
+    visible [T] int32: token t sees the first visible[t] rows only (padded
+    tokens: 0).  suffix_out [T, H, 128] bf16 and suffix_lse [T, H] fp32: what
+    each (token, head) attended to elsewhere (`decode_step`'s output through
+    `absorb_o`, and its LSE); the result is then the attention over both.
+    Returns (out [T, H, 128] bf16 or fp32, lse [T, H] fp32); out and lse may
+    be suffix_out and suffix_lse themselves.  `workspace` (uint8,
+    mla_prefix_attend_workspace_size bytes) is allocated if not given.
+    """
+    import torch
+    dev = q_nope.device
+    T, H = q_nope.shape[0], q_nope.shape[1]
+    _tensor(q_nope, "q_nope", torch.bfloat16, (T, H, 128), contiguous=False)
+    _tensor(q_pe, "q_pe", torch.bfloat16, (T, H, 64), dev, contiguous=False)
+    _tensor(k_nope, "k_nope", torch.bfloat16, (H, None, 128), dev)
+    R = k_nope.shape[1]
+    _tensor(k_pe, "k_pe", torch.bfloat16, (R, 64), dev)
+    _tensor(v, "v", torch.float16, (H, R, 128), dev)
+    if prefix_len is None:
+        prefix_len = R
+    elif prefix_len < 0 or prefix_len > R:
+        raise ValueError("prefix_len: outside the expanded rows")
+    if visible is not None:
+        _tensor(visible, "visible", torch.int32, (T,), dev)
+    if (suffix_out is None) != (suffix_lse is None):
+        raise ValueError("suffix_out and suffix_lse come together")
+    if suffix_out is not None:
+        _tensor(suffix_out, "suffix_out", torch.bfloat16, (T, H, 128), dev)
+        _tensor(suffix_lse, "suffix_lse", torch.float32, (T, H), dev)
+    if out is None:
+        out = torch.empty((T, H, 128), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=dev)
+    else:
+        _tensor(out, "out", torch.float32 if out_fp32 else torch.bfloat16, (T, H, 128), dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _tensor(lse, "lse", torch.float32, (T, H), dev)
+    if T == 0 or H == 0:
+        return out, lse
+    q_stride = _rows(q_nope, 128, "q_nope")
+    if _rows(q_pe, 64, "q_pe") != q_stride:
+        raise ValueError("q_pe must have the row stride of q_nope")
+    if workspace is None:
+        workspace = torch.empty(mla_prefix_attend_workspace_size(T, H, prefix_len), dtype=torch.uint8, device=dev)
+    else:
+        _tensor(workspace, "workspace", torch.uint8, (None,), dev)
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+    else:
+        _tensor(status, "status", torch.int32, (None,), dev)
+    stream = torch.cuda.current_stream(dev)
+    mla_prefix_attend(q_nope, q_pe, q_stride, k_nope, v, R, k_pe, prefix_len, visible, T, H, softmax_scale,
+                      suffix_out, suffix_lse, MLA_FLAG_OUT_FP32 if out_fp32 else 0, workspace, workspace.numel(), out,
+                      lse, status, stream)
+    return out, lse

@@ -30,6 +30,8 @@ MLA_FLAG_OUT_FP32 = 2
 MLA_FLAG_VALIDATE = 4
 MLA_FLAG_BF16_PV = 8
 MLA_FLAG_KV_FP8 = 16
+MLA_FLAG_ROPE_HALF = 32
+MLA_FLAG_ROPE_INVERSE = 64
 
 # every symbol the headers in include/ declare: name -> (restype, argtypes)
 _c_int, _c_size, _vp, _i64, _f32, _uint = (ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p,
@@ -54,6 +56,16 @@ SIGNATURES = {
     "mla_indexer_scores": (_c_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _c_int, _c_int, _uint, _c_int, _vp, _i64,
                                     _vp, _vp]),
     "mla_topk": (_c_int, [_vp, _i64, _vp, _c_int, _c_int, _uint, _c_int, _c_int, _vp, _vp, _vp]),
+    "mla_rope": (_c_int, [_vp, _i64, _i64, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _f32, _uint, _vp, _i64,
+                          _i64, _vp]),
+    "mla_cache_append": (_c_int, [_vp, _i64, _vp, _i64, _vp, _f32, _vp, _f32, _vp, _vp, _c_int, _vp, _i64, _c_int,
+                                  _vp, _i64, _uint, _vp, _vp]),
+    "mla_prefix_expand_workspace_size": (_c_size, [_c_int, _uint]),
+    "mla_prefix_expand": (_c_int, [_vp, _i64, _vp, _c_int, _vp, _vp, _c_int, _uint, _vp, _vp, _i64, _vp, _vp, _c_size,
+                                   _vp, _vp]),
+    "mla_prefix_attend_workspace_size": (_c_size, [_c_int, _c_int, _c_int, ctypes.POINTER(_c_int)]),
+    "mla_prefix_attend": (_c_int, [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _c_int, _vp, _c_int, _c_int, _f32, _vp, _vp,
+                                   _uint, _vp, _c_size, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -220,3 +232,47 @@ def mla_topk(scores, scores_stride: int, cache_lens, batch: int, s_q: int, flags
     _check("mla_topk", load().mla_topk(
         _ptr(scores), int(scores_stride), _ptr(cache_lens), int(batch), int(s_q), int(flags), int(max_len),
         int(topk), _ptr(out_idx), _ptr(status), _stream(stream)))
+
+
+def mla_rope(x, x_token_stride: int, x_head_stride: int, positions, num_tokens: int, num_heads: int, head_dim: int,
+             rope_offset: int, rope_dim: int, inv_freq, scale: float, flags: int, out, out_token_stride: int,
+             out_head_stride: int, stream=None) -> None:
+    _check("mla_rope", load().mla_rope(
+        _ptr(x), x_token_stride, x_head_stride, _ptr(positions), num_tokens, num_heads, head_dim, rope_offset,
+        rope_dim, _ptr(inv_freq), scale, flags, _ptr(out), out_token_stride, out_head_stride, _stream(stream)))
+
+
+def mla_cache_append(latent, latent_stride: int, k_pe, k_pe_stride: int, norm_weight, eps: float, inv_freq,
+                     rope_scale: float, positions, request_ids, num_tokens: int, block_table, bt_stride: int,
+                     num_requests: int, kv_cache, num_pages: int, flags: int, status, stream=None) -> None:
+    _check("mla_cache_append", load().mla_cache_append(
+        _ptr(latent), latent_stride, _ptr(k_pe), k_pe_stride, _ptr(norm_weight), eps, _ptr(inv_freq), rope_scale,
+        _ptr(positions), _ptr(request_ids), num_tokens, _ptr(block_table), bt_stride, num_requests, _ptr(kv_cache),
+        num_pages, flags, _ptr(status), _stream(stream)))
+
+
+def mla_prefix_expand_workspace_size(prefix_len: int, flags: int) -> int:
+    return load().mla_prefix_expand_workspace_size(prefix_len, flags)
+
+
+def mla_prefix_expand(kv_cache, num_pages: int, block_table, prefix_len: int, w_uk, w_uv, num_heads: int, flags: int,
+                      k_nope, v, head_rows: int, k_pe, workspace, ws_bytes: int, status, stream=None) -> None:
+    _check("mla_prefix_expand", load().mla_prefix_expand(
+        _ptr(kv_cache), num_pages, _ptr(block_table), prefix_len, _ptr(w_uk), _ptr(w_uv), num_heads, flags,
+        _ptr(k_nope), _ptr(v), head_rows, _ptr(k_pe), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)))
+
+
+def mla_prefix_attend_workspace_size(num_tokens: int, num_heads: int, prefix_len: int) -> int:
+    err = ctypes.c_int(0)
+    n = load().mla_prefix_attend_workspace_size(num_tokens, num_heads, prefix_len, ctypes.byref(err))
+    _check("mla_prefix_attend_workspace_size", err.value)
+    return n
+
+
+def mla_prefix_attend(q_nope, q_pe, q_stride: int, k_nope, v, head_rows: int, k_pe, prefix_len: int, visible,
+                      num_tokens: int, num_heads: int, softmax_scale: float, suffix_out, suffix_lse, flags: int,
+                      workspace, ws_bytes: int, out, lse, status, stream=None) -> None:
+    _check("mla_prefix_attend", load().mla_prefix_attend(
+        _ptr(q_nope), _ptr(q_pe), q_stride, _ptr(k_nope), _ptr(v), head_rows, _ptr(k_pe), prefix_len, _ptr(visible),
+        num_tokens, num_heads, softmax_scale, _ptr(suffix_out), _ptr(suffix_lse), flags, _ptr(workspace), ws_bytes,
+        _ptr(out), _ptr(lse), _ptr(status), _stream(stream)))

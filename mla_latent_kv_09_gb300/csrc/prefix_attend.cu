@@ -1,13 +1,45 @@
 // prefix_attend.cu — attention of a batch's query tokens over a shared,
 // expanded prefix, with the C ABI (include/mla_prefix.h).
+//
+// One head is ordinary attention: T query rows of 192 dims, P keys of 192 (128
+// of the head's, 64 RoPE dims shared by all heads), P values of 128.  A key
+// tile of 128 rows is 64 KiB from HBM for 128 * 2 * 320 operations a query
+// row: up to about 270 tokens the HBM bounds the call, above it the tensor
+// cores do.
+//
+// A CTA per SM works on blocks of 256 query rows of one head: two row tiles
+// of 128 ("streams"), each with its own scores S and output O in tensor
+// memory (2 * (128 + 128) columns, all of it), so that the tensor cores work
+// on one stream while the other's softmax runs.  Both streams use each key
+// tile in shared memory once.  A block of up to 128 rows has one row tile:
+// its two streams then take alternate key tiles and are joined at the end, so
+// that a small batch keeps the same overlap.
+//
+//   warps 0-3, 4-7  softmax of stream 0, 1: a thread owns a query row, reads
+//                   its 128 scores from tensor memory, keeps the running
+//                   maximum and sums, and writes the weights in fp16 over the
+//                   scores, where the value product reads them as its A operand
+//   warp 8          TMA: the block's queries (96 KiB), then key and value
+//                   chunks of 16 KiB through a ring of 8 slots
+//   warp 9          tcgen05.mma: S = Q K^T (12 steps of M128 N128 K16, bf16),
+//                   O += P V (8 steps, fp16)
+//
+// The running maximum is lazy: it moves only when a score beats it by 2^8, so
+// that weights stay below 2^8 (fp16 holds them with 11 bits) and O is rarely
+// rescaled.  O is normalised by the sum of the rounded weights that the value
+// product used, so that a weight's rounding acts on v_j - O and not on v_j;
+// the LSE takes the sum of the unrounded ones.
+//
+// Work split: all (head, key tile) steps of a row block form one line, cut
+// into equal ranges, one per CTA (see plan()).  A range that covers a head's
+// whole prefix writes the result; a head cut in pieces leaves normalised fp32
+// partial rows and their LSE, which the combine kernel joins.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <mutex>
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "kernel_common.cuh"
 #include "mla_prefix.h"
@@ -17,98 +49,695 @@ namespace {
 
 constexpr int kHeadDim = 128;
 constexpr int kRope = 64;
-constexpr int kKeys = 128;  // keys of a tile
+constexpr int kTile = 128;                  // query rows of a row tile, keys of a key tile
+constexpr int kSlot = 16384;                // a key chunk (128 keys x 64 dims) or half a value tile (64 keys x 128 dims)
+constexpr int kSlots = 8;
+constexpr int kQChunks = 3;                 // 64-dim chunks of a query or key row
+constexpr int kQTile = kQChunks * kSlot;    // 48 KiB
+constexpr int kOffRing = 2 * kQTile;        // 96 KiB
+constexpr int kOffBar = kOffRing + kSlots * kSlot;
+constexpr int kNumBars = 2 * kSlots + 10;
+constexpr int kSlack = 1024;                // dynamic shared memory is re-aligned to 1024 B (128-byte swizzle atoms)
+constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
+static_assert(kSmem <= 232448, "shared memory");
+// the two streams of a one-tile block exchange their sums in the second row tile's query space
+constexpr int kOffXchg = kQTile;
+constexpr int kThreads = 320;
+constexpr int kSoftmaxWarps = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256;  // + 128 * stream
+constexpr uint32_t kIdescQK = idesc_bf16(128, 128, 0);
+// fp16 A (weights, tensor memory) and B (values, MN-major): formats 0
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;               // log2 by which a score must beat the running maximum to move it
+
+// ---- work split
+struct Plan {
+  int nk;         // key tiles
+  int blocks;     // row blocks of 256
+  int width;      // row blocks worked on side by side by the CTAs of a group
+  int groups;     // CTA groups, each with a range of the line
+  int passes;     // ceil(blocks / width)
+  long long line; // passes * heads * nk steps
+};
 
 struct AttendParams {
-  const uint16_t* q_nope;
-  const uint16_t* q_pe;
-  long long q_stride;
-  const uint16_t* k_nope;
-  const uint16_t* v;
-  long long head_rows;
-  const uint16_t* k_pe;
-  int prefix_len;
   const int* visible;
-  int num_tokens, num_heads;
+  int num_tokens, num_heads, prefix_len;
   float scale_log2;
   const uint16_t* suffix_out;
   const float* suffix_lse;
   int out_fp32;
   void* out;
   float* lse;
+  float* part_o;    // [2 * CTAs][rows][128], normalised
+  float* part_lse;  // [2 * CTAs][rows], log2
+  int part_rows;
+  Plan plan;
+  int* status;
 };
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__host__ __device__ __forceinline__ long long cut(const Plan& w, int g) { return w.line * g / w.groups; }
 
-// One CTA: one (token, head).  Thread j scores key j of each tile of 128, then
-// sums dim j of the values; one pass with a running maximum and sum.
-__global__ void __launch_bounds__(kKeys) mla_prefix_attend_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ float q[kHeadDim + kRope], w[kKeys], red[4];
-  const int h = blockIdx.x, t = blockIdx.y, j = threadIdx.x, warp = j >> 5;
-  grid_dependency_wait();
-  const long long row = static_cast<long long>(t) * p.num_heads + h;
-  q[j] = bf(p.q_nope[row * p.q_stride + j]);
-  if (j < kRope) q[kHeadDim + j] = bf(p.q_pe[row * p.q_stride + j]);
-  const int seen = p.visible ? max(0, min(p.visible[t], p.prefix_len)) : p.prefix_len;
-  float m = -INFINITY, total = 0.f, used = 0.f, o = 0.f;  // exponents in the base 2
-  for (int k0 = 0; k0 < seen; k0 += kKeys) {
-    __syncthreads();
-    float s = -INFINITY;
-    if (k0 + j < seen) {
-      const uint16_t* kr = p.k_nope + (h * p.head_rows + k0 + j) * kHeadDim;
-      const uint16_t* pr = p.k_pe + static_cast<long long>(k0 + j) * kRope;
-      s = 0.f;
-      for (int d = 0; d < kHeadDim; ++d) s = fmaf(q[d], bf(kr[d]), s);
-      for (int d = 0; d < kRope; ++d) s = fmaf(q[kHeadDim + d], bf(pr[d]), s);
-      s *= p.scale_log2;
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 4-D tiled load (x: dim within a 64-dim chunk, y: row, z: chunk, w: head).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// D (+)= A B, A in tensor memory.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns (the store of tmem_ld16).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// One segment of a CTA's range: key tiles [k0, k1) of head h for row block `block`.
+struct Segment {
+  int h, block, k0, k1, rows;
+  bool first, whole;
+};
+
+struct SegmentIter {
+  const Plan& w;
+  int num_tokens, num_heads, lane_block;
+  long long at, begin, end;
+  __device__ SegmentIter(const AttendParams& p) : w(p.plan), num_tokens(p.num_tokens), num_heads(p.num_heads) {
+    const int g = blockIdx.x / w.width;
+    lane_block = blockIdx.x % w.width;
+    at = begin = cut(w, g);
+    end = cut(w, g + 1);
+  }
+  __device__ bool next(Segment& s) {
+    while (at < end) {
+      const int unit = static_cast<int>(at / w.nk);
+      const int k0 = static_cast<int>(at - static_cast<long long>(unit) * w.nk);
+      const long long left = end - at;
+      const int k1 = left < w.nk - k0 ? k0 + static_cast<int>(left) : w.nk;
+      s.first = at == begin;
+      at += k1 - k0;
+      s.block = unit / num_heads * w.width + lane_block;
+      if (s.block >= w.blocks) return false;  // blocks grow along the line
+      s.h = unit % num_heads;
+      s.k0 = k0;
+      s.k1 = k1;
+      s.whole = k1 - k0 == w.nk;
+      const int rows = num_tokens - s.block * 2 * kTile;
+      s.rows = rows < 2 * kTile ? rows : 2 * kTile;
+      return true;
     }
-    float top = s;
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    if ((j & 31) == 0) red[warp] = top;
-    __syncthreads();
-    const float next = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float e = exp2f(s - next), keep = exp2f(m - next);
-    total = total * keep + e;  // this thread's keys only; joined at the end
-    const float r = __half2float(__float2half_rn(e));
-    used = used * keep + r;
-    w[j] = r;
-    m = next;
-    o *= keep;
-    __syncthreads();
-    const int n = min(kKeys, seen - k0);
-    const uint16_t* vr = p.v + (h * p.head_rows + k0) * kHeadDim + j;
-    for (int i = 0; i < n; ++i) o = fmaf(w[i], __half2float(__ushort_as_half(vr[i * kHeadDim])), o);
+    return false;
   }
-  for (int pass = 0; pass < 2; ++pass) {
-    float x = pass ? used : total;
-    for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-    __syncthreads();
-    if ((j & 31) == 0) red[warp] = x;
-    __syncthreads();
-    (pass ? used : total) = red[0] + red[1] + red[2] + red[3];
-  }
-  float lse = seen > 0 ? m * kLn2 + logf(total) : -INFINITY;
-  o = seen > 0 ? o / used : 0.f;
-  if (p.suffix_out) {
-    const float other = p.suffix_lse[row];
-    const float top = fmaxf(lse, other);
-    if (top == -INFINITY) {
-      o = 0.f;
-    } else {
-      const float a = exp2f((lse - top) * kLog2e), b = exp2f((other - top) * kLog2e);
-      const float x = b > 0.f ? bf(p.suffix_out[row * kHeadDim + j]) * b : 0.f;
-      o = (o * a + x) / (a + b);
-      lse = top + logf(a + b);
+};
+
+// Weights of the prefix's and the suffix's result in their join, and the joined LSE (log2).
+struct Join {
+  float mine, other, lse2;
+};
+__device__ __forceinline__ Join join(float lse2, float other2) {
+  Join j;
+  const float top = fmaxf(lse2, other2);
+  const float base = top == -INFINITY ? 0.f : top;
+  const float a = ex2_approx(lse2 - base), b = ex2_approx(other2 - base);
+  const float sum = a + b;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+  j.mine = a * inv;
+  j.other = b * inv;
+  j.lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
+  return j;
+}
+
+// 16 bytes of 8 result columns, or 32 in fp32, joined with the suffix's.
+__device__ __forceinline__ void write8(const AttendParams& p, long long row, int col, const float* o, const Join& j) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = o[i] * j.mine;
+  const long long at = row * kHeadDim + col;
+  if (p.suffix_out && j.other != 0.f) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p.suffix_out + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = fmaf(__uint_as_float(w[i] << 16), j.other, x[2 * i]);
+      x[2 * i + 1] = fmaf(__uint_as_float(w[i] & 0xffff0000u), j.other, x[2 * i + 1]);
     }
   }
+  if (p.out_fp32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap tm_qn,
+                         const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t mis = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + mis;
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const uint32_t bar0 = sbase + kOffBar;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kSlots + s); };
+  const uint32_t bar_q_full = bar0 + 8u * (2 * kSlots), bar_q_empty = bar_q_full + 8u;
+  auto bar_s_full = [&](int s) { return bar_q_full + 8u * (2 + s); };  // scores of a stream are in tensor memory
+  auto bar_p_full = [&](int s) { return bar_q_full + 8u * (4 + s); };  // its weights are
+  auto bar_pv = [&](int s) { return bar_q_full + 8u * (6 + s); };      // its value product is done
+  const uint32_t bar_o_free = bar_q_full + 8u * 8, bar_drain = bar_q_full + 8u * 9;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
+  auto slot_addr = [&](uint32_t n) { return sbase + static_cast<uint32_t>(kOffRing) + (n % kSlots) * kSlot; };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * kSlots + 2; ++i) mbar_init(bar0 + 8u * i, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_s_full(s), 1);
+      mbar_init(bar_p_full(s), 4);
+      mbar_init(bar_pv(s), 1);
+    }
+    mbar_init(bar_o_free, kSoftmaxWarps);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  if (p.out_fp32)
-    static_cast<float*>(p.out)[row * kHeadDim + j] = o;
-  else
-    static_cast<uint16_t*>(p.out)[row * kHeadDim + j] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-  if (j == 0) p.lse[row] = lse;
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  Ctl ctl;
+  ctl.abort = abort_flag;
+  ctl.n_remote = 0;
+  ctl.status = p.status;
+
+  grid_dependency_wait();
+  SegmentIter it(p);
+  Segment sg;
+
+  // Chunks enter the ring in the order the MMAs use them.  Two row tiles: K0
+  // V0 K1 V1 ..; one row tile, key tiles alternating between the streams: K0
+  // K1 V0 K2 V1 K3 ..  A key tile is three chunks, a value tile two; these are
+  // the places of tile j's first chunk in a segment of n tiles.
+  auto place_k = [](bool two, int j) { return two ? 5 * j : (j < 2 ? 3 * j : 5 * j - 2); };
+  auto place_v = [](bool two, int j, int n) { return two ? 5 * j + 3 : (j == n - 1 ? 5 * n - 2 : 5 * j + 6); };
+
+  uint32_t issued = 0;  // chunks requested so far (warp 8)
+  int q_loads = 0;
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_qn);
+      tma_prefetch_desc(&tm_qp);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_kp);
+      tma_prefetch_desc(&tm_v);
+      bool ok = true;
+      auto slot_ready = [&]() -> bool {  // the next slot's previous chunk has been used
+        return issued < kSlots || wait_bar<false>(empty(issued % kSlots), ((issued / kSlots) - 1) & 1, ctl);
+      };
+      auto load_k = [&](int tile) -> bool {
+        for (int c = 0; c < kQChunks; ++c) {
+          if (!slot_ready()) return false;
+          const uint32_t bar = full(issued % kSlots);
+          mbar_arrive_expect_tx(bar, kSlot);
+          if (c < 2)
+            tma_load_4d(slot_addr(issued), &tm_k, 0, tile * kTile, c, sg.h, bar);
+          else
+            tma_load_2d(slot_addr(issued), &tm_kp, 0, tile * kTile, bar);
+          ++issued;
+        }
+        return true;
+      };
+      auto load_v = [&](int tile) -> bool {
+        for (int c = 0; c < 2; ++c) {
+          if (!slot_ready()) return false;
+          const uint32_t bar = full(issued % kSlots);
+          mbar_arrive_expect_tx(bar, kSlot);
+          tma_load_4d(slot_addr(issued), &tm_v, 0, tile * kTile + 64 * c, 0, sg.h, bar);
+          ++issued;
+        }
+        return true;
+      };
+      while (ok && it.next(sg)) {
+        const bool two = sg.rows > kTile;
+        if (q_loads > 0 && !wait_bar<false>(bar_q_empty, (q_loads - 1) & 1, ctl)) break;
+        mbar_arrive_expect_tx(bar_q_full, two ? 2 * kQTile : kQTile);
+        for (int r = 0; r < (two ? 2 : 1); ++r) {
+          const uint32_t dst = sbase + static_cast<uint32_t>(r * kQTile);
+          const int t0 = (2 * sg.block + r) * kTile;
+          tma_load_3d(dst, &tm_qn, 0, sg.h, t0, bar_q_full);
+          tma_load_3d(dst + kSlot, &tm_qn, 64, sg.h, t0, bar_q_full);
+          tma_load_3d(dst + 2 * kSlot, &tm_qp, 0, sg.h, t0, bar_q_full);
+        }
+        ++q_loads;
+        if (two) {
+          for (int j = sg.k0; ok && j < sg.k1; ++j) ok = load_k(j) && load_v(j);
+        } else {
+          ok = load_k(sg.k0);
+          if (ok && sg.k0 + 1 < sg.k1) ok = load_k(sg.k0 + 1);
+          for (int j = sg.k0; ok && j < sg.k1; ++j) {
+            ok = load_v(j);
+            if (ok && j + 2 < sg.k1) ok = load_k(j + 2);
+          }
+        }
+      }
+      grid_launch_dependents();
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {
+      uint32_t base = 0;             // chunks of the segments before this one
+      uint32_t n_pv[2] = {0, 0};     // value products issued per stream
+      uint32_t n_p[2] = {0, 0};      // weight tiles taken per stream
+      int seg = 0;
+      bool ok = true;
+      while (ok && it.next(sg)) {
+        const bool two = sg.rows > kTile;
+        const int n = sg.k1 - sg.k0;
+        const int steps[2] = {two ? n : (n + 1) / 2, two ? n : n / 2};
+        ok = wait_bar<false>(bar_q_full, seg & 1, ctl);
+        auto wait_chunk = [&](uint32_t c) { return wait_bar<false>(full(c % kSlots), (c / kSlots) & 1, ctl); };
+        // scores of stream s's step i
+        auto issue_qk = [&](int s, int i) -> bool {
+          const uint32_t c0 = base + place_k(two, two ? i : 2 * i + s);
+          // S holds the weights of the step before until its value product is done
+          if (n_pv[s] > 0 && !wait_bar<false>(bar_pv(s), (n_pv[s] - 1) & 1, ctl)) return false;
+          const uint32_t a = sbase + static_cast<uint32_t>(two ? s * kQTile : 0);
+          for (int c = 0; c < kQChunks; ++c) {
+            if (!wait_chunk(c0 + c)) return false;
+            tc_fence_after();
+            const uint64_t ad = smem_desc(a + c * kSlot, 16u, 1024u);
+            const uint64_t bd = smem_desc(slot_addr(c0 + c), 16u, 1024u);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16(tmem + kColS + 128u * s, ad + static_cast<uint64_t>((32 * kk) >> 4),
+                       bd + static_cast<uint64_t>((32 * kk) >> 4), kIdescQK, (c | kk) != 0 ? 1u : 0u);
+            if (!two || s == 1) umma_commit(empty((c0 + c) % kSlots));
+          }
+          umma_commit(bar_s_full(s));
+          return true;
+        };
+        auto issue_pv = [&](int s, int i) -> bool {
+          const uint32_t c0 = base + place_v(two, two ? i : 2 * i + s, n);
+          if (!wait_bar<false>(bar_p_full(s), n_p[s] & 1, ctl)) return false;
+          ++n_p[s];
+          for (int c = 0; c < 2; ++c) {
+            if (!wait_chunk(c0 + c)) return false;
+            tc_fence_after();
+            const uint64_t bd = smem_desc(slot_addr(c0 + c), 8192u, 1024u);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ta(tmem + kColO + 128u * s, tmem + kColS + 128u * s + 32u * c + 8u * kk,
+                          bd + static_cast<uint64_t>((2048 * kk) >> 4), kIdescPV, (i | c | kk) != 0 ? 1u : 0u);
+            if (!two || s == 1) umma_commit(empty((c0 + c) % kSlots));
+          }
+          umma_commit(bar_pv(s));
+          ++n_pv[s];
+          return true;
+        };
+        ok = ok && issue_qk(0, 0) && (steps[1] == 0 || issue_qk(1, 0));
+        if (ok && n <= (two ? 1 : 2)) umma_commit(bar_q_empty);
+        // O of the segment before has been read
+        if (ok && seg > 0) ok = wait_bar<false>(bar_o_free, (seg - 1) & 1, ctl);
+        for (int i = 0; ok && i < steps[0]; ++i) {
+          for (int s = 0; ok && s < 2; ++s) {
+            if (i >= steps[s]) continue;
+            ok = issue_pv(s, i);
+            if (ok && i + 1 < steps[s]) {
+              ok = issue_qk(s, i + 1);
+              // the segment's last scores: its queries are done with
+              if (ok && (two ? i + 2 == n && s == 1 : 2 * (i + 1) + s == n - 1)) umma_commit(bar_q_empty);
+            }
+          }
+        }
+        base += 5u * n;
+        ++seg;
+      }
+      umma_commit(bar_drain);  // arrives once every MMA issued above has completed
+    }
+    __syncwarp();
+  } else {
+    const int s = warp >> 2;                          // stream
+    const int r = (warp & 3) * 32 + lane;             // row of the tile, lane of tensor memory
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + kColS + 128u * s;
+    const uint32_t to = tmem + lane_base + kColO;
+    float* xchg = reinterpret_cast<float*>(smem + kOffXchg);
+    uint32_t n_s = 0;  // score tiles taken
+    bool ok = true;
+    while (it.next(sg)) {
+      const bool two = sg.rows > kTile;
+      const int n = sg.k1 - sg.k0;
+      const int steps = two ? n : (s == 0 ? (n + 1) / 2 : n / 2);
+      const int brow = two ? s * kTile + r : r;       // row within the block
+      const int t = sg.block * 2 * kTile + brow;
+      const bool real = brow < sg.rows;
+      const long long row = static_cast<long long>(t) * p.num_heads + sg.h;
+      int seen = p.prefix_len;
+      if (p.visible) seen = real ? max(0, min(p.visible[t], p.prefix_len)) : 0;
+      float other2 = -INFINITY;
+      if (p.suffix_lse && real && sg.whole) other2 = p.suffix_lse[row] * kLog2e;
+      float m = -INFINITY, total = 0.f, used = 0.f;   // running maximum (log2), sums of the weights and of the rounded ones
+      for (int i = 0; ok && i < steps; ++i) {
+        const int key0 = (sg.k0 + (two ? i : 2 * i + s)) * kTile;
+        ok = warp_wait(bar_s_full(s), n_s & 1, ctl);
+        if (!ok) break;
+        ++n_s;
+        tc_fence_after();
+        // The scores are read twice, half a row at a time: holding all 128
+        // would leave no registers for the rest.  The second half first, so
+        // that the half still held is the one whose columns the first weights
+        // overwrite.
+        const int limit = seen - key0;                // keys of this tile the row sees
+        const bool ragged = __any_sync(0xffffffffu, limit < kTile);
+        uint32_t x[2][32];
+        auto load_half = [&](int half) {
+          tmem_ld32(ts + 64u * half, x[0]);
+          tmem_ld32(ts + 64u * half + 32u, x[1]);
+          tmem_wait_ld();
+          if (ragged) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (64 * half + 32 * c + k >= limit) x[c][k] = 0xff800000u;  // -inf
+          }
+        };
+        auto half_max = [&]() -> float {
+          float a = __uint_as_float(x[0][0]), b = __uint_as_float(x[1][0]);
+#pragma unroll
+          for (int k = 1; k < 32; ++k) {
+            a = fmaxf(a, __uint_as_float(x[0][k]));
+            b = fmaxf(b, __uint_as_float(x[1][k]));
+          }
+          return fmaxf(a, b);
+        };
+        load_half(1);
+        float top = half_max();
+        load_half(0);
+        top = fmaxf(top, half_max());
+        top *= p.scale_log2;
+        const bool move = top > m + kLazy;
+        float keep = 1.f;
+        if (move) {
+          keep = ex2_approx(m - top);
+          m = top;
+          total *= keep;
+          used *= keep;
+        }
+        // This step's scores were issued after the value product of the step
+        // before had completed: O is at rest and may be rescaled here.
+        if (i > 0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + 128u * s + 16u * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+            tmem_st16(to + 128u * s + 16u * c, o);
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) load_half(1);
+          uint32_t w[32];
+          float t0 = 0.f, t1 = 0.f, u0 = 0.f, u1 = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float a = ex2_approx(fmaf(__uint_as_float(x[k / 16][2 * (k % 16)]), p.scale_log2, -base));
+            const float b = ex2_approx(fmaf(__uint_as_float(x[k / 16][2 * (k % 16) + 1]), p.scale_log2, -base));
+            t0 += a;
+            t1 += b;
+            w[k] = pack_f16x2(a, b);
+            if (k & 1)
+              u1 = add_f16x2_halves(u1, w[k]);
+            else
+              u0 = add_f16x2_halves(u0, w[k]);
+          }
+          total += t0 + t1;
+          used += u0 + u1;
+          tmem_st32(ts + 32u * half, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p_full(s));
+      }
+      // every value product of the stream in this segment (n_s counts them too)
+      if (ok && steps > 0) ok = warp_wait(bar_pv(s), (n_s - 1) & 1, ctl);
+      if (!two) {
+        float* mine = xchg + s * 3 * kTile + r;
+        mine[0] = m;
+        mine[kTile] = total;
+        mine[2 * kTile] = used;
+      }
+      // all softmax warps meet once per segment, so that a wait that ran out in one ends them all
+      ok = named_bar_all(1, kSoftmaxWarps * 32, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // scale of each stream's O in the row's result
+      float f0, f1 = 0.f, lse2;
+      if (two) {
+        f0 = used == 0.f ? 0.f : 1.f / used;
+        lse2 = total == 0.f ? -INFINITY : m + lg2(total);
+      } else {
+        const float m0 = xchg[r], m1 = xchg[3 * kTile + r];
+        const float top = fmaxf(m0, m1), base = top == -INFINITY ? 0.f : top;
+        const float a0 = ex2_approx(m0 - base), a1 = ex2_approx(m1 - base);
+        const float sum = xchg[kTile + r] * a0 + xchg[4 * kTile + r] * a1;
+        const float u = xchg[2 * kTile + r] * a0 + xchg[5 * kTile + r] * a1;
+        const float inv = u == 0.f ? 0.f : 1.f / u;
+        f0 = a0 * inv;
+        f1 = a1 * inv;
+        lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
+        named_bar_sync(2, kSoftmaxWarps * 32);  // the exchange may be written again
+      }
+      Join j = {1.f, 0.f, lse2};
+      if (p.suffix_lse && sg.whole) j = join(lse2, other2);
+      const long long prow = (2ll * blockIdx.x + (sg.first ? 0 : 1)) * p.part_rows + brow;
+      // two row tiles: a stream's own O, all columns; one: both O's, half of the columns each
+      const int c0 = two ? 0 : 2 * s, c1 = two ? 4 : 2 * s + 2;
+      const bool second = !two && n > 1;
+      for (int c = c0; c < c1; ++c) {
+        uint32_t a[32], b[32];
+        tmem_ld32(to + (two ? 128u * s : 0u) + 32u * c, a);
+        if (second) tmem_ld32(to + 128u + 32u * c, b);
+        tmem_wait_ld();
+        if (!real) continue;
+        float o[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          o[k] = f0 == 0.f ? 0.f : __uint_as_float(a[k]) * f0;  // an accumulator that took nothing is not read as a number
+          if (second && f1 != 0.f) o[k] = fmaf(__uint_as_float(b[k]), f1, o[k]);
+        }
+        if (sg.whole) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) write8(p, row, 32 * c + k, o + k, j);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (real && (two || s == 0)) {
+        if (sg.whole)
+          p.lse[row] = j.lse2 * kLn2;
+        else
+          p.part_lse[prow] = lse2;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_o_free);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 9 * 32) drain_bar(bar_drain, 0u);  // MMAs finish before TMEM is released
+  if (threadIdx.x == 8 * 32 && *abort_flag) {
+    // teardown after a wait ran out: loads still in flight land before the CTA exits
+    for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued; ++c)
+      drain_bar(full(c % kSlots), (c / kSlots) & 1);
+    if (q_loads > 0) drain_bar(bar_q_full, (q_loads - 1) & 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the partial rows of heads that were cut.  kWarps warps per (token,
+// head): a warp takes every kWarps-th piece, a lane four columns.
+template <int kWarps>
+__global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_constant__ AttendParams p) {
+  __shared__ float4 acc[4][32];
+  const Plan& w = p.plan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp % kWarps;
+  const long long row = static_cast<long long>(blockIdx.x) * (4 / kWarps) + warp / kWarps;
+  grid_dependency_wait();
+  const bool real = row < static_cast<long long>(p.num_tokens) * p.num_heads;
+  const int t = static_cast<int>(row / p.num_heads), h = static_cast<int>(row % p.num_heads);
+  const int block = t / (2 * kTile), brow = t % (2 * kTile);
+  const int unit = block / w.width * p.num_heads + h, lane_block = block % w.width;
+  const long long start = static_cast<long long>(unit) * w.nk, end = start + w.nk;
+  // the group whose range [cut(g), cut(g + 1)) holds a step x is the last with cut(g) <= x
+  const int g0 = static_cast<int>(((start + 1) * w.groups + w.line - 1) / w.line) - 1;
+  const int g1 = static_cast<int>((end * w.groups + w.line - 1) / w.line) - 1;
+  const bool work = real && g0 < g1;
+  const int n = g1 - g0 + 1;
+  auto piece = [&](int i) {  // row of piece i among the partial rows
+    const int g = g0 + i;
+    const int slot = 2 * (g * w.width + lane_block) + (cut(w, g) < start ? 1 : 0);
+    return static_cast<long long>(slot) * p.part_rows + brow;
+  };
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float lse2 = -INFINITY, other2 = -INFINITY;
+  if (work) {
+    if (p.suffix_lse) other2 = p.suffix_lse[row] * kLog2e;
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_lse[piece(i)]);
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int i = lane; i < n; i += 32) sum += ex2_approx(p.part_lse[piece(i)] - base);
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
+#pragma unroll 4
+    for (int i = sub; i < n; i += kWarps) {
+      const long long at = piece(i);
+      const float f = ex2_approx(p.part_lse[at] - base) * inv;
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[at * (kHeadDim / 4) + lane];
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  if (kWarps > 1) {
+    acc[warp][lane] = o;
+    __syncthreads();
+    if (sub == 0) {
+      for (int i = 1; i < kWarps; ++i) {
+        const float4 v = acc[warp + i][lane];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+    }
+  }
+  if (!work || sub != 0) return;
+  Join j = {1.f, 0.f, lse2};
+  if (p.suffix_lse) j = join(lse2, other2);
+  // two lanes write 8 columns (16 bytes of bf16)
+  const float y0 = __shfl_down_sync(0xffffffffu, o.x, 1), y1 = __shfl_down_sync(0xffffffffu, o.y, 1);
+  const float y2 = __shfl_down_sync(0xffffffffu, o.z, 1), y3 = __shfl_down_sync(0xffffffffu, o.w, 1);
+  const float all[8] = {o.x, o.y, o.z, o.w, y0, y1, y2, y3};
+  if ((lane & 1) == 0) write8(p, row, 4 * lane, all, j);
+  if (lane == 0) p.lse[row] = j.lse2 * kLn2;
+}
+
+// Nothing to attend to in the prefix: the suffix's result, or zeros.
+__global__ void __launch_bounds__(128) mla_prefix_empty_kernel(const __grid_constant__ AttendParams p) {
+  grid_dependency_wait();
+  const long long at = static_cast<long long>(blockIdx.x) * 128 + threadIdx.x;
+  const long long row = at / (kHeadDim / 8);
+  if (row >= static_cast<long long>(p.num_tokens) * p.num_heads) return;
+  const int col = static_cast<int>(at % (kHeadDim / 8)) * 8;
+  const float other2 = p.suffix_lse ? p.suffix_lse[row] * kLog2e : -INFINITY;
+  const float zero[8] = {};
+  write8(p, row, col, zero, join(-INFINITY, other2));
+  // 16 threads of one warp share the row: the one that writes its LSE does so after all have read it
+  __syncwarp(__activemask());
+  if (col == 0) p.lse[row] = p.suffix_lse ? p.suffix_lse[row] : -INFINITY;
+}
+
+// ============================================================ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+bool encode(CUtensorMap* m, bool fp16, int rank, const void* base, const cuuint64_t* size, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  EncodeTiledFn fn = encode_tiled();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn && fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                  const_cast<void*>(base), size, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows as boxes of {64 dims, 1 head, 128 tokens}.
+bool encode_q(CUtensorMap* m, const void* base, int dims, int64_t stride, int heads, int tokens) {
+  const cuuint64_t size[3] = {static_cast<cuuint64_t>(dims), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride) * 2,
+                                 static_cast<cuuint64_t>(stride) * 2 * static_cast<cuuint64_t>(heads)};
+  const cuuint32_t box[3] = {64u, 1u, static_cast<cuuint32_t>(kTile)};
+  return encode(m, false, 3, base, size, strides, box);
+}
+
+// Keys or values [heads, head_rows, 128] as boxes of {64 dims, `rows` rows, `chunks` 64-dim chunks, 1 head};
+// rows from prefix_len on read as zeros.
+bool encode_kv(CUtensorMap* m, bool fp16, const void* base, int prefix_len, int64_t head_rows, int heads,
+               uint32_t rows, uint32_t chunks) {
+  const cuuint64_t size[4] = {64, static_cast<cuuint64_t>(prefix_len), kHeadDim / 64, static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[3] = {kHeadDim * 2, 128, static_cast<cuuint64_t>(head_rows) * kHeadDim * 2};
+  const cuuint32_t box[4] = {64u, rows, chunks, 1u};
+  return encode(m, fp16, 4, base, size, strides, box);
 }
 
 constexpr int kMaxDev = 64;
@@ -127,11 +756,80 @@ int attend_device_ready(int* sms) {
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess || major != 10 ||
-        minor != 3 || cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        minor != 3 || cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        st.sms < 1) {
       st.status = MLA_ERR_DEVICE;
+      return;
+    }
+    if (cudaFuncSetAttribute(mla_prefix_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      st.status = MLA_ERR_CUDA;
+    }
   });
   *sms = st.sms;
   return st.status;
+}
+
+// Row blocks of a head that are worked on side by side read each key tile
+// from HBM once and from L2 after that, so a batch of several blocks wants
+// them side by side; but `width` must leave few SMs idle (sms / width groups)
+// and few blocks over in the last pass.  The cost of a width: steps of the
+// longest range, each the tensor cores' 2,560 cycles (two row tiles) or, when
+// all groups stream different tiles, their share of the HBM: 64 KiB a group
+// at 3.5 KB a cycle, 18.6 cycles a group.
+Plan plan(int num_tokens, int num_heads, int prefix_len, int sms) {
+  Plan w;
+  w.nk = (prefix_len + kTile - 1) / kTile;
+  w.blocks = (num_tokens + 2 * kTile - 1) / (2 * kTile);
+  double best = 0;
+  for (int width = 1; width <= w.blocks && width <= sms && width <= 16; ++width) {
+    const int groups = sms / width, passes = (w.blocks + width - 1) / width;
+    const double step = fmax(num_tokens > kTile ? 2560.0 : 1280.0, 18.6 * groups);
+    const double cost = passes * step / groups;
+    if (width == 1 || cost < 0.99 * best) {
+      best = cost;
+      w.width = width;
+      w.groups = groups;
+      w.passes = passes;
+    }
+  }
+  w.line = static_cast<long long>(w.passes) * num_heads * w.nk;
+  // at least two steps a range: one for each stream
+  if (w.groups > (w.line + 1) / 2) w.groups = static_cast<int>((w.line + 1) / 2);
+  return w;
+}
+
+struct WsLayout2 {
+  size_t lse, total;
+  int rows;
+};
+WsLayout2 attend_ws(const Plan& w, int num_tokens) {
+  WsLayout2 l;
+  l.rows = num_tokens > kTile ? 2 * kTile : kTile;
+  const size_t slots = 2 * static_cast<size_t>(w.groups) * w.width * l.rows;
+  l.lse = align256(slots * kHeadDim * sizeof(float));
+  l.total = l.lse + align256(slots * sizeof(float));
+  return l;
+}
+
+template <typename... A>
+int launch_dependent(void (*kernel)(A...), dim3 grid, dim3 block, int smem, mla_stream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
 }
 
 bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -149,7 +847,8 @@ size_t mla_prefix_attend_workspace_size(int num_tokens, int num_heads, int prefi
            : num_heads < 1 || num_heads > kHeads ? MLA_ERR_UNSUPPORTED : attend_device_ready(&sms);
   if (err) *err = rc;
   if (rc != MLA_OK) return 0;
-  return 256;
+  if (num_tokens == 0 || prefix_len == 0) return 256;
+  return attend_ws(plan(num_tokens, num_heads, prefix_len, sms), num_tokens).total;
 }
 
 int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, const void* k_nope, const void* v,
@@ -172,43 +871,52 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   if (num_heads < 1 || num_heads > kHeads) return MLA_ERR_UNSUPPORTED;
   if (head_rows > INT32_MAX || static_cast<int64_t>(num_tokens) * num_heads > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   int sms = 0;
-  const int rc = attend_device_ready(&sms);
+  int rc = attend_device_ready(&sms);
   if (rc != MLA_OK) return rc;
   if (ws_bytes < mla_prefix_attend_workspace_size(num_tokens, num_heads, prefix_len, nullptr))
     return MLA_ERR_WORKSPACE;
   if (num_tokens == 0) return MLA_OK;
-  AttendParams p;
-  p.q_nope = static_cast<const uint16_t*>(q_nope);
-  p.q_pe = static_cast<const uint16_t*>(q_pe);
-  p.q_stride = q_stride;
-  p.k_nope = static_cast<const uint16_t*>(k_nope);
-  p.v = static_cast<const uint16_t*>(v);
-  p.head_rows = head_rows;
-  p.k_pe = static_cast<const uint16_t*>(k_pe);
-  p.prefix_len = prefix_len;
+  AttendParams p = {};
   p.visible = visible;
   p.num_tokens = num_tokens;
   p.num_heads = num_heads;
+  p.prefix_len = prefix_len;
   p.scale_log2 = softmax_scale * kLog2e;
   p.suffix_out = static_cast<const uint16_t*>(suffix_out);
   p.suffix_lse = suffix_lse;
   p.out_fp32 = (flags & MLA_FLAG_OUT_FP32) != 0;
   p.out = out;
   p.lse = lse;
-  for (int t0 = 0; t0 < num_tokens; t0 += 65535) {  // grid.y's limit
-    AttendParams part = p;
-    const long long rows = static_cast<long long>(t0) * num_heads;
-    part.q_nope += rows * q_stride;
-    part.q_pe += rows * q_stride;
-    if (visible) part.visible += t0;
-    if (suffix_out) part.suffix_out += rows * kHeadDim;
-    if (suffix_lse) part.suffix_lse += rows;
-    part.out = static_cast<char*>(out) + rows * kHeadDim * (p.out_fp32 ? 4 : 2);
-    part.lse += rows;
-    const int n = num_tokens - t0 < 65535 ? num_tokens - t0 : 65535;
-    mla_prefix_attend_kernel<<<dim3(num_heads, n), kKeys, 0, static_cast<cudaStream_t>(stream)>>>(part);
-  }
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  p.status = status;
+  const long long rows = static_cast<long long>(num_tokens) * num_heads;
+  if (prefix_len == 0)
+    return launch_dependent(mla_prefix_empty_kernel, dim3(static_cast<unsigned>((rows * 16 + 127) / 128)), dim3(128), 0,
+                            stream, p);
+  p.plan = plan(num_tokens, num_heads, prefix_len, sms);
+  const WsLayout2 l = attend_ws(p.plan, num_tokens);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.lse);
+  p.part_rows = l.rows;
+  CUtensorMap qn, qp, k, kp, vm;
+  const cuuint64_t pe_size[2] = {kRope, static_cast<cuuint64_t>(prefix_len)};
+  const cuuint64_t pe_stride[1] = {kRope * 2};
+  const cuuint32_t pe_box[2] = {kRope, static_cast<cuuint32_t>(kTile)};
+  if (!encode_q(&qn, q_nope, kHeadDim, q_stride, num_heads, num_tokens) ||
+      !encode_q(&qp, q_pe, kRope, q_stride, num_heads, num_tokens) ||
+      !encode_kv(&k, false, k_nope, prefix_len, head_rows, num_heads, kTile, 1) ||
+      !encode(&kp, false, 2, k_pe, pe_size, pe_stride, pe_box) ||
+      !encode_kv(&vm, true, v, prefix_len, head_rows, num_heads, kTile / 2, 2))
+    return MLA_ERR_CUDA;
+  const int ctas = p.plan.groups * p.plan.width;
+  rc = launch_dependent(mla_prefix_attend_kernel, dim3(ctas), dim3(kThreads), kSmem, stream, p, qn, qp, k, kp, vm);
+  // heads are cut wherever a range does not end with one
+  if (rc != MLA_OK || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
+  // pieces a head can be cut in: the ranges that overlap its nk steps
+  const long long range = p.plan.line / p.plan.groups;
+  if (p.plan.nk / range + 2 <= 8)
+    return launch_dependent(mla_prefix_combine_kernel<1>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
+                            stream, p);
+  return launch_dependent(mla_prefix_combine_kernel<4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, p);
 }
 
 }  // extern "C"

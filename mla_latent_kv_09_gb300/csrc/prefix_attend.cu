@@ -15,14 +15,22 @@
 // its two streams then take alternate key tiles and are joined at the end, so
 // that a small batch keeps the same overlap.
 //
-//   warps 0-3, 4-7  softmax of stream 0, 1: a thread owns a query row, reads
-//                   its 128 scores from tensor memory, keeps the running
-//                   maximum and sums, and writes the weights in fp16 over the
-//                   scores, where the value product reads them as its A operand
-//   warp 8          TMA: the block's queries (96 KiB), then key and value
+//   warps 0-7, 8-15 softmax of stream 0, 1: two threads own a query row, each
+//                   64 of its 128 scores, which it reads from tensor memory;
+//                   they agree on the running maximum, keep their own sums
+//                   and write the weights in fp16 over the scores, where the
+//                   value product reads them as its A operand
+//   warp 16         TMA: the block's queries (96 KiB), then key and value
 //                   chunks of 16 KiB through a ring of 8 slots
-//   warp 9          tcgen05.mma: S = Q K^T (12 steps of M128 N128 K16, bf16),
+//   warp 17         tcgen05.mma: S = Q K^T (12 steps of M128 N128 K16, bf16),
 //                   O += P V (8 steps, fp16)
+//
+// A step's chain is scores -> softmax -> value product -> next scores (the
+// weights lie where the next scores go); the other stream fills the tensor
+// cores meanwhile, if a stream's softmax is no longer than the other's
+// products.  Hence two threads a row, and hence the weights are handed over
+// in two halves of 64 keys: the value product of the first runs under the
+// exponentials of the second.
 //
 // The running maximum is lazy: it moves only when a score beats it by 2^8, so
 // that weights stay below 2^8 (fp16 holds them with 11 bits) and O is rarely
@@ -40,6 +48,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "kernel_common.cuh"
 #include "mla_prefix.h"
@@ -56,14 +65,15 @@ constexpr int kQChunks = 3;                 // 64-dim chunks of a query or key r
 constexpr int kQTile = kQChunks * kSlot;    // 48 KiB
 constexpr int kOffRing = 2 * kQTile;        // 96 KiB
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
-constexpr int kNumBars = 2 * kSlots + 10;
-constexpr int kSlack = 1024;                // dynamic shared memory is re-aligned to 1024 B (128-byte swizzle atoms)
-constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
+constexpr int kNumBars = 2 * kSlots + 12;
+constexpr int kOffMax = kOffBar + kNumBars * 8 + 16;  // [stream][half][row]: exchange between a row's two threads
+constexpr int kSmem = kOffMax + 4 * kTile * 4;        // no room to re-align: the base must lie on 1024 B (checked)
 static_assert(kSmem <= 232448, "shared memory");
-// the two streams of a one-tile block exchange their sums in the second row tile's query space
+// the threads of a row of a one-tile block exchange their sums in the second row tile's query space
 constexpr int kOffXchg = kQTile;
-constexpr int kThreads = 320;
-constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 576;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kTmaWarp = 16, kMmaWarp = 17;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;  // + 128 * stream
 constexpr uint32_t kIdescQK = idesc_bf16(128, 128, 0);
@@ -117,13 +127,27 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// D (+)= A B, A in tensor memory.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Predicated forms for a warp of which one lane issues: D (+)= A B^T with A
+// in shared or in tensor memory, and the commit.
+__device__ __forceinline__ void umma_ss_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue) : "memory");
+}
+__device__ __forceinline__ void umma_ts_if(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue) : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t issue, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+      ::"r"(bar), "r"(issue) : "memory");
 }
 
 // 32 lanes x 16 consecutive 32-bit columns (the store of tmem_ld16).
@@ -136,6 +160,42 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// Two fp32 in a 64-bit register, and the packed operations on them.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// wait_bar with a rolled loop: this kernel waits in many places, and the
+// unrolled form made its code 110 KB, which the instruction caches do not hold.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*c.abort) return false;
+    if (globaltimer_ns() - t0 > kTimeoutNs) {
+      raise_timeout(c);
+      return false;
+    }
+  }
+  return true;
+}
+
 // One segment of a CTA's range: key tiles [k0, k1) of head h for row block `block`.
 struct Segment {
   int h, block, k0, k1, rows;
@@ -144,33 +204,34 @@ struct Segment {
 
 struct SegmentIter {
   const Plan& w;
-  int num_tokens, num_heads, lane_block;
-  long long at, begin, end;
+  int num_tokens, num_heads, lane_block, unit, k0;
+  long long left;
+  bool first;
   __device__ SegmentIter(const AttendParams& p) : w(p.plan), num_tokens(p.num_tokens), num_heads(p.num_heads) {
     const int g = blockIdx.x / w.width;
     lane_block = blockIdx.x % w.width;
-    at = begin = cut(w, g);
-    end = cut(w, g + 1);
+    const long long begin = cut(w, g);
+    left = cut(w, g + 1) - begin;
+    unit = static_cast<int>(begin / w.nk);
+    k0 = static_cast<int>(begin - static_cast<long long>(unit) * w.nk);
+    first = true;
   }
   __device__ bool next(Segment& s) {
-    while (at < end) {
-      const int unit = static_cast<int>(at / w.nk);
-      const int k0 = static_cast<int>(at - static_cast<long long>(unit) * w.nk);
-      const long long left = end - at;
-      const int k1 = left < w.nk - k0 ? k0 + static_cast<int>(left) : w.nk;
-      s.first = at == begin;
-      at += k1 - k0;
-      s.block = unit / num_heads * w.width + lane_block;
-      if (s.block >= w.blocks) return false;  // blocks grow along the line
-      s.h = unit % num_heads;
-      s.k0 = k0;
-      s.k1 = k1;
-      s.whole = k1 - k0 == w.nk;
-      const int rows = num_tokens - s.block * 2 * kTile;
-      s.rows = rows < 2 * kTile ? rows : 2 * kTile;
-      return true;
-    }
-    return false;
+    if (left <= 0) return false;
+    s.block = unit / num_heads * w.width + lane_block;
+    if (s.block >= w.blocks) return false;  // blocks grow along the line
+    s.h = unit % num_heads;
+    s.k0 = k0;
+    s.k1 = left < w.nk - k0 ? k0 + static_cast<int>(left) : w.nk;
+    s.whole = s.k1 - k0 == w.nk;
+    s.first = first;
+    const int rows = num_tokens - s.block * 2 * kTile;
+    s.rows = rows < 2 * kTile ? rows : 2 * kTile;
+    left -= s.k1 - k0;
+    k0 = 0;
+    ++unit;
+    first = false;
+    return true;
   }
 };
 
@@ -221,19 +282,22 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
                          const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_v) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t mis = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  uint8_t* smem = smem_raw + mis;
+  uint8_t* smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((sbase & 1023u) != 0) {  // the swizzled tiles need it; the kernel has no static shared memory ahead of it
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(MLA_ERR_CUDA));
+    return;
+  }
 
   const uint32_t bar0 = sbase + kOffBar;
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kSlots + s); };
   const uint32_t bar_q_full = bar0 + 8u * (2 * kSlots), bar_q_empty = bar_q_full + 8u;
   auto bar_s_full = [&](int s) { return bar_q_full + 8u * (2 + s); };  // scores of a stream are in tensor memory
-  auto bar_p_full = [&](int s) { return bar_q_full + 8u * (4 + s); };  // its weights are
-  auto bar_pv = [&](int s) { return bar_q_full + 8u * (6 + s); };      // its value product is done
-  const uint32_t bar_o_free = bar_q_full + 8u * 8, bar_drain = bar_q_full + 8u * 9;
+  auto bar_p_full = [&](int s, int half) { return bar_q_full + 8u * (4 + 2 * s + half); };  // its weights are
+  auto bar_pv = [&](int s) { return bar_q_full + 8u * (8 + s); };      // its value product is done
+  const uint32_t bar_o_free = bar_q_full + 8u * 10, bar_drain = bar_q_full + 8u * 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
   auto slot_addr = [&](uint32_t n) { return sbase + static_cast<uint32_t>(kOffRing) + (n % kSlots) * kSlot; };
@@ -242,7 +306,8 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
     for (int i = 0; i < 2 * kSlots + 2; ++i) mbar_init(bar0 + 8u * i, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_s_full(s), 1);
-      mbar_init(bar_p_full(s), 4);
+      mbar_init(bar_p_full(s, 0), kSoftmaxWarps / 2);
+      mbar_init(bar_p_full(s, 1), kSoftmaxWarps / 2);
       mbar_init(bar_pv(s), 1);
     }
     mbar_init(bar_o_free, kSoftmaxWarps);
@@ -250,7 +315,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
     *abort_flag = 0u;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -275,9 +340,9 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   auto place_k = [](bool two, int j) { return two ? 5 * j : (j < 2 ? 3 * j : 5 * j - 2); };
   auto place_v = [](bool two, int j, int n) { return two ? 5 * j + 3 : (j == n - 1 ? 5 * n - 2 : 5 * j + 6); };
 
-  uint32_t issued = 0;  // chunks requested so far (warp 8)
+  uint32_t issued = 0;  // chunks requested so far (TMA warp)
   int q_loads = 0;
-  if (warp == 8) {
+  if (warp == kTmaWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&tm_qn);
       tma_prefetch_desc(&tm_qp);
@@ -286,9 +351,10 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       tma_prefetch_desc(&tm_v);
       bool ok = true;
       auto slot_ready = [&]() -> bool {  // the next slot's previous chunk has been used
-        return issued < kSlots || wait_bar<false>(empty(issued % kSlots), ((issued / kSlots) - 1) & 1, ctl);
+        return issued < kSlots || wait(empty(issued % kSlots), ((issued / kSlots) - 1) & 1, ctl);
       };
       auto load_k = [&](int tile) -> bool {
+#pragma unroll 1
         for (int c = 0; c < kQChunks; ++c) {
           if (!slot_ready()) return false;
           const uint32_t bar = full(issued % kSlots);
@@ -313,7 +379,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       };
       while (ok && it.next(sg)) {
         const bool two = sg.rows > kTile;
-        if (q_loads > 0 && !wait_bar<false>(bar_q_empty, (q_loads - 1) & 1, ctl)) break;
+        if (q_loads > 0 && !wait(bar_q_empty, (q_loads - 1) & 1, ctl)) break;
         mbar_arrive_expect_tx(bar_q_full, two ? 2 * kQTile : kQTile);
         for (int r = 0; r < (two ? 2 : 1); ++r) {
           const uint32_t dst = sbase + static_cast<uint32_t>(r * kQTile);
@@ -337,85 +403,102 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       grid_launch_dependents();
     }
     __syncwarp();
-  } else if (warp == 9) {
-    if (lane == 0) {
-      uint32_t base = 0;             // chunks of the segments before this one
-      uint32_t n_pv[2] = {0, 0};     // value products issued per stream
-      uint32_t n_p[2] = {0, 0};      // weight tiles taken per stream
-      int seg = 0;
-      bool ok = true;
-      while (ok && it.next(sg)) {
-        const bool two = sg.rows > kTile;
-        const int n = sg.k1 - sg.k0;
-        const int steps[2] = {two ? n : (n + 1) / 2, two ? n : n / 2};
-        ok = wait_bar<false>(bar_q_full, seg & 1, ctl);
-        auto wait_chunk = [&](uint32_t c) { return wait_bar<false>(full(c % kSlots), (c / kSlots) & 1, ctl); };
-        // scores of stream s's step i
-        auto issue_qk = [&](int s, int i) -> bool {
-          const uint32_t c0 = base + place_k(two, two ? i : 2 * i + s);
-          // S holds the weights of the step before until its value product is done
-          if (n_pv[s] > 0 && !wait_bar<false>(bar_pv(s), (n_pv[s] - 1) & 1, ctl)) return false;
-          const uint32_t a = sbase + static_cast<uint32_t>(two ? s * kQTile : 0);
-          for (int c = 0; c < kQChunks; ++c) {
-            if (!wait_chunk(c0 + c)) return false;
-            tc_fence_after();
-            const uint64_t ad = smem_desc(a + c * kSlot, 16u, 1024u);
-            const uint64_t bd = smem_desc(slot_addr(c0 + c), 16u, 1024u);
+  } else if (warp == kMmaWarp) {
+    // The whole warp runs this loop and one lane issues, by predicates: the
+    // operands stay warp-uniform, and so in uniform registers.  (Issued from a
+    // divergent branch, with the counters in local memory, the 20 MMAs and 9
+    // waits of a step took 3,600 cycles against the tensor cores' 1,280.)
+    const uint32_t leader = lane == 0 ? 1u : 0u;
+    const uint64_t ring_k = smem_desc(sbase + kOffRing, 16u, 1024u), ring_v = smem_desc(sbase + kOffRing, 8192u, 1024u);
+    const uint64_t q_desc = smem_desc(sbase, 16u, 1024u);
+    uint32_t base = 0;             // chunks of the segments before this one
+    uint32_t pv0 = 0, pv1 = 0;     // value products issued per stream
+    uint32_t seg = 0;
+    bool ok = true;
+    auto wait_chunk = [&](uint32_t c) { return wait(full(c % kSlots), (c / kSlots) & 1, ctl); };
+    auto slot_off = [](uint32_t c) { return static_cast<uint64_t>(c % kSlots) * (kSlot >> 4); };
+    // Scores of stream s from the key chunks c0 ..; n_pv: value products the
+    // stream has had.  S holds the weights of the step before until its value
+    // product is done.
+    auto issue_qk = [&](auto stream, uint32_t n_pv, uint32_t c0, bool two) -> bool {
+      constexpr int s = decltype(stream)::value;
+      if (n_pv > 0 && !wait(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
+      const uint64_t ad = q_desc + (two && s == 1 ? kQTile >> 4 : 0);
+      const uint32_t release = !two || s == 1 ? leader : 0u;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16(tmem + kColS + 128u * s, ad + static_cast<uint64_t>((32 * kk) >> 4),
-                       bd + static_cast<uint64_t>((32 * kk) >> 4), kIdescQK, (c | kk) != 0 ? 1u : 0u);
-            if (!two || s == 1) umma_commit(empty((c0 + c) % kSlots));
-          }
-          umma_commit(bar_s_full(s));
-          return true;
-        };
-        auto issue_pv = [&](int s, int i) -> bool {
-          const uint32_t c0 = base + place_v(two, two ? i : 2 * i + s, n);
-          if (!wait_bar<false>(bar_p_full(s), n_p[s] & 1, ctl)) return false;
-          ++n_p[s];
-          for (int c = 0; c < 2; ++c) {
-            if (!wait_chunk(c0 + c)) return false;
-            tc_fence_after();
-            const uint64_t bd = smem_desc(slot_addr(c0 + c), 8192u, 1024u);
+      for (int c = 0; c < kQChunks; ++c) {
+        if (!wait_chunk(c0 + c)) return false;
+        tc_fence_after();
+        const uint64_t bd = ring_k + slot_off(c0 + c);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ta(tmem + kColO + 128u * s, tmem + kColS + 128u * s + 32u * c + 8u * kk,
-                          bd + static_cast<uint64_t>((2048 * kk) >> 4), kIdescPV, (i | c | kk) != 0 ? 1u : 0u);
-            if (!two || s == 1) umma_commit(empty((c0 + c) % kSlots));
-          }
-          umma_commit(bar_pv(s));
-          ++n_pv[s];
-          return true;
-        };
-        ok = ok && issue_qk(0, 0) && (steps[1] == 0 || issue_qk(1, 0));
-        if (ok && n <= (two ? 1 : 2)) umma_commit(bar_q_empty);
-        // O of the segment before has been read
-        if (ok && seg > 0) ok = wait_bar<false>(bar_o_free, (seg - 1) & 1, ctl);
-        for (int i = 0; ok && i < steps[0]; ++i) {
-          for (int s = 0; ok && s < 2; ++s) {
-            if (i >= steps[s]) continue;
-            ok = issue_pv(s, i);
-            if (ok && i + 1 < steps[s]) {
-              ok = issue_qk(s, i + 1);
-              // the segment's last scores: its queries are done with
-              if (ok && (two ? i + 2 == n && s == 1 : 2 * (i + 1) + s == n - 1)) umma_commit(bar_q_empty);
-            }
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ss_if(leader, tmem + kColS + 128u * s, ad + ((c * kSlot + 32 * kk) >> 4), bd + ((32 * kk) >> 4),
+                     kIdescQK, (c | kk) != 0 ? 1u : 0u);
+        umma_commit_if(release, empty((c0 + c) % kSlots));
+      }
+      umma_commit_if(leader, bar_s_full(s));
+      return true;
+    };
+    auto issue_pv = [&](auto stream, uint32_t n_pv, uint32_t c0, bool two, bool first) -> bool {
+      constexpr int s = decltype(stream)::value;
+      const uint32_t release = !two || s == 1 ? leader : 0u;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (!wait_chunk(c0 + c) || !wait(bar_p_full(s, c), n_pv & 1, ctl)) return false;
+        tc_fence_after();
+        const uint64_t bd = ring_v + slot_off(c0 + c);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ts_if(leader, tmem + kColO + 128u * s, tmem + kColS + 128u * s + 32u * c + 8u * kk,
+                     bd + ((2048 * kk) >> 4), kIdescPV, first && (c | kk) == 0 ? 0u : 1u);
+        umma_commit_if(release, empty((c0 + c) % kSlots));
+      }
+      umma_commit_if(leader, bar_pv(s));
+      return true;
+    };
+    const std::integral_constant<int, 0> s0{};
+    const std::integral_constant<int, 1> s1{};
+    while (ok && it.next(sg)) {
+      const bool two = sg.rows > kTile;
+      const int n = sg.k1 - sg.k0;
+      const int steps0 = two ? n : (n + 1) / 2, steps1 = two ? n : n / 2;
+      ok = wait(bar_q_full, seg & 1, ctl) && issue_qk(s0, pv0, base, two) &&
+           (steps1 == 0 || issue_qk(s1, pv1, base + place_k(two, two ? 0 : 1), two));
+      if (n <= (two ? 1 : 2)) umma_commit_if(leader, bar_q_empty);
+      // O of the segment before has been read
+      if (ok && seg > 0) ok = wait(bar_o_free, (seg - 1) & 1, ctl);
+      for (int i = 0; ok && i < steps0; ++i) {
+        ok = issue_pv(s0, pv0, base + place_v(two, two ? i : 2 * i, n), two, i == 0);
+        ++pv0;
+        if (ok && i + 1 < steps0) {
+          const int j = two ? i + 1 : 2 * i + 2;
+          ok = issue_qk(s0, pv0, base + place_k(two, j), two);
+          if (!two && j == n - 1) umma_commit_if(leader, bar_q_empty);  // the segment's last scores
+        }
+        if (ok && i < steps1) {
+          ok = issue_pv(s1, pv1, base + place_v(two, two ? i : 2 * i + 1, n), two, i == 0);
+          ++pv1;
+          if (ok && i + 1 < steps1) {
+            const int j = two ? i + 1 : 2 * i + 3;
+            ok = issue_qk(s1, pv1, base + place_k(two, j), two);
+            if (j == n - 1) umma_commit_if(leader, bar_q_empty);
           }
         }
-        base += 5u * n;
-        ++seg;
       }
-      umma_commit(bar_drain);  // arrives once every MMA issued above has completed
+      base += 5u * n;
+      ++seg;
     }
+    umma_commit_if(leader, bar_drain);  // arrives once every MMA issued above has completed
     __syncwarp();
   } else {
-    const int s = warp >> 2;                          // stream
+    const int s = warp >> 3, hf = (warp >> 2) & 1;    // stream, and which half of a row's scores
     const int r = (warp & 3) * 32 + lane;             // row of the tile, lane of tensor memory
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + kColS + 128u * s;
     const uint32_t to = tmem + lane_base + kColO;
+    float* xmax = reinterpret_cast<float*>(smem + kOffMax) + s * 2 * kTile + r;
     float* xchg = reinterpret_cast<float*>(smem + kOffXchg);
+    const int pair_bar = 1 + s * 4 + (warp & 3);      // the two warps that share rows
     uint32_t n_s = 0;  // score tiles taken
     bool ok = true;
     while (it.next(sg)) {
@@ -430,151 +513,168 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       if (p.visible) seen = real ? max(0, min(p.visible[t], p.prefix_len)) : 0;
       float other2 = -INFINITY;
       if (p.suffix_lse && real && sg.whole) other2 = p.suffix_lse[row] * kLog2e;
-      float m = -INFINITY, total = 0.f, used = 0.f;   // running maximum (log2), sums of the weights and of the rounded ones
-      for (int i = 0; ok && i < steps; ++i) {
+      float m = -INFINITY;                            // running maximum (log2)
+      float total = 0.f, used = 0.f;                  // this thread's sums of the weights and of the rounded ones
+      for (int i = 0; i < steps; ++i) {
         const int key0 = (sg.k0 + (two ? i : 2 * i + s)) * kTile;
-        ok = warp_wait(bar_s_full(s), n_s & 1, ctl);
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, wait(bar_s_full(s), n_s & 1, ctl));
         ++n_s;
         tc_fence_after();
-        // The scores are read twice, half a row at a time: holding all 128
-        // would leave no registers for the rest.  The second half first, so
-        // that the half still held is the one whose columns the first weights
-        // overwrite.
-        const int limit = seen - key0;                // keys of this tile the row sees
-        const bool ragged = __any_sync(0xffffffffu, limit < kTile);
-        uint32_t x[2][32];
-        auto load_half = [&](int half) {
-          tmem_ld32(ts + 64u * half, x[0]);
-          tmem_ld32(ts + 64u * half + 32u, x[1]);
+        // Keys [32 hf, 32 hf + 32) of the tile's first 64 and of its second.
+        // The second part is read twice: held across the step, it would push
+        // the thread over its 96 registers, into local memory.
+        const int limit = seen - key0 - 32 * hf;      // keys of this tile the row sees
+        const bool ragged = __any_sync(0xffffffffu, limit < 96);
+        uint32_t x[32];
+        auto load = [&](int c) {
+          tmem_ld32(ts + 64u * c + 32u * hf, x);
           tmem_wait_ld();
           if (ragged) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (64 * half + 32 * c + k >= limit) x[c][k] = 0xff800000u;  // -inf
+            for (int k = 0; k < 32; ++k)
+              if (64 * c + k >= limit) x[k] = 0xff800000u;  // -inf
           }
         };
-        auto half_max = [&]() -> float {
-          float a = __uint_as_float(x[0][0]), b = __uint_as_float(x[1][0]);
+        auto largest = [&]() -> float {
+          float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
 #pragma unroll
-          for (int k = 1; k < 32; ++k) {
-            a = fmaxf(a, __uint_as_float(x[0][k]));
-            b = fmaxf(b, __uint_as_float(x[1][k]));
+          for (int k = 2; k < 30; k += 4) {
+            a = fmaxf(fmaxf(a, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+            b = fmaxf(fmaxf(b, __uint_as_float(x[k + 2])), __uint_as_float(x[k + 3]));
           }
-          return fmaxf(a, b);
+          return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
         };
-        load_half(1);
-        float top = half_max();
-        load_half(0);
-        top = fmaxf(top, half_max());
-        top *= p.scale_log2;
+        load(1);
+        float top = largest();
+        load(0);
+        top = fmaxf(top, largest());
+        // The partner cannot write its next maximum before this one is read:
+        // its next scores wait for this warp's weights.
+        xmax[hf * kTile] = top;
+        ok = named_bar_all(pair_bar, 64, ok);         // votes: a wait that ran out in one warp ends both
+        if (!ok) break;
+        top = fmaxf(top, xmax[(hf ^ 1) * kTile]) * p.scale_log2;
         const bool move = top > m + kLazy;
-        float keep = 1.f;
-        if (move) {
-          keep = ex2_approx(m - top);
-          m = top;
+        // This step's scores were issued after the value product of the step
+        // before had completed: O is at rest and may be rescaled here, half
+        // of its columns by each of the row's threads.
+        if (__any_sync(0xffffffffu, move)) {
+          const float keep = move ? ex2_approx(m - top) : 1.f;
+          if (move) m = top;
           total *= keep;
           used *= keep;
-        }
-        // This step's scores were issued after the value product of the step
-        // before had completed: O is at rest and may be rescaled here.
-        if (i > 0 && __any_sync(0xffffffffu, move)) {
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[16];
+              const uint32_t at = to + 128u * s + 64u * hf + 16u * c;
+              tmem_ld16(at, o);
+              tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[16];
-            tmem_ld16(to + 128u * s + 16u * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-            tmem_st16(to + 128u * s + 16u * c, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+              tmem_st16(at, o);
+            }
           }
         }
         const float base = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet
+        const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), base2 = pack_f32x2(-base, -base);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) load_half(1);
-          uint32_t w[32];
-          float t0 = 0.f, t1 = 0.f, u0 = 0.f, u1 = 0.f;
+        for (int c = 0; c < 2; ++c) {
+          if (c == 1) load(1);
+          uint32_t w[16];
+          uint64_t t2 = 0;
+          float u0 = 0.f, u1 = 0.f;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float a = ex2_approx(fmaf(__uint_as_float(x[k / 16][2 * (k % 16)]), p.scale_log2, -base));
-            const float b = ex2_approx(fmaf(__uint_as_float(x[k / 16][2 * (k % 16) + 1]), p.scale_log2, -base));
-            t0 += a;
-            t1 += b;
-            w[k] = pack_f16x2(a, b);
+          for (int k = 0; k < 16; ++k) {
+            float a0, a1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2,
+                                   base2), a0, a1);
+            a0 = ex2_approx(a0);
+            a1 = ex2_approx(a1);
+            t2 = add_f32x2(t2, pack_f32x2(a0, a1));
+            w[k] = pack_f16x2(a0, a1);
             if (k & 1)
               u1 = add_f16x2_halves(u1, w[k]);
             else
               u0 = add_f16x2_halves(u0, w[k]);
           }
+          tmem_st16(ts + 32u * c + 16u * hf, w);
+          float t0, t1;
+          unpack_f32x2(t2, t0, t1);
           total += t0 + t1;
           used += u0 + u1;
-          tmem_st32(ts + 32u * half, w);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_p_full(s, c));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p_full(s));
       }
       // every value product of the stream in this segment (n_s counts them too)
-      if (ok && steps > 0) ok = warp_wait(bar_pv(s), (n_s - 1) & 1, ctl);
-      if (!two) {
-        float* mine = xchg + s * 3 * kTile + r;
-        mine[0] = m;
-        mine[kTile] = total;
-        mine[2 * kTile] = used;
-      }
-      // all softmax warps meet once per segment, so that a wait that ran out in one ends them all
-      ok = named_bar_all(1, kSoftmaxWarps * 32, ok);
-      if (!ok) break;
-      tc_fence_after();
-      // scale of each stream's O in the row's result
+      if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(bar_pv(s), (n_s - 1) & 1, ctl));
+      // The row's result: the sums of its two threads (two row tiles), or of
+      // the four of both streams, whose maxima differ.  All softmax warps vote,
+      // so that a wait that ran out in one ends them all.
       float f0, f1 = 0.f, lse2;
       if (two) {
+        xmax[hf * kTile] = total;
+        ok = named_bar_all(9, kSoftmaxWarps * 32, ok);
+        if (!ok) break;
+        total += xmax[(hf ^ 1) * kTile];
+        named_bar_sync(9, kSoftmaxWarps * 32);
+        xmax[hf * kTile] = used;
+        named_bar_sync(9, kSoftmaxWarps * 32);
+        used += xmax[(hf ^ 1) * kTile];
+        named_bar_sync(9, kSoftmaxWarps * 32);
         f0 = used == 0.f ? 0.f : 1.f / used;
         lse2 = total == 0.f ? -INFINITY : m + lg2(total);
       } else {
-        const float m0 = xchg[r], m1 = xchg[3 * kTile + r];
+        float* mine = xchg + (s * 2 + hf) * 3 * kTile + r;
+        mine[0] = m;
+        mine[kTile] = total;
+        mine[2 * kTile] = used;
+        ok = named_bar_all(9, kSoftmaxWarps * 32, ok);
+        if (!ok) break;
+        const float m0 = xchg[r], m1 = xchg[6 * kTile + r];
         const float top = fmaxf(m0, m1), base = top == -INFINITY ? 0.f : top;
         const float a0 = ex2_approx(m0 - base), a1 = ex2_approx(m1 - base);
-        const float sum = xchg[kTile + r] * a0 + xchg[4 * kTile + r] * a1;
-        const float u = xchg[2 * kTile + r] * a0 + xchg[5 * kTile + r] * a1;
+        const float sum = (xchg[kTile + r] + xchg[4 * kTile + r]) * a0 + (xchg[7 * kTile + r] + xchg[10 * kTile + r]) * a1;
+        const float u = (xchg[2 * kTile + r] + xchg[5 * kTile + r]) * a0 + (xchg[8 * kTile + r] + xchg[11 * kTile + r]) * a1;
         const float inv = u == 0.f ? 0.f : 1.f / u;
         f0 = a0 * inv;
         f1 = a1 * inv;
         lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
-        named_bar_sync(2, kSoftmaxWarps * 32);  // the exchange may be written again
+        named_bar_sync(9, kSoftmaxWarps * 32);  // the exchange may be written again
       }
+      tc_fence_after();
       Join j = {1.f, 0.f, lse2};
       if (p.suffix_lse && sg.whole) j = join(lse2, other2);
       const long long prow = (2ll * blockIdx.x + (sg.first ? 0 : 1)) * p.part_rows + brow;
-      // two row tiles: a stream's own O, all columns; one: both O's, half of the columns each
-      const int c0 = two ? 0 : 2 * s, c1 = two ? 4 : 2 * s + 2;
+      // two row tiles: a stream's own O, half of the columns each; one: both O's, a quarter each
+      const uint32_t c0 = two ? 64u * hf : 64u * s + 32u * hf, c1 = c0 + (two ? 64u : 32u);
       const bool second = !two && n > 1;
-      for (int c = c0; c < c1; ++c) {
-        uint32_t a[32], b[32];
-        tmem_ld32(to + (two ? 128u * s : 0u) + 32u * c, a);
-        if (second) tmem_ld32(to + 128u + 32u * c, b);
+#pragma unroll 1
+      for (uint32_t c = c0; c < c1; c += 16u) {
+        uint32_t a[16], b[16];
+        tmem_ld16(to + (two ? 128u * s : 0u) + c, a);
+        if (second) tmem_ld16(to + 128u + c, b);
         tmem_wait_ld();
         if (!real) continue;
-        float o[32];
+        float o[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
           o[k] = f0 == 0.f ? 0.f : __uint_as_float(a[k]) * f0;  // an accumulator that took nothing is not read as a number
           if (second && f1 != 0.f) o[k] = fmaf(__uint_as_float(b[k]), f1, o[k]);
         }
         if (sg.whole) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 8) write8(p, row, 32 * c + k, o + k, j);
+          write8(p, row, c, o, j);
+          write8(p, row, c + 8, o + 8, j);
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 32 * c);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + c);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      if (real && (two || s == 0)) {
+      if (real && hf == 0 && (two || s == 0)) {
         if (sg.whole)
           p.lse[row] = j.lse2 * kLn2;
         else
@@ -588,8 +688,8 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 9 * 32) drain_bar(bar_drain, 0u);  // MMAs finish before TMEM is released
-  if (threadIdx.x == 8 * 32 && *abort_flag) {
+  if (threadIdx.x == kMmaWarp * 32) drain_bar(bar_drain, 0u);  // MMAs finish before TMEM is released
+  if (threadIdx.x == kTmaWarp * 32 && *abort_flag) {
     // teardown after a wait ran out: loads still in flight land before the CTA exits
     for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued; ++c)
       drain_bar(full(c % kSlots), (c / kSlots) & 1);
@@ -597,7 +697,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -623,9 +723,10 @@ __global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_co
   const int g1 = static_cast<int>((end * w.groups + w.line - 1) / w.line) - 1;
   const bool work = real && g0 < g1;
   const int n = g1 - g0 + 1;
+  // a range's first segment has its even slot: only the head's first piece may be another's last segment
+  const int odd = work && cut(w, g0) < start ? 1 : 0;
   auto piece = [&](int i) {  // row of piece i among the partial rows
-    const int g = g0 + i;
-    const int slot = 2 * (g * w.width + lane_block) + (cut(w, g) < start ? 1 : 0);
+    const int slot = 2 * ((g0 + i) * w.width + lane_block) + (i == 0 ? odd : 0);
     return static_cast<long long>(slot) * p.part_rows + brow;
   };
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -633,10 +734,12 @@ __global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_co
   if (work) {
     if (p.suffix_lse) other2 = p.suffix_lse[row] * kLog2e;
     float top = -INFINITY;
+#pragma unroll 1
     for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_lse[piece(i)]);
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
+#pragma unroll 1
     for (int i = lane; i < n; i += 32) sum += ex2_approx(p.part_lse[piece(i)] - base);
     for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

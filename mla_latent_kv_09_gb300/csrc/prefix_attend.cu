@@ -22,8 +22,11 @@
 //                   value product reads them as its A operand
 //   warp 16         TMA: the block's queries (96 KiB), then key and value
 //                   chunks of 16 KiB through a ring of 8 slots
-//   warp 17         tcgen05.mma: S = Q K^T (12 steps of M128 N128 K16, bf16),
-//                   O += P V (8 steps, fp16)
+//   warps 17, 18    tcgen05.mma for stream 0, 1: S = Q K^T (12 steps of M128
+//                   N128 K16, bf16), O += P V (8 steps, fp16).  The tensor
+//                   core takes an MMA every 64 cycles and queues few, so a
+//                   wait of the issuing thread (100 to 250 cycles) is time
+//                   lost; two issuers fill each other's
 //
 // A step's chain is scores -> softmax -> value product -> next scores (the
 // weights lie where the next scores go); the other stream fills the tensor
@@ -48,7 +51,6 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
-#include <type_traits>
 
 #include "kernel_common.cuh"
 #include "mla_prefix.h"
@@ -65,15 +67,15 @@ constexpr int kQChunks = 3;                 // 64-dim chunks of a query or key r
 constexpr int kQTile = kQChunks * kSlot;    // 48 KiB
 constexpr int kOffRing = 2 * kQTile;        // 96 KiB
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
-constexpr int kNumBars = 2 * kSlots + 12;
+constexpr int kNumBars = 8 + 12;
 constexpr int kOffMax = kOffBar + kNumBars * 8 + 16;  // [stream][half][row]: exchange between a row's two threads
 constexpr int kSmem = kOffMax + 4 * kTile * 4;        // no room to re-align: the base must lie on 1024 B (checked)
 static_assert(kSmem <= 232448, "shared memory");
 // the threads of a row of a one-tile block exchange their sums in the second row tile's query space
 constexpr int kOffXchg = kQTile;
-constexpr int kThreads = 576;
+constexpr int kThreads = 608;
 constexpr int kSoftmaxWarps = 16;
-constexpr int kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kTmaWarp = 16, kMmaWarp = 17;  // and 18, for the second stream
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;  // + 128 * stream
 constexpr uint32_t kIdescQK = idesc_bf16(128, 128, 0);
@@ -291,9 +293,12 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   }
 
   const uint32_t bar0 = sbase + kOffBar;
-  auto full = [&](int s) { return bar0 + 8u * s; };
-  auto empty = [&](int s) { return bar0 + 8u * (kSlots + s); };
-  const uint32_t bar_q_full = bar0 + 8u * (2 * kSlots), bar_q_empty = bar_q_full + 8u;
+  // key (value) tile q of the CTA's run, by q & 1: landed, and used by every stream that uses it
+  auto k_full = [&](uint32_t q) { return bar0 + 8u * (q & 1u); };
+  auto k_empty = [&](uint32_t q) { return bar0 + 16u + 8u * (q & 1u); };
+  auto v_full = [&](uint32_t q) { return bar0 + 32u + 8u * (q & 1u); };
+  auto v_empty = [&](uint32_t q) { return bar0 + 48u + 8u * (q & 1u); };
+  const uint32_t bar_q_full = bar0 + 64u, bar_q_empty = bar_q_full + 8u;
   auto bar_s_full = [&](int s) { return bar_q_full + 8u * (2 + s); };  // scores of a stream are in tensor memory
   auto bar_p_full = [&](int s, int half) { return bar_q_full + 8u * (4 + 2 * s + half); };  // its weights are
   auto bar_pv = [&](int s) { return bar_q_full + 8u * (8 + s); };      // its value product is done
@@ -303,7 +308,14 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   auto slot_addr = [&](uint32_t n) { return sbase + static_cast<uint32_t>(kOffRing) + (n % kSlots) * kSlot; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * kSlots + 2; ++i) mbar_init(bar0 + 8u * i, 1);
+    for (uint32_t q = 0; q < 2; ++q) {
+      mbar_init(k_full(q), 1);
+      mbar_init(k_empty(q), 2);
+      mbar_init(v_full(q), 1);
+      mbar_init(v_empty(q), 2);
+    }
+    mbar_init(bar_q_full, 1);
+    mbar_init(bar_q_empty, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_s_full(s), 1);
       mbar_init(bar_p_full(s, 0), kSoftmaxWarps / 2);
@@ -311,7 +323,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       mbar_init(bar_pv(s), 1);
     }
     mbar_init(bar_o_free, kSoftmaxWarps);
-    mbar_init(bar_drain, 1);
+    mbar_init(bar_drain, 2);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -331,16 +343,18 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
 
   grid_dependency_wait();
   SegmentIter it(p);
-  Segment sg;
+  Segment sg{};
 
-  // Chunks enter the ring in the order the MMAs use them.  Two row tiles: K0
+  // Tiles enter the ring in the order the MMAs use them.  Two row tiles: K0
   // V0 K1 V1 ..; one row tile, key tiles alternating between the streams: K0
   // K1 V0 K2 V1 K3 ..  A key tile is three chunks, a value tile two; these are
-  // the places of tile j's first chunk in a segment of n tiles.
+  // the places of tile j's first chunk in a segment of n tiles.  Eight slots
+  // hold at most two key and two value tiles at a time, hence two barriers
+  // for each.
   auto place_k = [](bool two, int j) { return two ? 5 * j : (j < 2 ? 3 * j : 5 * j - 2); };
   auto place_v = [](bool two, int j, int n) { return two ? 5 * j + 3 : (j == n - 1 ? 5 * n - 2 : 5 * j + 6); };
 
-  uint32_t issued = 0;  // chunks requested so far (TMA warp)
+  uint32_t issued = 0, k_issued = 0, v_issued = 0;  // chunks and tiles requested so far (TMA warp)
   int q_loads = 0;
   if (warp == kTmaWarp) {
     if (lane == 0) {
@@ -350,31 +364,47 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       tma_prefetch_desc(&tm_kp);
       tma_prefetch_desc(&tm_v);
       bool ok = true;
-      auto slot_ready = [&]() -> bool {  // the next slot's previous chunk has been used
-        return issued < kSlots || wait(empty(issued % kSlots), ((issued / kSlots) - 1) & 1, ctl);
-      };
-      auto load_k = [&](int tile) -> bool {
-#pragma unroll 1
-        for (int c = 0; c < kQChunks; ++c) {
-          if (!slot_ready()) return false;
-          const uint32_t bar = full(issued % kSlots);
-          mbar_arrive_expect_tx(bar, kSlot);
-          if (c < 2)
-            tma_load_4d(slot_addr(issued), &tm_k, 0, tile * kTile, c, sg.h, bar);
-          else
-            tma_load_2d(slot_addr(issued), &tm_kp, 0, tile * kTile, bar);
-          ++issued;
+      // tiles in the ring: the oldest one's first chunk, how many of each kind
+      // have left, and their kinds in order (bit 0 the oldest, 1 = value)
+      uint32_t oldest = 0, k_left = 0, v_left = 0, kinds = 0, held = 0;
+      auto make_room = [&](uint32_t chunks) -> bool {
+        while (held > 0 && oldest + kSlots < issued + chunks) {
+          if (kinds & 1u) {
+            if (!wait(v_empty(v_left), (v_left >> 1) & 1, ctl)) return false;
+            ++v_left;
+            oldest += 2;
+          } else {
+            if (!wait(k_empty(k_left), (k_left >> 1) & 1, ctl)) return false;
+            ++k_left;
+            oldest += 3;
+          }
+          kinds >>= 1;
+          --held;
         }
         return true;
       };
+      auto load_k = [&](int tile) -> bool {
+        if (!make_room(3)) return false;
+        const uint32_t bar = k_full(k_issued);
+        mbar_arrive_expect_tx(bar, kQTile);
+        tma_load_4d(slot_addr(issued), &tm_k, 0, tile * kTile, 0, sg.h, bar);
+        tma_load_4d(slot_addr(issued + 1), &tm_k, 0, tile * kTile, 1, sg.h, bar);
+        tma_load_2d(slot_addr(issued + 2), &tm_kp, 0, tile * kTile, bar);
+        issued += 3;
+        ++k_issued;
+        ++held;
+        return true;
+      };
       auto load_v = [&](int tile) -> bool {
-        for (int c = 0; c < 2; ++c) {
-          if (!slot_ready()) return false;
-          const uint32_t bar = full(issued % kSlots);
-          mbar_arrive_expect_tx(bar, kSlot);
-          tma_load_4d(slot_addr(issued), &tm_v, 0, tile * kTile + 64 * c, 0, sg.h, bar);
-          ++issued;
-        }
+        if (!make_room(2)) return false;
+        const uint32_t bar = v_full(v_issued);
+        mbar_arrive_expect_tx(bar, 2 * kSlot);
+        tma_load_4d(slot_addr(issued), &tm_v, 0, tile * kTile, 0, sg.h, bar);
+        tma_load_4d(slot_addr(issued + 1), &tm_v, 0, tile * kTile + 64, 0, sg.h, bar);
+        issued += 2;
+        ++v_issued;
+        kinds |= 1u << held;
+        ++held;
         return true;
       };
       while (ok && it.next(sg)) {
@@ -403,89 +433,76 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       grid_launch_dependents();
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // The whole warp runs this loop and one lane issues, by predicates: the
     // operands stay warp-uniform, and so in uniform registers.  (Issued from a
-    // divergent branch, with the counters in local memory, the 20 MMAs and 9
-    // waits of a step took 3,600 cycles against the tensor cores' 1,280.)
+    // divergent branch, with the counters in local memory, the 20 MMAs of a
+    // step took 3,600 cycles against the tensor cores' 1,280.)
     const uint32_t leader = lane == 0 ? 1u : 0u;
+    const uint32_t s = warp - kMmaWarp;  // stream
     const uint64_t ring_k = smem_desc(sbase + kOffRing, 16u, 1024u), ring_v = smem_desc(sbase + kOffRing, 8192u, 1024u);
-    const uint64_t q_desc = smem_desc(sbase, 16u, 1024u);
-    uint32_t base = 0;             // chunks of the segments before this one
-    uint32_t pv0 = 0, pv1 = 0;     // value products issued per stream
+    const uint32_t t_s = tmem + kColS + 128u * s, t_o = tmem + kColO + 128u * s;
+    uint32_t base = 0, tiles = 0;  // chunks, key tiles of the segments before this one
+    uint32_t n_pv = 0;             // value products issued
     uint32_t seg = 0;
     bool ok = true;
-    auto wait_chunk = [&](uint32_t c) { return wait(full(c % kSlots), (c / kSlots) & 1, ctl); };
     auto slot_off = [](uint32_t c) { return static_cast<uint64_t>(c % kSlots) * (kSlot >> 4); };
-    // Scores of stream s from the key chunks c0 ..; n_pv: value products the
-    // stream has had.  S holds the weights of the step before until its value
-    // product is done.
-    auto issue_qk = [&](auto stream, uint32_t n_pv, uint32_t c0, bool two) -> bool {
-      constexpr int s = decltype(stream)::value;
-      if (n_pv > 0 && !wait(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
-      const uint64_t ad = q_desc + (two && s == 1 ? kQTile >> 4 : 0);
-      const uint32_t release = !two || s == 1 ? leader : 0u;
-#pragma unroll
-      for (int c = 0; c < kQChunks; ++c) {
-        if (!wait_chunk(c0 + c)) return false;
-        tc_fence_after();
-        const uint64_t bd = ring_k + slot_off(c0 + c);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ss_if(leader, tmem + kColS + 128u * s, ad + ((c * kSlot + 32 * kk) >> 4), bd + ((32 * kk) >> 4),
-                     kIdescQK, (c | kk) != 0 ? 1u : 0u);
-        umma_commit_if(release, empty((c0 + c) % kSlots));
-      }
-      umma_commit_if(leader, bar_s_full(s));
-      return true;
-    };
-    auto issue_pv = [&](auto stream, uint32_t n_pv, uint32_t c0, bool two, bool first) -> bool {
-      constexpr int s = decltype(stream)::value;
-      const uint32_t release = !two || s == 1 ? leader : 0u;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (!wait_chunk(c0 + c) || !wait(bar_p_full(s, c), n_pv & 1, ctl)) return false;
-        tc_fence_after();
-        const uint64_t bd = ring_v + slot_off(c0 + c);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ts_if(leader, tmem + kColO + 128u * s, tmem + kColS + 128u * s + 32u * c + 8u * kk,
-                     bd + ((2048 * kk) >> 4), kIdescPV, first && (c | kk) == 0 ? 0u : 1u);
-        umma_commit_if(release, empty((c0 + c) % kSlots));
-      }
-      umma_commit_if(leader, bar_pv(s));
-      return true;
-    };
-    const std::integral_constant<int, 0> s0{};
-    const std::integral_constant<int, 1> s1{};
     while (ok && it.next(sg)) {
       const bool two = sg.rows > kTile;
       const int n = sg.k1 - sg.k0;
-      const int steps0 = two ? n : (n + 1) / 2, steps1 = two ? n : n / 2;
-      ok = wait(bar_q_full, seg & 1, ctl) && issue_qk(s0, pv0, base, two) &&
-           (steps1 == 0 || issue_qk(s1, pv1, base + place_k(two, two ? 0 : 1), two));
-      if (n <= (two ? 1 : 2)) umma_commit_if(leader, bar_q_empty);
+      const int steps = two ? n : (n + 1 - static_cast<int>(s)) / 2;
+      const uint64_t ad = smem_desc(sbase + (two ? s * kQTile : 0u), 16u, 1024u);
+      // Scores of key tile j.  S holds the weights of the step before until
+      // its value product is done.
+      auto issue_qk = [&](int j) -> bool {
+        const uint32_t c0 = base + place_k(two, j), q = tiles + j;
+        if (!wait(k_full(q), (q >> 1) & 1, ctl)) return false;
+        if (n_pv > 0 && !wait(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kQChunks; ++c) {
+          const uint64_t bd = ring_k + slot_off(c0 + c);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ss_if(leader, t_s, ad + ((c * kSlot + 32 * kk) >> 4), bd + ((32 * kk) >> 4), kIdescQK,
+                       (c | kk) != 0 ? 1u : 0u);
+        }
+        umma_commit_if(leader, bar_s_full(s));
+        umma_commit_if(leader, k_empty(q));
+        if (!two) umma_commit_if(leader, k_empty(q));  // for the stream that does not use this tile
+        return true;
+      };
+      ok = wait(bar_q_full, seg & 1, ctl) && (steps == 0 || issue_qk(two ? 0 : s));
+      if (steps <= 1) umma_commit_if(leader, bar_q_empty);
       // O of the segment before has been read
       if (ok && seg > 0) ok = wait(bar_o_free, (seg - 1) & 1, ctl);
-      for (int i = 0; ok && i < steps0; ++i) {
-        ok = issue_pv(s0, pv0, base + place_v(two, two ? i : 2 * i, n), two, i == 0);
-        ++pv0;
-        if (ok && i + 1 < steps0) {
-          const int j = two ? i + 1 : 2 * i + 2;
-          ok = issue_qk(s0, pv0, base + place_k(two, j), two);
-          if (!two && j == n - 1) umma_commit_if(leader, bar_q_empty);  // the segment's last scores
+      for (int i = 0; ok && i < steps; ++i) {
+        const int j = two ? i : 2 * i + static_cast<int>(s);
+        const uint32_t c0 = base + place_v(two, j, n), q = tiles + j;
+        ok = wait(v_full(q), (q >> 1) & 1, ctl);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          ok = ok && wait(bar_p_full(s, c), n_pv & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bd = ring_v + slot_off(c0 + c);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts_if(leader, t_o, t_s + 32u * c + 8u * kk, bd + ((2048 * kk) >> 4), kIdescPV,
+                       i == 0 && (c | kk) == 0 ? 0u : 1u);
         }
-        if (ok && i < steps1) {
-          ok = issue_pv(s1, pv1, base + place_v(two, two ? i : 2 * i + 1, n), two, i == 0);
-          ++pv1;
-          if (ok && i + 1 < steps1) {
-            const int j = two ? i + 1 : 2 * i + 3;
-            ok = issue_qk(s1, pv1, base + place_k(two, j), two);
-            if (j == n - 1) umma_commit_if(leader, bar_q_empty);
-          }
+        if (!ok) break;
+        umma_commit_if(leader, bar_pv(s));
+        umma_commit_if(leader, v_empty(q));
+        if (!two) umma_commit_if(leader, v_empty(q));
+        ++n_pv;
+        if (i + 1 < steps) {
+          ok = issue_qk(two ? i + 1 : j + 2);
+          if (i + 2 == steps) umma_commit_if(leader, bar_q_empty);  // the segment's last scores
         }
       }
       base += 5u * n;
+      tiles += n;
       ++seg;
     }
     umma_commit_if(leader, bar_drain);  // arrives once every MMA issued above has completed
@@ -691,8 +708,8 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   if (threadIdx.x == kMmaWarp * 32) drain_bar(bar_drain, 0u);  // MMAs finish before TMEM is released
   if (threadIdx.x == kTmaWarp * 32 && *abort_flag) {
     // teardown after a wait ran out: loads still in flight land before the CTA exits
-    for (uint32_t c = issued > kSlots ? issued - kSlots : 0; c < issued; ++c)
-      drain_bar(full(c % kSlots), (c / kSlots) & 1);
+    for (uint32_t q = k_issued > 2 ? k_issued - 2 : 0; q < k_issued; ++q) drain_bar(k_full(q), (q >> 1) & 1);
+    for (uint32_t q = v_issued > 2 ? v_issued - 2 : 0; q < v_issued; ++q) drain_bar(v_full(q), (q >> 1) & 1);
     if (q_loads > 0) drain_bar(bar_q_full, (q_loads - 1) & 1);
   }
   tc_fence_before();

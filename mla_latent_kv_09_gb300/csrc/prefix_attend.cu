@@ -62,16 +62,18 @@ constexpr int kHeadDim = 128;
 constexpr int kRope = 64;
 constexpr int kTile = 128;                  // query rows of a row tile, keys of a key tile
 constexpr int kSlot = 16384;                // a key chunk (128 keys x 64 dims) or half a value tile (64 keys x 128 dims)
-constexpr int kSlots = 8;
 constexpr int kQChunks = 3;                 // 64-dim chunks of a query or key row
 constexpr int kQTile = kQChunks * kSlot;    // 48 KiB
-constexpr int kOffRing = 2 * kQTile;        // 96 KiB
-constexpr int kOffBar = kOffRing + kSlots * kSlot;
+// Up to 128 tokens one query tile and a ring of 10 slots (two key and two
+// value tiles), above two query tiles and 8 slots.
+constexpr int ring_slots(bool small) { return small ? 10 : 8; }
+constexpr int kOffBar = 14 * kSlot;         // 224 KiB
+constexpr int ring_offset(bool small) { return kOffBar - ring_slots(small) * kSlot; }
 constexpr int kNumBars = 8 + 12;
 constexpr int kOffMax = kOffBar + kNumBars * 8 + 16;  // [stream][half][row]: exchange between a row's two threads
 constexpr int kSmem = kOffMax + 4 * kTile * 4;        // no room to re-align: the base must lie on 1024 B (checked)
 static_assert(kSmem <= 232448, "shared memory");
-// the threads of a row of a one-tile block exchange their sums in the second row tile's query space
+// the threads of a row of a one-tile block exchange their sums behind the first query tile
 constexpr int kOffXchg = kQTile;
 constexpr int kThreads = 608;
 constexpr int kSoftmaxWarps = 16;
@@ -127,6 +129,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       " [%0], [%1, {%2, %3, %4, %5}], [%6];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+// Arrive `n` times.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
 // Predicated forms for a warp of which one lane issues: D (+)= A B^T with A
@@ -279,6 +286,8 @@ __device__ __forceinline__ void write8(const AttendParams& p, long long row, int
   }
 }
 
+// kSmall: up to 128 tokens, one row tile.
+template <bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
 mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap tm_qn,
                          const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_k,
@@ -305,7 +314,8 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   const uint32_t bar_o_free = bar_q_full + 8u * 10, bar_drain = bar_q_full + 8u * 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
-  auto slot_addr = [&](uint32_t n) { return sbase + static_cast<uint32_t>(kOffRing) + (n % kSlots) * kSlot; };
+  constexpr uint32_t kSlots = ring_slots(kSmall), kOffRing = ring_offset(kSmall);
+  auto slot_addr = [&](uint32_t n) { return sbase + kOffRing + (n % kSlots) * kSlot; };
 
   if (threadIdx.x == 0) {
     for (uint32_t q = 0; q < 2; ++q) {
@@ -348,8 +358,8 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   // Tiles enter the ring in the order the MMAs use them.  Two row tiles: K0
   // V0 K1 V1 ..; one row tile, key tiles alternating between the streams: K0
   // K1 V0 K2 V1 K3 ..  A key tile is three chunks, a value tile two; these are
-  // the places of tile j's first chunk in a segment of n tiles.  Eight slots
-  // hold at most two key and two value tiles at a time, hence two barriers
+  // the places of tile j's first chunk in a segment of n tiles.  At most
+  // two key and two value tiles are in the ring at a time, hence two barriers
   // for each.
   auto place_k = [](bool two, int j) { return two ? 5 * j : (j < 2 ? 3 * j : 5 * j - 2); };
   auto place_v = [](bool two, int j, int n) { return two ? 5 * j + 3 : (j == n - 1 ? 5 * n - 2 : 5 * j + 6); };
@@ -367,8 +377,8 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       // tiles in the ring: the oldest one's first chunk, how many of each kind
       // have left, and their kinds in order (bit 0 the oldest, 1 = value)
       uint32_t oldest = 0, k_left = 0, v_left = 0, kinds = 0, held = 0;
-      auto make_room = [&](uint32_t chunks) -> bool {
-        while (held > 0 && oldest + kSlots < issued + chunks) {
+      auto make_room = [&](uint32_t chunks, const uint32_t& requested, const uint32_t& left) -> bool {
+        while (held > 0 && (oldest + kSlots < issued + chunks || requested - left >= 2)) {
           if (kinds & 1u) {
             if (!wait(v_empty(v_left), (v_left >> 1) & 1, ctl)) return false;
             ++v_left;
@@ -384,7 +394,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         return true;
       };
       auto load_k = [&](int tile) -> bool {
-        if (!make_room(3)) return false;
+        if (!make_room(3, k_issued, k_left)) return false;
         const uint32_t bar = k_full(k_issued);
         mbar_arrive_expect_tx(bar, kQTile);
         tma_load_4d(slot_addr(issued), &tm_k, 0, tile * kTile, 0, sg.h, bar);
@@ -396,7 +406,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         return true;
       };
       auto load_v = [&](int tile) -> bool {
-        if (!make_room(2)) return false;
+        if (!make_room(2, v_issued, v_left)) return false;
         const uint32_t bar = v_full(v_issued);
         mbar_arrive_expect_tx(bar, 2 * kSlot);
         tma_load_4d(slot_addr(issued), &tm_v, 0, tile * kTile, 0, sg.h, bar);
@@ -408,7 +418,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         return true;
       };
       while (ok && it.next(sg)) {
-        const bool two = sg.rows > kTile;
+        const bool two = !kSmall && sg.rows > kTile;
         if (q_loads > 0 && !wait(bar_q_empty, (q_loads - 1) & 1, ctl)) break;
         mbar_arrive_expect_tx(bar_q_full, two ? 2 * kQTile : kQTile);
         for (int r = 0; r < (two ? 2 : 1); ++r) {
@@ -447,8 +457,19 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
     uint32_t seg = 0;
     bool ok = true;
     auto slot_off = [](uint32_t c) { return static_cast<uint64_t>(c % kSlots) * (kSlot >> 4); };
+    // Waits for the last value product and gives its tile back (for both
+    // streams, where only one uses it): a commit per tile and stream cost 125
+    // cycles of the issuing thread each, an arrive 20.
+    uint32_t v_held = 0;           // its barrier, 0: given back
+    auto release_v = [&](bool two) -> bool {
+      if (v_held == 0) return true;
+      if (!wait(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
+      if (leader) mbar_arrive_n(v_held, two ? 1 : 2);
+      v_held = 0;
+      return true;
+    };
     while (ok && it.next(sg)) {
-      const bool two = sg.rows > kTile;
+      const bool two = !kSmall && sg.rows > kTile;
       const int n = sg.k1 - sg.k0;
       const int steps = two ? n : (n + 1 - static_cast<int>(s)) / 2;
       const uint64_t ad = smem_desc(sbase + (two ? s * kQTile : 0u), 16u, 1024u);
@@ -457,7 +478,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       auto issue_qk = [&](int j) -> bool {
         const uint32_t c0 = base + place_k(two, j), q = tiles + j;
         if (!wait(k_full(q), (q >> 1) & 1, ctl)) return false;
-        if (n_pv > 0 && !wait(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
+        if (!release_v(two)) return false;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kQChunks; ++c) {
@@ -468,8 +489,6 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
                        (c | kk) != 0 ? 1u : 0u);
         }
         umma_commit_if(leader, bar_s_full(s));
-        umma_commit_if(leader, k_empty(q));
-        if (!two) umma_commit_if(leader, k_empty(q));  // for the stream that does not use this tile
         return true;
       };
       ok = wait(bar_q_full, seg & 1, ctl) && (steps == 0 || issue_qk(two ? 0 : s));
@@ -493,14 +512,14 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         }
         if (!ok) break;
         umma_commit_if(leader, bar_pv(s));
-        umma_commit_if(leader, v_empty(q));
-        if (!two) umma_commit_if(leader, v_empty(q));
+        v_held = v_empty(q);
         ++n_pv;
         if (i + 1 < steps) {
           ok = issue_qk(two ? i + 1 : j + 2);
           if (i + 2 == steps) umma_commit_if(leader, bar_q_empty);  // the segment's last scores
         }
       }
+      ok = ok && release_v(two);
       base += 5u * n;
       tiles += n;
       ++seg;
@@ -516,20 +535,17 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
     float* xmax = reinterpret_cast<float*>(smem + kOffMax) + s * 2 * kTile + r;
     float* xchg = reinterpret_cast<float*>(smem + kOffXchg);
     const int pair_bar = 1 + s * 4 + (warp & 3);      // the two warps that share rows
-    uint32_t n_s = 0;  // score tiles taken
+    uint32_t n_s = 0;    // score tiles taken
+    uint32_t tiles = 0;  // key tiles of the segments before this one
     bool ok = true;
     while (it.next(sg)) {
-      const bool two = sg.rows > kTile;
+      const bool two = !kSmall && sg.rows > kTile;
       const int n = sg.k1 - sg.k0;
       const int steps = two ? n : (s == 0 ? (n + 1) / 2 : n / 2);
       const int brow = two ? s * kTile + r : r;       // row within the block
-      const int t = sg.block * 2 * kTile + brow;
       const bool real = brow < sg.rows;
-      const long long row = static_cast<long long>(t) * p.num_heads + sg.h;
       int seen = p.prefix_len;
-      if (p.visible) seen = real ? max(0, min(p.visible[t], p.prefix_len)) : 0;
-      float other2 = -INFINITY;
-      if (p.suffix_lse && real && sg.whole) other2 = p.suffix_lse[row] * kLog2e;
+      if (p.visible) seen = real ? max(0, min(p.visible[sg.block * 2 * kTile + brow], p.prefix_len)) : 0;
       float m = -INFINITY;                            // running maximum (log2)
       float total = 0.f, used = 0.f;                  // this thread's sums of the weights and of the rounded ones
       for (int i = 0; i < steps; ++i) {
@@ -537,22 +553,21 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         ok = __all_sync(0xffffffffu, wait(bar_s_full(s), n_s & 1, ctl));
         ++n_s;
         tc_fence_after();
+        // the key tile has been read: its slots may be filled again
+        if (lane == 0 && (warp & 7) == 0) mbar_arrive_n(k_empty(tiles + (two ? i : 2 * i + s)), two ? 1 : 2);
         // Keys [32 hf, 32 hf + 32) of the tile's first 64 and of its second.
         // The second part is read twice: held across the step, it would push
         // the thread over its 96 registers, into local memory.
         const int limit = seen - key0 - 32 * hf;      // keys of this tile the row sees
-        const bool ragged = __any_sync(0xffffffffu, limit < 96);
-        uint32_t x[32];
-        auto load = [&](int c) {
-          tmem_ld32(ts + 64u * c + 32u * hf, x);
-          tmem_wait_ld();
-          if (ragged) {
+        // A row that sees none of them needs no masks (its weights become
+        // zeros below): only rows that end in this tile do.
+        const bool ragged = __any_sync(0xffffffffu, limit > 0 && limit < 96);
+        auto mask = [&](uint32_t (&x)[32], int c) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (64 * c + k >= limit) x[k] = 0xff800000u;  // -inf
-          }
+          for (int k = 0; k < 32; ++k)
+            if (64 * c + k >= limit) x[k] = 0xff800000u;  // -inf
         };
-        auto largest = [&]() -> float {
+        auto largest = [](const uint32_t (&x)[32]) -> float {
           float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
 #pragma unroll
           for (int k = 2; k < 30; k += 4) {
@@ -561,10 +576,16 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
           }
           return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
         };
-        load(1);
-        float top = largest();
-        load(0);
-        top = fmaxf(top, largest());
+        uint32_t x[32];
+        tmem_ld32(ts + 64u + 32u * hf, x);
+        tmem_wait_ld();
+        if (ragged) mask(x, 1);
+        float top = largest(x);
+        tmem_ld32(ts + 32u * hf, x);
+        tmem_wait_ld();
+        if (ragged) mask(x, 0);
+        top = fmaxf(top, largest(x));
+        if (limit <= 0) top = -INFINITY;
         // The partner cannot write its next maximum before this one is read:
         // its next scores wait for this warp's weights.
         xmax[hf * kTile] = top;
@@ -593,11 +614,16 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
             }
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet
+        // +inf makes every weight of a row that sees none of these keys zero, 0 those of one that saw none yet
+        const float base = limit <= 0 ? INFINITY : (m == -INFINITY ? 0.f : m);
         const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), base2 = pack_f32x2(-base, -base);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if (c == 1) load(1);
+          if (c == 1) {
+            tmem_ld32(ts + 64u + 32u * hf, x);
+            tmem_wait_ld();
+            if (ragged) mask(x, 1);
+          }
           uint32_t w[16];
           uint64_t t2 = 0;
           float u0 = 0.f, u1 = 0.f;
@@ -626,6 +652,10 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
           if (lane == 0) mbar_arrive(bar_p_full(s, c));
         }
       }
+      tiles += n;
+      const long long row = static_cast<long long>(sg.block * 2 * kTile + brow) * p.num_heads + sg.h;
+      float other2 = -INFINITY;
+      if (p.suffix_lse && real && sg.whole) other2 = p.suffix_lse[row] * kLog2e;
       // every value product of the stream in this segment (n_s counts them too)
       if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(bar_pv(s), (n_s - 1) & 1, ctl));
       // The row's result: the sums of its two threads (two row tiles), or of
@@ -881,8 +911,10 @@ int attend_device_ready(int* sms) {
       st.status = MLA_ERR_DEVICE;
       return;
     }
-    if (cudaFuncSetAttribute(mla_prefix_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
-        cudaSuccess) {
+    if (cudaFuncSetAttribute(mla_prefix_attend_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(mla_prefix_attend_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            cudaSuccess) {
       cudaGetLastError();
       st.status = MLA_ERR_CUDA;
     }
@@ -1028,7 +1060,7 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
       !encode_kv(&vm, true, v, prefix_len, head_rows, num_heads, kTile / 2, 2))
     return MLA_ERR_CUDA;
   const int ctas = p.plan.groups * p.plan.width;
-  rc = launch_dependent(mla_prefix_attend_kernel, dim3(ctas), dim3(kThreads), kSmem, stream, p, qn, qp, k, kp, vm);
+  rc = launch_dependent(num_tokens <= kTile ? mla_prefix_attend_kernel<true> : mla_prefix_attend_kernel<false>, dim3(ctas), dim3(kThreads), kSmem, stream, p, qn, qp, k, kp, vm);
   // heads are cut wherever a range does not end with one
   if (rc != MLA_OK || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
   // pieces a head can be cut in: the ranges that overlap its nk steps

@@ -750,35 +750,38 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   }
 }
 
-// Joins the partial rows of heads that were cut.  kWarps warps per (token,
-// head): a warp takes every kWarps-th piece, a lane four columns.
+// Joins the partial rows of the (row block, head)s that were cut.  Block
+// (g, lane block, chunk): the unit that the range of group g starts inside of,
+// if no earlier range does; 4 / kWarps of its rows, kWarps warps a row (a warp
+// takes every kWarps-th piece), four columns a lane.
 template <int kWarps>
 __global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_constant__ AttendParams p) {
   __shared__ float4 acc[4][32];
   const Plan& w = p.plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % kWarps;
-  const long long row = static_cast<long long>(blockIdx.x) * (4 / kWarps) + warp / kWarps;
-  grid_dependency_wait();
-  const bool real = row < static_cast<long long>(p.num_tokens) * p.num_heads;
-  const int t = static_cast<int>(row / p.num_heads), h = static_cast<int>(row % p.num_heads);
-  const int block = t / (2 * kTile), brow = t % (2 * kTile);
-  const int unit = block / w.width * p.num_heads + h, lane_block = block % w.width;
+  const int g = blockIdx.x + 1, lane_block = blockIdx.y;
+  const long long at = cut(w, g);
+  const int unit = static_cast<int>(at / w.nk);
   const long long start = static_cast<long long>(unit) * w.nk, end = start + w.nk;
-  // the group whose range [cut(g), cut(g + 1)) holds a step x is the last with cut(g) <= x
-  const int g0 = static_cast<int>(((start + 1) * w.groups + w.line - 1) / w.line) - 1;
-  const int g1 = static_cast<int>((end * w.groups + w.line - 1) / w.line) - 1;
-  const bool work = real && g0 < g1;
-  const int n = g1 - g0 + 1;
-  // a range's first segment has its even slot: only the head's first piece may be another's last segment
-  const int odd = work && cut(w, g0) < start ? 1 : 0;
+  if (at == start || cut(w, g - 1) > start) return;  // starts with the unit, or an earlier range is inside of it
+  const int block = unit / p.num_heads * w.width + lane_block, h = unit % p.num_heads;
+  if (block >= w.blocks) return;
+  const int g0 = g - 1;  // holds the unit's first step, as its first segment or, after another, its second
+  const int odd = cut(w, g0) < start ? 1 : 0;
+  int n = 2;
+  while (cut(w, g0 + n) < end) ++n;
+  grid_dependency_wait();
+  const int brow = blockIdx.z * (4 / kWarps) + warp / kWarps, t = block * 2 * kTile + brow;
+  const bool real = brow < p.part_rows && t < p.num_tokens;
+  const long long row = static_cast<long long>(t) * p.num_heads + h;
   auto piece = [&](int i) {  // row of piece i among the partial rows
     const int slot = 2 * ((g0 + i) * w.width + lane_block) + (i == 0 ? odd : 0);
     return static_cast<long long>(slot) * p.part_rows + brow;
   };
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float lse2 = -INFINITY, other2 = -INFINITY;
-  if (work) {
+  if (real) {
     if (p.suffix_lse) other2 = p.suffix_lse[row] * kLog2e;
     float top = -INFINITY;
 #pragma unroll 1
@@ -793,9 +796,9 @@ __global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_co
     lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
 #pragma unroll 4
     for (int i = sub; i < n; i += kWarps) {
-      const long long at = piece(i);
-      const float f = ex2_approx(p.part_lse[at] - base) * inv;
-      const float4 v = reinterpret_cast<const float4*>(p.part_o)[at * (kHeadDim / 4) + lane];
+      const long long from = piece(i);
+      const float f = ex2_approx(p.part_lse[from] - base) * inv;
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[from * (kHeadDim / 4) + lane];
       o.x = fmaf(v.x, f, o.x);
       o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z);
@@ -815,7 +818,7 @@ __global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_co
       }
     }
   }
-  if (!work || sub != 0) return;
+  if (!real || sub != 0) return;
   Join j = {1.f, 0.f, lse2};
   if (p.suffix_lse) j = join(lse2, other2);
   // two lanes write 8 columns (16 bytes of bf16)
@@ -1040,10 +1043,11 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   p.out = out;
   p.lse = lse;
   p.status = status;
-  const long long rows = static_cast<long long>(num_tokens) * num_heads;
-  if (prefix_len == 0)
-    return launch_dependent(mla_prefix_empty_kernel, dim3(static_cast<unsigned>((rows * 16 + 127) / 128)), dim3(128), 0,
+  if (prefix_len == 0) {
+    const long long threads = static_cast<long long>(num_tokens) * num_heads * (kHeadDim / 8);
+    return launch_dependent(mla_prefix_empty_kernel, dim3(static_cast<unsigned>((threads + 127) / 128)), dim3(128), 0,
                             stream, p);
+  }
   p.plan = plan(num_tokens, num_heads, prefix_len, sms);
   const WsLayout2 l = attend_ws(p.plan, num_tokens);
   p.part_o = static_cast<float*>(workspace);
@@ -1063,12 +1067,11 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   rc = launch_dependent(num_tokens <= kTile ? mla_prefix_attend_kernel<true> : mla_prefix_attend_kernel<false>, dim3(ctas), dim3(kThreads), kSmem, stream, p, qn, qp, k, kp, vm);
   // heads are cut wherever a range does not end with one
   if (rc != MLA_OK || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
+  const int rows = num_tokens < l.rows ? num_tokens : l.rows;
   // pieces a head can be cut in: the ranges that overlap its nk steps
-  const long long range = p.plan.line / p.plan.groups;
-  if (p.plan.nk / range + 2 <= 8)
-    return launch_dependent(mla_prefix_combine_kernel<1>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
-                            stream, p);
-  return launch_dependent(mla_prefix_combine_kernel<4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, p);
+  const bool few = p.plan.nk / (p.plan.line / p.plan.groups) + 2 <= 8;
+  return launch_dependent(few ? mla_prefix_combine_kernel<1> : mla_prefix_combine_kernel<4>,
+                          dim3(p.plan.groups - 1, p.plan.width, few ? (rows + 3) / 4 : rows), dim3(128), 0, stream, p);
 }
 
 }  // extern "C"

@@ -52,11 +52,13 @@
 #include <cstdint>
 #include <mutex>
 
-#include "kernel_common.cuh"
 #include "mla_prefix.h"
+#include "prefix_common.cuh"
 
 namespace mla {
 namespace {
+
+using namespace prefix;
 
 constexpr int kHeadDim = 128;
 constexpr int kRope = 64;
@@ -121,44 +123,6 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-// 4-D tiled load (x: dim within a 64-dim chunk, y: row, z: chunk, w: head).
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-
-// Arrive `n` times.
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
-}
-
-// Predicated forms for a warp of which one lane issues: D (+)= A B^T with A
-// in shared or in tensor memory, and the commit.
-__device__ __forceinline__ void umma_ss_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue) : "memory");
-}
-__device__ __forceinline__ void umma_ts_if(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue) : "memory");
-}
-__device__ __forceinline__ void umma_commit_if(uint32_t issue, uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
-      ::"r"(bar), "r"(issue) : "memory");
-}
-
 // 32 lanes x 16 consecutive 32-bit columns (the store of tmem_ld16).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -187,22 +151,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
-}
-
-// wait_bar with a rolled loop: this kernel waits in many places, and the
-// unrolled form made its code 110 KB, which the instruction caches do not hold.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (*c.abort) return false;
-    if (globaltimer_ns() - t0 > kTimeoutNs) {
-      raise_timeout(c);
-      return false;
-    }
-  }
-  return true;
 }
 
 // One segment of a CTA's range: key tiles [k0, k1) of head h for row block `block`.
@@ -845,34 +793,6 @@ __global__ void __launch_bounds__(128) mla_prefix_empty_kernel(const __grid_cons
 }
 
 // ============================================================ host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static std::once_flag once;
-  static EncodeTiledFn fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
-bool encode(CUtensorMap* m, bool fp16, int rank, const void* base, const cuuint64_t* size, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-  EncodeTiledFn fn = encode_tiled();
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn && fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
-                  const_cast<void*>(base), size, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Query rows as boxes of {64 dims, 1 head, 128 tokens}.
 bool encode_q(CUtensorMap* m, const void* base, int dims, int64_t stride, int heads, int tokens) {
   const cuuint64_t size[3] = {static_cast<cuuint64_t>(dims), static_cast<cuuint64_t>(heads),
@@ -881,16 +801,6 @@ bool encode_q(CUtensorMap* m, const void* base, int dims, int64_t stride, int he
                                  static_cast<cuuint64_t>(stride) * 2 * static_cast<cuuint64_t>(heads)};
   const cuuint32_t box[3] = {64u, 1u, static_cast<cuuint32_t>(kTile)};
   return encode(m, false, 3, base, size, strides, box);
-}
-
-// Keys or values [heads, head_rows, 128] as boxes of {64 dims, `rows` rows, `chunks` 64-dim chunks, 1 head};
-// rows from prefix_len on read as zeros.
-bool encode_kv(CUtensorMap* m, bool fp16, const void* base, int prefix_len, int64_t head_rows, int heads,
-               uint32_t rows, uint32_t chunks) {
-  const cuuint64_t size[4] = {64, static_cast<cuuint64_t>(prefix_len), kHeadDim / 64, static_cast<cuuint64_t>(heads)};
-  const cuuint64_t strides[3] = {kHeadDim * 2, 128, static_cast<cuuint64_t>(head_rows) * kHeadDim * 2};
-  const cuuint32_t box[4] = {64u, rows, chunks, 1u};
-  return encode(m, fp16, 4, base, size, strides, box);
 }
 
 constexpr int kMaxDev = 64;
@@ -968,27 +878,6 @@ WsLayout2 attend_ws(const Plan& w, int num_tokens) {
   return l;
 }
 
-template <typename... A>
-int launch_dependent(void (*kernel)(A...), dim3 grid, dim3 block, int smem, mla_stream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return MLA_ERR_CUDA;
-  }
-  return MLA_OK;
-}
-
-bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 }  // namespace
 }  // namespace mla
 
@@ -1046,7 +935,7 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   if (prefix_len == 0) {
     const long long threads = static_cast<long long>(num_tokens) * num_heads * (kHeadDim / 8);
     return launch_dependent(mla_prefix_empty_kernel, dim3(static_cast<unsigned>((threads + 127) / 128)), dim3(128), 0,
-                            stream, p);
+                            1, stream, p);
   }
   p.plan = plan(num_tokens, num_heads, prefix_len, sms);
   const WsLayout2 l = attend_ws(p.plan, num_tokens);
@@ -1064,14 +953,14 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
       !encode_kv(&vm, true, v, prefix_len, head_rows, num_heads, kTile / 2, 2))
     return MLA_ERR_CUDA;
   const int ctas = p.plan.groups * p.plan.width;
-  rc = launch_dependent(num_tokens <= kTile ? mla_prefix_attend_kernel<true> : mla_prefix_attend_kernel<false>, dim3(ctas), dim3(kThreads), kSmem, stream, p, qn, qp, k, kp, vm);
+  rc = launch_dependent(num_tokens <= kTile ? mla_prefix_attend_kernel<true> : mla_prefix_attend_kernel<false>, dim3(ctas), dim3(kThreads), kSmem, 1, stream, p, qn, qp, k, kp, vm);
   // heads are cut wherever a range does not end with one
   if (rc != MLA_OK || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
   const int rows = num_tokens < l.rows ? num_tokens : l.rows;
   // pieces a head can be cut in: the ranges that overlap its nk steps
   const bool few = p.plan.nk / (p.plan.line / p.plan.groups) + 2 <= 8;
   return launch_dependent(few ? mla_prefix_combine_kernel<1> : mla_prefix_combine_kernel<4>,
-                          dim3(p.plan.groups - 1, p.plan.width, few ? (rows + 3) / 4 : rows), dim3(128), 0, stream, p);
+                          dim3(p.plan.groups - 1, p.plan.width, few ? (rows + 3) / 4 : rows), dim3(128), 0, 1, stream, p);
 }
 
 }  // extern "C"

@@ -1,97 +1,339 @@
 // prefix_expand.cu — per-head keys and values of a shared prefix, from its
 // cached latents, with the C ABI (include/mla_prefix.h).
+//
+// K[h] = L W_UK[h] and V[h] = L W_UV[h] for the prefix's latents L [P, 512]:
+// one product of [P, 512] by [512, heads * 256], bound by the tensor cores
+// (4 * 512 * 128 operations a (row, head) for 512 bytes written).
+//
+// A pair of SMs computes 256 rows of one head's keys and values at a time
+// (tcgen05.mma.cta_group::2, M256 N256 K16): each CTA holds 128 rows of L and
+// one of the weights (rank 0 W_UK, rank 1 W_UV), and receives both products of
+// its rows, 128 key and 128 value columns, in its tensor memory.  The weights
+// stay in shared memory (128 KiB a CTA) over all row tiles of a head and are
+// replaced stage by stage under the last one; the latents stream through a
+// ring of 4 chunks of 64 dims, read from the cache's pages by TMA (they lie
+// in L2: every pair reads the same rows).  Two accumulators, so that a tile is
+// drained under the next one's products.  (row tile, head) items form one
+// line, head by head, cut into equal ranges, one per pair.
+//
+//   warp 0     TMA: latents and weights
+//   warp 1     MMA issue (rank 0, for both CTAs)
+//   warps 2-5  drain: tensor memory -> bf16 / fp16 -> swizzled staging -> TMA
+//              store, 64 columns at a time
+//   warp 6     copies the RoPE dims and checks the block table
+//
+// FP8 rows are first widened to bf16 in the workspace (exactly: 4 significant
+// bits and a power of two) by a kernel of their own, a warp a row: the product
+// then reads them as a cache of consecutive pages.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 #include <mutex>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include "kernel_common.cuh"
 #include "mla_prefix.h"
+#include "prefix_common.cuh"
 
 namespace mla {
 namespace {
 
+using namespace prefix;
+
 constexpr int kLatent = 512;
-constexpr int kHeadDim = 128;
 constexpr int kRope = 64;
 constexpr int kFp8Row = MLA_FP8_ROW_BYTES;
-constexpr int kRowsPerCta = 16;
+
+constexpr int kRows = 128;                   // rows of a CTA's tile
+constexpr int kStages = kLatent / 64;        // 64 latent dims each
+constexpr int kChunk = 16384;                // 128 rows x 64 dims, or 64 dims x 128 columns of a weight
+constexpr int kSlots = 4;
+constexpr int kStage = 32 * 128;             // one warp's 32 rows x 64 columns
+constexpr int kOffW = 0;
+constexpr int kOffRing = kStages * kChunk;                // 128 KiB
+constexpr int kOffStage = kOffRing + kSlots * kChunk;     // 192 KiB, 4 warps x 2 buffers
+constexpr int kOffBar = kOffStage + 4 * 2 * kStage;       // 224 KiB
+constexpr int kNumBars = 2 * kSlots + 2 * kStages + 4 + 1;
+constexpr int kSlack = 1024;                 // re-aligned to 1024 B (128-byte swizzle atoms)
+constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr int kThreads = 224;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdesc = idesc_bf16(256, 256, 1);
 
 struct ExpandParams {
-  const uint8_t* cache;
+  const uint8_t* cache;      // the pool (RoPE dims)
+  int row_bytes, rope_byte;  // of a pool row
   long long num_pages;
   const int* block_table;
-  int prefix_len, num_heads, fp8;
-  const uint16_t* w_uk;
-  const uint16_t* w_uv;
-  uint16_t* k_nope;
-  uint16_t* v;
-  long long head_rows;
+  int paged;                 // the latents come from the pool's pages (else row by row)
+  int prefix_len, num_heads;
   uint16_t* k_pe;
   int* status;
 };
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_constant__ CUtensorMap tm_lat,
+                         const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
+                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t mis = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + mis;
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int tiles = (p.prefix_len + 2 * kRows - 1) / (2 * kRows);
+  const long long items = static_cast<long long>(tiles) * p.num_heads;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const long long i0 = items * pair / pairs, i1 = items * (pair + 1) / pairs;
+  const int n = static_cast<int>(i1 - i0);
+  const int h0 = static_cast<int>(i0 / tiles), m0 = static_cast<int>(i0 % tiles);
 
-// One CTA: 16 rows of one head; thread d sums K's and V's dim d of each.
-__global__ void __launch_bounds__(kHeadDim) mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p) {
-  __shared__ float lat[kRowsPerCta][kLatent];
-  const int h = blockIdx.y, r0 = blockIdx.x * kRowsPerCta, d = threadIdx.x;
-  const long long row_bytes = p.fp8 ? kFp8Row : 2 * kDqk;
-  grid_dependency_wait();
-  for (int r = 0; r < kRowsPerCta; ++r) {
-    const int pos = r0 + r;
-    const long long page = pos < p.prefix_len ? p.block_table[pos / kPage] : -1;
-    const bool ok = page >= 0 && page < p.num_pages;
-    if (!ok && pos < p.prefix_len && d == 0) atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
-    const uint8_t* row = p.cache + (ok ? (page * kPage + pos % kPage) * row_bytes : 0);
-    for (int c = d; c < kLatent; c += kHeadDim) {
-      float x = 0.f;
-      if (ok && !p.fp8) x = bf(reinterpret_cast<const uint16_t*>(row)[c]);
-      if (ok && p.fp8) {
-        __nv_fp8_e4m3 q;
-        q.__x = row[c];
-        x = static_cast<float>(q) * exp2f(static_cast<float>(row[kLatent + c / 128]) - 127.f);
-      }
-      lat[r][c] = x;
-    }
-    if (h == 0 && d < kRope && pos < p.prefix_len)
-      p.k_pe[static_cast<long long>(pos) * kRope + d] =
-          ok ? reinterpret_cast<const uint16_t*>(row + (p.fp8 ? 528 : 2 * kLatent))[d] : 0;
+  const uint32_t bar0 = sbase + kOffBar;
+  auto a_full = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto a_empty = [&](uint32_t s) { return bar0 + 8u * (kSlots + s); };
+  auto w_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + s); };
+  auto w_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + kStages + s); };
+  auto acc_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + s); };
+  auto acc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 2 + s); };
+  const uint32_t bar_drain = bar0 + 8u * (kNumBars - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar0 + 8u * i, 1);
+    for (uint32_t s = 0; s < 2; ++s) mbar_init(acc_empty(s), 8);  // the drain warps of both CTAs
+    *abort_flag = 0u;
+    fence_mbar_init();
   }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
   __syncthreads();
-  float k[kRowsPerCta] = {}, v[kRowsPerCta] = {};
-  const uint16_t* wk = p.w_uk + static_cast<long long>(h) * kLatent * kHeadDim + d;
-  const uint16_t* wv = p.w_uv + static_cast<long long>(h) * kLatent * kHeadDim + d;
-  for (int c = 0; c < kLatent; ++c) {
-    const float a = bf(wk[c * kHeadDim]), b = bf(wv[c * kHeadDim]);
+  cluster_sync();  // both CTAs' barriers exist before any remote operation
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Ctl ctl;
+  ctl.abort = abort_flag;
+  ctl.n_remote = 1;
+  ctl.abort_remote[0] = mapa(smem_u32(const_cast<uint32_t*>(abort_flag)), rank ^ 1u);
+  ctl.status = p.status;
+
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_lat);
+      tma_prefetch_desc(rank == 0 ? &tm_wk : &tm_wv);
+      const CUtensorMap* tw = rank == 0 ? &tm_wk : &tm_wv;
+      const int pages = (p.prefix_len + kPage - 1) / kPage;
+      // Every copy completes on rank 0's barriers, which rank 0 arms with the bytes of both CTAs.
+      const uint32_t ra = mapa(a_full(0), 0), rw = mapa(w_full(0), 0);
+      uint32_t chunk = 0, heads = 0;
+      int h = h0, m = m0;
+      bool ok = true;
+      for (int i = 0; ok && i < n; ++i) {
+        // the tile's two pages; a page that is not there reads as zeros
+        int y[2], z[2];
 #pragma unroll
-    for (int r = 0; r < kRowsPerCta; ++r) {
-      k[r] = fmaf(lat[r][c], a, k[r]);
-      v[r] = fmaf(lat[r][c], b, v[r]);
+        for (int e = 0; e < 2; ++e) {
+          const int pg = (m * 2 + static_cast<int>(rank)) * 2 + e;
+          const int id = p.paged && pg < pages ? p.block_table[pg] : -1;
+          y[e] = p.paged ? 0 : pg * kPage;
+          z[e] = !p.paged ? 0 : (id >= 0 && id < p.num_pages ? id : static_cast<int>(p.num_pages));
+        }
+        const bool new_head = i == 0 || m == 0;
+        for (uint32_t k = 0; ok && k < kStages; ++k, ++chunk) {
+          if (new_head) {
+            if (heads > 0 && !(ok = wait<true>(w_empty(k), (heads - 1) & 1, ctl))) break;
+            if (rank == 0) mbar_arrive_expect_tx(w_full(k), 2 * kChunk);
+            const uint32_t dst = sbase + kOffW + k * kChunk;
+            tma_load_2d_pair(dst, tw, 0, h * kLatent + 64 * k, rw + 8u * k);
+            tma_load_2d_pair(dst + kChunk / 2, tw, 64, h * kLatent + 64 * k, rw + 8u * k);
+          }
+          const uint32_t s = chunk % kSlots;
+          if (chunk >= kSlots && !(ok = wait<true>(a_empty(s), ((chunk / kSlots) - 1) & 1, ctl))) break;
+          if (rank == 0) mbar_arrive_expect_tx(a_full(s), 2 * kChunk);
+          const uint32_t dst = sbase + kOffRing + s * kChunk;
+          tma_load_3d_pair(dst, &tm_lat, 64 * k, y[0], z[0], ra + 8u * s);
+          tma_load_3d_pair(dst + kChunk / 2, &tm_lat, 64 * k, y[1], z[1], ra + 8u * s);
+        }
+        if (new_head) ++heads;
+        if (++m == tiles) {
+          m = 0;
+          ++h;
+        }
+      }
+      grid_launch_dependents();
+      if (!ok) {  // let copies in flight land before the CTA goes away
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kDrainNs / 8) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // the whole warp runs, one lane issues (uniform operands)
+      const uint32_t leader = lane == 0 ? 1u : 0u;
+      const uint64_t wd = smem_desc(sbase + kOffW, kChunk / 2, 1024u);   // MN-major: 64-column halves kChunk / 2 apart
+      const uint64_t ad = smem_desc(sbase + kOffRing, 16u, 1024u);
+      uint32_t chunk = 0, heads = 0;
+      int m = m0;
+      bool ok = true;
+      for (int i = 0; ok && i < n; ++i) {
+        const uint32_t buf = i & 1;
+        const bool new_head = i == 0 || m == 0, last = m == tiles - 1;
+        if (i >= 2) ok = wait<true>(acc_empty(buf), ((i >> 1) - 1) & 1, ctl);
+#pragma unroll 1
+        for (uint32_t k = 0; ok && k < kStages; ++k, ++chunk) {
+          const uint32_t s = chunk % kSlots;
+          if (new_head && !(ok = wait<true>(w_full(k), heads & 1, ctl))) break;
+          if (!(ok = wait<true>(a_full(s), (chunk / kSlots) & 1, ctl))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_pair_ss_if(leader, tmem + 256u * buf, ad + static_cast<uint64_t>((s * kChunk + 32 * kk) >> 4),
+                            wd + static_cast<uint64_t>((k * kChunk + 2048 * kk) >> 4), kIdesc, (k | kk) != 0 ? 1u : 0u);
+          umma_commit_pair_if(leader, a_empty(s), 3);
+          if (last) umma_commit_pair_if(leader, w_empty(k), 3);
+        }
+        if (!ok) break;
+        umma_commit_pair_if(leader, acc_full(buf), 3);
+        if (new_head) ++heads;
+        m = last ? 0 : m + 1;
+      }
+      umma_commit_pair_if(leader, bar_drain, 1);  // arrives once every MMA issued above has completed
+      drain_bar(bar_drain, 0u);
+      __syncwarp();
+    }
+  } else if (warp < 6) {
+    const int q = warp & 3;  // tensor-memory lanes 32 q .. +31: those rows of the tile
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t racc = mapa(acc_empty(0), 0);
+    int h = h0, m = m0;
+    uint32_t stores = 0;
+    bool bad = false;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t buf = i & 1;
+      const int row0 = (m * 2 + static_cast<int>(rank)) * kRows + 32 * q;
+      if (!__all_sync(0xffffffffu, wait<true>(acc_full(buf), (i >> 1) & 1, ctl))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c, ++stores) {  // key columns 0 and 64, value columns 0 and 64
+        uint32_t x[2][32];
+        tmem_ld32(tl + 256u * buf + 64u * c, x[0]);
+        tmem_ld32(tl + 256u * buf + 64u * c + 32u, x[1]);
+        tmem_wait_ld();
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(racc + 8u * buf);  // the accumulator may take the tile after next
+        }
+        if (lane == 0) bulk_wait_read_1();  // this staging buffer's previous store has read it
+        __syncwarp();
+        const uint32_t stg = sbase + static_cast<uint32_t>(kOffStage + (q * 2 + (stores & 1)) * kStage);
+        const uint32_t rbase = stg + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t* v = &x[u >> 2][(u & 3) * 8];
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float lo = __uint_as_float(v[2 * k]), hi = __uint_as_float(v[2 * k + 1]);
+            if (c < 2) {
+              w[k] = pack_bf16x2(lo, hi);
+            } else {
+              w[k] = pack_f16x2(lo, hi);
+              // NaN compares false: tested as "not below"
+              bad |= !(fabsf(lo) < 65520.f) | !(fabsf(hi) < 65520.f);
+            }
+          }
+          st_shared_v4(rbase + ((static_cast<uint32_t>(u) ^ static_cast<uint32_t>(lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
+        if (c >= 2 && row0 + lane >= p.prefix_len) bad = false;  // rows behind the prefix may hold anything
+        if (bad) {
+          atomicCAS(p.status, 0, static_cast<int>(kStValueRange));
+          bad = false;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (row0 < p.prefix_len) tma_store_4d(c < 2 ? &tm_k : &tm_v, stg, 0, row0, c & 1, h);
+          bulk_commit();
+        }
+      }
+      if (++m == tiles) {
+        m = 0;
+        ++h;
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  } else {
+    // RoPE dims, 8 lanes a row, and the pages' check, over the whole grid
+    for (long long r = blockIdx.x * 4ll + (lane >> 3); r < p.prefix_len; r += gridDim.x * 4ll) {
+      const long long page = p.block_table[r / kPage];
+      const bool ok = page >= 0 && page < p.num_pages;
+      if (!ok && (lane & 7) == 0) atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (ok) v = *reinterpret_cast<const uint4*>(p.cache + (page * kPage + r % kPage) * p.row_bytes + p.rope_byte + 16 * (lane & 7));
+      *reinterpret_cast<uint4*>(p.k_pe + r * kRope + 8 * (lane & 7)) = v;
     }
   }
-  for (int r = 0; r < kRowsPerCta; ++r) {
-    if (r0 + r >= p.prefix_len) break;
-    const long long at = (h * p.head_rows + r0 + r) * kHeadDim + d;
-    p.k_nope[at] = __bfloat16_as_ushort(__float2bfloat16_rn(k[r]));
-    p.v[at] = __half_as_ushort(__float2half_rn(v[r]));
-    if (!(fabsf(v[r]) < 65520.f)) atomicCAS(p.status, 0, static_cast<int>(kStValueRange));
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA touches another's shared memory after this
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
+// FP8 rows to bf16: lane l takes the 16 codes of dims [16 l, 16 l + 16).
+__global__ void __launch_bounds__(256) mla_prefix_widen_kernel(const __grid_constant__ ExpandParams p, uint16_t* out) {
+  const long long r = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  if (r >= p.prefix_len) return;
+  const long long page = p.block_table[r / kPage];
+  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  if (page >= 0 && page < p.num_pages) {
+    const uint8_t* row = p.cache + (page * kPage + r % kPage) * kFp8Row;
+    const uint4 c = *reinterpret_cast<const uint4*>(row + 16 * lane);
+    const uint32_t e = row[kLatent + lane / 8];
+    // 2^(e - 127); the scale byte 0 is 2^-127, 255 is NaN
+    const float scale = __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t h2;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(in[i >> 1] >> (16 * (i & 1)))));
+      float a, b;
+      asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}" : "=f"(a), "=f"(b) : "r"(h2));
+      w[i] = pack_bf16x2(a * scale, b * scale);
+    }
+    lo = make_uint4(w[0], w[1], w[2], w[3]);
+    hi = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(out + r * kLatent + 16 * lane);
+  dst[0] = lo;
+  dst[1] = hi;
+}
+
+// ============================================================ host side
 constexpr int kMaxDev = 64;
 struct ExpandDevice {
   std::once_flag once;
   int status = MLA_OK;
+  int sms = 0;
 };
 ExpandDevice g_expand_dev[kMaxDev];
 
-int expand_device_ready() {
+int expand_device_ready(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return MLA_ERR_DEVICE;
   ExpandDevice& st = g_expand_dev[dev];
@@ -99,13 +341,28 @@ int expand_device_ready() {
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess || major != 10 ||
-        minor != 3)
+        minor != 3 || cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        st.sms < 2) {
       st.status = MLA_ERR_DEVICE;
+      return;
+    }
+    if (cudaFuncSetAttribute(mla_prefix_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      st.status = MLA_ERR_CUDA;
+    }
   });
+  *sms = st.sms;
   return st.status;
 }
 
-bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// A weight [H, 512, 128] as 2-D [H * 512 rows, 128 columns], boxes of 64 x 64.
+bool encode_weight(CUtensorMap* m, const void* base, int heads) {
+  const cuuint64_t size[2] = {128, static_cast<cuuint64_t>(heads) * kLatent};
+  const cuuint64_t strides[1] = {256};
+  const cuuint32_t box[2] = {64u, 64u};
+  return encode(m, false, 2, base, size, strides, box);
+}
 
 }  // namespace
 }  // namespace mla
@@ -134,26 +391,43 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
   const size_t need = mla_prefix_expand_workspace_size(prefix_len, flags);
   if (need > 0 && !workspace) return MLA_ERR_INVALID_ARG;
   if (ws_bytes < need) return MLA_ERR_WORKSPACE;
-  const int rc = expand_device_ready();
+  int sms = 0;
+  int rc = expand_device_ready(&sms);
   if (rc != MLA_OK) return rc;
   if (prefix_len == 0) return MLA_OK;
+  const bool fp8 = (flags & MLA_FLAG_KV_FP8) != 0;
   ExpandParams p;
   p.cache = static_cast<const uint8_t*>(kv_cache);
+  p.row_bytes = fp8 ? kFp8Row : 2 * kDqk;
+  p.rope_byte = fp8 ? 528 : 2 * kLatent;
   p.num_pages = num_pages;
   p.block_table = block_table;
+  p.paged = !fp8;
   p.prefix_len = prefix_len;
   p.num_heads = num_heads;
-  p.fp8 = (flags & MLA_FLAG_KV_FP8) != 0;
-  p.w_uk = static_cast<const uint16_t*>(w_uk);
-  p.w_uv = static_cast<const uint16_t*>(w_uv);
-  p.k_nope = static_cast<uint16_t*>(k_nope);
-  p.v = static_cast<uint16_t*>(v);
-  p.head_rows = head_rows;
   p.k_pe = static_cast<uint16_t*>(k_pe);
   p.status = status;
-  const dim3 grid((prefix_len + kRowsPerCta - 1) / kRowsPerCta, num_heads);
-  mla_prefix_expand_kernel<<<grid, kHeadDim, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  // latents: {dim, row of a page, page} of the pool, or {dim, row, 1} of the widened rows
+  CUtensorMap lat, wk, wv, tk, tv;
+  const cuuint64_t size[3] = {fp8 ? cuuint64_t{kLatent} : cuuint64_t{kDqk},
+                              fp8 ? static_cast<cuuint64_t>(prefix_len) : cuuint64_t{kPage},
+                              fp8 ? cuuint64_t{1} : static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t row = (fp8 ? kLatent : kDqk) * 2;
+  const cuuint64_t strides[2] = {row, row * size[1]};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(kPage), 1u};
+  if (!encode(&lat, false, 3, fp8 ? workspace : kv_cache, size, strides, box) || !encode_weight(&wk, w_uk, num_heads) ||
+      !encode_weight(&wv, w_uv, num_heads) || !encode_kv(&tk, false, k_nope, prefix_len, head_rows, num_heads, 32, 1) ||
+      !encode_kv(&tv, true, v, prefix_len, head_rows, num_heads, 32, 1))
+    return MLA_ERR_CUDA;
+  if (fp8) {
+    rc = launch_dependent(mla_prefix_widen_kernel, dim3((prefix_len + 7) / 8), dim3(256), 0, 1, stream, p,
+                          static_cast<uint16_t*>(workspace));
+    if (rc != MLA_OK) return rc;
+  }
+  const long long items = static_cast<long long>((prefix_len + 2 * kRows - 1) / (2 * kRows)) * num_heads;
+  const int pairs = static_cast<int>(items < sms / 2 ? items : sms / 2);
+  return launch_dependent(mla_prefix_expand_kernel, dim3(2 * pairs), dim3(kThreads), kSmem, 1, stream, p, lat, wk, wv,
+                          tk, tv);
 }
 
 }  // extern "C"

@@ -264,16 +264,16 @@ def topk_indices(scores, cache_lens, topk: int, *, causal: bool = False, max_len
     return out
 
 
-def _tensor(t, name: str, dtype, shape, device=None, contiguous: bool = True):
-    """Checks a tensor argument: its type, its device, its shape (None: any
-    size) and that it is contiguous, or with contiguous=False that its last
-    dim is."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name}: expected on {device or 'a GPU'}, got {t.device}")
-    if not (t.is_contiguous() if contiguous else t.shape[-1] == 1 or t.stride(-1) == 1):
-        raise ValueError(f"{name}: expected {'contiguous' if contiguous else 'unit stride in the last dim'}")
+def _tensor(t, name: str, dtype, shape, device, contiguous: bool = True):
+    """Checks a tensor argument: its type, shape and device, and that it is
+    contiguous, or with contiguous=False that its last dim is.  (Called for
+    every tensor of a call that may be shorter than ten of these checks: it
+    does little, and words are found only for a failure.)"""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not (
+            t.is_contiguous() if contiguous else t.stride(-1) == 1):
+        raise ValueError(f"{name}: expected {dtype} {list(shape)} on {device}, "
+                         f"{'contiguous' if contiguous else 'unit stride in the last dim'}; got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}, strides {list(t.stride())}")
 
 
 def _on_device(fn):
@@ -286,20 +286,27 @@ def _on_device(fn):
     def call(first, *args, stream=None, **kw):
         import torch
         dev = first.device
+        if stream is None and dev.index is not None and dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
         if dev.type != "cuda":
             raise ValueError(f"{fn.__name__}: expected tensors on a GPU, got {dev}")
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
-            if stream.device != dev:
-                raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {dev}")
-            with torch.cuda.stream(stream):
+        if stream is None:
+            with torch.cuda.device(dev):
                 return fn(first, *args, **kw)
-        if dev.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
-        with torch.cuda.device(dev):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        if stream.device != dev:
+            raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {dev}")
+        with torch.cuda.stream(stream):
             return fn(first, *args, **kw)
     return call
+
+
+def _current_stream(device) -> int:
+    """Raw handle of the current stream (torch.cuda.current_stream builds a
+    stream object for it, twenty times as long)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.0, yarn: float = 1.0,
@@ -351,18 +358,19 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
     """
     import torch
     dev = x.device
-    _tensor(x, "x", torch.bfloat16, (None, None, None), contiguous=False)
     T, H, D = x.shape
+    _tensor(x, "x", torch.bfloat16, (T, H, D), dev, contiguous=False)
     _tensor(positions, "positions", torch.int32, (T,), dev)
-    _tensor(inv_freq, "inv_freq", torch.float64, (None,), dev)
+    R2, = inv_freq.shape
+    _tensor(inv_freq, "inv_freq", torch.float64, (R2,), dev)
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
     else:
         _tensor(out, "out", torch.bfloat16, (T, H, D), dev, contiguous=False)
     if T == 0 or H == 0:
         return out
-    stream = torch.cuda.current_stream(dev)
-    mla_rope(x, x.stride(0), x.stride(1), positions, T, H, D, offset, 2 * inv_freq.shape[0], inv_freq, scale,
+    stream = _current_stream(dev)
+    mla_rope(x, x.stride(0), x.stride(1), positions, T, H, D, offset, 2 * R2, inv_freq, scale,
              (MLA_FLAG_ROPE_HALF if half else 0) | (MLA_FLAG_ROPE_INVERSE if inverse else 0), out, out.stride(0),
              out.stride(1), stream)
     return out
@@ -371,9 +379,9 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
 def _cache_flags(kv_cache, device) -> int:
     import torch
     if kv_cache.dtype == torch.uint8:
-        _tensor(kv_cache, "kv_cache", torch.uint8, (None, PAGE, 656), device)
+        _tensor(kv_cache, "kv_cache", torch.uint8, (kv_cache.shape[0], PAGE, 656), device)
         return MLA_FLAG_KV_FP8
-    _tensor(kv_cache, "kv_cache", torch.bfloat16, (None, PAGE, D_QK), device)
+    _tensor(kv_cache, "kv_cache", torch.bfloat16, (kv_cache.shape[0], PAGE, D_QK), device)
     return 0
 
 
@@ -397,11 +405,12 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
     """
     import torch
     dev = latent.device
-    _tensor(latent, "latent", torch.bfloat16, (None, D_V), contiguous=False)
     T = latent.shape[0]
+    _tensor(latent, "latent", torch.bfloat16, (T, D_V), dev, contiguous=False)
     _tensor(k_pe, "k_pe", torch.bfloat16, (T, D_QK - D_V), dev, contiguous=False)
     flags = _cache_flags(kv_cache, dev)
-    _tensor(block_table, "block_table", torch.int32, (None, None), dev, contiguous=False)
+    B, width = block_table.shape
+    _tensor(block_table, "block_table", torch.int32, (B, width), dev, contiguous=False)
     _tensor(positions, "positions", torch.int32, (T,), dev)
     if request_ids is not None:
         _tensor(request_ids, "request_ids", torch.int32, (T,), dev)
@@ -412,15 +421,15 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=dev)
     else:
-        _tensor(status, "status", torch.int32, (None,), dev)
+        _tensor(status, "status", torch.int32, status.shape, dev)
     if T == 0:
         return kv_cache
-    B = block_table.shape[0]
-    # a single row has no next one: its stride says nothing about the table's width
-    width = block_table.stride(0) if B > 1 else block_table.shape[1]
-    if width < block_table.shape[1]:
-        raise ValueError("block_table: its rows overlap")
-    stream = torch.cuda.current_stream(dev)
+    # (a single row has no next one: its stride says nothing about the table's width)
+    if B > 1:
+        if block_table.stride(0) < width:
+            raise ValueError("block_table: its rows overlap")
+        width = block_table.stride(0)
+    stream = _current_stream(dev)
     mla_cache_append(latent, latent.stride(0) if T > 1 else D_V, k_pe, k_pe.stride(0) if T > 1 else D_QK - D_V,
                      norm_weight, eps, inv_freq, rope_scale, positions, request_ids, T, block_table, width, B,
                      kv_cache, kv_cache.shape[0], flags | (MLA_FLAG_ROPE_HALF if half else 0), status, stream)
@@ -445,19 +454,20 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
     import torch
     dev = kv_cache.device
     flags = _cache_flags(kv_cache, dev)
-    _tensor(block_table, "block_table", torch.int32, (None,), dev)
-    if prefix_len < 0 or prefix_len > block_table.shape[0] * PAGE:
+    pages, = block_table.shape
+    _tensor(block_table, "block_table", torch.int32, (pages,), dev)
+    if prefix_len < 0 or prefix_len > pages * PAGE:
         raise ValueError("prefix_len: outside the block table")
     H = w_uk.shape[0]
-    _tensor(w_uk, "w_uk", torch.bfloat16, (None, D_V, 128), dev)
+    _tensor(w_uk, "w_uk", torch.bfloat16, (H, D_V, 128), dev)
     _tensor(w_uv, "w_uv", torch.bfloat16, (H, D_V, 128), dev)
     if out is None:
         out = (torch.empty((H, prefix_len, 128), dtype=torch.bfloat16, device=dev),
                torch.empty((prefix_len, D_QK - D_V), dtype=torch.bfloat16, device=dev),
                torch.empty((H, prefix_len, 128), dtype=torch.float16, device=dev))
     k_nope, k_pe, v = out
-    _tensor(k_nope, "k_nope", torch.bfloat16, (H, None, 128), dev)
     R = k_nope.shape[1]
+    _tensor(k_nope, "k_nope", torch.bfloat16, (H, R, 128), dev)
     _tensor(k_pe, "k_pe", torch.bfloat16, (R, D_QK - D_V), dev)
     _tensor(v, "v", torch.float16, (H, R, 128), dev)
     if R < prefix_len:
@@ -468,12 +478,12 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
-        _tensor(workspace, "workspace", torch.uint8, (None,), dev)
+        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=dev)
     else:
-        _tensor(status, "status", torch.int32, (None,), dev)
-    stream = torch.cuda.current_stream(dev)
+        _tensor(status, "status", torch.int32, status.shape, dev)
+    stream = _current_stream(dev)
     mla_prefix_expand(kv_cache, kv_cache.shape[0], block_table, prefix_len, w_uk, w_uv, H, flags, k_nope, v, R, k_pe,
                       workspace, 0 if workspace is None else workspace.numel(), status, stream)
     return out
@@ -499,11 +509,11 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
     """
     import torch
     dev = q_nope.device
-    T, H = q_nope.shape[0], q_nope.shape[1]
-    _tensor(q_nope, "q_nope", torch.bfloat16, (T, H, 128), contiguous=False)
+    T, H, _ = q_nope.shape
+    _tensor(q_nope, "q_nope", torch.bfloat16, (T, H, 128), dev, contiguous=False)
     _tensor(q_pe, "q_pe", torch.bfloat16, (T, H, 64), dev, contiguous=False)
-    _tensor(k_nope, "k_nope", torch.bfloat16, (H, None, 128), dev)
     R = k_nope.shape[1]
+    _tensor(k_nope, "k_nope", torch.bfloat16, (H, R, 128), dev)
     _tensor(k_pe, "k_pe", torch.bfloat16, (R, 64), dev)
     _tensor(v, "v", torch.float16, (H, R, 128), dev)
     if prefix_len is None:
@@ -527,18 +537,18 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
         _tensor(lse, "lse", torch.float32, (T, H), dev)
     if T == 0 or H == 0:
         return out, lse
-    q_stride = _rows(q_nope, 128, "q_nope")
-    if _rows(q_pe, 64, "q_pe") != q_stride:
-        raise ValueError("q_pe must have the row stride of q_nope")
+    q_stride = q_nope.stride(1)
+    if q_nope.stride(0) != H * q_stride or q_pe.stride(0) != H * q_stride or q_pe.stride(1) != q_stride:
+        raise ValueError("q_nope, q_pe: expected rows evenly spaced over (token, head), with one stride")
     if workspace is None:
         workspace = torch.empty(mla_prefix_attend_workspace_size(T, H, prefix_len), dtype=torch.uint8, device=dev)
     else:
-        _tensor(workspace, "workspace", torch.uint8, (None,), dev)
+        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=dev)
     else:
-        _tensor(status, "status", torch.int32, (None,), dev)
-    stream = torch.cuda.current_stream(dev)
+        _tensor(status, "status", torch.int32, status.shape, dev)
+    stream = _current_stream(dev)
     mla_prefix_attend(q_nope, q_pe, q_stride, k_nope, v, R, k_pe, prefix_len, visible, T, H, softmax_scale,
                       suffix_out, suffix_lse, MLA_FLAG_OUT_FP32 if out_fp32 else 0, workspace, workspace.numel(), out,
                       lse, status, stream)

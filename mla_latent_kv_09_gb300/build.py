@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmla_decode.so")
 SOURCES = ["decode_kernel.cu", "mtp_kernel.cu", "aux_kernels.cu", "api.cu", "noalloc.cu", "absorb_kernel.cu",
-           "indexer_kernel.cu", "cache_kernels.cu", "prefix_expand.cu", "prefix_attend.cu"]
-HEADERS = ["common.cuh", "kernel_common.cuh", "plan.cuh", "prefix_common.cuh", "ptx.cuh"]
+           "indexer_kernel.cu", "cache_kernels.cu", "prefix_expand.cu", "prefix_attend.cu",
+           "prefix_attend_pair.cu"]
+HEADERS = ["common.cuh", "kernel_common.cuh", "plan.cuh", "prefix_attend.cuh", "prefix_common.cuh", "ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,5 +1,6 @@
 // prefix_attend.cu — attention of a batch's query tokens over a shared,
-// expanded prefix, with the C ABI (include/mla_prefix.h).
+// expanded prefix: the kernel for up to 128 tokens, the join of cut heads, and
+// the C ABI (include/mla_prefix.h).
 //
 // One head is ordinary attention: T query rows of 192 dims, P keys of 192 (128
 // of the head's, 64 RoPE dims shared by all heads), P values of 128.  A key
@@ -7,33 +8,27 @@
 // row: up to about 270 tokens the HBM bounds the call, above it the tensor
 // cores do.
 //
-// A CTA per SM works on blocks of 256 query rows of one head: two row tiles
-// of 128 ("streams"), each with its own scores S and output O in tensor
-// memory (2 * (128 + 128) columns, all of it), so that the tensor cores work
-// on one stream while the other's softmax runs.  Both streams use each key
-// tile in shared memory once.  A block of up to 128 rows has one row tile:
-// its two streams then take alternate key tiles and are joined at the end, so
-// that a small batch keeps the same overlap.
+// This kernel (a CTA per SM, one row tile of up to 128 query rows, the rest of
+// the tile zeros) is bound by the HBM: the tensor cores need 1,280 of the
+// 2,850 cycles that a tile takes to arrive.  Its two streams take alternate
+// key tiles, each with its own scores S and output O in tensor memory (2 * (128
+// + 128) columns, all of it), and are joined at the end.
 //
 //   warps 0-7, 8-15 softmax of stream 0, 1: two threads own a query row, each
 //                   64 of its 128 scores, which it reads from tensor memory;
 //                   they agree on the running maximum, keep their own sums
 //                   and write the weights in fp16 over the scores, where the
 //                   value product reads them as its A operand
-//   warp 16         TMA: the block's queries (96 KiB), then key and value
-//                   chunks of 16 KiB through a ring of 8 slots
+//   warp 16         TMA: the queries (48 KiB), then key and value chunks of
+//                   16 KiB through a ring of 10 slots
 //   warps 17, 18    tcgen05.mma for stream 0, 1: S = Q K^T (12 steps of M128
 //                   N128 K16, bf16), O += P V (8 steps, fp16).  The tensor
 //                   core takes an MMA every 64 cycles and queues few, so a
 //                   wait of the issuing thread (100 to 250 cycles) is time
 //                   lost; two issuers fill each other's
 //
-// A step's chain is scores -> softmax -> value product -> next scores (the
-// weights lie where the next scores go); the other stream fills the tensor
-// cores meanwhile, if a stream's softmax is no longer than the other's
-// products.  Hence two threads a row, and hence the weights are handed over
-// in two halves of 64 keys: the value product of the first runs under the
-// exponentials of the second.
+// The weights are handed over in two halves of 64 keys: the value product of
+// the first runs under the exponentials of the second.
 //
 // The running maximum is lazy: it moves only when a score beats it by 2^8, so
 // that weights stay below 2^8 (fp16 holds them with 11 bits) and O is rarely
@@ -42,9 +37,9 @@
 // the LSE takes the sum of the unrounded ones.
 //
 // Work split: all (head, key tile) steps of a row block form one line, cut
-// into equal ranges, one per CTA (see plan()).  A range that covers a head's
-// whole prefix writes the result; a head cut in pieces leaves normalised fp32
-// partial rows and their LSE, which the combine kernel joins.
+// into equal ranges, one per CTA or pair (see plan()).  A range that covers a
+// head's whole prefix writes the result; a head cut in pieces leaves
+// normalised fp32 partial rows and their LSE, which the combine kernel joins.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -53,189 +48,29 @@
 #include <mutex>
 
 #include "mla_prefix.h"
-#include "prefix_common.cuh"
+#include "prefix_attend.cuh"
 
 namespace mla {
 namespace {
 
 using namespace prefix;
 
-constexpr int kHeadDim = 128;
-constexpr int kRope = 64;
-constexpr int kTile = 128;                  // query rows of a row tile, keys of a key tile
 constexpr int kSlot = 16384;                // a key chunk (128 keys x 64 dims) or half a value tile (64 keys x 128 dims)
-constexpr int kQChunks = 3;                 // 64-dim chunks of a query or key row
-constexpr int kQTile = kQChunks * kSlot;    // 48 KiB
-// Up to 128 tokens one query tile and a ring of 10 slots (two key and two
-// value tiles), above two query tiles and 8 slots.
-constexpr int ring_slots(bool small) { return small ? 10 : 8; }
-constexpr int kOffBar = 14 * kSlot;         // 224 KiB
-constexpr int ring_offset(bool small) { return kOffBar - ring_slots(small) * kSlot; }
+constexpr uint32_t kSlots = 10;             // two key and two value tiles
+constexpr int kOffXchg = kQTile;            // the threads of a row exchange their sums here
+constexpr int kOffRing = kQTile + kSlot;
+constexpr int kOffBar = kOffRing + kSlots * kSlot;      // 224 KiB
 constexpr int kNumBars = 8 + 12;
-constexpr int kOffMax = kOffBar + kNumBars * 8 + 16;  // [stream][half][row]: exchange between a row's two threads
-constexpr int kSmem = kOffMax + 4 * kTile * 4;        // no room to re-align: the base must lie on 1024 B (checked)
+constexpr int kOffMax = kOffBar + kNumBars * 8 + 16;    // [stream][half][row]: exchange between a row's two threads
+constexpr int kSmem = kOffMax + 4 * kTile * 4;          // no room to re-align: the base must lie on 1024 B (checked)
 static_assert(kSmem <= 232448, "shared memory");
-// the threads of a row of a one-tile block exchange their sums behind the first query tile
-constexpr int kOffXchg = kQTile;
 constexpr int kThreads = 608;
-constexpr int kSoftmaxWarps = 16;
 constexpr int kTmaWarp = 16, kMmaWarp = 17;  // and 18, for the second stream
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;  // + 128 * stream
 constexpr uint32_t kIdescQK = idesc_bf16(128, 128, 0);
 // fp16 A (weights, tensor memory) and B (values, MN-major): formats 0
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.0f;               // log2 by which a score must beat the running maximum to move it
-
-// ---- work split
-struct Plan {
-  int nk;         // key tiles
-  int blocks;     // row blocks of 256
-  int width;      // row blocks worked on side by side by the CTAs of a group
-  int groups;     // CTA groups, each with a range of the line
-  int passes;     // ceil(blocks / width)
-  long long line; // passes * heads * nk steps
-};
-
-struct AttendParams {
-  const int* visible;
-  int num_tokens, num_heads, prefix_len;
-  float scale_log2;
-  const uint16_t* suffix_out;
-  const float* suffix_lse;
-  int out_fp32;
-  void* out;
-  float* lse;
-  float* part_o;    // [2 * CTAs][rows][128], normalised
-  float* part_lse;  // [2 * CTAs][rows], log2
-  int part_rows;
-  Plan plan;
-  int* status;
-};
-
-__host__ __device__ __forceinline__ long long cut(const Plan& w, int g) { return w.line * g / w.groups; }
-
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 32 lanes x 16 consecutive 32-bit columns (the store of tmem_ld16).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-// Two fp32 in a 64-bit register, and the packed operations on them.
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// One segment of a CTA's range: key tiles [k0, k1) of head h for row block `block`.
-struct Segment {
-  int h, block, k0, k1, rows;
-  bool first, whole;
-};
-
-struct SegmentIter {
-  const Plan& w;
-  int num_tokens, num_heads, lane_block, unit, k0;
-  long long left;
-  bool first;
-  __device__ SegmentIter(const AttendParams& p) : w(p.plan), num_tokens(p.num_tokens), num_heads(p.num_heads) {
-    const int g = blockIdx.x / w.width;
-    lane_block = blockIdx.x % w.width;
-    const long long begin = cut(w, g);
-    left = cut(w, g + 1) - begin;
-    unit = static_cast<int>(begin / w.nk);
-    k0 = static_cast<int>(begin - static_cast<long long>(unit) * w.nk);
-    first = true;
-  }
-  __device__ bool next(Segment& s) {
-    if (left <= 0) return false;
-    s.block = unit / num_heads * w.width + lane_block;
-    if (s.block >= w.blocks) return false;  // blocks grow along the line
-    s.h = unit % num_heads;
-    s.k0 = k0;
-    s.k1 = left < w.nk - k0 ? k0 + static_cast<int>(left) : w.nk;
-    s.whole = s.k1 - k0 == w.nk;
-    s.first = first;
-    const int rows = num_tokens - s.block * 2 * kTile;
-    s.rows = rows < 2 * kTile ? rows : 2 * kTile;
-    left -= s.k1 - k0;
-    k0 = 0;
-    ++unit;
-    first = false;
-    return true;
-  }
-};
-
-// Weights of the prefix's and the suffix's result in their join, and the joined LSE (log2).
-struct Join {
-  float mine, other, lse2;
-};
-__device__ __forceinline__ Join join(float lse2, float other2) {
-  Join j;
-  const float top = fmaxf(lse2, other2);
-  const float base = top == -INFINITY ? 0.f : top;
-  const float a = ex2_approx(lse2 - base), b = ex2_approx(other2 - base);
-  const float sum = a + b;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
-  j.mine = a * inv;
-  j.other = b * inv;
-  j.lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
-  return j;
-}
-
-// 16 bytes of 8 result columns, or 32 in fp32, joined with the suffix's.
-__device__ __forceinline__ void write8(const AttendParams& p, long long row, int col, const float* o, const Join& j) {
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = o[i] * j.mine;
-  const long long at = row * kHeadDim + col;
-  if (p.suffix_out && j.other != 0.f) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p.suffix_out + at);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = fmaf(__uint_as_float(w[i] << 16), j.other, x[2 * i]);
-      x[2 * i + 1] = fmaf(__uint_as_float(w[i] & 0xffff0000u), j.other, x[2 * i + 1]);
-    }
-  }
-  if (p.out_fp32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-  }
-}
-
-// kSmall: up to 128 tokens, one row tile.
-template <bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
 mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap tm_qn,
                          const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_k,
@@ -262,15 +97,14 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   const uint32_t bar_o_free = bar_q_full + 8u * 10, bar_drain = bar_q_full + 8u * 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
-  constexpr uint32_t kSlots = ring_slots(kSmall), kOffRing = ring_offset(kSmall);
   auto slot_addr = [&](uint32_t n) { return sbase + kOffRing + (n % kSlots) * kSlot; };
 
   if (threadIdx.x == 0) {
     for (uint32_t q = 0; q < 2; ++q) {
       mbar_init(k_full(q), 1);
-      mbar_init(k_empty(q), 2);
+      mbar_init(k_empty(q), 1);
       mbar_init(v_full(q), 1);
-      mbar_init(v_empty(q), 2);
+      mbar_init(v_empty(q), 1);
     }
     mbar_init(bar_q_full, 1);
     mbar_init(bar_q_empty, 2);
@@ -300,17 +134,15 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   ctl.status = p.status;
 
   grid_dependency_wait();
-  SegmentIter it(p);
+  SegmentIter it(p, blockIdx.x);
   Segment sg{};
 
-  // Tiles enter the ring in the order the MMAs use them.  Two row tiles: K0
-  // V0 K1 V1 ..; one row tile, key tiles alternating between the streams: K0
-  // K1 V0 K2 V1 K3 ..  A key tile is three chunks, a value tile two; these are
-  // the places of tile j's first chunk in a segment of n tiles.  At most
-  // two key and two value tiles are in the ring at a time, hence two barriers
-  // for each.
-  auto place_k = [](bool two, int j) { return two ? 5 * j : (j < 2 ? 3 * j : 5 * j - 2); };
-  auto place_v = [](bool two, int j, int n) { return two ? 5 * j + 3 : (j == n - 1 ? 5 * n - 2 : 5 * j + 6); };
+  // Tiles enter the ring in the order the MMAs use them: K0 K1 V0 K2 V1 K3 ..
+  // A key tile is three chunks, a value tile two; these are the places of tile
+  // j's first chunk in a segment of n tiles.  At most two key and two value
+  // tiles are in the ring at a time, hence two barriers for each.
+  auto place_k = [](int j) { return j < 2 ? 3 * j : 5 * j - 2; };
+  auto place_v = [](int j, int n) { return j == n - 1 ? 5 * n - 2 : 5 * j + 6; };
 
   uint32_t issued = 0, k_issued = 0, v_issued = 0;  // chunks and tiles requested so far (TMA warp)
   int q_loads = 0;
@@ -366,26 +198,17 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         return true;
       };
       while (ok && it.next(sg)) {
-        const bool two = !kSmall && sg.rows > kTile;
         if (q_loads > 0 && !wait(bar_q_empty, (q_loads - 1) & 1, ctl)) break;
-        mbar_arrive_expect_tx(bar_q_full, two ? 2 * kQTile : kQTile);
-        for (int r = 0; r < (two ? 2 : 1); ++r) {
-          const uint32_t dst = sbase + static_cast<uint32_t>(r * kQTile);
-          const int t0 = (2 * sg.block + r) * kTile;
-          tma_load_3d(dst, &tm_qn, 0, sg.h, t0, bar_q_full);
-          tma_load_3d(dst + kSlot, &tm_qn, 64, sg.h, t0, bar_q_full);
-          tma_load_3d(dst + 2 * kSlot, &tm_qp, 0, sg.h, t0, bar_q_full);
-        }
+        mbar_arrive_expect_tx(bar_q_full, kQTile);
+        tma_load_3d(sbase, &tm_qn, 0, sg.h, 0, bar_q_full);
+        tma_load_3d(sbase + kSlot, &tm_qn, 64, sg.h, 0, bar_q_full);
+        tma_load_3d(sbase + 2 * kSlot, &tm_qp, 0, sg.h, 0, bar_q_full);
         ++q_loads;
-        if (two) {
-          for (int j = sg.k0; ok && j < sg.k1; ++j) ok = load_k(j) && load_v(j);
-        } else {
-          ok = load_k(sg.k0);
-          if (ok && sg.k0 + 1 < sg.k1) ok = load_k(sg.k0 + 1);
-          for (int j = sg.k0; ok && j < sg.k1; ++j) {
-            ok = load_v(j);
-            if (ok && j + 2 < sg.k1) ok = load_k(j + 2);
-          }
+        ok = load_k(sg.k0);
+        if (ok && sg.k0 + 1 < sg.k1) ok = load_k(sg.k0 + 1);
+        for (int j = sg.k0; ok && j < sg.k1; ++j) {
+          ok = load_v(j);
+          if (ok && j + 2 < sg.k1) ok = load_k(j + 2);
         }
       }
       grid_launch_dependents();
@@ -405,28 +228,26 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
     uint32_t seg = 0;
     bool ok = true;
     auto slot_off = [](uint32_t c) { return static_cast<uint64_t>(c % kSlots) * (kSlot >> 4); };
-    // Waits for the last value product and gives its tile back (for both
-    // streams, where only one uses it): a commit per tile and stream cost 125
-    // cycles of the issuing thread each, an arrive 20.
+    // Waits for the last value product and gives its tile back: a commit per
+    // tile cost 125 cycles of the issuing thread each, an arrive 20.
     uint32_t v_held = 0;           // its barrier, 0: given back
-    auto release_v = [&](bool two) -> bool {
+    auto release_v = [&]() -> bool {
       if (v_held == 0) return true;
       if (!wait(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
-      if (leader) mbar_arrive_n(v_held, two ? 1 : 2);
+      if (leader) mbar_arrive(v_held);
       v_held = 0;
       return true;
     };
     while (ok && it.next(sg)) {
-      const bool two = !kSmall && sg.rows > kTile;
       const int n = sg.k1 - sg.k0;
-      const int steps = two ? n : (n + 1 - static_cast<int>(s)) / 2;
-      const uint64_t ad = smem_desc(sbase + (two ? s * kQTile : 0u), 16u, 1024u);
+      const int steps = (n + 1 - static_cast<int>(s)) / 2;
+      const uint64_t ad = smem_desc(sbase, 16u, 1024u);
       // Scores of key tile j.  S holds the weights of the step before until
       // its value product is done.
       auto issue_qk = [&](int j) -> bool {
-        const uint32_t c0 = base + place_k(two, j), q = tiles + j;
+        const uint32_t c0 = base + place_k(j), q = tiles + j;
         if (!wait(k_full(q), (q >> 1) & 1, ctl)) return false;
-        if (!release_v(two)) return false;
+        if (!release_v()) return false;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kQChunks; ++c) {
@@ -439,13 +260,13 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         umma_commit_if(leader, bar_s_full(s));
         return true;
       };
-      ok = wait(bar_q_full, seg & 1, ctl) && (steps == 0 || issue_qk(two ? 0 : s));
+      ok = wait(bar_q_full, seg & 1, ctl) && (steps == 0 || issue_qk(s));
       if (steps <= 1) umma_commit_if(leader, bar_q_empty);
       // O of the segment before has been read
       if (ok && seg > 0) ok = wait(bar_o_free, (seg - 1) & 1, ctl);
       for (int i = 0; ok && i < steps; ++i) {
-        const int j = two ? i : 2 * i + static_cast<int>(s);
-        const uint32_t c0 = base + place_v(two, j, n), q = tiles + j;
+        const int j = 2 * i + static_cast<int>(s);
+        const uint32_t c0 = base + place_v(j, n), q = tiles + j;
         ok = wait(v_full(q), (q >> 1) & 1, ctl);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -463,11 +284,11 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         v_held = v_empty(q);
         ++n_pv;
         if (i + 1 < steps) {
-          ok = issue_qk(two ? i + 1 : j + 2);
+          ok = issue_qk(j + 2);
           if (i + 2 == steps) umma_commit_if(leader, bar_q_empty);  // the segment's last scores
         }
       }
-      ok = ok && release_v(two);
+      ok = ok && release_v();
       base += 5u * n;
       tiles += n;
       ++seg;
@@ -487,22 +308,20 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
     uint32_t tiles = 0;  // key tiles of the segments before this one
     bool ok = true;
     while (it.next(sg)) {
-      const bool two = !kSmall && sg.rows > kTile;
       const int n = sg.k1 - sg.k0;
-      const int steps = two ? n : (s == 0 ? (n + 1) / 2 : n / 2);
-      const int brow = two ? s * kTile + r : r;       // row within the block
-      const bool real = brow < sg.rows;
+      const int steps = (n + 1 - s) / 2;
+      const bool real = r < sg.rows;
       int seen = p.prefix_len;
-      if (p.visible) seen = real ? max(0, min(p.visible[sg.block * 2 * kTile + brow], p.prefix_len)) : 0;
+      if (p.visible) seen = real ? max(0, min(p.visible[r], p.prefix_len)) : 0;
       float m = -INFINITY;                            // running maximum (log2)
       float total = 0.f, used = 0.f;                  // this thread's sums of the weights and of the rounded ones
       for (int i = 0; i < steps; ++i) {
-        const int key0 = (sg.k0 + (two ? i : 2 * i + s)) * kTile;
+        const int key0 = (sg.k0 + 2 * i + s) * kTile;
         ok = __all_sync(0xffffffffu, wait(bar_s_full(s), n_s & 1, ctl));
         ++n_s;
         tc_fence_after();
         // the key tile has been read: its slots may be filled again
-        if (lane == 0 && (warp & 7) == 0) mbar_arrive_n(k_empty(tiles + (two ? i : 2 * i + s)), two ? 1 : 2);
+        if (lane == 0 && (warp & 7) == 0) mbar_arrive(k_empty(tiles + 2 * i + s));
         // Keys [32 hf, 32 hf + 32) of the tile's first 64 and of its second.
         // The second part is read twice: held across the step, it would push
         // the thread over its 96 registers, into local memory.
@@ -510,30 +329,15 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         // A row that sees none of them needs no masks (its weights become
         // zeros below): only rows that end in this tile do.
         const bool ragged = __any_sync(0xffffffffu, limit > 0 && limit < 96);
-        auto mask = [&](uint32_t (&x)[32], int c) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (64 * c + k >= limit) x[k] = 0xff800000u;  // -inf
-        };
-        auto largest = [](const uint32_t (&x)[32]) -> float {
-          float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
-#pragma unroll
-          for (int k = 2; k < 30; k += 4) {
-            a = fmaxf(fmaxf(a, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
-            b = fmaxf(fmaxf(b, __uint_as_float(x[k + 2])), __uint_as_float(x[k + 3]));
-          }
-          return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
-        };
         uint32_t x[32];
         tmem_ld32(ts + 64u + 32u * hf, x);
         tmem_wait_ld();
-        if (ragged) mask(x, 1);
-        float top = largest(x);
+        if (ragged) mask32(x, limit - 64);
+        float top = max32(x);
         tmem_ld32(ts + 32u * hf, x);
         tmem_wait_ld();
-        if (ragged) mask(x, 0);
-        top = fmaxf(top, largest(x));
-        if (limit <= 0) top = -INFINITY;
+        if (ragged) mask32(x, limit);
+        top = limit <= 0 ? -INFINITY : fmaxf(top, max32(x));
         // The partner cannot write its next maximum before this one is read:
         // its next scores wait for this warp's weights.
         xmax[hf * kTile] = top;
@@ -551,49 +355,19 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
           used *= keep;
           if (i > 0) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[16];
-              const uint32_t at = to + 128u * s + 64u * hf + 16u * c;
-              tmem_ld16(at, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-              tmem_st16(at, o);
-            }
+            for (uint32_t c = 0; c < 64u; c += 16u) rescale16(to + 128u * s + 64u * hf + c, keep);
           }
         }
         // +inf makes every weight of a row that sees none of these keys zero, 0 those of one that saw none yet
         const float base = limit <= 0 ? INFINITY : (m == -INFINITY ? 0.f : m);
-        const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), base2 = pack_f32x2(-base, -base);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (c == 1) {
             tmem_ld32(ts + 64u + 32u * hf, x);
             tmem_wait_ld();
-            if (ragged) mask(x, 1);
+            if (ragged) mask32(x, limit - 64);
           }
-          uint32_t w[16];
-          uint64_t t2 = 0;
-          float u0 = 0.f, u1 = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float a0, a1;
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2,
-                                   base2), a0, a1);
-            a0 = ex2_approx(a0);
-            a1 = ex2_approx(a1);
-            t2 = add_f32x2(t2, pack_f32x2(a0, a1));
-            w[k] = pack_f16x2(a0, a1);
-            if (k & 1)
-              u1 = add_f16x2_halves(u1, w[k]);
-            else
-              u0 = add_f16x2_halves(u0, w[k]);
-          }
-          tmem_st16(ts + 32u * c + 16u * hf, w);
-          float t0, t1;
-          unpack_f32x2(t2, t0, t1);
-          total += t0 + t1;
-          used += u0 + u1;
+          weights32(x, p.scale_log2, base, ts + 32u * c + 16u * hf, total, used);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -601,56 +375,40 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         }
       }
       tiles += n;
-      const long long row = static_cast<long long>(sg.block * 2 * kTile + brow) * p.num_heads + sg.h;
+      const long long row = static_cast<long long>(r) * p.num_heads + sg.h;
       float other2 = -INFINITY;
       if (p.suffix_lse && real && sg.whole) other2 = p.suffix_lse[row] * kLog2e;
       // every value product of the stream in this segment (n_s counts them too)
       if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(bar_pv(s), (n_s - 1) & 1, ctl));
-      // The row's result: the sums of its two threads (two row tiles), or of
-      // the four of both streams, whose maxima differ.  All softmax warps vote,
-      // so that a wait that ran out in one ends them all.
-      float f0, f1 = 0.f, lse2;
-      if (two) {
-        xmax[hf * kTile] = total;
-        ok = named_bar_all(9, kSoftmaxWarps * 32, ok);
-        if (!ok) break;
-        total += xmax[(hf ^ 1) * kTile];
-        named_bar_sync(9, kSoftmaxWarps * 32);
-        xmax[hf * kTile] = used;
-        named_bar_sync(9, kSoftmaxWarps * 32);
-        used += xmax[(hf ^ 1) * kTile];
-        named_bar_sync(9, kSoftmaxWarps * 32);
-        f0 = used == 0.f ? 0.f : 1.f / used;
-        lse2 = total == 0.f ? -INFINITY : m + lg2(total);
-      } else {
-        float* mine = xchg + (s * 2 + hf) * 3 * kTile + r;
-        mine[0] = m;
-        mine[kTile] = total;
-        mine[2 * kTile] = used;
-        ok = named_bar_all(9, kSoftmaxWarps * 32, ok);
-        if (!ok) break;
-        const float m0 = xchg[r], m1 = xchg[6 * kTile + r];
-        const float top = fmaxf(m0, m1), base = top == -INFINITY ? 0.f : top;
-        const float a0 = ex2_approx(m0 - base), a1 = ex2_approx(m1 - base);
-        const float sum = (xchg[kTile + r] + xchg[4 * kTile + r]) * a0 + (xchg[7 * kTile + r] + xchg[10 * kTile + r]) * a1;
-        const float u = (xchg[2 * kTile + r] + xchg[5 * kTile + r]) * a0 + (xchg[8 * kTile + r] + xchg[11 * kTile + r]) * a1;
-        const float inv = u == 0.f ? 0.f : 1.f / u;
-        f0 = a0 * inv;
-        f1 = a1 * inv;
-        lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
-        named_bar_sync(9, kSoftmaxWarps * 32);  // the exchange may be written again
-      }
+      // The row's result: the sums of its four threads; the streams' maxima
+      // differ.  All softmax warps vote, so that a wait that ran out in one
+      // ends them all.
+      float* mine = xchg + (s * 2 + hf) * 3 * kTile + r;
+      mine[0] = m;
+      mine[kTile] = total;
+      mine[2 * kTile] = used;
+      ok = named_bar_all(9, kSoftmaxWarps * 32, ok);
+      if (!ok) break;
+      const float m0 = xchg[r], m1 = xchg[6 * kTile + r];
+      const float top = fmaxf(m0, m1), base = top == -INFINITY ? 0.f : top;
+      const float a0 = ex2_approx(m0 - base), a1 = ex2_approx(m1 - base);
+      const float sum = (xchg[kTile + r] + xchg[4 * kTile + r]) * a0 + (xchg[7 * kTile + r] + xchg[10 * kTile + r]) * a1;
+      const float u = (xchg[2 * kTile + r] + xchg[5 * kTile + r]) * a0 + (xchg[8 * kTile + r] + xchg[11 * kTile + r]) * a1;
+      const float inv = u == 0.f ? 0.f : 1.f / u;
+      const float f0 = a0 * inv, f1 = a1 * inv;       // scale of each stream's O in the row's result
+      const float lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
+      named_bar_sync(9, kSoftmaxWarps * 32);          // the exchange may be written again
       tc_fence_after();
       Join j = {1.f, 0.f, lse2};
       if (p.suffix_lse && sg.whole) j = join(lse2, other2);
-      const long long prow = (2ll * blockIdx.x + (sg.first ? 0 : 1)) * p.part_rows + brow;
-      // two row tiles: a stream's own O, half of the columns each; one: both O's, a quarter each
-      const uint32_t c0 = two ? 64u * hf : 64u * s + 32u * hf, c1 = c0 + (two ? 64u : 32u);
-      const bool second = !two && n > 1;
+      const long long prow = (2ll * blockIdx.x + (sg.first ? 0 : 1)) * p.part_rows + r;
+      // both streams' O, a quarter of the columns each
+      const uint32_t c0 = 64u * s + 32u * hf;
+      const bool second = n > 1;
 #pragma unroll 1
-      for (uint32_t c = c0; c < c1; c += 16u) {
+      for (uint32_t c = c0; c < c0 + 32u; c += 16u) {
         uint32_t a[16], b[16];
-        tmem_ld16(to + (two ? 128u * s : 0u) + c, a);
+        tmem_ld16(to + c, a);
         if (second) tmem_ld16(to + 128u + c, b);
         tmem_wait_ld();
         if (!real) continue;
@@ -669,7 +427,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
           for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      if (real && hf == 0 && (two || s == 0)) {
+      if (real && hf == 0 && s == 0) {
         if (sg.whole)
           p.lse[row] = j.lse2 * kLn2;
         else
@@ -824,10 +582,9 @@ int attend_device_ready(int* sms) {
       st.status = MLA_ERR_DEVICE;
       return;
     }
-    if (cudaFuncSetAttribute(mla_prefix_attend_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+    if (cudaFuncSetAttribute(mla_prefix_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(mla_prefix_attend_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
-            cudaSuccess) {
+        attend_pair_set_attrs() != cudaSuccess) {
       cudaGetLastError();
       st.status = MLA_ERR_CUDA;
     }
@@ -836,21 +593,23 @@ int attend_device_ready(int* sms) {
   return st.status;
 }
 
+// Units: up to 128 tokens CTAs, above pairs of SMs, which take 256 rows.
 // Row blocks of a head that are worked on side by side read each key tile
 // from HBM once and from L2 after that, so a batch of several blocks wants
-// them side by side; but `width` must leave few SMs idle (sms / width groups)
-// and few blocks over in the last pass.  The cost of a width: steps of the
-// longest range, each the tensor cores' 2,560 cycles (two row tiles) or, when
-// all groups stream different tiles, their share of the HBM: 64 KiB a group
-// at 3.5 KB a cycle, 18.6 cycles a group.
+// them side by side; but `width` must leave few units idle (units / width
+// groups) and few blocks over in the last pass.  The cost of a width: steps
+// of the longest range, each the tensor cores' 1,280 cycles or, when all
+// groups stream different tiles, their share of the HBM: 64 KiB a group at
+// 3.5 KB a cycle, 18.6 cycles a group.
 Plan plan(int num_tokens, int num_heads, int prefix_len, int sms) {
   Plan w;
+  const int units = num_tokens > kTile ? sms / 2 : sms;
   w.nk = (prefix_len + kTile - 1) / kTile;
   w.blocks = (num_tokens + 2 * kTile - 1) / (2 * kTile);
   double best = 0;
-  for (int width = 1; width <= w.blocks && width <= sms && width <= 16; ++width) {
-    const int groups = sms / width, passes = (w.blocks + width - 1) / width;
-    const double step = fmax(num_tokens > kTile ? 2560.0 : 1280.0, 18.6 * groups);
+  for (int width = 1; width <= w.blocks && width <= units && width <= 16; ++width) {
+    const int groups = units / width, passes = (w.blocks + width - 1) / width;
+    const double step = fmax(1280.0, 18.6 * groups);
     const double cost = passes * step / groups;
     if (width == 1 || cost < 0.99 * best) {
       best = cost;
@@ -942,18 +701,23 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.lse);
   p.part_rows = l.rows;
+  const bool small = num_tokens <= kTile;
+  const cuuint32_t half = kTile / 2;
   CUtensorMap qn, qp, k, kp, vm;
   const cuuint64_t pe_size[2] = {kRope, static_cast<cuuint64_t>(prefix_len)};
   const cuuint64_t pe_stride[1] = {kRope * 2};
-  const cuuint32_t pe_box[2] = {kRope, static_cast<cuuint32_t>(kTile)};
+  const cuuint32_t pe_box[2] = {kRope, small ? kTile : half};
+  // boxes: keys {64 dims, 128 rows} or a rank's 64 of them; values {64 dims,
+  // 64 rows, both chunks} or {64 dims, 128 rows} of a rank's chunk
   if (!encode_q(&qn, q_nope, kHeadDim, q_stride, num_heads, num_tokens) ||
       !encode_q(&qp, q_pe, kRope, q_stride, num_heads, num_tokens) ||
-      !encode_kv(&k, false, k_nope, prefix_len, head_rows, num_heads, kTile, 1) ||
+      !encode_kv(&k, false, k_nope, prefix_len, head_rows, num_heads, small ? kTile : half, 1) ||
       !encode(&kp, false, 2, k_pe, pe_size, pe_stride, pe_box) ||
-      !encode_kv(&vm, true, v, prefix_len, head_rows, num_heads, kTile / 2, 2))
+      !encode_kv(&vm, true, v, prefix_len, head_rows, num_heads, small ? half : kTile, small ? 2 : 1))
     return MLA_ERR_CUDA;
-  const int ctas = p.plan.groups * p.plan.width;
-  rc = launch_dependent(num_tokens <= kTile ? mla_prefix_attend_kernel<true> : mla_prefix_attend_kernel<false>, dim3(ctas), dim3(kThreads), kSmem, 1, stream, p, qn, qp, k, kp, vm);
+  const int units = p.plan.groups * p.plan.width;
+  rc = small ? launch_dependent(mla_prefix_attend_kernel, dim3(units), dim3(kThreads), kSmem, 1, stream, p, qn, qp, k, kp, vm)
+             : attend_pair_launch(units, stream, p, qn, qp, k, kp, vm);
   // heads are cut wherever a range does not end with one
   if (rc != MLA_OK || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
   const int rows = num_tokens < l.rows ? num_tokens : l.rows;

@@ -1,0 +1,234 @@
+// prefix_attend.cuh — what the two attention kernels over a shared prefix have
+// in common: the work split and its walk, a softmax step on 32 scores, and the
+// join with a suffix's result.
+#pragma once
+#include <cmath>
+#include <cstdint>
+
+#include "prefix_common.cuh"
+
+namespace mla {
+namespace prefix {
+
+constexpr int kHeadDim = 128;
+constexpr int kRope = 64;
+constexpr int kTile = 128;                  // query rows of a row tile, keys of a key tile
+constexpr int kQChunks = 3;                 // 64-dim chunks of a query or key row
+constexpr int kQTile = kQChunks * 16384;    // 48 KiB: 128 query rows
+constexpr int kSoftmaxWarps = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;               // log2 by which a score must beat the running maximum to move it
+
+// ---- work split
+struct Plan {
+  int nk;         // key tiles
+  int blocks;     // row blocks of 256
+  int width;      // row blocks worked on side by side by the CTAs of a group
+  int groups;     // CTA groups, each with a range of the line
+  int passes;     // ceil(blocks / width)
+  long long line; // passes * heads * nk steps
+};
+
+struct AttendParams {
+  const int* visible;
+  int num_tokens, num_heads, prefix_len;
+  float scale_log2;
+  const uint16_t* suffix_out;
+  const float* suffix_lse;
+  int out_fp32;
+  void* out;
+  float* lse;
+  float* part_o;    // [2 * units][rows][128], normalised
+  float* part_lse;  // [2 * units][rows], log2
+  int part_rows;
+  Plan plan;
+  int* status;
+};
+
+__host__ __device__ __forceinline__ long long cut(const Plan& w, int g) { return w.line * g / w.groups; }
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 32 lanes x 16 consecutive 32-bit columns (the store of tmem_ld16).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Two fp32 in a 64-bit register, and the packed operations on them.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// ---- a softmax step on 32 consecutive scores of a row
+// Scores `limit` and up become -inf.
+__device__ __forceinline__ void mask32(uint32_t (&x)[32], int limit) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (k >= limit) x[k] = 0xff800000u;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
+  float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
+#pragma unroll
+  for (int k = 2; k < 30; k += 4) {
+    a = fmaxf(fmaxf(a, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+    b = fmaxf(fmaxf(b, __uint_as_float(x[k + 2])), __uint_as_float(x[k + 3]));
+  }
+  return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
+}
+
+// Weights 2^(x * scale - base) to 16 columns of tensor memory in fp16, and
+// their sums: of the fp32 values, and of the fp16 ones that the value product
+// takes (each widened exactly).
+__device__ __forceinline__ void weights32(const uint32_t (&x)[32], float scale, float base, uint32_t taddr, float& total,
+                                          float& used) {
+  const uint64_t scale2 = pack_f32x2(scale, scale), base2 = pack_f32x2(-base, -base);
+  uint32_t w[16];
+  uint64_t t2 = 0;
+  float u0 = 0.f, u1 = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float a0, a1;
+    unpack_f32x2(
+        fma_f32x2(pack_f32x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2, base2), a0, a1);
+    a0 = ex2_approx(a0);
+    a1 = ex2_approx(a1);
+    t2 = add_f32x2(t2, pack_f32x2(a0, a1));
+    w[k] = pack_f16x2(a0, a1);
+    if (k & 1)
+      u1 = add_f16x2_halves(u1, w[k]);
+    else
+      u0 = add_f16x2_halves(u0, w[k]);
+  }
+  tmem_st16(taddr, w);
+  float t0, t1;
+  unpack_f32x2(t2, t0, t1);
+  total += t0 + t1;
+  used += u0 + u1;
+}
+
+// 16 consecutive columns of O times `keep`.
+__device__ __forceinline__ void rescale16(uint32_t taddr, float keep) {
+  uint32_t o[16];
+  tmem_ld16(taddr, o);
+  tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+  tmem_st16(taddr, o);
+}
+
+// One segment of a CTA's range: key tiles [k0, k1) of head h for row block `block`.
+struct Segment {
+  int h, block, k0, k1, rows;
+  bool first, whole;
+};
+
+struct SegmentIter {
+  const Plan& w;
+  int num_tokens, num_heads, lane_block, unit, k0;
+  long long left;
+  bool first;
+  // `unit_id`: the CTA's number, or the pair's
+  __device__ SegmentIter(const AttendParams& p, int unit_id)
+      : w(p.plan), num_tokens(p.num_tokens), num_heads(p.num_heads) {
+    const int g = unit_id / w.width;
+    lane_block = unit_id % w.width;
+    const long long begin = cut(w, g);
+    left = cut(w, g + 1) - begin;
+    unit = static_cast<int>(begin / w.nk);
+    k0 = static_cast<int>(begin - static_cast<long long>(unit) * w.nk);
+    first = true;
+  }
+  __device__ bool next(Segment& s) {
+    if (left <= 0) return false;
+    s.block = unit / num_heads * w.width + lane_block;
+    if (s.block >= w.blocks) return false;  // blocks grow along the line
+    s.h = unit % num_heads;
+    s.k0 = k0;
+    s.k1 = left < w.nk - k0 ? k0 + static_cast<int>(left) : w.nk;
+    s.whole = s.k1 - k0 == w.nk;
+    s.first = first;
+    const int rows = num_tokens - s.block * 2 * kTile;
+    s.rows = rows < 2 * kTile ? rows : 2 * kTile;
+    left -= s.k1 - k0;
+    k0 = 0;
+    ++unit;
+    first = false;
+    return true;
+  }
+};
+
+// Weights of the prefix's and the suffix's result in their join, and the joined LSE (log2).
+struct Join {
+  float mine, other, lse2;
+};
+__device__ __forceinline__ Join join(float lse2, float other2) {
+  Join j;
+  const float top = fmaxf(lse2, other2);
+  const float base = top == -INFINITY ? 0.f : top;
+  const float a = ex2_approx(lse2 - base), b = ex2_approx(other2 - base);
+  const float sum = a + b;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
+  j.mine = a * inv;
+  j.other = b * inv;
+  j.lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
+  return j;
+}
+
+// 16 bytes of 8 result columns, or 32 in fp32, joined with the suffix's.
+__device__ __forceinline__ void write8(const AttendParams& p, long long row, int col, const float* o, const Join& j) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = o[i] * j.mine;
+  const long long at = row * kHeadDim + col;
+  if (p.suffix_out && j.other != 0.f) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p.suffix_out + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = fmaf(__uint_as_float(w[i] << 16), j.other, x[2 * i]);
+      x[2 * i + 1] = fmaf(__uint_as_float(w[i] & 0xffff0000u), j.other, x[2 * i + 1]);
+    }
+  }
+  if (p.out_fp32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+}
+
+// The kernel for more than 128 tokens (prefix_attend_pair.cu).
+cudaError_t attend_pair_set_attrs();
+int attend_pair_launch(int pairs, mla_stream_t stream, const AttendParams& p, const CUtensorMap& qn,
+                       const CUtensorMap& qp, const CUtensorMap& k, const CUtensorMap& kp, const CUtensorMap& v);
+
+}  // namespace prefix
+}  // namespace mla

@@ -11,15 +11,18 @@
 //
 // Tensor memory of a CTA: O (128 columns) and three score buffers (128 each).
 // Tile j's scores S(j) lie in buffer j % 3; its weights P(j) replace them in
-// fp16.  The tensor cores run PV(j), QK(j + 2), PV(j + 1), QK(j + 3) ..: the
-// buffer that QK(j + 2) overwrites is that of P(j - 1), two products back, so
-// nothing waits on a product just issued, and two tiles are in the softmax at
-// a time.
+// fp16.  In the steady state the tensor cores run PV(j), QK(j + 2), PV(j + 1),
+// QK(j + 3) ..: the buffer that QK(j + 2) overwrites is that of P(j - 1), two
+// products back, so nothing waits on a product just issued, and two tiles are
+// in the softmax at a time.
 //
 //   warps 0-7, 8-15 softmax of even and odd tiles: two threads a query row,
 //                   64 scores each
 //   warp 16         TMA
-//   warp 17         tcgen05.mma (rank 0, for both CTAs)
+//   warps 17, 18    tcgen05.mma (rank 0, for both CTAs): scores, value products.
+//                   One warp issuing both lost 830 of a tile's 2,370 cycles
+//                   to its waits (the tensor core queues few MMAs); each now
+//                   waits under the other's products
 //
 // The running maximum passes from tile to tile, from one group of warps to the
 // other, through shared memory (a barrier for each 32 rows); it is lazy, so
@@ -56,8 +59,8 @@ constexpr int kNumBars = 4 + 4 * kStagesKV + 4 + 8;
 constexpr int kSlack = 1024;                // re-aligned to 1024 B (128-byte swizzle atoms)
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
 static_assert(kSmem <= 232448, "shared memory");
-constexpr int kThreads = 576;
-constexpr int kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 608;
+constexpr int kTmaWarp = 16, kQkWarp = 17;  // and 18 for the value products
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 128;  // + 128 * buffer
 constexpr uint32_t kIdescQK = idesc_bf16(256, 128, 0);
@@ -99,7 +102,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
     mbar_init(bar_q_full, 1);
     mbar_init(bar_q_empty, 1);
     mbar_init(bar_o_free, 2 * kSoftmaxWarps);
-    mbar_init(bar_drain, 1);
+    mbar_init(bar_drain, 2);
     for (uint32_t q = 0; q < kStagesKV; ++q) {
       mbar_init(k_full(q), 1);
       mbar_init(v_full(q), 1);
@@ -113,7 +116,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
     *abort_flag = 0u;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_pair();
   }
@@ -173,58 +176,65 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kQkWarp) {
     if (rank == 0) {
       // the whole warp runs, one lane issues (uniform operands)
       const uint32_t leader = lane == 0 ? 1u : 0u;
-      const uint64_t ad = smem_desc(sbase, 16u, 1024u);
-      const uint64_t kd = smem_desc(sbase + kOffK, 16u, 1024u), vd = smem_desc(sbase + kOffV, 16384u, 1024u);
       uint32_t q0 = 0, seg = 0;  // the segment's first tile
       bool ok = true;
-      auto issue_qk = [&](uint32_t q) -> bool {
-        // its score buffer last held the weights of tile q - 3
-        if (!wait<true>(k_full(q), par4(q), ctl) || (q >= 3 && !wait<true>(bar_pv(q - 3), par4(q - 3), ctl))) return false;
-        tc_fence_after();
-        const uint64_t bd = kd + static_cast<uint64_t>((q & 3u) * (kKStage >> 4));
-        const uint32_t d = tmem + kColS + 128u * (q % 3u);
-#pragma unroll
-        for (int c = 0; c < kQChunks; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_pair_ss_if(leader, d, ad + ((c * 16384 + 32 * kk) >> 4), bd + ((c * 8192 + 32 * kk) >> 4), kIdescQK,
-                            (c | kk) != 0 ? 1u : 0u);
-        umma_commit_pair_if(leader, bar_s(q), kBoth);
-        return true;
-      };
-      while (ok && it.next(sg)) {
-        const uint32_t n = static_cast<uint32_t>(sg.k1 - sg.k0), q1 = q0 + n;
-        ok = wait<true>(bar_q_full, seg & 1, ctl) && issue_qk(q0) && (n < 2 || issue_qk(q0 + 1));
-        if (n <= 2) umma_commit_pair_if(leader, bar_q_empty, kBoth);
-        // O of the segment before has been read
-        if (ok && seg > 0) ok = wait<true>(bar_o_free, (seg - 1) & 1, ctl);
-        for (uint32_t q = q0; ok && q < q1; ++q) {
-          ok = wait<true>(v_full(q), par4(q), ctl);
-          const uint64_t bd = vd + static_cast<uint64_t>((q & 3u) * (kVStage >> 4));
-          const uint32_t a = tmem + kColS + 128u * (q % 3u);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && wait<true>(p_full(q, half), par2(q), ctl);
+      if (warp == kQkWarp) {
+        const uint64_t ad = smem_desc(sbase, 16u, 1024u), kd = smem_desc(sbase + kOffK, 16u, 1024u);
+        while (ok && it.next(sg)) {
+          const uint32_t q1 = q0 + static_cast<uint32_t>(sg.k1 - sg.k0);
+          ok = wait<true>(bar_q_full, seg & 1, ctl);
+          for (uint32_t q = q0; ok && q < q1; ++q) {
+            // Its score buffer last held the weights of tile q - 3.  And the
+            // softmax warps that take it have all finished with tile q - 2:
+            // one that ran ahead would arrive twice on a barrier of theirs.
+            ok = wait<true>(k_full(q), par4(q), ctl) && (q < 2 || wait<true>(p_full(q - 2, 1), par2(q - 2), ctl)) &&
+                 (q < 3 || wait<true>(bar_pv(q - 3), par4(q - 3), ctl));
             if (!ok) break;
             tc_fence_after();
+            const uint64_t bd = kd + static_cast<uint64_t>((q & 3u) * (kKStage >> 4));
+            const uint32_t d = tmem + kColS + 128u * (q % 3u);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_pair_ts_if(leader, tmem + kColO, a + 32u * half + 8u * kk, bd + ((8192 * half + 2048 * kk) >> 4),
-                              kIdescPV, q == q0 && (half | kk) == 0 ? 0u : 1u);
+            for (int c = 0; c < kQChunks; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_pair_ss_if(leader, d, ad + ((c * 16384 + 32 * kk) >> 4), bd + ((c * 8192 + 32 * kk) >> 4), kIdescQK,
+                                (c | kk) != 0 ? 1u : 0u);
+            umma_commit_pair_if(leader, bar_s(q), kBoth);
           }
-          if (!ok) break;
-          umma_commit_pair_if(leader, bar_pv(q), kBoth);
-          if (q + 2 < q1) {
-            ok = issue_qk(q + 2);
-            if (q + 3 == q1) umma_commit_pair_if(leader, bar_q_empty, kBoth);  // the segment's last scores
-          }
+          umma_commit_pair_if(leader, bar_q_empty, kBoth);
+          q0 = q1;
+          ++seg;
         }
-        q0 = q1;
-        ++seg;
+      } else {
+        const uint64_t vd = smem_desc(sbase + kOffV, 16384u, 1024u);
+        while (ok && it.next(sg)) {
+          const uint32_t q1 = q0 + static_cast<uint32_t>(sg.k1 - sg.k0);
+          // O of the segment before has been read
+          if (seg > 0) ok = wait<true>(bar_o_free, (seg - 1) & 1, ctl);
+          for (uint32_t q = q0; ok && q < q1; ++q) {
+            ok = wait<true>(v_full(q), par4(q), ctl);
+            const uint64_t bd = vd + static_cast<uint64_t>((q & 3u) * (kVStage >> 4));
+            const uint32_t a = tmem + kColS + 128u * (q % 3u);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && wait<true>(p_full(q, half), par2(q), ctl);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_pair_ts_if(leader, tmem + kColO, a + 32u * half + 8u * kk, bd + ((8192 * half + 2048 * kk) >> 4),
+                                kIdescPV, q == q0 && (half | kk) == 0 ? 0u : 1u);
+            }
+            if (!ok) break;
+            umma_commit_pair_if(leader, bar_pv(q), kBoth);
+          }
+          q0 = q1;
+          ++seg;
+        }
       }
       umma_commit_pair_if(leader, bar_drain, 1);  // arrives once every MMA issued above has completed
       drain_bar(bar_drain, 0u);
@@ -272,7 +282,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
         if (ragged) mask32(x, limit);
         top = limit <= 0 ? -INFINITY : fmaxf(top, max32(x));
         // The partner cannot write its next maximum before this one is read:
-        // its next scores wait for this warp's weights.
+        // its next scores wait for this warp's weights of this tile.
         xmax[hf * kTile] = top;
         ok = named_bar_all(pair_bar, 64, ok);         // votes: a wait that ran out in one warp ends both
         if (!ok) break;
@@ -384,7 +394,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA touches another's shared memory after this
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }

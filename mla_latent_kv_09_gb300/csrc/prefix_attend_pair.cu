@@ -50,12 +50,12 @@ constexpr int kKStage = 3 * 8192;           // 64 keys x 192 dims, as 64-dim chu
 constexpr int kVStage = 16384;              // 128 keys x 64 dims
 constexpr int kOffK = kQTile;               // 48 KiB of queries first
 constexpr int kOffV = kOffK + kStagesKV * kKStage;
-constexpr int kOffMax = kOffV + kStagesKV * kVStage;    // 208 KiB: [group][half][row] maxima
-constexpr int kOffRef = kOffMax + 4 * kTile * 4;        // [tile & 1][row] the running maximum
+constexpr int kOffMax = kOffV + kStagesKV * kVStage;    // 208 KiB: [group][2][half][row] maxima
+constexpr int kOffRef = kOffMax + 8 * kTile * 4;        // [tile & 1][row] the running maximum
 constexpr int kOffXchg = kOffRef + 2 * kTile * 4;           // [group][half][maximum, two sums][row]
 constexpr int kOffBar = kOffXchg + 12 * kTile * 4;
-// q_full q_empty o_free drain; by stage k_full v_full s_full pv; p_full[2][2]; m_done[2][4]
-constexpr int kNumBars = 4 + 4 * kStagesKV + 4 + 8;
+// q_full q_empty o_free drain; by stage k_full v_full s_full pv; p_full[4][2]; m_done[2][4]
+constexpr int kNumBars = 4 + 4 * kStagesKV + 8 + 8;
 constexpr int kSlack = 1024;                // re-aligned to 1024 B (128-byte swizzle atoms)
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
 static_assert(kSmem <= 232448, "shared memory");
@@ -89,10 +89,13 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
   auto v_full = [&](uint32_t q) { return bar0 + 64u + 8u * (q & 3u); };
   auto bar_s = [&](uint32_t q) { return bar0 + 96u + 8u * (q & 3u); };
   auto bar_pv = [&](uint32_t q) { return bar0 + 128u + 8u * (q & 3u); };
-  // weights of tile q's first and second 64 keys (rank 0)
-  auto p_full = [&](uint32_t q, uint32_t half) { return bar0 + 160u + 16u * (q & 1u) + 8u * half; };
+  // Weights of tile q's first and second 64 keys (rank 0).  Scores of tile q +
+  // 2 may come while a slower warp of the group still works on tile q, those
+  // of q + 4 not (they need PV(q + 1)): four barriers, and two buffers for
+  // what a group's warps exchange.
+  auto p_full = [&](uint32_t q, uint32_t half) { return bar0 + 160u + 16u * (q & 3u) + 8u * half; };
   // the running maximum after tile q, of 32 rows
-  auto m_done = [&](uint32_t q, int quarter) { return bar0 + 192u + 32u * (q & 1u) + 8u * quarter; };
+  auto m_done = [&](uint32_t q, int quarter) { return bar0 + 224u + 32u * (q & 1u) + 8u * quarter; };
   auto par4 = [](uint32_t q) { return (q >> 2) & 1u; };
   auto par2 = [](uint32_t q) { return (q >> 1) & 1u; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
@@ -109,8 +112,9 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
       mbar_init(bar_s(q), 1);
       mbar_init(bar_pv(q), 1);
     }
-    for (uint32_t q = 0; q < 2; ++q) {
+    for (uint32_t q = 0; q < 4; ++q)
       for (uint32_t half = 0; half < 2; ++half) mbar_init(p_full(q, half), kSoftmaxWarps);  // 8 warps of both CTAs
+    for (uint32_t q = 0; q < 2; ++q) {
       for (int quarter = 0; quarter < 4; ++quarter) mbar_init(m_done(q, quarter), 2);
     }
     *abort_flag = 0u;
@@ -188,11 +192,8 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
           const uint32_t q1 = q0 + static_cast<uint32_t>(sg.k1 - sg.k0);
           ok = wait<true>(bar_q_full, seg & 1, ctl);
           for (uint32_t q = q0; ok && q < q1; ++q) {
-            // Its score buffer last held the weights of tile q - 3.  And the
-            // softmax warps that take it have all finished with tile q - 2:
-            // one that ran ahead would arrive twice on a barrier of theirs.
-            ok = wait<true>(k_full(q), par4(q), ctl) && (q < 2 || wait<true>(p_full(q - 2, 1), par2(q - 2), ctl)) &&
-                 (q < 3 || wait<true>(bar_pv(q - 3), par4(q - 3), ctl));
+            // its score buffer last held the weights of tile q - 3
+            ok = wait<true>(k_full(q), par4(q), ctl) && (q < 3 || wait<true>(bar_pv(q - 3), par4(q - 3), ctl));
             if (!ok) break;
             tc_fence_after();
             const uint64_t bd = kd + static_cast<uint64_t>((q & 3u) * (kKStage >> 4));
@@ -221,7 +222,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
             const uint32_t a = tmem + kColS + 128u * (q % 3u);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = ok && wait<true>(p_full(q, half), par2(q), ctl);
+              ok = ok && wait<true>(p_full(q, half), par4(q), ctl);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -246,7 +247,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
     const int r = quarter * 32 + lane;                // row of the CTA's 128, lane of tensor memory
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t to = tmem + lane_base + kColO;
-    float* xmax = reinterpret_cast<float*>(smem + kOffMax) + g * 2 * kTile + r;
+    float* xmax2 = reinterpret_cast<float*>(smem + kOffMax) + g * 4 * kTile + r;
     float* ref = reinterpret_cast<float*>(smem + kOffRef) + r;
     float* xchg = reinterpret_cast<float*>(smem + kOffXchg) + r;
     const int pair_bar = 1 + static_cast<int>(g) * 4 + quarter;  // the two warps that share rows of a tile
@@ -281,8 +282,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
         tmem_wait_ld();
         if (ragged) mask32(x, limit);
         top = limit <= 0 ? -INFINITY : fmaxf(top, max32(x));
-        // The partner cannot write its next maximum before this one is read:
-        // its next scores wait for this warp's weights of this tile.
+        float* xmax = xmax2 + ((q >> 1) & 1u) * 2 * kTile;
         xmax[hf * kTile] = top;
         ok = named_bar_all(pair_bar, 64, ok);         // votes: a wait that ran out in one warp ends both
         if (!ok) break;
@@ -328,7 +328,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
           tc_fence_before();
           __syncwarp();
           // (orders tensor-memory accesses only, which tcgen05.wait has completed)
-          if (lane == 0) mbar_arrive_remote_relaxed(rp0 + 16u * (q & 1u) + 8u * c);
+          if (lane == 0) mbar_arrive_remote_relaxed(rp0 + 16u * (q & 3u) + 8u * c);
         }
       }
       q0 = q1;

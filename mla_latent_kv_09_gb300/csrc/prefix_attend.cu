@@ -30,9 +30,8 @@
 // The weights are handed over in two halves of 64 keys: the value product of
 // the first runs under the exponentials of the second.
 //
-// The running maximum is lazy: it moves only when a score beats it by 2^8, so
-// that weights stay below 2^8 (fp16 holds them with 11 bits) and O is rarely
-// rescaled.  O is normalised by the sum of the rounded weights that the value
+// The running maximum is lazy: it moves only when a score beats it by 2^14, so
+// that O is rarely rescaled.  O is normalised by the sum of the rounded weights that the value
 // product used, so that a weight's rounding acts on v_j - O and not on v_j;
 // the LSE takes the sum of the unrounded ones.
 //

@@ -274,14 +274,18 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
         // only rows that end in this tile need masks (a row that sees none of it gets zeros below)
         const bool ragged = __any_sync(0xffffffffu, limit > 0 && limit < 96);
         uint32_t x[32];
-        tmem_ld32(ts + 64u + 32u * hf, x);
-        tmem_wait_ld();
-        if (ragged) mask32(x, limit - 64);
-        float top = max32(x);
-        tmem_ld32(ts + 32u * hf, x);
-        tmem_wait_ld();
-        if (ragged) mask32(x, limit);
-        top = limit <= 0 ? -INFINITY : fmaxf(top, max32(x));
+        float top;
+        {
+          uint32_t y[32];
+          tmem_ld32(ts + 32u * hf, x);
+          tmem_ld32(ts + 64u + 32u * hf, y);
+          tmem_wait_ld();
+          if (ragged) {
+            mask32(x, limit);
+            mask32(y, limit - 64);
+          }
+          top = limit <= 0 ? -INFINITY : fmaxf(max32(x), max32(y));
+        }
         float* xmax = xmax2 + ((q >> 1) & 1u) * 2 * kTile;
         xmax[hf * kTile] = top;
         ok = named_bar_all(pair_bar, 64, ok);         // votes: a wait that ran out in one warp ends both

@@ -204,28 +204,124 @@ __device__ __forceinline__ Join join(float lse2, float other2) {
   return j;
 }
 
-// 16 bytes of 8 result columns, or 32 in fp32, joined with the suffix's.
-__device__ __forceinline__ void write8(const AttendParams& p, long long row, int col, const float* o, const Join& j) {
-  float x[8];
+// 8 result columns of a row: their share of the join with the suffix's 8.
+__device__ __forceinline__ void join8(float* x, const Join& j, const uint4& suffix) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = o[i] * j.mine;
-  const long long at = row * kHeadDim + col;
-  if (p.suffix_out && j.other != 0.f) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p.suffix_out + at);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < 8; ++i) x[i] *= j.mine;
+  if (j.other != 0.f) {  // a suffix without a share is not read as numbers
+    const uint32_t w[4] = {suffix.x, suffix.y, suffix.z, suffix.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = fmaf(__uint_as_float(w[i] << 16), j.other, x[2 * i]);
       x[2 * i + 1] = fmaf(__uint_as_float(w[i] & 0xffff0000u), j.other, x[2 * i + 1]);
     }
   }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ uint4 pack4(const float* x) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+
+// Joins and writes 8 columns of a row (16-byte pieces).
+__device__ __forceinline__ void write8(const AttendParams& p, long long row, int col, const float* o, const Join& j) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = o[i];
+  const long long at = row * kHeadDim + col;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (p.suffix_out) v = *reinterpret_cast<const uint4*>(p.suffix_out + at);
+  join8(x, j, v);
   if (p.out_fp32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at);
+    dst[0] = pack4(x);
+    dst[1] = pack4(x + 4);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = pack8(x);
+  }
+}
+
+// 4 x 4 transpose of 16-byte pieces over four lanes: piece i of lane q becomes
+// piece q of lane i.
+__device__ __forceinline__ void quad_transpose(uint4 (&c)[4], int lane) {
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool up = (lane & b) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & b) continue;
+      uint4& lo = c[i];
+      uint4& hi = c[i | b];
+      uint4 v = up ? lo : hi;
+      v.x = __shfl_xor_sync(0xffffffffu, v.x, b);
+      v.y = __shfl_xor_sync(0xffffffffu, v.y, b);
+      v.z = __shfl_xor_sync(0xffffffffu, v.z, b);
+      v.w = __shfl_xor_sync(0xffffffffu, v.w, b);
+      if (up)
+        lo = v;
+      else
+        hi = v;
+    }
+  }
+}
+
+// The segment epilogue of a warp: 32 rows (one a lane), 32 columns from `col`.
+// Rows lie heads * 256 bytes apart, so that a warp that stored its rows as it
+// holds them would touch 32 lines with every 16-byte store (7,000 cycles for
+// a CTA's 128 rows); transposed over four lanes, 64 bytes of 8 rows, it
+// touches 8.  (Up to 128 tokens the plain stores are as fast or faster: few of
+// the rows are real, and the code is shorter.)
+struct RowOut {
+  long long quad_row;  // first of the quad's four rows, in the result or among the partial rows
+  int step;            // rows between them
+  int left;            // rows from the first on that are real
+  bool whole;
+};
+
+// The suffix's columns, four lanes to a row (asked for early; see write32).
+__device__ __forceinline__ void load_suffix(const AttendParams& p, const RowOut& w, uint32_t col, int lane, uint4 (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.suffix_out && w.whole && i < w.left)
+      c[i] = *reinterpret_cast<const uint4*>(p.suffix_out + (w.quad_row + static_cast<long long>(i) * w.step) * kHeadDim +
+                                             col + 8 * (lane & 3));
+  }
+}
+
+// `read16(h, o)` gives columns col + 16 h .. of the lane's row.
+template <typename F>
+__device__ __forceinline__ void write32(const AttendParams& p, const RowOut& w, uint32_t col, int lane, const Join& j,
+                                        uint4 (&c)[4], F read16) {
+  const bool joined = p.suffix_out && w.whole, fp32 = !w.whole || p.out_fp32;
+  float* dst32 = w.whole ? static_cast<float*>(p.out) : p.part_o;
+  const long long at = w.quad_row * kHeadDim + col, step = static_cast<long long>(w.step) * kHeadDim;
+  if (joined) quad_transpose(c, lane);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float o[16];
+    read16(h, o);
+    if (joined) {
+      join8(o, j, c[2 * h]);
+      join8(o + 8, j, c[2 * h + 1]);
+    }
+    if (!fp32) {
+      c[2 * h] = pack8(o);
+      c[2 * h + 1] = pack8(o + 8);
+    } else {
+      uint4 d[4] = {pack4(o), pack4(o + 4), pack4(o + 8), pack4(o + 12)};
+      quad_transpose(d, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < w.left) *reinterpret_cast<uint4*>(dst32 + at + i * step + 16 * h + 4 * (lane & 3)) = d[i];
+    }
+  }
+  if (!fp32) {
+    quad_transpose(c, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < w.left) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + i * step + 8 * (lane & 3)) = c[i];
   }
 }
 

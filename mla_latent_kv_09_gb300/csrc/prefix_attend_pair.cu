@@ -339,6 +339,13 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
       const long long row = static_cast<long long>(sg.block * 2 * kTile + brow) * p.num_heads + sg.h;
       float other2 = -INFINITY;
       if (p.suffix_lse && real && sg.whole) other2 = p.suffix_lse[row] * kLog2e;
+      const long long prow = (2ll * pair + (sg.first ? 0 : 1)) * p.part_rows + brow;
+      const int quad = lane & 3;
+      const RowOut w = {sg.whole ? row - static_cast<long long>(quad) * p.num_heads : prow - quad,
+                        sg.whole ? p.num_heads : 1, sg.rows - (brow - quad), sg.whole};
+      const uint32_t c0 = 64u * g + 32u * hf;         // a quarter of the columns
+      uint4 suffix[4];
+      load_suffix(p, w, c0, lane, suffix);
       if (ok) ok = __all_sync(0xffffffffu, wait<true>(bar_pv(q1 - 1), par4(q1 - 1), ctl));
       // The row's result: the sums of its four threads, against the last
       // maximum.  All softmax warps vote, so that a wait that ran out in one
@@ -363,26 +370,14 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
       tc_fence_after();
       Join j = {1.f, 0.f, lse2};
       if (p.suffix_lse && sg.whole) j = join(lse2, other2);
-      const long long prow = (2ll * pair + (sg.first ? 0 : 1)) * p.part_rows + brow;
-      const uint32_t c0 = 64u * g + 32u * hf;         // a quarter of the columns
-#pragma unroll 1
-      for (uint32_t c = c0; c < c0 + 32u; c += 16u) {
+      write32(p, w, c0, lane, j, suffix, [&](int h, float (&o)[16]) {
         uint32_t a[16];
-        tmem_ld16(to + c, a);
+        tmem_ld16(to + c0 + 16u * h, a);
         tmem_wait_ld();
-        if (!real) continue;
-        float o[16];
+        // an accumulator that took nothing is not read as a number
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[k] = f0 == 0.f ? 0.f : __uint_as_float(a[k]) * f0;
-        if (sg.whole) {
-          write8(p, row, c, o, j);
-          write8(p, row, c + 8, o + 8, j);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
-      }
+      });
       if (real && hf == 0 && g == 0) {
         if (sg.whole)
           p.lse[row] = j.lse2 * kLn2;

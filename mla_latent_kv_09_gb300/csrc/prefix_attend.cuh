@@ -242,30 +242,6 @@ __device__ __forceinline__ void write8(const AttendParams& p, long long row, int
   }
 }
 
-// 4 x 4 transpose of 16-byte pieces over four lanes: piece i of lane q becomes
-// piece q of lane i.
-__device__ __forceinline__ void quad_transpose(uint4 (&c)[4], int lane) {
-#pragma unroll
-  for (int b = 1; b < 4; b <<= 1) {
-    const bool up = (lane & b) != 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i & b) continue;
-      uint4& lo = c[i];
-      uint4& hi = c[i | b];
-      uint4 v = up ? lo : hi;
-      v.x = __shfl_xor_sync(0xffffffffu, v.x, b);
-      v.y = __shfl_xor_sync(0xffffffffu, v.y, b);
-      v.z = __shfl_xor_sync(0xffffffffu, v.z, b);
-      v.w = __shfl_xor_sync(0xffffffffu, v.w, b);
-      if (up)
-        lo = v;
-      else
-        hi = v;
-    }
-  }
-}
-
 // The segment epilogue of a warp: 32 rows (one a lane), 32 columns from `col`.
 // Rows lie heads * 256 bytes apart, so that a warp that stored its rows as it
 // holds them would touch 32 lines with every 16-byte store (7,000 cycles for

@@ -34,13 +34,6 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar_cluster)
       : "memory");
 }
-// 4-D tiled store (completes in the thread's bulk group).
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, uint32_t src, int x, int y, int z, int w) {
-  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];"
-               ::"l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
-               : "memory");
-}
-
 // Arrive `n` times.
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
@@ -107,6 +100,39 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c
     }
   }
   return true;
+}
+
+// The same for a whole warp, with one answer: what depends on it stays
+// warp-uniform (an MMA takes its operands from uniform registers; issued from
+// code that may have diverged, each one first moves them there).
+template <bool kCluster = false>
+__device__ __forceinline__ bool warp_wait_uniform(uint32_t bar, uint32_t parity, const Ctl& c) {
+  return __all_sync(0xffffffffu, wait<kCluster>(bar, parity, c));
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// 4 x 4 transpose of 16-byte pieces over four lanes: piece i of lane q becomes
+// piece q of lane i.
+__device__ __forceinline__ void quad_transpose(uint4 (&c)[4], int lane) {
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool up = (lane & b) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & b) continue;
+      uint4& lo = c[i];
+      uint4& hi = c[i | b];
+      uint4 v = up ? lo : hi;
+      v.x = __shfl_xor_sync(0xffffffffu, v.x, b);
+      v.y = __shfl_xor_sync(0xffffffffu, v.y, b);
+      v.z = __shfl_xor_sync(0xffffffffu, v.z, b);
+      v.w = __shfl_xor_sync(0xffffffffu, v.w, b);
+      if (up)
+        lo = v;
+      else
+        hi = v;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host side

@@ -11,16 +11,16 @@
 // its rows, 128 key and 128 value columns, in its tensor memory.  The weights
 // stay in shared memory (128 KiB a CTA) over all row tiles of a head and are
 // replaced stage by stage under the last one; the latents stream through a
-// ring of 4 chunks of 64 dims, read from the cache's pages by TMA (they lie
+// ring of 6 chunks of 64 dims, read from the cache's pages by TMA (they lie
 // in L2: every pair reads the same rows).  Two accumulators, so that a tile is
 // drained under the next one's products.  (row tile, head) items form one
 // line, head by head, cut into equal ranges, one per pair.
 //
 //   warp 0     TMA: latents and weights
-//   warp 1     MMA issue (rank 0, for both CTAs)
-//   warps 2-5  drain: tensor memory -> bf16 / fp16 -> swizzled staging -> TMA
-//              store, 64 columns at a time
-//   warp 6     copies the RoPE dims and checks the block table
+//   warps 1, 11  MMA issue (rank 0, for both CTAs), in turns
+//   warps 2-9  drain: tensor memory -> bf16 / fp16 -> global memory, 64 columns
+//              at a time; keys and values by four warps each
+//   warp 10    copies the RoPE dims and checks the block table
 //
 // FP8 rows are first widened to bf16 in the workspace (exactly: 4 significant
 // bits and a power of two) by a kernel of their own, a warp a row: the product
@@ -41,22 +41,22 @@ using namespace prefix;
 
 constexpr int kLatent = 512;
 constexpr int kRope = 64;
+constexpr int kHeadDim = 128;
 constexpr int kFp8Row = MLA_FP8_ROW_BYTES;
 
 constexpr int kRows = 128;                   // rows of a CTA's tile
 constexpr int kStages = kLatent / 64;        // 64 latent dims each
 constexpr int kChunk = 16384;                // 128 rows x 64 dims, or 64 dims x 128 columns of a weight
-constexpr int kSlots = 4;
-constexpr int kStage = 32 * 128;             // one warp's 32 rows x 64 columns
+constexpr int kSlots = 6;
 constexpr int kOffW = 0;
 constexpr int kOffRing = kStages * kChunk;                // 128 KiB
-constexpr int kOffStage = kOffRing + kSlots * kChunk;     // 192 KiB, 4 warps x 2 buffers
-constexpr int kOffBar = kOffStage + 4 * 2 * kStage;       // 224 KiB
-constexpr int kNumBars = 2 * kSlots + 2 * kStages + 4 + 1;
+constexpr int kOffBar = kOffRing + kSlots * kChunk;       // 224 KiB
+constexpr int kNumBars = 2 * kSlots + 2 * kStages + 4 + 3;
 constexpr int kSlack = 1024;                 // re-aligned to 1024 B (128-byte swizzle atoms)
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
 static_assert(kSmem <= 232448, "shared memory");
-constexpr int kThreads = 224;
+constexpr int kThreads = 384;
+constexpr int kIssuerB = 11;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = idesc_bf16(256, 256, 1);
 
@@ -67,20 +67,22 @@ struct ExpandParams {
   const int* block_table;
   int paged;                 // the latents come from the pool's pages (else row by row)
   int prefix_len, num_heads;
+  uint16_t* k_nope;
+  uint16_t* v;
+  long long head_rows;
   uint16_t* k_pe;
   int* status;
 };
 
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_constant__ CUtensorMap tm_lat,
-                         const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
-                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+                         const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t mis = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + mis;
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t rank = uniform(cluster_ctarank());
   const int tiles = (p.prefix_len + 2 * kRows - 1) / (2 * kRows);
   const long long items = static_cast<long long>(tiles) * p.num_heads;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -95,13 +97,18 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
   auto w_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + kStages + s); };
   auto acc_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + s); };
   auto acc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 2 + s); };
+  auto turn = [&](uint32_t issuer) { return bar0 + 8u * (kNumBars - 3 + issuer); };
   const uint32_t bar_drain = bar0 + 8u * (kNumBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bar0 + 8u * i, 1);
-    for (uint32_t s = 0; s < 2; ++s) mbar_init(acc_empty(s), 8);  // the drain warps of both CTAs
+    for (uint32_t s = 0; s < 2; ++s) {
+      mbar_init(acc_full(s), 2);    // both issuers
+      mbar_init(acc_empty(s), 16);  // the drain warps of both CTAs
+    }
+    mbar_init(bar_drain, 2);  // both issuers
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -113,7 +120,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any remote operation
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   Ctl ctl;
   ctl.abort = abort_flag;
   ctl.n_remote = 1;
@@ -173,34 +180,46 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == kIssuerB) {
     if (rank == 0) {
-      // the whole warp runs, one lane issues (uniform operands)
+      // Two warps issue, stages of 64 latent dims (512 cycles of products) in
+      // turns, all into the tile's accumulator: between its four MMAs and its
+      // next ones a warp commits, gives the turn away and waits for its next
+      // chunk, 300 cycles in which the tensor core, which queues one or two
+      // MMAs, would run dry (one issuer: 5,700 cycles a tile).  The whole warp
+      // runs, one lane issues (uniform operands).
+      const uint32_t me = warp == 1 ? 0u : 1u;
       const uint32_t leader = lane == 0 ? 1u : 0u;
       const uint64_t wd = smem_desc(sbase + kOffW, kChunk / 2, 1024u);   // MN-major: 64-column halves kChunk / 2 apart
       const uint64_t ad = smem_desc(sbase + kOffRing, 16u, 1024u);
-      uint32_t chunk = 0, heads = 0;
+      uint32_t heads = 0, turns = 0, chunk = me;
       int m = m0;
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
-        const uint32_t buf = i & 1;
+        const uint32_t buf = i & 1, d = tmem + 256u * buf;
         const bool new_head = i == 0 || m == 0, last = m == tiles - 1;
-        if (i >= 2) ok = wait<true>(acc_empty(buf), ((i >> 1) - 1) & 1, ctl);
-#pragma unroll 1
-        for (uint32_t k = 0; ok && k < kStages; ++k, ++chunk) {
-          const uint32_t s = chunk % kSlots;
-          if (new_head && !(ok = wait<true>(w_full(k), heads & 1, ctl))) break;
-          if (!(ok = wait<true>(a_full(s), (chunk / kSlots) & 1, ctl))) break;
+#pragma unroll
+        for (uint32_t e = 0; e < kStages / 2; ++e) {
+          const uint32_t k = 2 * e + me, s = chunk % kSlots;
+          if (k == 0 && i >= 2) ok = warp_wait_uniform<true>(acc_empty(buf), ((i >> 1) - 1) & 1, ctl);
+          if (new_head) ok = ok && warp_wait_uniform<true>(w_full(k), heads & 1, ctl);
+          ok = ok && warp_wait_uniform<true>(a_full(s), (chunk / kSlots) & 1, ctl);
+          chunk += 2;
+          if (k != 0 || i != 0) ok = ok && warp_wait_uniform(turn(me), turns++ & 1, ctl);
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_pair_ss_if(leader, tmem + 256u * buf, ad + static_cast<uint64_t>((s * kChunk + 32 * kk) >> 4),
-                            wd + static_cast<uint64_t>((k * kChunk + 2048 * kk) >> 4), kIdesc, (k | kk) != 0 ? 1u : 0u);
+            umma_pair_ss_if(leader, d, ad + static_cast<uint64_t>((s * kChunk + 32 * kk) >> 4),
+                            wd + static_cast<uint64_t>((k * kChunk + 2048 * kk) >> 4), kIdesc,
+                            (k | kk) != 0 ? 1u : 0u);
+          tc_fence_before();
+          if (leader) mbar_arrive_relaxed(turn(me ^ 1u));
           umma_commit_pair_if(leader, a_empty(s), 3);
           if (last) umma_commit_pair_if(leader, w_empty(k), 3);
         }
         if (!ok) break;
-        umma_commit_pair_if(leader, acc_full(buf), 3);
+        umma_commit_pair_if(leader, acc_full(buf), 3);  // both issuers' products
         if (new_head) ++heads;
         m = last ? 0 : m + 1;
       }
@@ -208,60 +227,59 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       drain_bar(bar_drain, 0u);
       __syncwarp();
     }
-  } else if (warp < 6) {
+  } else if (warp < 10) {
     const int q = warp & 3;  // tensor-memory lanes 32 q .. +31: those rows of the tile
-    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const bool keys = warp < 6;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + (keys ? 0u : 128u);
     const uint32_t racc = mapa(acc_empty(0), 0);
+    uint16_t* out = keys ? p.k_nope : p.v;
+    const int quad = lane & 3;
     int h = h0, m = m0;
-    uint32_t stores = 0;
-    bool bad = false;
     for (int i = 0; i < n; ++i) {
       const uint32_t buf = i & 1;
       const int row0 = (m * 2 + static_cast<int>(rank)) * kRows + 32 * q;
       if (!__all_sync(0xffffffffu, wait<true>(acc_full(buf), (i >> 1) & 1, ctl))) break;
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 4; ++c, ++stores) {  // key columns 0 and 64, value columns 0 and 64
+      for (int c = 0; c < 2; ++c) {
         uint32_t x[2][32];
         tmem_ld32(tl + 256u * buf + 64u * c, x[0]);
         tmem_ld32(tl + 256u * buf + 64u * c + 32u, x[1]);
         tmem_wait_ld();
-        if (c == 3) {
+        if (c == 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(racc + 8u * buf);  // the accumulator may take the tile after next
         }
-        if (lane == 0) bulk_wait_read_1();  // this staging buffer's previous store has read it
-        __syncwarp();
-        const uint32_t stg = sbase + static_cast<uint32_t>(kOffStage + (q * 2 + (stores & 1)) * kStage);
-        const uint32_t rbase = stg + static_cast<uint32_t>(lane) * 128u;
+        uint32_t w[32];
+        if (keys) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint32_t* v = &x[u >> 2][(u & 3) * 8];
-          uint32_t w[4];
+          for (int k = 0; k < 32; ++k)
+            w[k] = pack_bf16x2(__uint_as_float(x[k >> 4][2 * (k & 15)]), __uint_as_float(x[k >> 4][2 * (k & 15) + 1]));
+        } else {
+          bool fine = true;  // NaN compares false
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float lo = __uint_as_float(v[2 * k]), hi = __uint_as_float(v[2 * k + 1]);
-            if (c < 2) {
-              w[k] = pack_bf16x2(lo, hi);
-            } else {
-              w[k] = pack_f16x2(lo, hi);
-              // NaN compares false: tested as "not below"
-              bad |= !(fabsf(lo) < 65520.f) | !(fabsf(hi) < 65520.f);
-            }
+          for (int k = 0; k < 32; ++k) {
+            const float lo = __uint_as_float(x[k >> 4][2 * (k & 15)]), hi = __uint_as_float(x[k >> 4][2 * (k & 15) + 1]);
+            w[k] = pack_f16x2(lo, hi);
+            fine = fine && fmaxf(fabsf(lo), fabsf(hi)) < 65520.f && lo == lo && hi == hi;
           }
-          st_shared_v4(rbase + ((static_cast<uint32_t>(u) ^ static_cast<uint32_t>(lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+          // rows behind the prefix may hold anything
+          if (!fine && row0 + lane < p.prefix_len) atomicCAS(p.status, 0, static_cast<int>(kStValueRange));
         }
-        if (c >= 2 && row0 + lane >= p.prefix_len) bad = false;  // rows behind the prefix may hold anything
-        if (bad) {
-          atomicCAS(p.status, 0, static_cast<int>(kStValueRange));
-          bad = false;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (row0 < p.prefix_len) tma_store_4d(c < 2 ? &tm_k : &tm_v, stg, 0, row0, c & 1, h);
-          bulk_commit();
+        // four lanes to 64 bytes of a row (the rows, as threads hold them, lie 256 bytes apart)
+        const int first = row0 + lane - quad;
+        uint16_t* dst = out + (h * p.head_rows + first) * kHeadDim + 64 * c + 8 * quad;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint4 piece[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            piece[j] = make_uint4(w[16 * g + 4 * j], w[16 * g + 4 * j + 1], w[16 * g + 4 * j + 2], w[16 * g + 4 * j + 3]);
+          quad_transpose(piece, lane);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (first + j < p.prefix_len) *reinterpret_cast<uint4*>(dst + j * kHeadDim + 32 * g) = piece[j];
         }
       }
       if (++m == tiles) {
@@ -269,8 +287,6 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
         ++h;
       }
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   } else {
     // RoPE dims, 8 lanes a row, and the pages' check, over the whole grid
     for (long long r = blockIdx.x * 4ll + (lane >> 3); r < p.prefix_len; r += gridDim.x * 4ll) {
@@ -405,10 +421,13 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
   p.paged = !fp8;
   p.prefix_len = prefix_len;
   p.num_heads = num_heads;
+  p.k_nope = static_cast<uint16_t*>(k_nope);
+  p.v = static_cast<uint16_t*>(v);
+  p.head_rows = head_rows;
   p.k_pe = static_cast<uint16_t*>(k_pe);
   p.status = status;
   // latents: {dim, row of a page, page} of the pool, or {dim, row, 1} of the widened rows
-  CUtensorMap lat, wk, wv, tk, tv;
+  CUtensorMap lat, wk, wv;
   const cuuint64_t size[3] = {fp8 ? cuuint64_t{kLatent} : cuuint64_t{kDqk},
                               fp8 ? static_cast<cuuint64_t>(prefix_len) : cuuint64_t{kPage},
                               fp8 ? cuuint64_t{1} : static_cast<cuuint64_t>(num_pages)};
@@ -416,8 +435,7 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
   const cuuint64_t strides[2] = {row, row * size[1]};
   const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(kPage), 1u};
   if (!encode(&lat, false, 3, fp8 ? workspace : kv_cache, size, strides, box) || !encode_weight(&wk, w_uk, num_heads) ||
-      !encode_weight(&wv, w_uv, num_heads) || !encode_kv(&tk, false, k_nope, prefix_len, head_rows, num_heads, 32, 1) ||
-      !encode_kv(&tv, true, v, prefix_len, head_rows, num_heads, 32, 1))
+      !encode_weight(&wv, w_uv, num_heads))
     return MLA_ERR_CUDA;
   if (fp8) {
     rc = launch_dependent(mla_prefix_widen_kernel, dim3((prefix_len + 7) / 8), dim3(256), 0, 1, stream, p,
@@ -426,8 +444,7 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
   }
   const long long items = static_cast<long long>((prefix_len + 2 * kRows - 1) / (2 * kRows)) * num_heads;
   const int pairs = static_cast<int>(items < sms / 2 ? items : sms / 2);
-  return launch_dependent(mla_prefix_expand_kernel, dim3(2 * pairs), dim3(kThreads), kSmem, 1, stream, p, lat, wk, wv,
-                          tk, tv);
+  return launch_dependent(mla_prefix_expand_kernel, dim3(2 * pairs), dim3(kThreads), kSmem, 1, stream, p, lat, wk, wv);
 }
 
 }  // extern "C"

@@ -77,7 +77,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if ((sbase & 1023u) != 0) {  // the swizzled tiles need it; the kernel has no static shared memory ahead of it
     if (threadIdx.x == 0) atomicCAS(p.status, 0, static_cast<int>(MLA_ERR_CUDA));
     return;
@@ -125,7 +125,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
   Ctl ctl;
   ctl.abort = abort_flag;
@@ -232,7 +232,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
     uint32_t v_held = 0;           // its barrier, 0: given back
     auto release_v = [&]() -> bool {
       if (v_held == 0) return true;
-      if (!wait(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
+      if (!warp_wait_uniform(bar_pv(s), (n_pv - 1) & 1, ctl)) return false;
       if (leader) mbar_arrive(v_held);
       v_held = 0;
       return true;
@@ -245,7 +245,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       // its value product is done.
       auto issue_qk = [&](int j) -> bool {
         const uint32_t c0 = base + place_k(j), q = tiles + j;
-        if (!wait(k_full(q), (q >> 1) & 1, ctl)) return false;
+        if (!warp_wait_uniform(k_full(q), (q >> 1) & 1, ctl)) return false;
         if (!release_v()) return false;
         tc_fence_after();
 #pragma unroll
@@ -259,17 +259,17 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
         umma_commit_if(leader, bar_s_full(s));
         return true;
       };
-      ok = wait(bar_q_full, seg & 1, ctl) && (steps == 0 || issue_qk(s));
+      ok = warp_wait_uniform(bar_q_full, seg & 1, ctl) && (steps == 0 || issue_qk(s));
       if (steps <= 1) umma_commit_if(leader, bar_q_empty);
       // O of the segment before has been read
-      if (ok && seg > 0) ok = wait(bar_o_free, (seg - 1) & 1, ctl);
+      if (ok && seg > 0) ok = warp_wait_uniform(bar_o_free, (seg - 1) & 1, ctl);
       for (int i = 0; ok && i < steps; ++i) {
         const int j = 2 * i + static_cast<int>(s);
         const uint32_t c0 = base + place_v(j, n), q = tiles + j;
-        ok = wait(v_full(q), (q >> 1) & 1, ctl);
+        ok = warp_wait_uniform(v_full(q), (q >> 1) & 1, ctl);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          ok = ok && wait(bar_p_full(s, c), n_pv & 1, ctl);
+          ok = ok && warp_wait_uniform(bar_p_full(s, c), n_pv & 1, ctl);
           if (!ok) break;
           tc_fence_after();
           const uint64_t bd = ring_v + slot_off(c0 + c);

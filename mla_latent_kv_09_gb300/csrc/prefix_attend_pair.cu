@@ -76,8 +76,8 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
   const uint32_t mis = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + mis;
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t rank = uniform(cluster_ctarank());
   const int pair = blockIdx.x >> 1;
 
   const uint32_t bar0 = sbase + kOffBar;
@@ -128,7 +128,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any remote operation
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   Ctl ctl;
   ctl.abort = abort_flag;
   ctl.n_remote = 1;
@@ -190,10 +190,10 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
         const uint64_t ad = smem_desc(sbase, 16u, 1024u), kd = smem_desc(sbase + kOffK, 16u, 1024u);
         while (ok && it.next(sg)) {
           const uint32_t q1 = q0 + static_cast<uint32_t>(sg.k1 - sg.k0);
-          ok = wait<true>(bar_q_full, seg & 1, ctl);
+          ok = warp_wait_uniform<true>(bar_q_full, seg & 1, ctl);
           for (uint32_t q = q0; ok && q < q1; ++q) {
             // its score buffer last held the weights of tile q - 3
-            ok = wait<true>(k_full(q), par4(q), ctl) && (q < 3 || wait<true>(bar_pv(q - 3), par4(q - 3), ctl));
+            ok = warp_wait_uniform<true>(k_full(q), par4(q), ctl) && (q < 3 || warp_wait_uniform<true>(bar_pv(q - 3), par4(q - 3), ctl));
             if (!ok) break;
             tc_fence_after();
             const uint64_t bd = kd + static_cast<uint64_t>((q & 3u) * (kKStage >> 4));
@@ -215,14 +215,14 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
         while (ok && it.next(sg)) {
           const uint32_t q1 = q0 + static_cast<uint32_t>(sg.k1 - sg.k0);
           // O of the segment before has been read
-          if (seg > 0) ok = wait<true>(bar_o_free, (seg - 1) & 1, ctl);
+          if (seg > 0) ok = warp_wait_uniform<true>(bar_o_free, (seg - 1) & 1, ctl);
           for (uint32_t q = q0; ok && q < q1; ++q) {
-            ok = wait<true>(v_full(q), par4(q), ctl);
+            ok = warp_wait_uniform<true>(v_full(q), par4(q), ctl);
             const uint64_t bd = vd + static_cast<uint64_t>((q & 3u) * (kVStage >> 4));
             const uint32_t a = tmem + kColS + 128u * (q % 3u);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = ok && wait<true>(p_full(q, half), par4(q), ctl);
+              ok = ok && warp_wait_uniform<true>(p_full(q, half), par4(q), ctl);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll

@@ -53,10 +53,10 @@ size_t mla_prefix_expand_workspace_size(int prefix_len, unsigned flags);
  *   k_nope       bf16 [num_heads, head_rows, 128], rows 0 .. prefix_len - 1 of
  *                each head written, the others left as they were
  *   v            fp16, laid out as k_nope (fp16, as every value product of
- *                the library takes: 11 significant bits; a value that is not
- *                finite or reaches 65,520 in magnitude sets *status to
- *                MLA_ERR_VALUE_RANGE)
- *   head_rows    rows between heads, >= prefix_len
+ *                the library takes: 11 significant bits).  A key or value
+ *                that is not finite after its rounding (values from 65,520 on
+ *                are not) sets *status to MLA_ERR_VALUE_RANGE
+ *   head_rows    rows between heads, >= prefix_len, at most 2^30
  *   k_pe         bf16 [prefix_len, 64]: the rows' RoPE dims, copied
  *   workspace    16-byte aligned; NULL where none is needed
  *   status       also MLA_ERR_TIMEOUT if a bounded wait runs out

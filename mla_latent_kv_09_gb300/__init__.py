@@ -449,7 +449,7 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
     further rows are left as they are.  `workspace` (uint8, for an FP8 cache
     only, mla_prefix_expand_workspace_size bytes) is allocated if not given.
     `status` receives MLA_ERR_BAD_TABLE for a page outside the pool and
-    MLA_ERR_VALUE_RANGE for a value that is not finite in fp16.
+    MLA_ERR_VALUE_RANGE for a key or value that is not finite once rounded.
     """
     import torch
     dev = kv_cache.device

@@ -646,7 +646,9 @@ extern "C" {
 size_t mla_prefix_attend_workspace_size(int num_tokens, int num_heads, int prefix_len, int* err) {
   int sms = 0;
   int rc = num_tokens < 0 || prefix_len < 0 ? MLA_ERR_INVALID_ARG
-           : num_heads < 1 || num_heads > kHeads ? MLA_ERR_UNSUPPORTED : attend_device_ready(&sms);
+           : num_heads < 1 || num_heads > kHeads || num_tokens > kMaxRows || prefix_len > kMaxRows
+               ? MLA_ERR_UNSUPPORTED
+               : attend_device_ready(&sms);
   if (err) *err = rc;
   if (rc != MLA_OK) return 0;
   if (num_tokens == 0 || prefix_len == 0) return 256;
@@ -671,7 +673,8 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   if (flags & ~static_cast<unsigned>(MLA_FLAG_OUT_FP32)) return MLA_ERR_INVALID_ARG;
   if (out == suffix_out && (flags & MLA_FLAG_OUT_FP32)) return MLA_ERR_INVALID_ARG;
   if (num_heads < 1 || num_heads > kHeads) return MLA_ERR_UNSUPPORTED;
-  if (head_rows > INT32_MAX || static_cast<int64_t>(num_tokens) * num_heads > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (head_rows > kMaxRows || num_tokens > kMaxRows || static_cast<int64_t>(num_tokens) * num_heads > INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
   int sms = 0;
   int rc = attend_device_ready(&sms);
   if (rc != MLA_OK) return rc;

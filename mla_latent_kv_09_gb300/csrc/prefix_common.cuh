@@ -14,6 +14,8 @@
 namespace mla {
 namespace prefix {
 
+constexpr int kMaxRows = 1 << 30;  // of a prefix, and query tokens (row counts are rounded up in 32 bits)
+
 // 4-D tiled load (x: dim within a 64-dim chunk, y: row, z: chunk, w: head).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w,
                                             uint32_t bar) {

@@ -233,6 +233,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + (keys ? 0u : 128u);
     const uint32_t racc = mapa(acc_empty(0), 0);
     uint16_t* out = keys ? p.k_nope : p.v;
+    const uint32_t one = keys ? 0x00800080u : 0x04000400u;  // one in the exponents of a bf16 or an fp16 pair
     const int quad = lane & 3;
     int h = h0, m = m0;
     for (int i = 0; i < n; ++i) {
@@ -251,22 +252,18 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(racc + 8u * buf);  // the accumulator may take the tile after next
         }
-        uint32_t w[32];
-        if (keys) {
+        // A value that its type does not hold shows as exponent bits all ones
+        // after the rounding: adding one to the exponent carries out of them.
+        uint32_t w[32], carry = 0;
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            w[k] = pack_bf16x2(__uint_as_float(x[k >> 4][2 * (k & 15)]), __uint_as_float(x[k >> 4][2 * (k & 15) + 1]));
-        } else {
-          bool fine = true;  // NaN compares false
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float lo = __uint_as_float(x[k >> 4][2 * (k & 15)]), hi = __uint_as_float(x[k >> 4][2 * (k & 15) + 1]);
-            w[k] = pack_f16x2(lo, hi);
-            fine = fine && fmaxf(fabsf(lo), fabsf(hi)) < 65520.f && lo == lo && hi == hi;
-          }
-          // rows behind the prefix may hold anything
-          if (!fine && row0 + lane < p.prefix_len) atomicCAS(p.status, 0, static_cast<int>(kStValueRange));
+        for (int k = 0; k < 32; ++k) {
+          const float lo = __uint_as_float(x[k >> 4][2 * (k & 15)]), hi = __uint_as_float(x[k >> 4][2 * (k & 15) + 1]);
+          w[k] = keys ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+          carry |= (w[k] & 0x7fff7fffu) + one;
         }
+        // rows behind the prefix may hold anything
+        if ((carry & 0x80008000u) != 0 && row0 + lane < p.prefix_len)
+          atomicCAS(p.status, 0, static_cast<int>(kStValueRange));
         // four lanes to 64 bytes of a row (the rows, as threads hold them, lie 256 bytes apart)
         const int first = row0 + lane - quad;
         uint16_t* dst = out + (h * p.head_rows + first) * kHeadDim + 64 * c + 8 * quad;
@@ -403,7 +400,7 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
   if (num_pages < 1 || prefix_len < 0 || head_rows < prefix_len) return MLA_ERR_INVALID_ARG;
   if (flags & ~static_cast<unsigned>(MLA_FLAG_KV_FP8)) return MLA_ERR_INVALID_ARG;
   if (num_heads < 1 || num_heads > kHeads) return MLA_ERR_UNSUPPORTED;
-  if (num_pages > (INT32_MAX / kPage) - 1 || head_rows > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (num_pages > (INT32_MAX / kPage) - 1 || head_rows > kMaxRows) return MLA_ERR_UNSUPPORTED;
   const size_t need = mla_prefix_expand_workspace_size(prefix_len, flags);
   if (need > 0 && !workspace) return MLA_ERR_INVALID_ARG;
   if (ws_bytes < need) return MLA_ERR_WORKSPACE;

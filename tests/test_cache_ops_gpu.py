@@ -351,6 +351,34 @@ def test_calls_captured_replayed_and_on_another_stream():
         assert torch.equal(cache, want_cache) and torch.equal(out, m.rope(q, pos, inv))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_pool_and_rows_beyond_32_bit_offsets(fp8):
+    pages, width = 120000, 656 if fp8 else 576
+    cache = torch.zeros((pages, 64, width), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    x = rand((3, 576), 1)
+    bt = torch.tensor([[0, pages - 1, pages // 2]], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([0, 127, 128], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.cache_append(x[:, :512], x[:, 512:], cache, bt, pos, request_ids=torch.zeros(3, dtype=torch.int32, device="cuda"),
+                   status=status)
+    assert int(status) == 0
+    lat, pe = oracle.appended_rows(f64(x[:, :512]), f64(x[:, 512:]), [0, 127, 128])
+    got = torch.stack([cache[0, 0], cache[pages - 1, 63], cache[pages // 2, 0]])
+    assert_rows(got, lat, pe, x[:, 512:], False, fp8)
+    assert int((cache.view(torch.int16) != 0).any(-1).sum()) == 3  # three rows written
+
+
+def test_rope_beyond_32_bit_offsets():
+    T, H, D = 120000, 128, 192
+    x = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda")
+    x[-1] = rand((H, D), 1)
+    pos = torch.full((T,), 77, dtype=torch.int32, device="cuda")
+    inv, _ = m.rope_frequencies(64)
+    y = m.rope(x, pos, inv, offset=128)
+    assert_rope(y[-1:], x[-1:], pos[-1:], inv, 128, False, False, 1.0)
+    assert not y[:-1].any()
+
+
 def test_append_refusals():
     x, pos = rand((4, 576), 1), torch.zeros(4, dtype=torch.int32, device="cuda")
     bt, cache = torch.zeros((4, 1), dtype=torch.int32, device="cuda"), pool(4, False, 2)

@@ -144,6 +144,42 @@ def test_pages_outside_the_pool_and_values_outside_fp16_are_reported(fp8):
     assert_expanded(out[0][:2], out[1], out[2][:2], lat, pe, w_uk[:2], w_uv[:2])
 
 
+def test_keys_that_are_not_finite_are_reported():
+    kv, bt, lat, pe = cache_and_rows(200, False, 4)
+    w_uk, w_uv = rand((2, 512, 128), 1), rand((2, 512, 128), 2)
+    for bad, expected in ((1e38, m.MLA_ERR_VALUE_RANGE), (float("inf"), m.MLA_ERR_VALUE_RANGE), (1e30, 0)):
+        w, status = w_uk.clone(), status_word()
+        w[1, :, 5] = bad
+        m.prefix_expand(kv, bt, 200, w, w_uv, status=status)
+        assert int(status) == expected
+
+
+def test_rows_and_pages_beyond_32_bit_offsets():
+    """More than 2^31 elements between the first and the last head's rows, and
+    between the first and the last page."""
+    H, R, P = 128, 140000, 300
+    k_nope = torch.empty((H, R, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty((H, R, 128), dtype=torch.float16, device="cuda")
+    k_pe = torch.empty((R, 64), dtype=torch.bfloat16, device="cuda")
+    for fp8 in (False, True):
+        small, bt, lat, pe = cache_and_rows(P, fp8, 8)
+        pages = 120000
+        kv = torch.empty((pages, *small.shape[1:]), dtype=small.dtype, device="cuda")
+        kv[pages - small.shape[0]:] = small
+        w_uk, w_uv = rand((H, 512, 128), 1) * 512 ** -0.5, rand((H, 512, 128), 2) * 512 ** -0.5
+        status = status_word()
+        m.prefix_expand(kv, bt + (pages - small.shape[0]), P, w_uk, w_uv, out=(k_nope, k_pe, v), status=status)
+        assert int(status) == 0
+        last = slice(H - 1, H)
+        assert_expanded(k_nope[last, :P], k_pe[:P], v[last, :P], lat, pe, w_uk[last], w_uv[last])
+        del kv
+    for T in (3, 140):
+        q = rand((T, H, 192), 9)
+        out, lse = m.prefix_attend(q[..., :128], q[..., 128:], k_nope, k_pe, v, SCALE, prefix_len=P, out_fp32=True)
+        assert_attended(out, lse, q[..., :128], q[..., 128:], k_nope[:, :P], k_pe[:P], v[:, :P], tokens=np.array([0, T - 1]),
+                        heads=np.array([0, H - 1]))
+
+
 def test_expansion_refusals():
     kv, bt, _, _ = cache_and_rows(70, False, 1)
     w = rand((2, 512, 128), 1)

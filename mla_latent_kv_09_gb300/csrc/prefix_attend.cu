@@ -457,11 +457,13 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
 
 // Joins the partial rows of the (row block, head)s that were cut.  Block
 // (g, lane block, chunk): the unit that the range of group g starts inside of,
-// if no earlier range does; 4 / kWarps of its rows, kWarps warps a row (a warp
-// takes every kWarps-th piece), four columns a lane.
+// if no earlier range does; kCombineWarps / kWarps of its rows, kWarps warps a
+// row (a warp takes every kWarps-th piece, eight loads in flight), four columns
+// a lane.
+constexpr int kCombineWarps = 8;
 template <int kWarps>
-__global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ float4 acc[4][32];
+__global__ void __launch_bounds__(32 * kCombineWarps) mla_prefix_combine_kernel(const __grid_constant__ AttendParams p) {
+  __shared__ float4 acc[kCombineWarps][32];
   const Plan& w = p.plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % kWarps;
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_co
   int n = 2;
   while (cut(w, g0 + n) < end) ++n;
   grid_dependency_wait();
-  const int brow = blockIdx.z * (4 / kWarps) + warp / kWarps, t = block * 2 * kTile + brow;
+  const int brow = blockIdx.z * (kCombineWarps / kWarps) + warp / kWarps, t = block * 2 * kTile + brow;
   const bool real = brow < p.part_rows && t < p.num_tokens;
   const long long row = static_cast<long long>(t) * p.num_heads + h;
   auto piece = [&](int i) {  // row of piece i among the partial rows
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(128) mla_prefix_combine_kernel(const __grid_co
     for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = sub; i < n; i += kWarps) {
       const long long from = piece(i);
       const float f = ex2_approx(p.part_lse[from] - base) * inv;
@@ -618,8 +620,10 @@ Plan plan(int num_tokens, int num_heads, int prefix_len, int sms) {
     }
   }
   w.line = static_cast<long long>(w.passes) * num_heads * w.nk;
-  // at least two steps a range: one for each stream
-  if (w.groups > (w.line + 1) / 2) w.groups = static_cast<int>((w.line + 1) / 2);
+  // At least two steps a range, one for each stream, unless the prefix is one
+  // tile: then nothing is cut, and a range is a head.
+  const long long most = w.nk > 1 ? (w.line + 1) / 2 : w.line;
+  if (w.groups > most) w.groups = static_cast<int>(most);
   return w;
 }
 
@@ -725,8 +729,9 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   const int rows = num_tokens < l.rows ? num_tokens : l.rows;
   // pieces a head can be cut in: the ranges that overlap its nk steps
   const bool few = p.plan.nk / (p.plan.line / p.plan.groups) + 2 <= 8;
-  return launch_dependent(few ? mla_prefix_combine_kernel<1> : mla_prefix_combine_kernel<4>,
-                          dim3(p.plan.groups - 1, p.plan.width, few ? (rows + 3) / 4 : rows), dim3(128), 0, 1, stream, p);
+  return launch_dependent(few ? mla_prefix_combine_kernel<1> : mla_prefix_combine_kernel<kCombineWarps>,
+                          dim3(p.plan.groups - 1, p.plan.width, few ? (rows + kCombineWarps - 1) / kCombineWarps : rows),
+                          dim3(32 * kCombineWarps), 0, 1, stream, p);
 }
 
 }  // extern "C"

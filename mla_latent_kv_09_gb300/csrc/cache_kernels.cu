@@ -26,7 +26,8 @@ namespace mla {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeItems = 4;  // 16-byte units per thread, all loads in flight together
+constexpr int kRopeItems = 4;     // 16-byte units per thread and turn, all loads in flight together
+constexpr int kRopeCtas = 8 * 152;  // CTAs wanted before a token's heads stay in one CTA
 constexpr int kLatent = 512;
 constexpr int kRopeDim = 64;
 constexpr int kFp8Row = MLA_FP8_ROW_BYTES;
@@ -50,9 +51,10 @@ struct RopeParams {
   const uint16_t* x;
   long long x_ts, x_hs;
   const int* positions;
-  int heads, head_dim, offset, rope;
-  int units;  // 16-byte units per head that a thread handles (rotated ones, and copied ones out of place)
-  int copy;   // dims outside the rotated range are copied
+  int heads, offset, rope;
+  int units;     // 16-byte units per head that a thread handles (rotated ones, and copied ones out of place)
+  int per_turn;  // heads that a CTA's threads cover side by side
+  int copy;      // dims outside the rotated range are copied
   const double* inv_freq;
   float scale;
   int inverse;
@@ -60,71 +62,79 @@ struct RopeParams {
   long long out_ts, out_hs;
 };
 
-// One CTA: one token, kRopeThreads * kRopeItems units of its heads.  A unit is
+// One CTA: one token, its heads in turns of per_turn * kRopeItems.  A unit is
 // 8 contiguous dims: 4 interleaved pairs, or (half layout) 8 dims and their
-// 8 partners, or 8 copied dims; a warp's units are neighbours in memory.  The
-// loads are issued before the angles are computed, which hides sincospif and
-// the position's load behind them; the token's cosines and sines are shared
-// by all heads through shared memory.
+// 8 partners, or 8 copied dims; a warp's units are neighbours in memory.  A
+// thread keeps one unit for all its heads: its cosines and sines stay in
+// registers, and nothing is divided in the loop.  The first turn's loads are
+// issued before the angles are computed (once a token, through shared
+// memory), which hides sincospif and the position's load behind them.
 template <bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 cs[MLA_MAX_ROPE_DIM / 2];
   const int t = blockIdx.x;
-  const int n = p.heads * p.units;
-  const int first = blockIdx.y * (kRopeThreads * kRopeItems) + threadIdx.x;
+  const bool wide = p.units > kRopeThreads;  // a head is more than a CTA: units in blocks of kRopeThreads
+  const int u = wide ? blockIdx.z * kRopeThreads + threadIdx.x : threadIdx.x % p.units;
+  const int h0 = wide ? 0 : threadIdx.x / p.units;
+  const bool mine = wide ? u < p.units : h0 < p.per_turn;
   const int before = p.copy ? p.offset / 8 : 0;     // copied units ahead of the rotated ones
   const int turned = kHalf ? p.rope / 16 : p.rope / 8;
+  const int r = u - before;
+  const bool turns = r >= 0 && r < turned;
+  const int dim = turns ? p.offset + 8 * r : (r < 0 ? 8 * u : p.offset + p.rope + 8 * (r - turned));
+  const int pair = turns ? (kHalf ? 8 * r : 4 * r) : 0;
+  const int step = p.per_turn * kRopeItems;
   grid_dependency_wait();
+  const uint16_t* src = p.x + t * p.x_ts + dim;
+  uint16_t* dst = p.out + t * p.out_ts + dim;
   uint4 a[kRopeItems], b[kRopeItems];
-  int dim[kRopeItems], head[kRopeItems], pair[kRopeItems];  // pair < 0: copied; dim < 0: nothing
+  auto load = [&](int base) {
 #pragma unroll
-  for (int i = 0; i < kRopeItems; ++i) {
-    const int item = first + i * kRopeThreads;
-    dim[i] = -1;
-    if (item >= n) continue;
-    const int h = item / p.units, u = item - h * p.units;
-    const int r = u - before;
-    head[i] = h;
-    if (r >= 0 && r < turned) {
-      dim[i] = p.offset + 8 * r;
-      pair[i] = kHalf ? 8 * r : 4 * r;
-    } else {
-      dim[i] = r < 0 ? 8 * u : p.offset + p.rope + 8 * (r - turned);
-      pair[i] = -1;
+    for (int i = 0; i < kRopeItems; ++i) {
+      const int h = base + h0 + i * p.per_turn;
+      if (!mine || h >= p.heads) continue;
+      a[i] = *reinterpret_cast<const uint4*>(src + h * p.x_hs);
+      if (kHalf && turns) b[i] = *reinterpret_cast<const uint4*>(src + h * p.x_hs + p.rope / 2);
     }
-    const uint16_t* src = p.x + t * p.x_ts + h * p.x_hs + dim[i];
-    a[i] = *reinterpret_cast<const uint4*>(src);
-    if (kHalf && pair[i] >= 0) b[i] = *reinterpret_cast<const uint4*>(src + p.rope / 2);
-  }
+  };
+  int base = blockIdx.y * step;
+  load(base);
   const int pos = p.positions[t];
   for (int i = threadIdx.x; i < p.rope / 2; i += kRopeThreads) cs[i] = turn(p.inv_freq[i], pos, p.inverse != 0, p.scale);
   __syncthreads();
+  float2 c[kHalf ? 8 : 4];
 #pragma unroll
-  for (int i = 0; i < kRopeItems; ++i) {
-    if (dim[i] < 0) continue;
-    uint16_t* dst = p.out + t * p.out_ts + head[i] * p.out_hs + dim[i];
-    if (pair[i] >= 0) {
-      uint32_t* x = reinterpret_cast<uint32_t*>(&a[i]);
-      if (kHalf) {
-        uint32_t* y = reinterpret_cast<uint32_t*>(&b[i]);
+  for (int j = 0; j < (kHalf ? 8 : 4); ++j) c[j] = cs[pair + j];
+#pragma unroll 1
+  while (base < p.heads) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 c0 = cs[pair[i] + 2 * j], c1 = cs[pair[i] + 2 * j + 1];
-          const float x0 = lo_f(x[j]), x1 = hi_f(x[j]), y0 = lo_f(y[j]), y1 = hi_f(y[j]);
-          x[j] = pack_bf16x2(x0 * c0.x - y0 * c0.y, x1 * c1.x - y1 * c1.y);
-          y[j] = pack_bf16x2(x0 * c0.y + y0 * c0.x, x1 * c1.y + y1 * c1.x);
-        }
-        *reinterpret_cast<uint4*>(dst + p.rope / 2) = b[i];
-      } else {
+    for (int i = 0; i < kRopeItems; ++i) {
+      const int h = base + h0 + i * p.per_turn;
+      if (!mine || h >= p.heads) continue;
+      if (turns) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(&a[i]);
+        if (kHalf) {
+          uint32_t* y = reinterpret_cast<uint32_t*>(&b[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 c = cs[pair[i] + j];
-          const float x0 = lo_f(x[j]), x1 = hi_f(x[j]);
-          x[j] = pack_bf16x2(x0 * c.x - x1 * c.y, x0 * c.y + x1 * c.x);
+          for (int j = 0; j < 4; ++j) {
+            const float2 c0 = c[2 * j], c1 = c[2 * j + 1];
+            const float x0 = lo_f(x[j]), x1 = hi_f(x[j]), y0 = lo_f(y[j]), y1 = hi_f(y[j]);
+            x[j] = pack_bf16x2(x0 * c0.x - y0 * c0.y, x1 * c1.x - y1 * c1.y);
+            y[j] = pack_bf16x2(x0 * c0.y + y0 * c0.x, x1 * c1.y + y1 * c1.x);
+          }
+          *reinterpret_cast<uint4*>(dst + h * p.out_hs + p.rope / 2) = b[i];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x0 = lo_f(x[j]), x1 = hi_f(x[j]);
+            x[j] = pack_bf16x2(x0 * c[j].x - x1 * c[j].y, x0 * c[j].y + x1 * c[j].x);
+          }
         }
       }
+      *reinterpret_cast<uint4*>(dst + h * p.out_hs) = a[i];
     }
-    *reinterpret_cast<uint4*>(dst) = a[i];
+    base += gridDim.y * step;
+    if (base < p.heads) load(base);
   }
 }
 
@@ -340,7 +350,8 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
   if (num_tokens < 0 || num_heads < 1 || head_dim < 8 || rope_offset < 0 || rope_dim < 2) return MLA_ERR_INVALID_ARG;
   if (flags & ~static_cast<unsigned>(MLA_FLAG_ROPE_HALF | MLA_FLAG_ROPE_INVERSE)) return MLA_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
-  if (head_dim % 8 || rope_offset % 8 || rope_dim % 16 || rope_dim > MLA_MAX_ROPE_DIM || head_dim > (1 << 16))
+  if (head_dim % 8 || rope_offset % 8 || rope_dim % 16 || rope_dim > MLA_MAX_ROPE_DIM || head_dim > (1 << 16) ||
+      num_heads > (1 << 30))
     return MLA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(rope_offset) + rope_dim > head_dim) return MLA_ERR_INVALID_ARG;
   if (!row_stride_ok(x_token_stride, 0) || !row_stride_ok(x_head_stride, 0) || !row_stride_ok(out_token_stride, 0) ||
@@ -363,7 +374,6 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
   p.x_hs = x_head_stride;
   p.positions = positions;
   p.heads = num_heads;
-  p.head_dim = head_dim;
   p.offset = rope_offset;
   p.rope = rope_dim;
   p.copy = in_place ? 0 : 1;
@@ -374,13 +384,15 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
   p.out = static_cast<uint16_t*>(out);
   p.out_ts = out_token_stride;
   p.out_hs = out_head_stride;
-  const int64_t items = static_cast<int64_t>(num_heads) * p.units;
-  const int64_t per_cta = kRopeThreads * kRopeItems;
-  if (items > INT32_MAX - per_cta || (items + per_cta - 1) / per_cta > 65535) return MLA_ERR_UNSUPPORTED;
+  p.per_turn = p.units < kRopeThreads ? kRopeThreads / p.units : 1;
   const int rc = cache_device_ready();
   if (rc != MLA_OK) return rc;
   if (num_tokens == 0) return MLA_OK;
-  const dim3 grid(num_tokens, static_cast<unsigned>((items + per_cta - 1) / per_cta), 1);
+  // few tokens: their heads spread over CTAs; many: a CTA takes all of a token's
+  const int64_t blocks = (static_cast<int64_t>(num_heads) + p.per_turn * kRopeItems - 1) / (p.per_turn * kRopeItems);
+  int64_t y = (kRopeCtas + num_tokens - 1) / num_tokens;
+  if (y > blocks) y = blocks;
+  const dim3 grid(num_tokens, static_cast<unsigned>(y), (p.units + kRopeThreads - 1) / kRopeThreads);
   return launch_dependent(half ? mla_rope_kernel<true> : mla_rope_kernel<false>, grid, dim3(kRopeThreads), stream, p);
 }
 

@@ -269,9 +269,9 @@ def _tensor(t, name: str, dtype, shape, device, contiguous: bool = True):
     contiguous, or with contiguous=False that its last dim is.  (Called for
     every tensor of a call that may be shorter than ten of these checks: it
     does little, and words are found only for a failure.)"""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not (
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not (
             t.is_contiguous() if contiguous else t.stride(-1) == 1):
-        raise ValueError(f"{name}: expected {dtype} {list(shape)} on {device}, "
+        raise ValueError(f"{name}: expected {dtype} {list(shape)} on GPU {device}, "
                          f"{'contiguous' if contiguous else 'unit stride in the last dim'}; got {t.dtype} "
                          f"{list(t.shape)} on {t.device}, strides {list(t.stride())}")
 
@@ -285,9 +285,10 @@ def _on_device(fn):
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         import torch
-        dev = first.device
-        if stream is None and dev.index is not None and dev.index == torch.cuda.current_device():
+        index = first.get_device()  # -1: not on a GPU
+        if stream is None and index >= 0 and index == torch.cuda.current_device():
             return fn(first, *args, **kw)
+        dev = first.device
         if dev.type != "cuda":
             raise ValueError(f"{fn.__name__}: expected tensors on a GPU, got {dev}")
         if stream is None:
@@ -302,11 +303,11 @@ def _on_device(fn):
     return call
 
 
-def _current_stream(device) -> int:
+def _current_stream(device: int) -> int:
     """Raw handle of the current stream (torch.cuda.current_stream builds a
     stream object for it, twenty times as long)."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.0, yarn: float = 1.0,
@@ -357,7 +358,7 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
     tensor; out=x turns in place (and leaves the other dims alone).
     """
     import torch
-    dev = x.device
+    dev = x.get_device()
     T, H, D = x.shape
     _tensor(x, "x", torch.bfloat16, (T, H, D), dev, contiguous=False)
     _tensor(positions, "positions", torch.int32, (T,), dev)
@@ -404,7 +405,7 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
     that token is skipped.  Returns kv_cache.
     """
     import torch
-    dev = latent.device
+    dev = latent.get_device()
     T = latent.shape[0]
     _tensor(latent, "latent", torch.bfloat16, (T, D_V), dev, contiguous=False)
     _tensor(k_pe, "k_pe", torch.bfloat16, (T, D_QK - D_V), dev, contiguous=False)
@@ -452,7 +453,7 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
     MLA_ERR_VALUE_RANGE for a key or value that is not finite once rounded.
     """
     import torch
-    dev = kv_cache.device
+    dev = kv_cache.get_device()
     flags = _cache_flags(kv_cache, dev)
     pages, = block_table.shape
     _tensor(block_table, "block_table", torch.int32, (pages,), dev)
@@ -508,7 +509,7 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
     mla_prefix_attend_workspace_size bytes) is allocated if not given.
     """
     import torch
-    dev = q_nope.device
+    dev = q_nope.get_device()
     T, H, _ = q_nope.shape
     _tensor(q_nope, "q_nope", torch.bfloat16, (T, H, 128), dev, contiguous=False)
     _tensor(q_pe, "q_pe", torch.bfloat16, (T, H, 64), dev, contiguous=False)

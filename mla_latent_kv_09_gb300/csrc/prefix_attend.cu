@@ -383,6 +383,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
       // differ.  All softmax warps vote, so that a wait that ran out in one
       // ends them all.
       float* mine = xchg + (s * 2 + hf) * 3 * kTile + r;
+      if (seen <= sg.k0 * kTile) total = used = 0.f;  // sees none of the segment: so too if its scores are no numbers
       mine[0] = m;
       mine[kTile] = total;
       mine[2 * kTile] = used;
@@ -465,6 +466,10 @@ template <int kWarps>
 __global__ void __launch_bounds__(32 * kCombineWarps) mla_prefix_combine_kernel(const __grid_constant__ AttendParams p) {
   __shared__ float4 acc[kCombineWarps][32];
   const Plan& w = p.plan;
+  // Every block waits, those without work too: what follows on the stream
+  // waits for this kernel, and this kernel's end must not come before the end
+  // of the one that wrote the pieces.
+  grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % kWarps;
   const int g = blockIdx.x + 1, lane_block = blockIdx.y;
@@ -478,7 +483,6 @@ __global__ void __launch_bounds__(32 * kCombineWarps) mla_prefix_combine_kernel(
   const int odd = cut(w, g0) < start ? 1 : 0;
   int n = 2;
   while (cut(w, g0 + n) < end) ++n;
-  grid_dependency_wait();
   const int brow = blockIdx.z * (kCombineWarps / kWarps) + warp / kWarps, t = block * 2 * kTile + brow;
   const bool real = brow < p.part_rows && t < p.num_tokens;
   const long long row = static_cast<long long>(t) * p.num_heads + h;
@@ -533,6 +537,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) mla_prefix_combine_kernel(
   const float y2 = __shfl_down_sync(0xffffffffu, o.z, 1), y3 = __shfl_down_sync(0xffffffffu, o.w, 1);
   const float all[8] = {o.x, o.y, o.z, o.w, y0, y1, y2, y3};
   if ((lane & 1) == 0) write8(p, row, 4 * lane, all, j);
+  __syncwarp();  // lse may be suffix_lse: all lanes have read it
   if (lane == 0) p.lse[row] = j.lse2 * kLn2;
 }
 
@@ -724,8 +729,8 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   const int units = p.plan.groups * p.plan.width;
   rc = small ? launch_dependent(mla_prefix_attend_kernel, dim3(units), dim3(kThreads), kSmem, 1, stream, p, qn, qp, k, kp, vm)
              : attend_pair_launch(units, stream, p, qn, qp, k, kp, vm);
-  // heads are cut wherever a range does not end with one
-  if (rc != MLA_OK || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
+  // heads are cut wherever a range does not end with one (one of a single tile cannot be)
+  if (rc != MLA_OK || p.plan.nk == 1 || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
   const int rows = num_tokens < l.rows ? num_tokens : l.rows;
   // pieces a head can be cut in: the ranges that overlap its nk steps
   const bool few = p.plan.nk / (p.plan.line / p.plan.groups) + 2 <= 8;

@@ -351,6 +351,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
       // maximum.  All softmax warps vote, so that a wait that ran out in one
       // ends them all.
       float* mine = xchg + (g * 2 + hf) * 3 * kTile;
+      if (seen <= sg.k0 * kTile) total = used = 0.f;  // sees none of the segment: so too if its scores are no numbers
       mine[0] = m;
       mine[kTile] = total;
       mine[2 * kTile] = used;

@@ -323,6 +323,26 @@ def test_tokens_that_see_nothing_at_all(T):
     assert not out.any() and bool((lse == -math.inf).all())
 
 
+@pytest.mark.parametrize("P", [100, 1000])
+@pytest.mark.parametrize("T", [6, 150, 300])
+def test_queries_of_padded_tokens_may_hold_anything(T, P):
+    """A token that sees nothing gets the suffix's result or zeros, whatever its
+    query holds, and the other tokens theirs."""
+    H = 3
+    x = inputs(T, H, P)
+    pad = torch.arange(T, device="cuda") % 3 == 1
+    vis = torch.where(pad, 0, P).to(torch.int32)
+    so, sl = rand((T, H, 128), 6), math.log(P) + rand((T, H), 7, torch.float32)
+    sl[::2] = -math.inf
+    want = [m.prefix_attend(*x, SCALE, visible=vis), m.prefix_attend(*x, SCALE, visible=vis, suffix_out=so, suffix_lse=sl)]
+    assert not want[0][0][pad].any() and bool((want[0][1][pad] == -math.inf).all())
+    for bad in (float("nan"), float("inf"), 3e38):
+        x[0][pad], x[1][pad] = bad, bad
+        for (out, lse), kw in zip(want, ({}, dict(suffix_out=so, suffix_lse=sl))):
+            got, got_lse = m.prefix_attend(*x, SCALE, visible=vis, **kw)
+            assert torch.equal(got, out) and torch.equal(got_lse, lse)
+
+
 def test_suffix_joined_in_place():
     T, H, P = 20, 3, 333
     x = inputs(T, H, P)
@@ -354,6 +374,26 @@ def test_strided_queries():
     out, lse = m.prefix_attend(wide[..., 64:192], wide[..., 512:], *x[2:], SCALE)
     want, want_lse = m.prefix_attend(*x, SCALE)
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("T,H", [(1, 5), (5, 1), (1, 1)])
+def test_queries_whose_strides_of_a_dim_of_one_say_nothing(T, H):
+    P = 150
+    x = inputs(T, H, P)
+    want, want_lse = m.prefix_attend(*x, SCALE)
+    q = torch.cat((x[0], x[1]), -1)
+    odd = torch.empty_strided(q.shape, (7 if T == 1 else 192, 7 if H == 1 else 192, 1), dtype=q.dtype, device="cuda")
+    odd.copy_(q)
+    assert torch.equal(odd, q)
+    out, lse = m.prefix_attend(odd[..., :128], odd[..., 128:], *x[2:], SCALE)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    # one head of several, one token of several
+    many = rand((T + 3, H + 3, 192), 9)
+    many[2:2 + T, 1:1 + H] = q
+    if T == 1 or H == 1:
+        part = many[2:2 + T, 1:1 + H]
+        out, lse = m.prefix_attend(part[..., :128], part[..., 128:], *x[2:], SCALE)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
 def test_results_repeat_bit_for_bit():

@@ -52,7 +52,8 @@ enum {
  *                turned, the others copied
  *   rope_offset  multiple of 8
  *   rope_dim     multiple of 16, at most MLA_MAX_ROPE_DIM
- *   inv_freq     fp64 [rope_dim / 2], radians per position, 8-byte aligned
+ *   inv_freq     fp64 [rope_dim / 2], radians per position, finite, 8-byte
+ *                aligned
  *   scale        factor on the turned dims (finite)
  *   flags        MLA_FLAG_ROPE_HALF, MLA_FLAG_ROPE_INVERSE
  *   out          bf16, rows as x with its own strides; may be x itself with
@@ -71,7 +72,7 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
  *   norm_weight  bf16 [512] or NULL.  With it the stored latent is
  *                latent * norm_weight / sqrt(mean(latent^2) + eps)
  *   eps          >= 0, used with norm_weight only
- *   inv_freq     fp64 [32] or NULL (k_pe is stored as it is)
+ *   inv_freq     fp64 [32], finite, or NULL (k_pe is stored as it is)
  *   rope_scale   factor on the turned dims (with inv_freq only)
  *   positions    int32 [num_tokens]: token t's position in its request's
  *                sequence, which is also its angle's; a negative position

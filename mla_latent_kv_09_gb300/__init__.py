@@ -355,7 +355,8 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
     `scale`, the others copied.  Pairs are (2i, 2i + 1), or (i, i + R / 2)
     with half=True; inverse=True turns back (the gradient of the rotation, and
     with scale 1 its inverse).  Returns `out`, by default a new [T, H, D]
-    tensor; out=x turns in place (and leaves the other dims alone).
+    tensor; out=x turns in place (and leaves the other dims alone); `out` and
+    x must not overlap otherwise.
     """
     import torch
     dev = x.get_device()
@@ -371,9 +372,10 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
     if T == 0 or H == 0:
         return out
     stream = _current_stream(dev)
-    mla_rope(x, x.stride(0), x.stride(1), positions, T, H, D, offset, 2 * R2, inv_freq, scale,
-             (MLA_FLAG_ROPE_HALF if half else 0) | (MLA_FLAG_ROPE_INVERSE if inverse else 0), out, out.stride(0),
-             out.stride(1), stream)
+    # (the stride of a dim of one says nothing)
+    mla_rope(x, x.stride(0) if T > 1 else 0, x.stride(1) if H > 1 else 0, positions, T, H, D, offset, 2 * R2, inv_freq,
+             scale, (MLA_FLAG_ROPE_HALF if half else 0) | (MLA_FLAG_ROPE_INVERSE if inverse else 0), out,
+             out.stride(0) if T > 1 else 0, out.stride(1) if H > 1 else 0, stream)
     return out
 
 
@@ -538,8 +540,10 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
         _tensor(lse, "lse", torch.float32, (T, H), dev)
     if T == 0 or H == 0:
         return out, lse
-    q_stride = q_nope.stride(1)
-    if q_nope.stride(0) != H * q_stride or q_pe.stride(0) != H * q_stride or q_pe.stride(1) != q_stride:
+    # the distance between rows (the stride of a dim of one says nothing about it)
+    q_stride = q_nope.stride(1) if H > 1 else q_nope.stride(0) if T > 1 else D_QK
+    if (T > 1 and not q_nope.stride(0) == q_pe.stride(0) == H * q_stride) or (
+            H > 1 and not q_nope.stride(1) == q_pe.stride(1) == q_stride):
         raise ValueError("q_nope, q_pe: expected rows evenly spaced over (token, head), with one stride")
     if workspace is None:
         workspace = torch.empty(mla_prefix_attend_workspace_size(T, H, prefix_len), dtype=torch.uint8, device=dev)

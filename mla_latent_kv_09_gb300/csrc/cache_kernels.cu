@@ -390,7 +390,7 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
   if (num_tokens == 0) return MLA_OK;
   // few tokens: their heads spread over CTAs; many: a CTA takes all of a token's
   const int64_t blocks = (static_cast<int64_t>(num_heads) + p.per_turn * kRopeItems - 1) / (p.per_turn * kRopeItems);
-  int64_t y = (kRopeCtas + num_tokens - 1) / num_tokens;
+  int64_t y = (static_cast<int64_t>(kRopeCtas) + num_tokens - 1) / num_tokens;
   if (y > blocks) y = blocks;
   const dim3 grid(num_tokens, static_cast<unsigned>(y), (p.units + kRopeThreads - 1) / kRopeThreads);
   return launch_dependent(half ? mla_rope_kernel<true> : mla_rope_kernel<false>, grid, dim3(kRopeThreads), stream, p);
@@ -411,7 +411,7 @@ int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe
   if (norm_weight && !(eps >= 0.f && std::isfinite(eps))) return MLA_ERR_INVALID_ARG;
   if (inv_freq && !std::isfinite(rope_scale)) return MLA_ERR_INVALID_ARG;
   if (!request_ids && num_tokens % num_requests != 0) return MLA_ERR_INVALID_ARG;
-  if (num_pages > (INT32_MAX / kPage) - 1) return MLA_ERR_UNSUPPORTED;
+  if (num_pages > (INT32_MAX / kPage) - 1 || num_tokens > INT32_MAX - kAppendWarps) return MLA_ERR_UNSUPPORTED;
   const int rc = cache_device_ready();
   if (rc != MLA_OK) return rc;
   if (num_tokens == 0) return MLA_OK;

@@ -104,6 +104,19 @@ def test_strided_rows_in_and_out_and_what_lies_between_is_left_alone(half):
     assert torch.equal(m.rope(proj[:, :1, 128:].expand(T, H, 64), pos, inv, half=half)[:, 3], out[:, 0])
 
 
+@pytest.mark.parametrize("T,H", [(1, 5), (5, 1), (1, 1)])
+def test_strides_of_a_dim_of_one_say_nothing(T, H):
+    x = rand((T, H, 64), 7)
+    pos = torch.arange(9, 9 + T, device="cuda", dtype=torch.int32)
+    inv, _ = m.rope_frequencies(64)
+    want = m.rope(x, pos, inv)
+    odd = torch.empty_strided(x.shape, (7 if T == 1 else 64, 7 if H == 1 else 64, 1), dtype=x.dtype, device="cuda")
+    odd.copy_(x)
+    assert torch.equal(m.rope(odd, pos, inv), want)
+    assert torch.equal(m.rope(x, pos, inv, out=torch.empty_like(odd)), want)
+    assert torch.equal(m.rope(odd, pos, inv, out=odd), want)
+
+
 @pytest.mark.parametrize("half", [False, True])
 def test_in_place_equals_out_of_place_and_leaves_the_rest(half):
     x = rand((33, 4, 192), 8)

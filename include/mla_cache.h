@@ -81,8 +81,9 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
  *                tokens are num_requests equal runs in order (num_tokens must
  *                be a multiple of num_requests)
  *   block_table, bt_stride, num_requests: as for mla_decode (rows of
- *                num_requests requests, bt_stride entries apart; a position
- *                must lie below 64 * bt_stride)
+ *                num_requests requests, bt_stride entries apart)
+ *   bt_width     entries of a row that may be read, 1 .. bt_stride: a position
+ *                must lie below 64 * bt_width
  *   kv_cache     bf16 [num_pages, 64, 576], or with MLA_FLAG_KV_FP8 bytes
  *                [num_pages, 64, 656]
  *   flags        MLA_FLAG_KV_FP8, MLA_FLAG_ROPE_HALF
@@ -99,7 +100,7 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
 int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe, int64_t k_pe_stride,
                      const void* norm_weight, float eps, const double* inv_freq, float rope_scale,
                      const int32_t* positions, const int32_t* request_ids, int num_tokens,
-                     const int32_t* block_table, int64_t bt_stride, int num_requests, void* kv_cache,
+                     const int32_t* block_table, int64_t bt_stride, int bt_width, int num_requests, void* kv_cache,
                      int64_t num_pages, unsigned flags, int* status, mla_stream_t stream);
 
 #ifdef __cplusplus

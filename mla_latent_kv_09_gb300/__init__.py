@@ -282,24 +282,29 @@ def _on_device(fn):
     kernels are launched there, and what the call allocates belongs to it."""
     import functools
 
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         import torch
+        first = args[0] if args else kw.get(name)
+        if first is None:
+            raise TypeError(f"{fn.__name__}: missing argument {name}")
         index = first.get_device()  # -1: not on a GPU
         if stream is None and index >= 0 and index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         dev = first.device
         if dev.type != "cuda":
             raise ValueError(f"{fn.__name__}: expected tensors on a GPU, got {dev}")
         if stream is None:
             with torch.cuda.device(dev):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)
         if stream.device != dev:
             raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {dev}")
         with torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 
@@ -396,7 +401,8 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
 
     latent [T, 512] and k_pe [T, 64] bf16 (rows may be strided: the two parts
     of a [T, 576] projection output); kv_cache [num_pages, 64, 576] bf16 or
-    uint8 [num_pages, 64, 656] FP8 rows; block_table [B, W] int32; positions
+    uint8 [num_pages, 64, 656] FP8 rows; block_table [B, W] int32 (rows may be
+    strided), positions
     [T] int32, token t's position in its request (negative: padding, nothing
     is written); request_ids [T] int32, or None when the tokens are B equal
     runs in order.  With norm_weight [512] bf16 the latent is RMS-normed with
@@ -427,15 +433,14 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
         _tensor(status, "status", torch.int32, status.shape, dev)
     if T == 0:
         return kv_cache
-    # (a single row has no next one: its stride says nothing about the table's width)
-    if B > 1:
-        if block_table.stride(0) < width:
-            raise ValueError("block_table: its rows overlap")
-        width = block_table.stride(0)
+    # (the stride of a dim of one says nothing)
+    bt_stride = block_table.stride(0) if B > 1 else width
+    if bt_stride < width:
+        raise ValueError("block_table: its rows overlap")
     stream = _current_stream(dev)
     mla_cache_append(latent, latent.stride(0) if T > 1 else D_V, k_pe, k_pe.stride(0) if T > 1 else D_QK - D_V,
-                     norm_weight, eps, inv_freq, rope_scale, positions, request_ids, T, block_table, width, B,
-                     kv_cache, kv_cache.shape[0], flags | (MLA_FLAG_ROPE_HALF if half else 0), status, stream)
+                     norm_weight, eps, inv_freq, rope_scale, positions, request_ids, T, block_table, bt_stride, width,
+                     B, kv_cache, kv_cache.shape[0], flags | (MLA_FLAG_ROPE_HALF if half else 0), status, stream)
     return kv_cache
 
 

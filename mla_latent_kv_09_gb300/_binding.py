@@ -59,7 +59,7 @@ SIGNATURES = {
     "mla_rope": (_c_int, [_vp, _i64, _i64, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _f32, _uint, _vp, _i64,
                           _i64, _vp]),
     "mla_cache_append": (_c_int, [_vp, _i64, _vp, _i64, _vp, _f32, _vp, _f32, _vp, _vp, _c_int, _vp, _i64, _c_int,
-                                  _vp, _i64, _uint, _vp, _vp]),
+                                  _c_int, _vp, _i64, _uint, _vp, _vp]),
     "mla_prefix_expand_workspace_size": (_c_size, [_c_int, _uint]),
     "mla_prefix_expand": (_c_int, [_vp, _i64, _vp, _c_int, _vp, _vp, _c_int, _uint, _vp, _vp, _i64, _vp, _vp, _c_size,
                                    _vp, _vp]),
@@ -244,11 +244,12 @@ def mla_rope(x, x_token_stride: int, x_head_stride: int, positions, num_tokens: 
 
 def mla_cache_append(latent, latent_stride: int, k_pe, k_pe_stride: int, norm_weight, eps: float, inv_freq,
                      rope_scale: float, positions, request_ids, num_tokens: int, block_table, bt_stride: int,
-                     num_requests: int, kv_cache, num_pages: int, flags: int, status, stream=None) -> None:
+                     bt_width: int, num_requests: int, kv_cache, num_pages: int, flags: int, status,
+                     stream=None) -> None:
     _check("mla_cache_append", load().mla_cache_append(
         _ptr(latent), latent_stride, _ptr(k_pe), k_pe_stride, _ptr(norm_weight), eps, _ptr(inv_freq), rope_scale,
-        _ptr(positions), _ptr(request_ids), num_tokens, _ptr(block_table), bt_stride, num_requests, _ptr(kv_cache),
-        num_pages, flags, _ptr(status), _stream(stream)))
+        _ptr(positions), _ptr(request_ids), num_tokens, _ptr(block_table), bt_stride, bt_width, num_requests,
+        _ptr(kv_cache), num_pages, flags, _ptr(status), _stream(stream)))
 
 
 def mla_prefix_expand_workspace_size(prefix_len: int, flags: int) -> int:

@@ -152,6 +152,7 @@ struct AppendParams {
   int num_tokens, per_request;
   const int* block_table;
   long long bt_stride;
+  int bt_width;
   int num_requests;
   uint8_t* cache;
   long long num_pages;
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
     pb = hi_f(w);
   }
   // the row; a request, position or page out of range skips the token
-  bool ok = req >= 0 && req < p.num_requests && pos / kPage < p.bt_stride;
+  bool ok = req >= 0 && req < p.num_requests && pos / kPage < p.bt_width;
   long long page = -1;
   if (ok) page = p.block_table[req * p.bt_stride + pos / kPage];
   if (page < 0 || page >= p.num_pages) {
@@ -399,13 +400,13 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
 int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe, int64_t k_pe_stride,
                      const void* norm_weight, float eps, const double* inv_freq, float rope_scale,
                      const int32_t* positions, const int32_t* request_ids, int num_tokens,
-                     const int32_t* block_table, int64_t bt_stride, int num_requests, void* kv_cache,
+                     const int32_t* block_table, int64_t bt_stride, int bt_width, int num_requests, void* kv_cache,
                      int64_t num_pages, unsigned flags, int* status, mla_stream_t stream) {
   if (!latent || !k_pe || !positions || !block_table || !kv_cache || !status) return MLA_ERR_INVALID_ARG;
   if (!al(latent, 16) || !al(k_pe, 16) || !al(norm_weight, 16) || !al(inv_freq, 8) || !al(positions, 4) ||
       !al(request_ids, 4) || !al(block_table, 4) || !al(kv_cache, 16) || !al(status, 4))
     return MLA_ERR_INVALID_ARG;
-  if (num_tokens < 0 || num_requests < 1 || bt_stride < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_requests < 1 || bt_width < 1 || bt_stride < bt_width || num_pages < 1) return MLA_ERR_INVALID_ARG;
   if (flags & ~static_cast<unsigned>(MLA_FLAG_KV_FP8 | MLA_FLAG_ROPE_HALF)) return MLA_ERR_INVALID_ARG;
   if (!row_stride_ok(latent_stride, kLatent) || !row_stride_ok(k_pe_stride, kRopeDim)) return MLA_ERR_INVALID_ARG;
   if (norm_weight && !(eps >= 0.f && std::isfinite(eps))) return MLA_ERR_INVALID_ARG;
@@ -430,6 +431,7 @@ int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe
   p.per_request = request_ids ? 1 : num_tokens / num_requests;
   p.block_table = block_table;
   p.bt_stride = bt_stride;
+  p.bt_width = bt_width;
   p.num_requests = num_requests;
   p.cache = static_cast<uint8_t*>(kv_cache);
   p.num_pages = num_pages;

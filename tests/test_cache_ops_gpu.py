@@ -293,6 +293,24 @@ def test_padding_is_skipped_and_bad_places_are_reported(fp8):
         assert torch.equal(cache.flatten(0, 1)[rest], before.flatten(0, 1)[rest])
 
 
+def test_a_slice_of_a_wider_block_table():
+    """Entries outside the slice are neither used nor taken for the row's next ones."""
+    x = rand((4, 576), 1)
+    wide = torch.arange(12, device="cuda", dtype=torch.int32).view(3, 4)
+    ints = lambda *a: torch.tensor(a, device="cuda", dtype=torch.int32)  # noqa: E731
+    for lo, hi in ((0, 2), (1, 3), (2, 4)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kw = dict(positions=ints(3, 64, 127, 5), request_ids=ints(0, 1, 2, 2), status=status)
+        a, b = pool(12, False, 5), pool(12, False, 5)
+        m.cache_append(latent=x[:, :512], k_pe=x[:, 512:], kv_cache=a, block_table=wide[:, lo:hi], **kw)
+        m.cache_append(x[:, :512], x[:, 512:], b, wide[:, lo:hi].contiguous(), **kw)
+        assert torch.equal(a, b) and int(status) == 0
+        before = a.clone()
+        m.cache_append(x[:, :512], x[:, 512:], a, wide[:, lo:hi], ints(128, 128, 128, 200), request_ids=ints(0, 1, 2, 2),
+                       status=status)
+        assert int(status) == m.MLA_ERR_BAD_TABLE and torch.equal(a, before)
+
+
 def test_fp8_groups_of_zeros_tiny_huge_and_not_finite_values():
     x = rand((8, 576), 3).float()
     x[0, :128] = 0

@@ -46,17 +46,17 @@ def test_rope_checks_its_arguments(lib):
     assert lib.mla_rope(*a) == m.MLA_ERR_INVALID_ARG
 
 
-#         lat  ls   kpe  ks  wt  eps   freq sc  pos req T  bt  w  B  cache pages flags status stream
-APPEND = [OK, 576, OK, 576, OK, 1e-6, OK, 1.0, OK, OK, 4, OK, 3, 2, OK, 10, 0, OK, None]
+#         lat  ls   kpe  ks  wt  eps   freq sc  pos req T  bt  s  w  B  cache pages flags status stream
+APPEND = [OK, 576, OK, 576, OK, 1e-6, OK, 1.0, OK, OK, 4, OK, 3, 3, 2, OK, 10, 0, OK, None]
 
 
 def test_append_checks_its_arguments(lib):
     check(lib.mla_cache_append, APPEND,
-          [(0, None), (2, None), (8, None), (11, None), (14, None), (17, None), (0, OK + 8), (2, OK + 2), (4, OK + 8),
-           (6, OK + 4), (8, OK + 2), (9, OK + 1), (11, OK + 2), (14, OK + 8), (17, OK + 2), (1, 504), (1, 577), (3, 56),
-           (10, -1), (12, 0), (13, 0), (15, 0), (16, 1), (16, 64), (5, -1.0), (5, math.nan), (7, math.inf)],
-          m.MLA_ERR_INVALID_ARG)
-    check(lib.mla_cache_append, APPEND, [(15, 1 << 40)], m.MLA_ERR_UNSUPPORTED)
+          [(0, None), (2, None), (8, None), (11, None), (15, None), (18, None), (0, OK + 8), (2, OK + 2), (4, OK + 8),
+           (6, OK + 4), (8, OK + 2), (9, OK + 1), (11, OK + 2), (15, OK + 8), (18, OK + 2), (1, 504), (1, 577), (3, 56),
+           (10, -1), (12, 2), (13, 0), (13, 4), (14, 0), (16, 0), (17, 1), (17, 64), (5, -1.0), (5, math.nan),
+           (7, math.inf)], m.MLA_ERR_INVALID_ARG)
+    check(lib.mla_cache_append, APPEND, [(16, 1 << 40), (10, 2 ** 31 - 1)], m.MLA_ERR_UNSUPPORTED)
     a = list(APPEND)  # equal runs that are not
     a[9], a[10] = None, 5
     assert lib.mla_cache_append(*a) == m.MLA_ERR_INVALID_ARG
@@ -107,6 +107,10 @@ def test_python_calls_refuse_tensors_off_the_gpu():
         m.prefix_expand(x, x, 1, x, x)
     with pytest.raises(ValueError):
         m.prefix_attend(x, x, x, x, x, 1.0)
+    with pytest.raises(ValueError):  # by name
+        m.rope(x=x, positions=torch.zeros(2, dtype=torch.int32), inv_freq=torch.ones(32, dtype=torch.float64))
+    with pytest.raises(TypeError):
+        m.rope(positions=torch.zeros(2, dtype=torch.int32))
 
 
 # ---------------------------------------------------------------- frequencies

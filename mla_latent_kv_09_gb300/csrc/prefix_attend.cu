@@ -603,32 +603,54 @@ int attend_device_ready(int* sms) {
 // Row blocks of a head that are worked on side by side read each key tile
 // from HBM once and from L2 after that, so a batch of several blocks wants
 // them side by side; but `width` must leave few units idle (units / width
-// groups) and few blocks over in the last pass.  The cost of a width: steps
-// of the longest range, each the tensor cores' 1,280 cycles or, when all
-// groups stream different tiles, their share of the HBM: 64 KiB a group at
-// 3.5 KB a cycle, 18.6 cycles a group.
+// groups) and few blocks over in the last pass.  And the groups either share
+// the line equally, cutting heads, or take whole heads, some groups staying
+// idle.  The cost of a choice, in cycles, is that of the steps of the longest
+// range and of the join.  A step takes a pair 600 cycles besides the tensor
+// cores' 1,280 or, when all groups stream different tiles, their share of the
+// HBM (64 KiB a group at 3.5 KB a cycle: 18.6 a group); a CTA 2,500 or that
+// share, so that 128 CTAs with a head each are as fast as 152.  A join takes
+// 5,000 and 0.75 for each partial row (written, read and summed by the next
+// kernel).  Measured, cut / whole: 1 token x 777 rows x 128 heads 16.8 / 14.2
+// us, 128 x 4096 x 128 65.5 / 54.2, 64 x 8192 x 128 93 / 93.5, 8 x 4096 x 64
+// 31.7 / 45.4, 256 x 500 x 128 31.2 / 20.1.
 Plan plan(int num_tokens, int num_heads, int prefix_len, int sms) {
   Plan w;
-  const int units = num_tokens > kTile ? sms / 2 : sms;
+  const bool pairs = num_tokens > kTile;
+  const int units = pairs ? sms / 2 : sms, rows = num_tokens < 2 * kTile ? num_tokens : 2 * kTile;
   w.nk = (prefix_len + kTile - 1) / kTile;
   w.blocks = (num_tokens + 2 * kTile - 1) / (2 * kTile);
   double best = 0;
+  bool any = false;
+  auto take = [&](int width, int passes, long long groups, double cost) {
+    if (any && cost >= 0.99 * best) return;
+    any = true;
+    best = cost;
+    w.width = width;
+    w.groups = static_cast<int>(groups);
+    w.passes = passes;
+  };
+  auto step = [pairs](long long groups) {
+    const double hbm = 18.6 * static_cast<double>(groups);
+    return pairs ? 600.0 + fmax(1280.0, hbm) : fmax(2500.0, hbm);
+  };
   for (int width = 1; width <= w.blocks && width <= units && width <= 16; ++width) {
-    const int groups = units / width, passes = (w.blocks + width - 1) / width;
-    const double step = fmax(1280.0, 18.6 * groups);
-    const double cost = passes * step / groups;
-    if (width == 1 || cost < 0.99 * best) {
-      best = cost;
-      w.width = width;
-      w.groups = groups;
-      w.passes = passes;
+    const int passes = (w.blocks + width - 1) / width;
+    const long long heads = static_cast<long long>(passes) * num_heads, line = heads * w.nk;
+    const long long most = units / width, whole = (heads + most - 1) / most;  // heads a group
+    if (w.nk == 1) {  // heads of a single tile cannot be cut
+      const long long groups = most < heads ? most : heads;
+      take(width, passes, groups, static_cast<double>(whole) * step(groups));
+      continue;
     }
+    if (heads % whole == 0)
+      take(width, passes, heads / whole, static_cast<double>(whole * w.nk) * step(heads / whole));
+    // at least two steps a range, one for each stream
+    const long long groups = most < (line + 1) / 2 ? most : (line + 1) / 2;
+    take(width, passes, groups, static_cast<double>((line + groups - 1) / groups) * step(groups) + 5000.0 +
+             0.75 * static_cast<double>(groups * width * rows));
   }
   w.line = static_cast<long long>(w.passes) * num_heads * w.nk;
-  // At least two steps a range, one for each stream, unless the prefix is one
-  // tile: then nothing is cut, and a range is a head.
-  const long long most = w.nk > 1 ? (w.line + 1) / 2 : w.line;
-  if (w.groups > most) w.groups = static_cast<int>(most);
   return w;
 }
 

@@ -456,89 +456,160 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
   }
 }
 
-// Joins the partial rows of the (row block, head)s that were cut.  Block
-// (g, lane block, chunk): the unit that the range of group g starts inside of,
-// if no earlier range does; kCombineWarps / kWarps of its rows, kWarps warps a
-// row (a warp takes every kWarps-th piece, eight loads in flight), four columns
-// a lane.
-constexpr int kCombineWarps = 8;
-template <int kWarps>
+// Joins the partial rows of the (row block, head)s that were cut.  Block (x,
+// lane block, chunk) takes one of them: unit x of the line if there are fewer
+// units than ranges, else the unit that range x + 1 starts inside of, if no
+// earlier range does; and of it kCombineRows rows a warp (kWide = false, up to
+// 8 pieces: lane l takes the LSE of row l / 8 and piece l % 8, and all four
+// rows' loads are in flight together) or one row (kWide: a thread takes the LSE
+// of a piece, a warp every eighth piece, eight loads in flight).  Four columns
+// a lane.  Latency is all it costs, so loads do not wait for one another: one
+// row a warp, its LSEs first, took 13.4 us for 75 heads of 256 rows (9.5 so),
+// and for one row of 118 pieces 25 us.
+constexpr int kCombineWarps = 8, kCombineRows = 4;
+__host__ __device__ __forceinline__ bool few_units(const Plan& w, int num_heads) {
+  return static_cast<long long>(w.passes) * num_heads < w.groups;
+}
+template <bool kWide>
 __global__ void __launch_bounds__(32 * kCombineWarps) mla_prefix_combine_kernel(const __grid_constant__ AttendParams p) {
-  __shared__ float4 acc[kCombineWarps][32];
+  __shared__ float4 acc[kWide ? kCombineWarps : 1][32];
+  constexpr int kRowsWarp = kWide ? 1 : kCombineRows;
   const Plan& w = p.plan;
   // Every block waits, those without work too: what follows on the stream
   // waits for this kernel, and this kernel's end must not come before the end
   // of the one that wrote the pieces.
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp % kWarps;
-  const int g = blockIdx.x + 1, lane_block = blockIdx.y;
-  const long long at = cut(w, g);
-  const int unit = static_cast<int>(at / w.nk);
+  const int lane_block = blockIdx.y;
+  int unit, g0;  // g0: the range that holds the unit's first step, as its first segment or, after another, its second
+  if (few_units(w, p.num_heads)) {
+    unit = blockIdx.x;
+    g0 = static_cast<int>(quotient((static_cast<long long>(unit) * w.nk + 1) * w.groups - 1, w.line));
+  } else {
+    g0 = blockIdx.x;
+    unit = static_cast<int>(quotient(cut(w, g0 + 1), w.nk));
+  }
   const long long start = static_cast<long long>(unit) * w.nk, end = start + w.nk;
-  if (at == start || cut(w, g - 1) > start) return;  // starts with the unit, or an earlier range is inside of it
+  const long long before = cut(w, g0), at = cut(w, g0 + 1);
+  if (before > start || at <= start || at >= end) return;  // not the range of the unit's first step, or the unit is whole
   const int block = unit / p.num_heads * w.width + lane_block, h = unit % p.num_heads;
   if (block >= w.blocks) return;
-  const int g0 = g - 1;  // holds the unit's first step, as its first segment or, after another, its second
-  const int odd = cut(w, g0) < start ? 1 : 0;
-  int n = 2;
-  while (cut(w, g0 + n) < end) ++n;
-  const int brow = blockIdx.z * (kCombineWarps / kWarps) + warp / kWarps, t = block * 2 * kTile + brow;
-  const bool real = brow < p.part_rows && t < p.num_tokens;
-  const long long row = static_cast<long long>(t) * p.num_heads + h;
-  auto piece = [&](int i) {  // row of piece i among the partial rows
+  const int odd = before < start ? 1 : 0;
+  const int n = static_cast<int>(quotient(end * w.groups - 1, w.line)) - g0 + 1;  // up to the range of its last step
+  const int brow = kWide ? blockIdx.z : (blockIdx.z * kCombineWarps + warp) * kRowsWarp;
+  const int left = min(p.part_rows - brow, p.num_tokens - block * 2 * kTile - brow);  // real rows from brow on
+  if (left <= 0) return;  // (kWide: the block's warps all have the same row)
+  const long long row0 = static_cast<long long>(block * 2 * kTile + brow) * p.num_heads + h;
+  auto piece = [&](int i) {  // first row of piece i among the partial rows
     const int slot = 2 * ((g0 + i) * w.width + lane_block) + (i == 0 ? odd : 0);
     return static_cast<long long>(slot) * p.part_rows + brow;
   };
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float lse2 = -INFINITY, other2 = -INFINITY;
-  if (real) {
-    if (p.suffix_lse) other2 = p.suffix_lse[row] * kLog2e;
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_lse[piece(i)]);
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+  const float4* part_o = reinterpret_cast<const float4*>(p.part_o) + lane;
+  float4 o[kRowsWarp];
+  float lse2, f;  // of the lane's row; the share of its piece
+  float other2 = -INFINITY;
+  if (!kWide) {
+    const int r = min(lane >> 3, left - 1);
+    if (p.suffix_lse) other2 = p.suffix_lse[row0 + static_cast<long long>(r) * p.num_heads] * kLog2e;
+    const float mine = (lane & 7) < n ? p.part_lse[piece(lane & 7) + r] : -INFINITY;
+    float top = mine;
+#pragma unroll
+    for (int i = 4; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
     const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32) sum += ex2_approx(p.part_lse[piece(i)] - base);
-    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    f = ex2_approx(mine - base);
+    float sum = f;
+#pragma unroll
+    for (int i = 4; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    f *= sum == 0.f ? 0.f : 1.f / sum;
     lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
-#pragma unroll 8
-    for (int i = sub; i < n; i += kWarps) {
+#pragma unroll
+    for (int k = 0; k < kRowsWarp; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
       const long long from = piece(i);
-      const float f = ex2_approx(p.part_lse[from] - base) * inv;
-      const float4 v = reinterpret_cast<const float4*>(p.part_o)[from * (kHeadDim / 4) + lane];
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
-    }
-  }
-  if (kWarps > 1) {
-    acc[warp][lane] = o;
-    __syncthreads();
-    if (sub == 0) {
-      for (int i = 1; i < kWarps; ++i) {
-        const float4 v = acc[warp + i][lane];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
+      float4 v[kRowsWarp];
+#pragma unroll
+      for (int k = 0; k < kRowsWarp; ++k)
+        v[k] = k < left ? part_o[(from + k) * (kHeadDim / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kRowsWarp; ++k) {
+        const float share = __shfl_sync(0xffffffffu, f, 8 * k + i);
+        o[k].x = fmaf(v[k].x, share, o[k].x);
+        o[k].y = fmaf(v[k].y, share, o[k].y);
+        o[k].z = fmaf(v[k].z, share, o[k].z);
+        o[k].w = fmaf(v[k].w, share, o[k].w);
       }
     }
+  } else {
+    // thread i: the LSE of piece i; a warp's first eight pieces come under them
+    __shared__ float red[2][kCombineWarps], share[32 * kCombineWarps];
+    if (p.suffix_lse) other2 = p.suffix_lse[row0] * kLog2e;
+    const int i0 = threadIdx.x;
+    const float mine = i0 < n ? p.part_lse[piece(i0)] : -INFINITY;
+    auto load = [&](int first, float4 (&v)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = first + k * kCombineWarps;
+        v[k] = i < n ? part_o[piece(i) * (kHeadDim / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    float4 v[8];
+    load(warp, v);
+    float top = mine;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    red[0][warp] = top;
+    __syncthreads();
+    top = red[0][lane & 7];
+#pragma unroll
+    for (int i = 4; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    const float base = top == -INFINITY ? 0.f : top;
+    f = ex2_approx(mine - base);
+    float sum = f;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    red[1][warp] = sum;
+    share[i0] = f;
+    __syncthreads();
+    sum = red[1][lane & 7];
+#pragma unroll
+    for (int i = 4; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    lse2 = sum == 0.f ? -INFINITY : base + lg2(sum);
+    o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int first = warp; first < n; first += 8 * kCombineWarps) {
+      if (first != warp) load(first, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = first + k * kCombineWarps;
+        const float part = i < n ? share[i] * inv : 0.f;
+        o[0].x = fmaf(v[k].x, part, o[0].x);
+        o[0].y = fmaf(v[k].y, part, o[0].y);
+        o[0].z = fmaf(v[k].z, part, o[0].z);
+        o[0].w = fmaf(v[k].w, part, o[0].w);
+      }
+    }
+    acc[warp][lane] = o[0];
+    __syncthreads();
+    if (warp != 0) return;
+    for (int i = 1; i < kCombineWarps; ++i) {
+      const float4 v = acc[i][lane];
+      o[0].x += v.x;
+      o[0].y += v.y;
+      o[0].z += v.z;
+      o[0].w += v.w;
+    }
   }
-  if (!real || sub != 0) return;
   Join j = {1.f, 0.f, lse2};
   if (p.suffix_lse) j = join(lse2, other2);
-  // two lanes write 8 columns (16 bytes of bf16)
-  const float y0 = __shfl_down_sync(0xffffffffu, o.x, 1), y1 = __shfl_down_sync(0xffffffffu, o.y, 1);
-  const float y2 = __shfl_down_sync(0xffffffffu, o.z, 1), y3 = __shfl_down_sync(0xffffffffu, o.w, 1);
-  const float all[8] = {o.x, o.y, o.z, o.w, y0, y1, y2, y3};
-  if ((lane & 1) == 0) write8(p, row, 4 * lane, all, j);
   __syncwarp();  // lse may be suffix_lse: all lanes have read it
-  if (lane == 0) p.lse[row] = j.lse2 * kLn2;
+  if (kWide ? lane == 0 : (lane & 7) == 0 && (lane >> 3) < left)
+    p.lse[row0 + static_cast<long long>(kWide ? 0 : lane >> 3) * p.num_heads] = j.lse2 * kLn2;
+#pragma unroll
+  for (int k = 0; k < kRowsWarp; ++k) {
+    const Join of = {__shfl_sync(0xffffffffu, j.mine, 8 * k), __shfl_sync(0xffffffffu, j.other, 8 * k), 0.f};
+    if (k < left) write4(p, row0 + static_cast<long long>(k) * p.num_heads, 4 * lane, o[k], of);
+  }
 }
 
 // Nothing to attend to in the prefix: the suffix's result, or zeros.
@@ -617,7 +688,8 @@ int attend_device_ready(int* sms) {
 Plan plan(int num_tokens, int num_heads, int prefix_len, int sms) {
   Plan w;
   const bool pairs = num_tokens > kTile;
-  const int units = pairs ? sms / 2 : sms, rows = num_tokens < 2 * kTile ? num_tokens : 2 * kTile;
+  // (the join gives each piece of a head a thread)
+  const int units = min(pairs ? sms / 2 : sms, 32 * kCombineWarps), rows = num_tokens < 2 * kTile ? num_tokens : 2 * kTile;
   w.nk = (prefix_len + kTile - 1) / kTile;
   w.blocks = (num_tokens + 2 * kTile - 1) / (2 * kTile);
   double best = 0;
@@ -756,8 +828,10 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   const int rows = num_tokens < l.rows ? num_tokens : l.rows;
   // pieces a head can be cut in: the ranges that overlap its nk steps
   const bool few = p.plan.nk / (p.plan.line / p.plan.groups) + 2 <= 8;
-  return launch_dependent(few ? mla_prefix_combine_kernel<1> : mla_prefix_combine_kernel<kCombineWarps>,
-                          dim3(p.plan.groups - 1, p.plan.width, few ? (rows + kCombineWarps - 1) / kCombineWarps : rows),
+  const int block_rows = few ? kCombineWarps * kCombineRows : 1;
+  return launch_dependent(few ? mla_prefix_combine_kernel<false> : mla_prefix_combine_kernel<true>,
+                          dim3(few_units(p.plan, num_heads) ? p.plan.passes * num_heads : p.plan.groups - 1, p.plan.width,
+                               (rows + block_rows - 1) / block_rows),
                           dim3(32 * kCombineWarps), 0, 1, stream, p);
 }
 

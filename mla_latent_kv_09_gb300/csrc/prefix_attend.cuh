@@ -50,7 +50,11 @@ struct AttendParams {
   int* status;
 };
 
-__host__ __device__ __forceinline__ long long cut(const Plan& w, int g) { return w.line * g / w.groups; }
+// x / n, x >= 0, n > 0: almost always in 32 bits (a 64-bit division is a hundred instructions).
+__host__ __device__ __forceinline__ long long quotient(long long x, long long n) {
+  return (x | n) >> 32 ? x / n : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(n));
+}
+__host__ __device__ __forceinline__ long long cut(const Plan& w, int g) { return quotient(w.line * g, w.groups); }
 
 __device__ __forceinline__ float lg2(float x) {
   float y;
@@ -164,7 +168,7 @@ struct SegmentIter {
     lane_block = unit_id % w.width;
     const long long begin = cut(w, g);
     left = cut(w, g + 1) - begin;
-    unit = static_cast<int>(begin / w.nk);
+    unit = static_cast<int>(quotient(begin, w.nk));
     k0 = static_cast<int>(begin - static_cast<long long>(unit) * w.nk);
     first = true;
   }
@@ -240,6 +244,23 @@ __device__ __forceinline__ void write8(const AttendParams& p, long long row, int
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = pack8(x);
   }
+}
+
+// The same for 4 columns.
+__device__ __forceinline__ void write4(const AttendParams& p, long long row, int col, const float4& o, const Join& j) {
+  float x[4] = {o.x * j.mine, o.y * j.mine, o.z * j.mine, o.w * j.mine};
+  const long long at = row * kHeadDim + col;
+  if (p.suffix_out && j.other != 0.f) {  // a suffix without a share is not read as numbers
+    const uint2 s = *reinterpret_cast<const uint2*>(p.suffix_out + at);
+    x[0] = fmaf(__uint_as_float(s.x << 16), j.other, x[0]);
+    x[1] = fmaf(__uint_as_float(s.x & 0xffff0000u), j.other, x[1]);
+    x[2] = fmaf(__uint_as_float(s.y << 16), j.other, x[2]);
+    x[3] = fmaf(__uint_as_float(s.y & 0xffff0000u), j.other, x[3]);
+  }
+  if (p.out_fp32)
+    *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at) = pack4(x);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
 }
 
 // The segment epilogue of a warp: 32 rows (one a lane), 32 columns from `col`.

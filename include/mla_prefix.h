@@ -66,8 +66,9 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
                       int64_t head_rows, void* k_pe, void* workspace, size_t ws_bytes, int* status,
                       mla_stream_t stream);
 
-/* Bytes of workspace mla_prefix_attend needs on the current device; 0 and
- * *err set on failure (err may be NULL).  Host-only. */
+/* Bytes of workspace mla_prefix_attend needs on the current device, 0 where no
+ * head's rows are split over SMs; 0 and *err set on failure (err may be NULL).
+ * Host-only. */
 size_t mla_prefix_attend_workspace_size(int num_tokens, int num_heads, int prefix_len, int* err);
 
 /* Attention of num_tokens query tokens over one prefix.
@@ -91,7 +92,8 @@ size_t mla_prefix_attend_workspace_size(int num_tokens, int num_heads, int prefi
  *   out          [num_tokens, num_heads, 128] bf16 (fp32); may be suffix_out
  *                itself where both are bf16
  *   lse          fp32 [num_tokens, num_heads]; may be suffix_lse itself
- *   workspace    256-byte aligned, mla_prefix_attend_workspace_size bytes
+ *   workspace    256-byte aligned, mla_prefix_attend_workspace_size bytes;
+ *                NULL where none is needed
  *   status       MLA_ERR_TIMEOUT if a bounded wait runs out
  * A token that sees nothing, here and in the suffix, gets out = 0 and lse =
  * -inf.  Weights are exp in fp32, rounded to fp16 for the value product and

@@ -551,7 +551,8 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
             H > 1 and not q_nope.stride(1) == q_pe.stride(1) == q_stride):
         raise ValueError("q_nope, q_pe: expected rows evenly spaced over (token, head), with one stride")
     if workspace is None:
-        workspace = torch.empty(mla_prefix_attend_workspace_size(T, H, prefix_len), dtype=torch.uint8, device=dev)
+        need = mla_prefix_attend_workspace_size(T, H, prefix_len)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
         _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
     if status is None:
@@ -560,6 +561,6 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
         _tensor(status, "status", torch.int32, status.shape, dev)
     stream = _current_stream(dev)
     mla_prefix_attend(q_nope, q_pe, q_stride, k_nope, v, R, k_pe, prefix_len, visible, T, H, softmax_scale,
-                      suffix_out, suffix_lse, MLA_FLAG_OUT_FP32 if out_fp32 else 0, workspace, workspace.numel(), out,
-                      lse, status, stream)
+                      suffix_out, suffix_lse, MLA_FLAG_OUT_FP32 if out_fp32 else 0, workspace,
+                      0 if workspace is None else workspace.numel(), out, lse, status, stream)
     return out, lse

@@ -726,14 +726,17 @@ Plan plan(int num_tokens, int num_heads, int prefix_len, int sms) {
   return w;
 }
 
-struct WsLayout2 {
+// Heads are cut wherever a range does not end with one (one of a single tile cannot be).
+bool cuts_heads(const Plan& w) { return w.nk > 1 && (w.line / w.nk) % w.groups != 0; }
+
+struct AttendWs {
   size_t lse, total;
-  int rows;
+  int rows;  // of a unit's two partial tiles
 };
-WsLayout2 attend_ws(const Plan& w, int num_tokens) {
-  WsLayout2 l;
-  l.rows = num_tokens > kTile ? 2 * kTile : kTile;
-  const size_t slots = 2 * static_cast<size_t>(w.groups) * w.width * l.rows;
+AttendWs attend_ws(const Plan& w, int num_tokens) {
+  AttendWs l;
+  l.rows = num_tokens < 2 * kTile ? num_tokens : 2 * kTile;
+  const size_t slots = cuts_heads(w) ? 2 * static_cast<size_t>(w.groups) * w.width * l.rows : 0;
   l.lse = align256(slots * kHeadDim * sizeof(float));
   l.total = l.lse + align256(slots * sizeof(float));
   return l;
@@ -754,7 +757,7 @@ size_t mla_prefix_attend_workspace_size(int num_tokens, int num_heads, int prefi
                : attend_device_ready(&sms);
   if (err) *err = rc;
   if (rc != MLA_OK) return 0;
-  if (num_tokens == 0 || prefix_len == 0) return 256;
+  if (num_tokens == 0 || prefix_len == 0) return 0;
   return attend_ws(plan(num_tokens, num_heads, prefix_len, sms), num_tokens).total;
 }
 
@@ -763,7 +766,7 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
                       int num_heads, float softmax_scale, const void* suffix_out, const float* suffix_lse,
                       unsigned flags, void* workspace, size_t ws_bytes, void* out, float* lse, int* status,
                       mla_stream_t stream) {
-  if (!q_nope || !q_pe || !workspace || !out || !lse || !status) return MLA_ERR_INVALID_ARG;
+  if (!q_nope || !q_pe || !out || !lse || !status) return MLA_ERR_INVALID_ARG;
   if (prefix_len != 0 && (!k_nope || !v || !k_pe)) return MLA_ERR_INVALID_ARG;
   if (!al(q_nope, 16) || !al(q_pe, 16) || !al(k_nope, 16) || !al(v, 16) || !al(k_pe, 16) || !al(visible, 4) ||
       !al(suffix_out, 16) || !al(suffix_lse, 4) || !al(workspace, 256) || !al(out, 16) || !al(lse, 4) ||
@@ -781,8 +784,9 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   int sms = 0;
   int rc = attend_device_ready(&sms);
   if (rc != MLA_OK) return rc;
-  if (ws_bytes < mla_prefix_attend_workspace_size(num_tokens, num_heads, prefix_len, nullptr))
-    return MLA_ERR_WORKSPACE;
+  const size_t need = mla_prefix_attend_workspace_size(num_tokens, num_heads, prefix_len, nullptr);
+  if (need > 0 && !workspace) return MLA_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MLA_ERR_WORKSPACE;
   if (num_tokens == 0) return MLA_OK;
   AttendParams p = {};
   p.visible = visible;
@@ -802,7 +806,7 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
                             1, stream, p);
   }
   p.plan = plan(num_tokens, num_heads, prefix_len, sms);
-  const WsLayout2 l = attend_ws(p.plan, num_tokens);
+  const AttendWs l = attend_ws(p.plan, num_tokens);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.lse);
   p.part_rows = l.rows;
@@ -823,12 +827,10 @@ int mla_prefix_attend(const void* q_nope, const void* q_pe, int64_t q_stride, co
   const int units = p.plan.groups * p.plan.width;
   rc = small ? launch_dependent(mla_prefix_attend_kernel, dim3(units), dim3(kThreads), kSmem, 1, stream, p, qn, qp, k, kp, vm)
              : attend_pair_launch(units, stream, p, qn, qp, k, kp, vm);
-  // heads are cut wherever a range does not end with one (one of a single tile cannot be)
-  if (rc != MLA_OK || p.plan.nk == 1 || (p.plan.line / p.plan.nk) % p.plan.groups == 0) return rc;
-  const int rows = num_tokens < l.rows ? num_tokens : l.rows;
+  if (rc != MLA_OK || !cuts_heads(p.plan)) return rc;
   // pieces a head can be cut in: the ranges that overlap its nk steps
   const bool few = p.plan.nk / (p.plan.line / p.plan.groups) + 2 <= 8;
-  const int block_rows = few ? kCombineWarps * kCombineRows : 1;
+  const int rows = l.rows, block_rows = few ? kCombineWarps * kCombineRows : 1;
   return launch_dependent(few ? mla_prefix_combine_kernel<false> : mla_prefix_combine_kernel<true>,
                           dim3(few_units(p.plan, num_heads) ? p.plan.passes * num_heads : p.plan.groups - 1, p.plan.width,
                                (rows + block_rows - 1) / block_rows),

@@ -446,8 +446,12 @@ def test_attention_refusals():
                 lambda: m.prefix_attend(*x[:2], x[2].transpose(1, 2).contiguous().transpose(1, 2), *x[3:], SCALE)]:
         with pytest.raises(ValueError):
             bad()
+    y = inputs(4, 2, 5000)  # two heads, split over many SMs
+    need = m.mla_prefix_attend_workspace_size(4, 2, 5000)
+    assert need > 0
     for bad in [lambda: m.prefix_attend(*x, 0.0), lambda: m.prefix_attend(*x, float("nan")),
-                lambda: m.prefix_attend(*x, SCALE, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))]:
+                lambda: m.prefix_attend(*y, SCALE, workspace=torch.empty(0, dtype=torch.uint8, device="cuda")),
+                lambda: m.prefix_attend(*y, SCALE, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))]:
         with pytest.raises(m.MlaError):
             bad()
     assert m.prefix_attend(x[0][:0], x[1][:0], *x[2:], SCALE)[0].shape == (0, 2, 128)

@@ -87,7 +87,7 @@ ATTEND = [OK, OK + 256, 192, OK, OK, 64, OK, 64, None, 4, 16, 0.07, None, None, 
 
 def test_attend_checks_its_arguments(lib):
     check(lib.mla_prefix_attend, ATTEND,
-          [(0, None), (1, None), (3, None), (4, None), (6, None), (15, None), (17, None), (18, None), (19, None),
+          [(0, None), (1, None), (3, None), (4, None), (6, None), (17, None), (18, None), (19, None),
            (0, OK + 8), (1, OK + 8), (3, OK + 8), (4, OK + 8), (6, OK + 8), (8, OK + 2), (12, OK), (13, OK),
            (15, OK + 128), (17, OK + 8), (18, OK + 2), (19, OK + 1), (2, 120), (2, 196), (2, 1 << 40), (5, 63),
            (7, -1), (9, -1), (11, 0.0), (11, -1.0), (11, math.nan), (11, math.inf), (14, 1)], m.MLA_ERR_INVALID_ARG)

@@ -31,14 +31,20 @@
 // the first runs under the exponentials of the second.
 //
 // The running maximum is lazy: it moves only when a score beats it by 2^14, so
-// that O is rarely rescaled.  O is normalised by the sum of the rounded weights that the value
-// product used, so that a weight's rounding acts on v_j - O and not on v_j;
-// the LSE takes the sum of the unrounded ones.
+// that O is rarely rescaled.  O is normalised by the sum of the rounded weights
+// that the value product used, so that a weight's rounding acts on v_j - O and
+// not on v_j; the LSE takes the sum of the unrounded ones.  fp16 for the weights
+// and values: 11 bits, against bf16's 8; a weight below 2^-25 of the running
+// maximum's rounds to zero, so P rows lose at most P 2^-25 of their sum.
 //
 // Work split: all (head, key tile) steps of a row block form one line, cut
 // into equal ranges, one per CTA or pair (see plan()).  A range that covers a
 // head's whole prefix writes the result; a head cut in pieces leaves
 // normalised fp32 partial rows and their LSE, which the combine kernel joins.
+//
+// Measured, whole calls: 64 tokens x 8192 rows x 128 heads 93.5 us (545 MB, 5.8
+// TB/s), 1 x 777 x 128 14.3 us (51 MB, of which 6 us are the launch, the first
+// tile's way in and the last one's way out).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -30,10 +30,14 @@
 // before is done.  Each thread keeps its own sums, against the maximum it last
 // saw.
 //
-// Measured against two row tiles in one CTA (two streams with their own O and
-// one score buffer each, whose chain scores -> softmax -> value product ->
-// next scores is as long as both streams' products): 256 tokens x 16384 rows x
-// 128 heads 307 us, 2048 x 4096 x 16 102 us.
+// Measured, whole calls: 256 tokens x 16384 rows x 128 heads 238 us (4.5 TB/s,
+// 1.2 PFLOP/s; 245 to 252 with scores that move the maximum late), 2048 x 4096 x
+// 16 59 us (1.46 PFLOP/s).  A key tile takes a pair about 1,950 cycles, of which
+// the products are 1,550 (an MMA with A in shared memory takes 83 cycles, with
+// A in tensor memory 69, of the 64 that M = 256 N = 128 K = 16 would need); the
+// rest are waits along the chain scores -> softmax -> value product.  Two row
+// tiles in one CTA (two streams with their own O and one score buffer each,
+// whose chain is as long as both streams' products) took 307 and 102 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

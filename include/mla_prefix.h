@@ -26,8 +26,8 @@
  * strides in elements and multiples of 8, asynchronous on `stream`, no
  * allocation, no host synchronisation, graph-capturable).  `status` is a
  * device int the kernels set (from 0, atomically); the calls never clear it;
- * mla_workspace_status() reads it.  Calls whose work overlaps on the GPU need
- * workspaces of their own.
+ * mla_workspace_status() reads it.  mla_prefix_attend calls whose work overlaps
+ * on the GPU need workspaces of their own.
  */
 #ifndef MLA_PREFIX_H_
 #define MLA_PREFIX_H_
@@ -37,10 +37,6 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
-
-/* Bytes of workspace mla_prefix_expand needs (0 without MLA_FLAG_KV_FP8, or
- * for invalid arguments).  Pure host arithmetic. */
-size_t mla_prefix_expand_workspace_size(int prefix_len, unsigned flags);
 
 /* Keys and values of a shared prefix.
  *   kv_cache, num_pages  as for mla_decode (FP8 rows with MLA_FLAG_KV_FP8)
@@ -58,13 +54,11 @@ size_t mla_prefix_expand_workspace_size(int prefix_len, unsigned flags);
  *                are not) sets *status to MLA_ERR_VALUE_RANGE
  *   head_rows    rows between heads, >= prefix_len, at most 2^30
  *   k_pe         bf16 [prefix_len, 64]: the rows' RoPE dims, copied
- *   workspace    16-byte aligned; NULL where none is needed
  *   status       also MLA_ERR_TIMEOUT if a bounded wait runs out
  * Sums are fp32, rounded once. */
 int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* block_table, int prefix_len,
                       const void* w_uk, const void* w_uv, int num_heads, unsigned flags, void* k_nope, void* v,
-                      int64_t head_rows, void* k_pe, void* workspace, size_t ws_bytes, int* status,
-                      mla_stream_t stream);
+                      int64_t head_rows, void* k_pe, int* status, mla_stream_t stream);
 
 /* Bytes of workspace mla_prefix_attend needs on the current device, 0 where no
  * head's rows are split over SMs; 0 and *err set on failure (err may be NULL).

@@ -51,7 +51,6 @@ from ._binding import (  # noqa: F401
     mla_prefix_attend,
     mla_prefix_attend_workspace_size,
     mla_prefix_expand,
-    mla_prefix_expand_workspace_size,
     mla_rope,
     mla_topk,
     mla_combine,
@@ -445,8 +444,7 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
 
 
 @_on_device
-def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=None, workspace=None, status=None,
-                  stream=None):
+def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=None, status=None, stream=None):
     """Per-head keys and values of a shared prefix, from its cached latents.
 
     kv_cache [num_pages, 64, 576] bf16 or uint8 [num_pages, 64, 656] FP8
@@ -454,10 +452,9 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
     [H, 512, 128] bf16 (as for `absorb_q` / `absorb_o`).  Returns (k_nope
     [H, R, 128] bf16, k_pe [R, 64] bf16, v [H, R, 128] fp16), by default new
     with R = prefix_len; `out` may hold them with any R >= prefix_len, whose
-    further rows are left as they are.  `workspace` (uint8, for an FP8 cache
-    only, mla_prefix_expand_workspace_size bytes) is allocated if not given.
-    `status` receives MLA_ERR_BAD_TABLE for a page outside the pool and
-    MLA_ERR_VALUE_RANGE for a key or value that is not finite once rounded.
+    further rows are left as they are.  `status` receives MLA_ERR_BAD_TABLE for
+    a page outside the pool and MLA_ERR_VALUE_RANGE for a key or value that is
+    not finite once rounded.
     """
     import torch
     dev = kv_cache.get_device()
@@ -482,18 +479,13 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
         raise ValueError("out: fewer rows than prefix_len")
     if prefix_len == 0:
         return out
-    need = mla_prefix_expand_workspace_size(prefix_len, flags)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    else:
-        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=dev)
     else:
         _tensor(status, "status", torch.int32, status.shape, dev)
     stream = _current_stream(dev)
     mla_prefix_expand(kv_cache, kv_cache.shape[0], block_table, prefix_len, w_uk, w_uv, H, flags, k_nope, v, R, k_pe,
-                      workspace, 0 if workspace is None else workspace.numel(), status, stream)
+                      status, stream)
     return out
 
 

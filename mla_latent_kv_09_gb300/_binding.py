@@ -60,9 +60,7 @@ SIGNATURES = {
                           _i64, _vp]),
     "mla_cache_append": (_c_int, [_vp, _i64, _vp, _i64, _vp, _f32, _vp, _f32, _vp, _vp, _c_int, _vp, _i64, _c_int,
                                   _c_int, _vp, _i64, _uint, _vp, _vp]),
-    "mla_prefix_expand_workspace_size": (_c_size, [_c_int, _uint]),
-    "mla_prefix_expand": (_c_int, [_vp, _i64, _vp, _c_int, _vp, _vp, _c_int, _uint, _vp, _vp, _i64, _vp, _vp, _c_size,
-                                   _vp, _vp]),
+    "mla_prefix_expand": (_c_int, [_vp, _i64, _vp, _c_int, _vp, _vp, _c_int, _uint, _vp, _vp, _i64, _vp, _vp, _vp]),
     "mla_prefix_attend_workspace_size": (_c_size, [_c_int, _c_int, _c_int, ctypes.POINTER(_c_int)]),
     "mla_prefix_attend": (_c_int, [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _c_int, _vp, _c_int, _c_int, _f32, _vp, _vp,
                                    _uint, _vp, _c_size, _vp, _vp, _vp, _vp]),
@@ -252,15 +250,11 @@ def mla_cache_append(latent, latent_stride: int, k_pe, k_pe_stride: int, norm_we
         _ptr(kv_cache), num_pages, flags, _ptr(status), _stream(stream)))
 
 
-def mla_prefix_expand_workspace_size(prefix_len: int, flags: int) -> int:
-    return load().mla_prefix_expand_workspace_size(prefix_len, flags)
-
-
 def mla_prefix_expand(kv_cache, num_pages: int, block_table, prefix_len: int, w_uk, w_uv, num_heads: int, flags: int,
-                      k_nope, v, head_rows: int, k_pe, workspace, ws_bytes: int, status, stream=None) -> None:
+                      k_nope, v, head_rows: int, k_pe, status, stream=None) -> None:
     _check("mla_prefix_expand", load().mla_prefix_expand(
         _ptr(kv_cache), num_pages, _ptr(block_table), prefix_len, _ptr(w_uk), _ptr(w_uv), num_heads, flags,
-        _ptr(k_nope), _ptr(v), head_rows, _ptr(k_pe), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)))
+        _ptr(k_nope), _ptr(v), head_rows, _ptr(k_pe), _ptr(status), _stream(stream)))
 
 
 def mla_prefix_attend_workspace_size(num_tokens: int, num_heads: int, prefix_len: int) -> int:

@@ -18,8 +18,7 @@
 //
 // Measured: 8192 rows x 128 heads 162 to 169 us (1.65 PFLOP/s; the rate falls
 // with the clock, which the power limit holds at 1.75 to 1.85 GHz), 537 MB
-// written at 3.2 TB/s, where writes alone reach 4.0; 1000 rows x 16 heads from
-// FP8 rows 10.9 us, two launches.  Not kept: the weights as A operand in tensor
+// written at 3.2 TB/s, where writes alone reach 4.0.  Not kept: the weights as A operand in tensor
 // memory (69 cycles an MMA against 83, but dims come out as rows and have to be
 // transposed on their way: 197 us with 4-byte stores, 253 with shuffles, 263
 // through shared memory).
@@ -30,9 +29,17 @@
 //              at a time; keys and values by four warps each
 //   warp 10    copies the RoPE dims and checks the block table
 //
-// FP8 rows are first widened to bf16 in the workspace (exactly: 4 significant
-// bits and a power of two) by a kernel of their own, a warp a row: the product
-// then reads them as a cache of consecutive pages.
+//   warps 12-19  (FP8 cache only) widen the latents: TMA brings a chunk's codes
+//              into the upper half of its slot, bf16 replaces them
+//
+// FP8 rows are widened on their way into shared memory (exactly: 4 significant
+// bits and a power of two), by every pair for every head, so that a prefix needs
+// one launch and no workspace.  Against a kernel that widens the prefix once, in
+// a workspace, for the bf16 product: 100 rows x 16 heads 8.2 / 9.0 us, 1000 x 16
+// 10.0 / 10.9 (and 8 us less of the host's time), 4000 x 64 57.6 / 52.3, 8192 x
+// 128 205 / 165: there the widening, 890 cycles a chunk, holds up the products'
+// 690.  Not kept: four warps 274 us, six or three warps with a chunk each 277
+// and 375, the next chunk's codes read ahead 322, integer widening 219.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -59,21 +66,22 @@ constexpr int kSlots = 6;
 constexpr int kOffW = 0;
 constexpr int kOffRing = kStages * kChunk;                // 128 KiB
 constexpr int kOffBar = kOffRing + kSlots * kChunk;       // 224 KiB
-constexpr int kNumBars = 2 * kSlots + 2 * kStages + 4 + 3;
+constexpr int kNumBars = 3 * kSlots + 2 * kStages + 4 + 3;
 constexpr int kSlack = 1024;                 // re-aligned to 1024 B (128-byte swizzle atoms)
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr int kThreads = 384;
-constexpr int kIssuerB = 11;
+constexpr int kConverters = 8;               // further warps, FP8 cache only: two groups of four
+static_assert(kSlots % 2 == 0, "a slot's chunks are one group's");
+constexpr int kThreadsFp8 = kThreads + 32 * kConverters;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = idesc_bf16(256, 256, 1);
 
 struct ExpandParams {
-  const uint8_t* cache;      // the pool (RoPE dims)
+  const uint8_t* cache;      // the pool (RoPE dims, FP8 rows)
   int row_bytes, rope_byte;  // of a pool row
   long long num_pages;
   const int* block_table;
-  int paged;                 // the latents come from the pool's pages (else row by row)
   int prefix_len, num_heads;
   uint16_t* k_nope;
   uint16_t* v;
@@ -82,7 +90,17 @@ struct ExpandParams {
   int* status;
 };
 
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+// Arrives at a barrier of either CTA of the pair with release semantics for
+// this CTA only: what was written is in this CTA's shared memory, and this SM's
+// own tensor core reads it; the other CTA's thread only issues.  (A release for
+// the cluster waits for far more: 2,150 cycles a chunk against 1,180 with four
+// warps.)
+__device__ __forceinline__ void arrive_cta(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1) __cluster_dims__(2, 1, 1)
 mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_constant__ CUtensorMap tm_lat,
                          const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -105,18 +123,21 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
   auto w_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + kStages + s); };
   auto acc_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + s); };
   auto acc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 2 + s); };
+  auto raw_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 4 + s); };  // codes (FP8 cache)
   auto turn = [&](uint32_t issuer) { return bar0 + 8u * (kNumBars - 3 + issuer); };
   const uint32_t bar_drain = bar0 + 8u * (kNumBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar0 + 8u * i, 1);
+    for (uint32_t i = kFp8 ? kSlots : 0; i < kNumBars; ++i) mbar_init(bar0 + 8u * i, 1);
     for (uint32_t s = 0; s < 2; ++s) {
       mbar_init(acc_full(s), 2);    // both issuers
       mbar_init(acc_empty(s), 16);  // the drain warps of both CTAs
     }
     mbar_init(bar_drain, 2);  // both issuers
+    if (kFp8)
+      for (uint32_t s = 0; s < kSlots; ++s) mbar_init(a_full(s), kConverters);  // a group of each CTA
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -150,13 +171,12 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         // the tile's two pages; a page that is not there reads as zeros
-        int y[2], z[2];
+        int z[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int pg = (m * 2 + static_cast<int>(rank)) * 2 + e;
-          const int id = p.paged && pg < pages ? p.block_table[pg] : -1;
-          y[e] = p.paged ? 0 : pg * kPage;
-          z[e] = !p.paged ? 0 : (id >= 0 && id < p.num_pages ? id : static_cast<int>(p.num_pages));
+          const int id = pg < pages ? p.block_table[pg] : -1;
+          z[e] = id >= 0 && id < p.num_pages ? id : static_cast<int>(p.num_pages);
         }
         const bool new_head = i == 0 || m == 0;
         for (uint32_t k = 0; ok && k < kStages; ++k, ++chunk) {
@@ -169,10 +189,16 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
           }
           const uint32_t s = chunk % kSlots;
           if (chunk >= kSlots && !(ok = wait<true>(a_empty(s), ((chunk / kSlots) - 1) & 1, ctl))) break;
-          if (rank == 0) mbar_arrive_expect_tx(a_full(s), 2 * kChunk);
           const uint32_t dst = sbase + kOffRing + s * kChunk;
-          tma_load_3d_pair(dst, &tm_lat, 64 * k, y[0], z[0], ra + 8u * s);
-          tma_load_3d_pair(dst + kChunk / 2, &tm_lat, 64 * k, y[1], z[1], ra + 8u * s);
+          if (kFp8) {  // codes, for this CTA's own converters
+            mbar_arrive_expect_tx(raw_full(s), kChunk / 2);
+            tma_load_3d(dst + kChunk / 2, &tm_lat, 64 * k, 0, z[0], raw_full(s));
+            tma_load_3d(dst + kChunk / 2 + kChunk / 4, &tm_lat, 64 * k, 0, z[1], raw_full(s));
+            continue;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(a_full(s), 2 * kChunk);
+          tma_load_3d_pair(dst, &tm_lat, 64 * k, 0, z[0], ra + 8u * s);
+          tma_load_3d_pair(dst + kChunk / 2, &tm_lat, 64 * k, 0, z[1], ra + 8u * s);
         }
         if (new_head) ++heads;
         if (++m == tiles) {
@@ -188,7 +214,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == kIssuerB) {
+  } else if (warp == 1 || warp == 11) {
     if (rank == 0) {
       // Two warps issue, stages of 64 latent dims (512 cycles of products) in
       // turns, all into the tile's accumulator: between its four MMAs and its
@@ -292,6 +318,72 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
         ++h;
       }
     }
+  } else if (kFp8 && warp >= kThreads / 32) {
+    // Latents from FP8 rows: a chunk's codes (8 KiB) land in the upper half of
+    // its slot, each thread of four warps takes 4 x 16 of them (4 lanes a row, 8
+    // rows of the warp's 32 at a time), and when all have, bf16 replaces them.
+    // That is 1,180 cycles a chunk, most of them latency beside the MMAs' reads
+    // of shared memory; two groups of warps, each with every second chunk
+    // (always of the same slots, so that it sees all their phases), hide it.
+    const uint32_t g = static_cast<uint32_t>(warp - kThreads / 32) >> 2;
+    const int w = warp & 3, sub = lane >> 2, u = lane & 3;
+    const uint32_t ra = mapa(a_full(0), 0);
+    const uint32_t in = sbase + kOffRing + kChunk / 2 + static_cast<uint32_t>(32 * w) * 64u + static_cast<uint32_t>(lane) * 16u;
+    // the lane's two 16-byte pieces of a row, swizzled (the row's number modulo 8 is sub)
+    const uint32_t out = sbase + kOffRing + static_cast<uint32_t>(32 * w + sub) * 128u;
+    const uint32_t c0 = static_cast<uint32_t>((2 * u) ^ sub) << 4, c1 = static_cast<uint32_t>((2 * u + 1) ^ sub) << 4;
+    // the four groups' scales of the thread's rows in tile m (what is not there reads as zeros)
+    auto load_scales = [&](int m, uint32_t (&scales)[4]) {
+      const int row0 = (m * 2 + static_cast<int>(rank)) * kRows + 32 * w;
+      const long long page = row0 < p.prefix_len ? p.block_table[row0 / kPage] : -1;
+      const int rows = page >= 0 && page < p.num_pages ? p.prefix_len - row0 - sub : 0;
+      const uint8_t* src = p.cache + ((rows > 0 ? page * kPage : 0) + row0 % kPage + sub) * kFp8Row + kLatent;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) scales[r] = 8 * r < rows ? *reinterpret_cast<const uint32_t*>(src + 8 * r * kFp8Row) : 0u;
+    };
+    uint32_t chunk = g, next[4];
+    int m = m0;
+    bool ok = true;
+    if (n > 0) load_scales(m, next);
+    for (int i = 0; ok && i < n; ++i) {
+      uint32_t scales[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) scales[r] = next[r];
+      if (++m == tiles) m = 0;
+      if (i + 1 < n) load_scales(m, next);
+#pragma unroll 1
+      for (int k = 0; k < kStages; k += 2, chunk += 2) {
+        const uint32_t s = chunk % kSlots;
+        ok = warp_wait_uniform(raw_full(s), (chunk / kSlots) & 1, ctl);
+        uint4 code[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) code[r] = ld_shared_v4u(in + s * kChunk + 512u * r);
+        ok = named_bar_all(1 + g, 128, ok);  // all codes are in registers (and votes: a wait that ran out ends the four)
+        if (!ok) break;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          // 2^(e - 127); the scale byte 0 is 2^-127, 255 is NaN
+          const uint32_t e = (scales[r] >> (4 * k)) & 255u;
+          const float scale = __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
+          const uint32_t words[4] = {code[r].x, code[r].y, code[r].z, code[r].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t h2;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(words[j >> 1] >> (16 * (j & 1)))));
+            float a, b;
+            asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}" : "=f"(a), "=f"(b) : "r"(h2));
+            o[j] = pack_bf16x2(a * scale, b * scale);
+          }
+          const uint32_t dst = out + s * kChunk + 1024u * r;
+          st_shared_v4(dst + c0, o[0], o[1], o[2], o[3]);
+          st_shared_v4(dst + c1, o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_cta(ra + 8u * s);
+      }
+    }
   } else {
     // RoPE dims, 8 lanes a row, and the pages' check, over the whole grid
     for (long long r = blockIdx.x * 4ll + (lane >> 3); r < p.prefix_len; r += gridDim.x * 4ll) {
@@ -311,38 +403,6 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
-}
-
-// FP8 rows to bf16: lane l takes the 16 codes of dims [16 l, 16 l + 16).
-__global__ void __launch_bounds__(256) mla_prefix_widen_kernel(const __grid_constant__ ExpandParams p, uint16_t* out) {
-  const long long r = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  grid_dependency_wait();
-  if (r >= p.prefix_len) return;
-  const long long page = p.block_table[r / kPage];
-  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-  if (page >= 0 && page < p.num_pages) {
-    const uint8_t* row = p.cache + (page * kPage + r % kPage) * kFp8Row;
-    const uint4 c = *reinterpret_cast<const uint4*>(row + 16 * lane);
-    const uint32_t e = row[kLatent + lane / 8];
-    // 2^(e - 127); the scale byte 0 is 2^-127, 255 is NaN
-    const float scale = __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
-    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t h2;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(in[i >> 1] >> (16 * (i & 1)))));
-      float a, b;
-      asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}" : "=f"(a), "=f"(b) : "r"(h2));
-      w[i] = pack_bf16x2(a * scale, b * scale);
-    }
-    lo = make_uint4(w[0], w[1], w[2], w[3]);
-    hi = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-  uint4* dst = reinterpret_cast<uint4*>(out + r * kLatent + 16 * lane);
-  dst[0] = lo;
-  dst[1] = hi;
 }
 
 // ============================================================ host side
@@ -367,8 +427,10 @@ int expand_device_ready(int* sms) {
       st.status = MLA_ERR_DEVICE;
       return;
     }
-    if (cudaFuncSetAttribute(mla_prefix_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
-        cudaSuccess) {
+    if (cudaFuncSetAttribute(mla_prefix_expand_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(mla_prefix_expand_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            cudaSuccess) {
       cudaGetLastError();
       st.status = MLA_ERR_CUDA;
     }
@@ -385,6 +447,20 @@ bool encode_weight(CUtensorMap* m, const void* base, int heads) {
   return encode(m, false, 2, base, size, strides, box);
 }
 
+// Latents as {dim, row of a page, page} of the pool, boxes of 64 dims of a page's
+// rows: bf16, swizzled as the MMA takes them, or codes, as they are.
+bool encode_latents(CUtensorMap* m, const void* base, int64_t num_pages, bool fp8) {
+  const cuuint64_t row = fp8 ? kFp8Row : 2 * kDqk;
+  const cuuint64_t size[3] = {fp8 ? cuuint64_t{kLatent} : cuuint64_t{kDqk}, kPage, static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t strides[2] = {row, row * kPage};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(kPage), 1u}, one[3] = {1, 1, 1};
+  if (!fp8) return encode(m, false, 3, base, size, strides, box);
+  EncodeTiledFn fn = encode_tiled();
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), size, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 }  // namespace mla
 
@@ -392,28 +468,19 @@ using namespace mla;
 
 extern "C" {
 
-size_t mla_prefix_expand_workspace_size(int prefix_len, unsigned flags) {
-  if (prefix_len < 1 || !(flags & MLA_FLAG_KV_FP8)) return 0;
-  return static_cast<size_t>(prefix_len) * kLatent * 2;
-}
-
 int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* block_table, int prefix_len,
                       const void* w_uk, const void* w_uv, int num_heads, unsigned flags, void* k_nope, void* v,
-                      int64_t head_rows, void* k_pe, void* workspace, size_t ws_bytes, int* status,
-                      mla_stream_t stream) {
+                      int64_t head_rows, void* k_pe, int* status, mla_stream_t stream) {
   if (!kv_cache || !block_table || !w_uk || !w_uv || !k_nope || !v || !k_pe || !status) return MLA_ERR_INVALID_ARG;
   if (!al(kv_cache, 16) || !al(block_table, 4) || !al(w_uk, 16) || !al(w_uv, 16) || !al(k_nope, 16) || !al(v, 16) ||
-      !al(k_pe, 16) || !al(workspace, 16) || !al(status, 4))
+      !al(k_pe, 16) || !al(status, 4))
     return MLA_ERR_INVALID_ARG;
   if (num_pages < 1 || prefix_len < 0 || head_rows < prefix_len) return MLA_ERR_INVALID_ARG;
   if (flags & ~static_cast<unsigned>(MLA_FLAG_KV_FP8)) return MLA_ERR_INVALID_ARG;
   if (num_heads < 1 || num_heads > kHeads) return MLA_ERR_UNSUPPORTED;
   if (num_pages > (INT32_MAX / kPage) - 1 || head_rows > kMaxRows) return MLA_ERR_UNSUPPORTED;
-  const size_t need = mla_prefix_expand_workspace_size(prefix_len, flags);
-  if (need > 0 && !workspace) return MLA_ERR_INVALID_ARG;
-  if (ws_bytes < need) return MLA_ERR_WORKSPACE;
   int sms = 0;
-  int rc = expand_device_ready(&sms);
+  const int rc = expand_device_ready(&sms);
   if (rc != MLA_OK) return rc;
   if (prefix_len == 0) return MLA_OK;
   const bool fp8 = (flags & MLA_FLAG_KV_FP8) != 0;
@@ -423,7 +490,6 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
   p.rope_byte = fp8 ? 528 : 2 * kLatent;
   p.num_pages = num_pages;
   p.block_table = block_table;
-  p.paged = !fp8;
   p.prefix_len = prefix_len;
   p.num_heads = num_heads;
   p.k_nope = static_cast<uint16_t*>(k_nope);
@@ -431,25 +497,14 @@ int mla_prefix_expand(const void* kv_cache, int64_t num_pages, const int32_t* bl
   p.head_rows = head_rows;
   p.k_pe = static_cast<uint16_t*>(k_pe);
   p.status = status;
-  // latents: {dim, row of a page, page} of the pool, or {dim, row, 1} of the widened rows
   CUtensorMap lat, wk, wv;
-  const cuuint64_t size[3] = {fp8 ? cuuint64_t{kLatent} : cuuint64_t{kDqk},
-                              fp8 ? static_cast<cuuint64_t>(prefix_len) : cuuint64_t{kPage},
-                              fp8 ? cuuint64_t{1} : static_cast<cuuint64_t>(num_pages)};
-  const cuuint64_t row = (fp8 ? kLatent : kDqk) * 2;
-  const cuuint64_t strides[2] = {row, row * size[1]};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(kPage), 1u};
-  if (!encode(&lat, false, 3, fp8 ? workspace : kv_cache, size, strides, box) || !encode_weight(&wk, w_uk, num_heads) ||
+  if (!encode_latents(&lat, kv_cache, num_pages, fp8) || !encode_weight(&wk, w_uk, num_heads) ||
       !encode_weight(&wv, w_uv, num_heads))
     return MLA_ERR_CUDA;
-  if (fp8) {
-    rc = launch_dependent(mla_prefix_widen_kernel, dim3((prefix_len + 7) / 8), dim3(256), 0, 1, stream, p,
-                          static_cast<uint16_t*>(workspace));
-    if (rc != MLA_OK) return rc;
-  }
   const long long items = static_cast<long long>((prefix_len + 2 * kRows - 1) / (2 * kRows)) * num_heads;
   const int pairs = static_cast<int>(items < sms / 2 ? items : sms / 2);
-  return launch_dependent(mla_prefix_expand_kernel, dim3(2 * pairs), dim3(kThreads), kSmem, 1, stream, p, lat, wk, wv);
+  return launch_dependent(fp8 ? mla_prefix_expand_kernel<true> : mla_prefix_expand_kernel<false>, dim3(2 * pairs),
+                          dim3(fp8 ? kThreadsFp8 : kThreads), kSmem, 1, stream, p, lat, wk, wv);
 }
 
 }  // extern "C"

@@ -63,22 +63,15 @@ def test_append_checks_its_arguments(lib):
 
 
 #         cache pages bt  P   wk  wv  H  fl k   v   rows kpe ws bytes status stream
-EXPAND = [OK, 10, OK, 100, OK, OK, 16, 0, OK, OK, 100, OK, None, 0, OK, None]
+EXPAND = [OK, 10, OK, 100, OK, OK, 16, 0, OK, OK, 100, OK, OK, None]
 
 
 def test_expand_checks_its_arguments(lib):
     check(lib.mla_prefix_expand, EXPAND,
-          [(0, None), (2, None), (4, None), (5, None), (8, None), (9, None), (11, None), (14, None), (0, OK + 8),
-           (4, OK + 8), (5, OK + 2), (8, OK + 8), (9, OK + 8), (11, OK + 8), (12, OK + 8), (14, OK + 1), (1, 0),
+          [(0, None), (2, None), (4, None), (5, None), (8, None), (9, None), (11, None), (12, None), (0, OK + 8),
+           (4, OK + 8), (5, OK + 2), (8, OK + 8), (9, OK + 8), (11, OK + 8), (12, OK + 1), (1, 0),
            (3, -1), (3, 101), (7, 1), (7, 32)], m.MLA_ERR_INVALID_ARG)
     check(lib.mla_prefix_expand, EXPAND, [(6, 0), (6, 129), (1, 1 << 40)], m.MLA_ERR_UNSUPPORTED)
-    need = m.mla_prefix_expand_workspace_size(100, m.MLA_FLAG_KV_FP8)
-    assert need >= 100 * 512 * 2 and m.mla_prefix_expand_workspace_size(100, 0) == 0
-    a = list(EXPAND)
-    a[7] = m.MLA_FLAG_KV_FP8
-    assert lib.mla_prefix_expand(*a) == m.MLA_ERR_INVALID_ARG  # no workspace
-    a[12], a[13] = OK, need - 1
-    assert lib.mla_prefix_expand(*a) == m.MLA_ERR_WORKSPACE
 
 
 #         qn  qp        qs  k   v  rows kpe  P  vis  T   H  scale so    sl   fl ws  bytes  out lse status stream

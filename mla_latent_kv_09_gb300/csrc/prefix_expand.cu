@@ -36,7 +36,7 @@
 // bits and a power of two), by every pair for every head, so that a prefix needs
 // one launch and no workspace.  Against a kernel that widens the prefix once, in
 // a workspace, for the bf16 product: 100 rows x 16 heads 8.2 / 9.0 us, 1000 x 16
-// 10.0 / 10.9 (and 8 us less of the host's time), 4000 x 64 57.6 / 52.3, 8192 x
+// 9.3 to 10.0 / 10.9 (and 9 us less of the host's time), 4000 x 64 57.6 / 52.3, 8192 x
 // 128 205 / 165: there the widening, 890 cycles a chunk, holds up the products'
 // 690.  Not kept: four warps 274 us, six or three warps with a chunk each 277
 // and 375, the next chunk's codes read ahead 322, integer widening 219.

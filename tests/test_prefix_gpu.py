@@ -144,6 +144,32 @@ def test_pages_outside_the_pool_and_values_outside_fp16_are_reported(fp8):
     assert_expanded(out[0][:2], out[1], out[2][:2], lat, pe, w_uk[:2], w_uv[:2])
 
 
+def test_fp8_scales_of_every_size_and_codes_that_are_no_numbers():
+    """Scales from 2^-27 to 2^23 (and 2^-127: next to nothing); a NaN code or a
+    NaN scale makes its row's keys and values NaN, and no other's."""
+    P, H = 300, 2
+    kv, bt, lat, _ = cache_and_rows(P, True, seed=12)
+    table = bt.cpu().numpy()
+    place = lambda p: (int(table[p // 64]), p % 64)  # noqa: E731
+    g = torch.Generator(device="cuda").manual_seed(13)
+    kv[..., 512:516] = torch.randint(100, 151, kv[..., 512:516].shape, generator=g, device="cuda").to(torch.uint8)
+    kv[place(70)][512:516] = 0
+    kv[place(5)][300] = 0x7f
+    kv[place(64)][17] = 0xff
+    kv[place(299)][514] = 255
+    bad, tiny = [5, 64, 299], 70
+    rows = [p for p in range(P) if p not in bad and p != tiny]
+    w_uk, w_uv = rand((H, 512, 128), 14) * 2.0 ** -30, rand((H, 512, 128), 15) * 2.0 ** -24
+    status = status_word()
+    k_nope, k_pe, v = m.prefix_expand(kv, bt, P, w_uk, w_uv, status=status)
+    assert int(status) == m.MLA_ERR_VALUE_RANGE
+    assert bool(k_nope[:, bad].isnan().all()) and bool(v[:, bad].isnan().all())
+    assert float(k_nope[:, tiny].abs().max()) < 1e-30 and not v[:, tiny].any()
+    flat = oracle.fp8_rows_to_f64(kv.cpu().numpy().reshape(-1, 656))
+    held = flat[[table[p // 64] * 64 + p % 64 for p in range(P)]]
+    assert_expanded(k_nope, k_pe, v, held[:, :512], held[:, 512:], w_uk, w_uv, rows)
+
+
 def test_keys_that_are_not_finite_are_reported():
     kv, bt, lat, pe = cache_and_rows(200, False, 4)
     w_uk, w_uv = rand((2, 512, 128), 1), rand((2, 512, 128), 2)

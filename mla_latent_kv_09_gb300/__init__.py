@@ -275,43 +275,21 @@ def _tensor(t, name: str, dtype, shape, device, contiguous: bool = True):
                          f"{list(t.shape)} on {t.device}, strides {list(t.stride())}")
 
 
-def _on_device(fn):
-    """Runs fn with its first argument's device current and, where `stream` is
-    given (a torch stream, or its raw handle), with that stream current: the
-    kernels are launched there, and what the call allocates belongs to it."""
-    import functools
-
-    name = fn.__code__.co_varnames[0]
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        import torch
-        first = args[0] if args else kw.get(name)
-        if first is None:
-            raise TypeError(f"{fn.__name__}: missing argument {name}")
-        index = first.get_device()  # -1: not on a GPU
-        if stream is None and index >= 0 and index == torch.cuda.current_device():
-            return fn(*args, **kw)
-        dev = first.device
-        if dev.type != "cuda":
-            raise ValueError(f"{fn.__name__}: expected tensors on a GPU, got {dev}")
-        if stream is None:
-            with torch.cuda.device(dev):
-                return fn(*args, **kw)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        if stream.device != dev:
-            raise ValueError(f"{fn.__name__}: a stream of {stream.device} for tensors of {dev}")
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
-def _current_stream(device: int) -> int:
-    """Raw handle of the current stream (torch.cuda.current_stream builds a
-    stream object for it, twenty times as long)."""
+def _elsewhere(first, stream, name: str):
+    """What has to be entered for a call on first's device and on `stream` (a
+    torch stream, or its raw handle): with that stream current the kernels are
+    launched there, and what the call allocates belongs to it."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device)
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: expected tensors on a GPU, got {dev}")
+    if stream is None:
+        return torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"{name}: a stream of {stream.device} for tensors of {dev}")
+    return torch.cuda.stream(stream)
 
 
 def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.0, yarn: float = 1.0,
@@ -348,7 +326,6 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.
     return inv.to(device), factor
 
 
-@_on_device
 def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse: bool = False, scale: float = 1.0,
          out=None, stream=None):
     """Rotary positions over part of each head.
@@ -364,6 +341,9 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
     """
     import torch
     dev = x.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(x, stream, "rope"):
+            return rope(x, positions, inv_freq, offset=offset, half=half, inverse=inverse, scale=scale, out=out)
     T, H, D = x.shape
     _tensor(x, "x", torch.bfloat16, (T, H, D), dev, contiguous=False)
     _tensor(positions, "positions", torch.int32, (T,), dev)
@@ -375,7 +355,8 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
         _tensor(out, "out", torch.bfloat16, (T, H, D), dev, contiguous=False)
     if T == 0 or H == 0:
         return out
-    stream = _current_stream(dev)
+    # (torch.cuda.current_stream builds a stream object, twenty times as long)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     # (the stride of a dim of one says nothing)
     mla_rope(x, x.stride(0) if T > 1 else 0, x.stride(1) if H > 1 else 0, positions, T, H, D, offset, 2 * R2, inv_freq,
              scale, (MLA_FLAG_ROPE_HALF if half else 0) | (MLA_FLAG_ROPE_INVERSE if inverse else 0), out,
@@ -392,7 +373,6 @@ def _cache_flags(kv_cache, device) -> int:
     return 0
 
 
-@_on_device
 def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=None, norm_weight=None,
                  eps: float = 1e-6, inv_freq=None, half: bool = False, rope_scale: float = 1.0, status=None,
                  stream=None):
@@ -413,6 +393,11 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
     """
     import torch
     dev = latent.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(latent, stream, "cache_append"):
+            return cache_append(latent, k_pe, kv_cache, block_table, positions, request_ids=request_ids,
+                                norm_weight=norm_weight, eps=eps, inv_freq=inv_freq, half=half, rope_scale=rope_scale,
+                                status=status)
     T = latent.shape[0]
     _tensor(latent, "latent", torch.bfloat16, (T, D_V), dev, contiguous=False)
     _tensor(k_pe, "k_pe", torch.bfloat16, (T, D_QK - D_V), dev, contiguous=False)
@@ -436,14 +421,13 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
     bt_stride = block_table.stride(0) if B > 1 else width
     if bt_stride < width:
         raise ValueError("block_table: its rows overlap")
-    stream = _current_stream(dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     mla_cache_append(latent, latent.stride(0) if T > 1 else D_V, k_pe, k_pe.stride(0) if T > 1 else D_QK - D_V,
                      norm_weight, eps, inv_freq, rope_scale, positions, request_ids, T, block_table, bt_stride, width,
                      B, kv_cache, kv_cache.shape[0], flags | (MLA_FLAG_ROPE_HALF if half else 0), status, stream)
     return kv_cache
 
 
-@_on_device
 def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=None, status=None, stream=None):
     """Per-head keys and values of a shared prefix, from its cached latents.
 
@@ -458,6 +442,9 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
     """
     import torch
     dev = kv_cache.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(kv_cache, stream, "prefix_expand"):
+            return prefix_expand(kv_cache, block_table, prefix_len, w_uk, w_uv, out=out, status=status)
     flags = _cache_flags(kv_cache, dev)
     pages, = block_table.shape
     _tensor(block_table, "block_table", torch.int32, (pages,), dev)
@@ -483,13 +470,12 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
         status = torch.zeros(1, dtype=torch.int32, device=dev)
     else:
         _tensor(status, "status", torch.int32, status.shape, dev)
-    stream = _current_stream(dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     mla_prefix_expand(kv_cache, kv_cache.shape[0], block_table, prefix_len, w_uk, w_uv, H, flags, k_nope, v, R, k_pe,
                       status, stream)
     return out
 
 
-@_on_device
 def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix_len: int | None = None, visible=None,
                   suffix_out=None, suffix_lse=None, out_fp32: bool = False, out=None, lse=None, workspace=None,
                   status=None, stream=None):
@@ -509,6 +495,11 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
     """
     import torch
     dev = q_nope.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(q_nope, stream, "prefix_attend"):
+            return prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale, prefix_len=prefix_len, visible=visible,
+                                 suffix_out=suffix_out, suffix_lse=suffix_lse, out_fp32=out_fp32, out=out, lse=lse,
+                                 workspace=workspace, status=status)
     T, H, _ = q_nope.shape
     _tensor(q_nope, "q_nope", torch.bfloat16, (T, H, 128), dev, contiguous=False)
     _tensor(q_pe, "q_pe", torch.bfloat16, (T, H, 64), dev, contiguous=False)
@@ -551,7 +542,7 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
         status = torch.zeros(1, dtype=torch.int32, device=dev)
     else:
         _tensor(status, "status", torch.int32, status.shape, dev)
-    stream = _current_stream(dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     mla_prefix_attend(q_nope, q_pe, q_stride, k_nope, v, R, k_pe, prefix_len, visible, T, H, softmax_scale,
                       suffix_out, suffix_lse, MLA_FLAG_OUT_FP32 if out_fp32 else 0, workspace,
                       0 if workspace is None else workspace.numel(), out, lse, status, stream)

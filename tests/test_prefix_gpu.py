@@ -206,6 +206,34 @@ def test_rows_and_pages_beyond_32_bit_offsets():
                         heads=np.array([0, H - 1]))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_expansion_captured_replayed_and_beside_another(fp8):
+    """A replay reads the cache as it is then; two calls at once on two streams
+    do not disturb each other."""
+    P, H = 500, 8
+    kv, bt, _, _ = cache_and_rows(P, fp8, 21)
+    kv2, bt2, _, _ = cache_and_rows(P, fp8, 22)
+    w_uk, w_uv = rand((H, 512, 128), 5) / 16, rand((H, 512, 128), 6) / 16
+    first, second = m.prefix_expand(kv, bt, P, w_uk, w_uv), m.prefix_expand(kv2, bt2, P, w_uk, w_uv)
+    status = status_word()
+    out = tuple(torch.empty_like(t) for t in first)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        m.prefix_expand(kv, bt, P, w_uk, w_uv, out=out, status=status)
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        beside = m.prefix_expand(kv2, bt2, P, w_uk, w_uv, stream=side)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, first)) and all(torch.equal(x, y) for x, y in zip(beside, second))
+    kv.copy_(kv2)
+    bt.copy_(bt2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, second)) and int(status) == 0
+
+
 def test_expansion_refusals():
     kv, bt, _, _ = cache_and_rows(70, False, 1)
     w = rand((2, 512, 128), 1)

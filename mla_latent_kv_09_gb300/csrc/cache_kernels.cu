@@ -4,8 +4,9 @@
 // Both are streams: every element is read once and written once, a few
 // operations each, so HBM bounds the long calls and launch latency the short
 // ones.  Measured: rotation of 8192 tokens x 128 heads x 192 dims 117.6 us (805
-// MB at 6.85 TB/s, a copy's rate), 1332 x 64 x 128 7.8 us (44 MB, 5.6 TB/s), 64 x
-// 128 x 64 2.0 us; append of 8192 tokens 5.4 us (19 MB), of 64 tokens 2.5 us.
+// MB at 6.85 TB/s, a copy's rate; half layout 122), 1332 x 64 x 128 in the half
+// layout 6.7 us where the rows lie in L2, 9.9 from the HBM (44 MB), 64 x 128 x 64
+// 2.0 us; append of 8192 tokens 5.4 us (19 MB), of 64 tokens 2.5 us.
 //
 // Angles.  Pair i at position p turns by p * f_i radians.  In fp32 that loses
 // the angle at far positions (at p = 2^20 one ulp is 1/16 radian), and fp64
@@ -65,14 +66,18 @@ struct RopeParams {
 };
 
 // One CTA: one token, its heads in turns of per_turn * kRopeItems.  A unit is
-// 8 contiguous dims: 4 interleaved pairs, or (half layout) 8 dims and their
-// 8 partners, or 8 copied dims; a warp's units are neighbours in memory.  A
-// thread keeps one unit for all its heads: its cosines and sines stay in
-// registers, and nothing is divided in the loop.  The first turn's loads are
-// issued before the angles are computed (once a token, through shared
-// memory), which hides sincospif and the position's load behind them.
+// 8 contiguous dims: 4 interleaved pairs, or 8 copied dims; a warp's units are
+// neighbours in memory.  A thread keeps one unit for all its heads: its cosines
+// and sines stay in registers, and nothing is divided in the loop.  In the half
+// layout a unit's 8 dims need their 8 partners: there the two threads of a unit
+// and its partner's each take both for half of the heads, so that every thread
+// has the same four loads in flight (a thread with two loads a head and its
+// copying neighbours with one: 8192 tokens x 128 heads x 192 dims 168 us
+// instead of 122).  The first turn's loads are issued before the angles are
+// computed (once a token, through shared memory), which hides sincospif and the
+// position's load behind them.
 template <bool kHalf>
-__global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kHalf ? 4 : 5) mla_rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 cs[MLA_MAX_ROPE_DIM / 2];
   const int t = blockIdx.x;
   const bool wide = p.units > kRopeThreads;  // a head is more than a CTA: units in blocks of kRopeThreads
@@ -80,23 +85,25 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
   const int h0 = wide ? 0 : threadIdx.x / p.units;
   const bool mine = wide ? u < p.units : h0 < p.per_turn;
   const int before = p.copy ? p.offset / 8 : 0;     // copied units ahead of the rotated ones
-  const int turned = kHalf ? p.rope / 16 : p.rope / 8;
   const int r = u - before;
-  const bool turns = r >= 0 && r < turned;
-  const int dim = turns ? p.offset + 8 * r : (r < 0 ? 8 * u : p.offset + p.rope + 8 * (r - turned));
-  const int pair = turns ? (kHalf ? 8 * r : 4 * r) : 0;
+  const bool turns = r >= 0 && r < p.rope / 8;
+  const int second = kHalf && turns && r >= p.rope / 16 ? 1 : 0;  // takes the second half of the heads
+  const int unit = second ? r - p.rope / 16 : r;
+  const int dim = turns ? p.offset + 8 * unit : (r < 0 ? 8 * u : p.offset + p.rope + 8 * (r - p.rope / 8));
+  const int pair = turns ? (kHalf ? 8 * unit : 4 * unit) : 0;
   const int step = p.per_turn * kRopeItems;
   grid_dependency_wait();
   const uint16_t* src = p.x + t * p.x_ts + dim;
   uint16_t* dst = p.out + t * p.out_ts + dim;
-  uint4 a[kRopeItems], b[kRopeItems];
+  const bool both = kHalf && turns;  // items are a unit and its partner of two heads, not a unit of four
+  uint4 v[kRopeItems] = {};
+  auto head = [&](int base, int i) { return base + h0 + (both ? 2 * second + (i >> 1) : i) * p.per_turn; };
   auto load = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kRopeItems; ++i) {
-      const int h = base + h0 + i * p.per_turn;
+      const int h = head(base, i);
       if (!mine || h >= p.heads) continue;
-      a[i] = *reinterpret_cast<const uint4*>(src + h * p.x_hs);
-      if (kHalf && turns) b[i] = *reinterpret_cast<const uint4*>(src + h * p.x_hs + p.rope / 2);
+      v[i] = *reinterpret_cast<const uint4*>(src + h * p.x_hs + (both && (i & 1) ? p.rope / 2 : 0));
     }
   };
   int base = blockIdx.y * step;
@@ -109,31 +116,35 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
   for (int j = 0; j < (kHalf ? 8 : 4); ++j) c[j] = cs[pair + j];
 #pragma unroll 1
   while (base < p.heads) {
+    if (kHalf && turns) {
 #pragma unroll
-    for (int i = 0; i < kRopeItems; ++i) {
-      const int h = base + h0 + i * p.per_turn;
-      if (!mine || h >= p.heads) continue;
-      if (turns) {
-        uint32_t* x = reinterpret_cast<uint32_t*>(&a[i]);
-        if (kHalf) {
-          uint32_t* y = reinterpret_cast<uint32_t*>(&b[i]);
+      for (int i = 0; i < kRopeItems; i += 2) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(&v[i]);
+        uint32_t* y = reinterpret_cast<uint32_t*>(&v[i + 1]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 c0 = c[2 * j], c1 = c[2 * j + 1];
-            const float x0 = lo_f(x[j]), x1 = hi_f(x[j]), y0 = lo_f(y[j]), y1 = hi_f(y[j]);
-            x[j] = pack_bf16x2(x0 * c0.x - y0 * c0.y, x1 * c1.x - y1 * c1.y);
-            y[j] = pack_bf16x2(x0 * c0.y + y0 * c0.x, x1 * c1.y + y1 * c1.x);
-          }
-          *reinterpret_cast<uint4*>(dst + h * p.out_hs + p.rope / 2) = b[i];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x0 = lo_f(x[j]), x1 = hi_f(x[j]);
-            x[j] = pack_bf16x2(x0 * c[j].x - x1 * c[j].y, x0 * c[j].y + x1 * c[j].x);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 c0 = c[2 * j], c1 = c[2 * j + 1];
+          const float x0 = lo_f(x[j]), x1 = hi_f(x[j]), y0 = lo_f(y[j]), y1 = hi_f(y[j]);
+          x[j] = pack_bf16x2(x0 * c0.x - y0 * c0.y, x1 * c1.x - y1 * c1.y);
+          y[j] = pack_bf16x2(x0 * c0.y + y0 * c0.x, x1 * c1.y + y1 * c1.x);
         }
       }
-      *reinterpret_cast<uint4*>(dst + h * p.out_hs) = a[i];
+    } else if (turns) {
+#pragma unroll
+      for (int i = 0; i < kRopeItems; ++i) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(&v[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = lo_f(x[j]), x1 = hi_f(x[j]);
+          x[j] = pack_bf16x2(x0 * c[j].x - x1 * c[j].y, x0 * c[j].y + x1 * c[j].x);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeItems; ++i) {
+      const int h = head(base, i);
+      if (!mine || h >= p.heads) continue;
+      *reinterpret_cast<uint4*>(dst + h * p.out_hs + (both && (i & 1) ? p.rope / 2 : 0)) = v[i];
     }
     base += gridDim.y * step;
     if (base < p.heads) load(base);
@@ -380,7 +391,7 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
   p.offset = rope_offset;
   p.rope = rope_dim;
   p.copy = in_place ? 0 : 1;
-  p.units = (in_place ? 0 : (head_dim - rope_dim) / 8) + rope_dim / (half ? 16 : 8);
+  p.units = (in_place ? rope_dim : head_dim) / 8;
   p.inv_freq = inv_freq;
   p.scale = scale;
   p.inverse = (flags & MLA_FLAG_ROPE_INVERSE) != 0;

@@ -5,7 +5,7 @@
 // operations each, so HBM bounds the long calls and launch latency the short
 // ones.  Measured: rotation of 8192 tokens x 128 heads x 192 dims 117.6 us (805
 // MB at 6.85 TB/s, a copy's rate; half layout 122), 1332 x 64 x 128 in the half
-// layout 6.7 us where the rows lie in L2, 9.9 from the HBM (44 MB), 64 x 128 x 64
+// layout 7.2 us where the rows lie in L2, 9.6 from the HBM (44 MB), 64 x 128 x 64
 // 2.0 us; append of 8192 tokens 5.4 us (19 MB), of 64 tokens 2.5 us.
 //
 // Angles.  Pair i at position p turns by p * f_i radians.  In fp32 that loses
@@ -54,9 +54,10 @@ struct RopeParams {
   const uint16_t* x;
   long long x_ts, x_hs;
   const int* positions;
-  int heads, offset, rope;
+  int tokens, heads, offset, rope;
   int units;     // 16-byte units per head that a thread handles (rotated ones, and copied ones out of place)
-  int per_turn;  // heads that a CTA's threads cover side by side
+  int per_turn;  // heads of a token that a CTA's threads cover side by side
+  int together;  // tokens of a CTA
   int copy;      // dims outside the rotated range are copied
   const double* inv_freq;
   float scale;
@@ -65,8 +66,9 @@ struct RopeParams {
   long long out_ts, out_hs;
 };
 
-// One CTA: one token, its heads in turns of per_turn * kRopeItems.  A unit is
-// 8 contiguous dims: 4 interleaved pairs, or 8 copied dims; a warp's units are
+// One CTA: one token, its heads in turns of per_turn * kRopeItems, or several
+// tokens of few heads (8192 tokens x 1 head x 64 dims 22 us with a CTA each,
+// 4.8 so).  A unit is 8 contiguous dims: 4 interleaved pairs, or 8 copied dims; a warp's units are
 // neighbours in memory.  A thread keeps one unit for all its heads: its cosines
 // and sines stay in registers, and nothing is divided in the loop.  In the half
 // layout a unit's 8 dims need their 8 partners: there the two threads of a unit
@@ -78,12 +80,13 @@ struct RopeParams {
 // position's load behind them.
 template <bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads, kHalf ? 4 : 5) mla_rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 cs[MLA_MAX_ROPE_DIM / 2];
-  const int t = blockIdx.x;
+  __shared__ float2 cs[4 * kRopeThreads];   // [token][pair]: a token has at least rope / 8 threads
   const bool wide = p.units > kRopeThreads;  // a head is more than a CTA: units in blocks of kRopeThreads
   const int u = wide ? blockIdx.z * kRopeThreads + threadIdx.x : threadIdx.x % p.units;
-  const int h0 = wide ? 0 : threadIdx.x / p.units;
-  const bool mine = wide ? u < p.units : h0 < p.per_turn;
+  const int place = wide ? 0 : threadIdx.x / p.units;  // (token, head) of those side by side
+  const int token = place / p.per_turn, h0 = place - token * p.per_turn;
+  const long long t = static_cast<long long>(blockIdx.x) * p.together + token;
+  const bool mine = (wide ? u < p.units : token < p.together) && t < p.tokens;
   const int before = p.copy ? p.offset / 8 : 0;     // copied units ahead of the rotated ones
   const int r = u - before;
   const bool turns = r >= 0 && r < p.rope / 8;
@@ -108,12 +111,15 @@ __global__ void __launch_bounds__(kRopeThreads, kHalf ? 4 : 5) mla_rope_kernel(c
   };
   int base = blockIdx.y * step;
   load(base);
-  const int pos = p.positions[t];
-  for (int i = threadIdx.x; i < p.rope / 2; i += kRopeThreads) cs[i] = turn(p.inv_freq[i], pos, p.inverse != 0, p.scale);
+  for (int i = threadIdx.x; i < p.together * (p.rope / 2); i += kRopeThreads) {
+    const int of = i / (p.rope / 2);
+    const long long at = static_cast<long long>(blockIdx.x) * p.together + of;
+    if (at < p.tokens) cs[i] = turn(p.inv_freq[i - of * (p.rope / 2)], p.positions[at], p.inverse != 0, p.scale);
+  }
   __syncthreads();
   float2 c[kHalf ? 8 : 4];
 #pragma unroll
-  for (int j = 0; j < (kHalf ? 8 : 4); ++j) c[j] = cs[pair + j];
+  for (int j = 0; j < (kHalf ? 8 : 4); ++j) c[j] = cs[mine ? token * (p.rope / 2) + pair + j : 0];
 #pragma unroll 1
   while (base < p.heads) {
     if (kHalf && turns) {
@@ -387,6 +393,7 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
   p.x_ts = x_token_stride;
   p.x_hs = x_head_stride;
   p.positions = positions;
+  p.tokens = num_tokens;
   p.heads = num_heads;
   p.offset = rope_offset;
   p.rope = rope_dim;
@@ -398,15 +405,23 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
   p.out = static_cast<uint16_t*>(out);
   p.out_ts = out_token_stride;
   p.out_hs = out_head_stride;
-  p.per_turn = p.units < kRopeThreads ? kRopeThreads / p.units : 1;
+  // heads side by side, no more than a turn takes; the room left goes to further
+  // tokens, once there are more of them than CTAs to keep the SMs busy (64 tokens
+  // x 1 head together 4.1 us, apart 1.9)
+  const int room = p.units < kRopeThreads ? kRopeThreads / p.units : 1, need = (num_heads + kRopeItems - 1) / kRopeItems;
+  p.per_turn = room < need ? room : need;
+  const int64_t spread = (static_cast<int64_t>(num_tokens) + kRopeCtas / 2 - 1) / (kRopeCtas / 2);
+  p.together = room / p.per_turn;
+  if (p.together > spread) p.together = spread > 1 ? static_cast<int>(spread) : 1;
   const int rc = cache_device_ready();
   if (rc != MLA_OK) return rc;
   if (num_tokens == 0) return MLA_OK;
   // few tokens: their heads spread over CTAs; many: a CTA takes all of a token's
+  const int64_t x_blocks = (static_cast<int64_t>(num_tokens) + p.together - 1) / p.together;
   const int64_t blocks = (static_cast<int64_t>(num_heads) + p.per_turn * kRopeItems - 1) / (p.per_turn * kRopeItems);
-  int64_t y = (static_cast<int64_t>(kRopeCtas) + num_tokens - 1) / num_tokens;
+  int64_t y = (kRopeCtas + x_blocks - 1) / x_blocks;
   if (y > blocks) y = blocks;
-  const dim3 grid(num_tokens, static_cast<unsigned>(y), (p.units + kRopeThreads - 1) / kRopeThreads);
+  const dim3 grid(static_cast<unsigned>(x_blocks), static_cast<unsigned>(y), (p.units + kRopeThreads - 1) / kRopeThreads);
   return launch_dependent(half ? mla_rope_kernel<true> : mla_rope_kernel<false>, grid, dim3(kRopeThreads), stream, p);
 }
 

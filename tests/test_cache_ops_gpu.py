@@ -69,6 +69,20 @@ def test_rope_matches_the_oracle(T, H, D, offset, R, half):
 
 
 @pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("T,H,D,offset,R", [(1217, 1, 64, 0, 64), (4099, 1, 16, 0, 16), (2000, 3, 192, 128, 64),
+                                            (1300, 5, 264, 8, 256), (6000, 2, 64, 32, 32), (700, 17, 32, 0, 32)])
+def test_many_tokens_of_few_heads(T, H, D, offset, R, half):
+    """Several tokens share a CTA; in place too."""
+    x = rand((T, H, D), T + D)
+    pos = torch.randint(-1000, 1 << 20, (T,), device="cuda", dtype=torch.int32)
+    inv, scale = m.rope_frequencies(R, yarn=4.0)
+    out = m.rope(x, pos, inv, offset=offset, half=half, scale=scale)
+    assert_rope(out, x, pos, inv, offset, half, False, scale)
+    y = x.clone()
+    assert torch.equal(m.rope(y, pos, inv, offset=offset, half=half, scale=scale, out=y), out)
+
+
+@pytest.mark.parametrize("half", [False, True])
 def test_far_and_negative_positions_keep_their_angle(half):
     pos = torch.tensor([2 ** 31 - 1, -2 ** 31, -1, 1 << 30, 12345678, 0], device="cuda", dtype=torch.int32)
     x = rand((6, 2, 64), 3)

@@ -385,14 +385,26 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       }
     }
   } else {
-    // RoPE dims, 8 lanes a row, and the pages' check, over the whole grid
-    for (long long r = blockIdx.x * 4ll + (lane >> 3); r < p.prefix_len; r += gridDim.x * 4ll) {
-      const long long page = p.block_table[r / kPage];
-      const bool ok = page >= 0 && page < p.num_pages;
-      if (!ok && (lane & 7) == 0) atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (ok) v = *reinterpret_cast<const uint4*>(p.cache + (page * kPage + r % kPage) * p.row_bytes + p.rope_byte + 16 * (lane & 7));
-      *reinterpret_cast<uint4*>(p.k_pe + r * kRope + 8 * (lane & 7)) = v;
+    // RoPE dims, 8 lanes a row, and the pages' check, over the whole grid; eight
+    // rows a lane in flight (one by one, 1000 rows x 1 head took 11.5 us)
+    constexpr int kFlight = 8;
+    for (long long r0 = blockIdx.x * (4ll * kFlight) + (lane >> 3); r0 < p.prefix_len; r0 += gridDim.x * (4ll * kFlight)) {
+      long long page[kFlight];
+      uint4 v[kFlight];
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) page[j] = r0 + 4 * j < p.prefix_len ? p.block_table[(r0 + 4 * j) / kPage] : 0;
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        const long long r = r0 + 4 * j;
+        const bool ok = page[j] >= 0 && page[j] < p.num_pages;
+        if (!ok && (lane & 7) == 0) atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok && r < p.prefix_len)
+          v[j] = *reinterpret_cast<const uint4*>(p.cache + (page[j] * kPage + r % kPage) * p.row_bytes + p.rope_byte + 16 * (lane & 7));
+      }
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j)
+        if (r0 + 4 * j < p.prefix_len) *reinterpret_cast<uint4*>(p.k_pe + (r0 + 4 * j) * kRope + 8 * (lane & 7)) = v[j];
     }
   }
 

@@ -16,9 +16,9 @@
 // drained under the next one's products.  (row tile, head) items form one
 // line, head by head, cut into equal ranges, one per pair.
 //
-// Measured: 8192 rows x 128 heads 162 to 169 us (1.65 PFLOP/s; the rate falls
-// with the clock, which the power limit holds at 1.75 to 1.85 GHz), 537 MB
-// written at 3.2 TB/s, where writes alone reach 4.0.  Not kept: the weights as A operand in tensor
+// Measured: 8192 rows x 128 heads 162 to 169 us (1.65 PFLOP/s; called for seconds
+// on end 191, as the power limit, 1,378 W, then holds the clock at 1.5 GHz), 537
+// MB written at 3.2 TB/s, where writes alone reach 4.0.  Not kept: the weights as A operand in tensor
 // memory (69 cycles an MMA against 83, but dims come out as rows and have to be
 // transposed on their way: 197 us with 4-byte stores, 253 with shuffles, 263
 // through shared memory).

@@ -16,12 +16,17 @@
 // drained under the next one's products.  (row tile, head) items form one
 // line, head by head, cut into equal ranges, one per pair.
 //
-// Measured: 8192 rows x 128 heads 162 to 169 us (1.65 PFLOP/s; called for seconds
-// on end 191, as the power limit, 1,378 W, then holds the clock at 1.5 GHz), 537
-// MB written at 3.2 TB/s, where writes alone reach 4.0.  Not kept: the weights as A operand in tensor
-// memory (69 cycles an MMA against 83, but dims come out as rows and have to be
-// transposed on their way: 197 us with 4-byte stores, 253 with shuffles, 263
-// through shared memory).
+// Measured: 8192 rows x 128 heads 157 to 163 us (1.7 PFLOP/s, 3.35 TB/s written;
+// called for seconds on end 182 to 187, as the power limit, 1,378 W, then holds
+// the clock at 1.5 GHz).  Without its stores the kernel takes 133 us, with half
+// of its products 156: the results' way out (shuffles and stores share the data
+// path that the MMAs read their operands on) and the products get in each
+// other's way.  Streaming stores, 64 bytes a row over four lanes, are the best of
+// those tried: not streaming 165 to 170, 128 bytes over eight lanes 161, 32-byte
+// stores 171, through shared memory and TMA more.  Not kept either: the weights
+// as A operand in tensor memory (dims come out as rows and have to be transposed
+// on their way: 197 us with 4-byte stores, 253 with shuffles, 263 through shared
+// memory); keys and values as two N = 128 products that share A (184).
 //
 //   warp 0     TMA: latents and weights
 //   warps 1, 11  MMA issue (rank 0, for both CTAs), in turns
@@ -298,7 +303,8 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
         // rows behind the prefix may hold anything
         if ((carry & 0x80008000u) != 0 && row0 + lane < p.prefix_len)
           atomicCAS(p.status, 0, static_cast<int>(kStValueRange));
-        // four lanes to 64 bytes of a row (the rows, as threads hold them, lie 256 bytes apart)
+        // four lanes to 64 bytes of a row (the rows, as threads hold them, lie 256
+        // bytes apart), streaming: most of a long prefix leaves the L2 before it is read
         const int first = row0 + lane - quad;
         uint16_t* dst = out + (h * p.head_rows + first) * kHeadDim + 64 * c + 8 * quad;
 #pragma unroll
@@ -310,7 +316,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
           quad_transpose(piece, lane);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (first + j < p.prefix_len) *reinterpret_cast<uint4*>(dst + j * kHeadDim + 32 * g) = piece[j];
+            if (first + j < p.prefix_len) __stcs(reinterpret_cast<uint4*>(dst + j * kHeadDim + 32 * g), piece[j]);
         }
       }
       if (++m == tiles) {

@@ -29,7 +29,8 @@
 // memory); keys and values as two N = 128 products that share A (184).
 //
 //   warp 0     TMA: latents and weights
-//   warps 1, 11  MMA issue (rank 0, for both CTAs), in turns
+//   warps 1, 11  MMA issue (rank 0, for both CTAs), in turns; with an FP8 cache
+//              rank 1's pass its converters' arrivals on to them
 //   warps 2-9  drain: tensor memory -> bf16 / fp16 -> global memory, 64 columns
 //              at a time; keys and values by four warps each
 //   warp 10    copies the RoPE dims and checks the block table
@@ -40,11 +41,13 @@
 // FP8 rows are widened on their way into shared memory (exactly: 4 significant
 // bits and a power of two), by every pair for every head, so that a prefix needs
 // one launch and no workspace.  Against a kernel that widens the prefix once, in
-// a workspace, for the bf16 product: 100 rows x 16 heads 8.2 / 9.0 us, 1000 x 16
-// 9.3 to 10.0 / 10.9 (and 9 us less of the host's time), 4000 x 64 57.6 / 52.3, 8192 x
-// 128 205 / 165: there the widening, 890 cycles a chunk, holds up the products'
-// 690.  Not kept: four warps 274 us, six or three warps with a chunk each 277
-// and 375, the next chunk's codes read ahead 322, integer widening 219.
+// a workspace, for the bf16 product: 100 rows x 16 heads 8.4 / 9.0 us, 1000 x 16
+// 10.4 / 10.9 (and 9 us less of the host's time), 4000 x 64 65 / 52.3, 8192 x 128
+// 238 / 165: there the widening (890 cycles a chunk) and the way to the other
+// SM's issuers hold up the products' 690.  Not kept (measured while rank 1's
+// converters released to their own CTA only, which orders nothing for an issuer
+// in the other; 205 us so): four warps 274 us, six or three warps with a chunk
+// each 277 and 375, the next chunk's codes read ahead 322, integer widening 219.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -71,7 +74,7 @@ constexpr int kSlots = 6;
 constexpr int kOffW = 0;
 constexpr int kOffRing = kStages * kChunk;                // 128 KiB
 constexpr int kOffBar = kOffRing + kSlots * kChunk;       // 224 KiB
-constexpr int kNumBars = 3 * kSlots + 2 * kStages + 4 + 3;
+constexpr int kNumBars = 4 * kSlots + 2 * kStages + 4 + 3;
 constexpr int kSlack = 1024;                 // re-aligned to 1024 B (128-byte swizzle atoms)
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
 static_assert(kSmem <= 232448, "shared memory");
@@ -94,15 +97,6 @@ struct ExpandParams {
   uint16_t* k_pe;
   int* status;
 };
-
-// Arrives at a barrier of either CTA of the pair with release semantics for
-// this CTA only: what was written is in this CTA's shared memory, and this SM's
-// own tensor core reads it; the other CTA's thread only issues.  (A release for
-// the cluster waits for far more: 2,150 cycles a chunk against 1,180 with four
-// warps.)
-__device__ __forceinline__ void arrive_cta(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -129,6 +123,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
   auto acc_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + s); };
   auto acc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 2 + s); };
   auto raw_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 4 + s); };  // codes (FP8 cache)
+  auto widened = [&](uint32_t s) { return bar0 + 8u * (3 * kSlots + 2 * kStages + 4 + s); };  // bf16 (FP8 cache, rank 1)
   auto turn = [&](uint32_t issuer) { return bar0 + 8u * (kNumBars - 3 + issuer); };
   const uint32_t bar_drain = bar0 + 8u * (kNumBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
@@ -142,7 +137,10 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
     }
     mbar_init(bar_drain, 2);  // both issuers
     if (kFp8)
-      for (uint32_t s = 0; s < kSlots; ++s) mbar_init(a_full(s), kConverters);  // a group of each CTA
+      for (uint32_t s = 0; s < kSlots; ++s) {
+        mbar_init(a_full(s), kConverters / 2 + 1);  // rank 0's group, and rank 1's relay
+        mbar_init(widened(s), kConverters / 2);
+      }
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -220,6 +218,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
     }
     __syncwarp();
   } else if (warp == 1 || warp == 11) {
+    const uint32_t me = warp == 1 ? 0u : 1u;
     if (rank == 0) {
       // Two warps issue, stages of 64 latent dims (512 cycles of products) in
       // turns, all into the tile's accumulator: between its four MMAs and its
@@ -227,7 +226,6 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       // chunk, 300 cycles in which the tensor core, which queues one or two
       // MMAs, would run dry (one issuer: 5,700 cycles a tile).  The whole warp
       // runs, one lane issues (uniform operands).
-      const uint32_t me = warp == 1 ? 0u : 1u;
       const uint32_t leader = lane == 0 ? 1u : 0u;
       const uint64_t wd = smem_desc(sbase + kOffW, kChunk / 2, 1024u);   // MN-major: 64-column halves kChunk / 2 apart
       const uint64_t ad = smem_desc(sbase + kOffRing, 16u, 1024u);
@@ -264,6 +262,23 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       }
       umma_commit_pair_if(leader, bar_drain, 1);  // arrives once every MMA issued above has completed
       drain_bar(bar_drain, 0u);
+      __syncwarp();
+    } else if (kFp8) {
+      // Rank 1's issuers have nothing to issue: they relay its converters'
+      // arrivals to rank 0, whose MMAs read this CTA's rows too.  The converters
+      // release to their own CTA; a thread without stores of its own, which has
+      // acquired their rows, releases to the cluster.  That is slow beside the
+      // drain's stores (8192 x 128: 236 us; a third relay 232, but then no warp
+      // is left for rank 1's RoPE rows; the converters releasing to the cluster
+      // themselves 337).
+      if (lane == 0) {
+        const uint32_t ra = mapa(a_full(0), 0), chunks = static_cast<uint32_t>(n) * kStages;
+        for (uint32_t chunk = me; chunk < chunks; chunk += 2) {
+          const uint32_t s = chunk % kSlots;
+          if (!wait(widened(s), (chunk / kSlots) & 1, ctl)) break;
+          mbar_arrive_remote(ra + 8u * s);
+        }
+      }
       __syncwarp();
     }
   } else if (warp < 10) {
@@ -333,7 +348,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
     // (always of the same slots, so that it sees all their phases), hide it.
     const uint32_t g = static_cast<uint32_t>(warp - kThreads / 32) >> 2;
     const int w = warp & 3, sub = lane >> 2, u = lane & 3;
-    const uint32_t ra = mapa(a_full(0), 0);
+    const uint32_t done = rank == 0 ? a_full(0) : widened(0);
     const uint32_t in = sbase + kOffRing + kChunk / 2 + static_cast<uint32_t>(32 * w) * 64u + static_cast<uint32_t>(lane) * 16u;
     // the lane's two 16-byte pieces of a row, swizzled (the row's number modulo 8 is sub)
     const uint32_t out = sbase + kOffRing + static_cast<uint32_t>(32 * w + sub) * 128u;
@@ -387,7 +402,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_cta(ra + 8u * s);
+        if (lane == 0) mbar_arrive(done + 8u * s);
       }
     }
   } else {

@@ -170,6 +170,31 @@ def test_fp8_scales_of_every_size_and_codes_that_are_no_numbers():
     assert_expanded(k_nope, k_pe, v, held[:, :512], held[:, 512:], w_uk, w_uv, rows)
 
 
+@pytest.mark.parametrize("P,H", [(100, 3), (1000, 16), (3000, 40), (8192, 128)])
+def test_fp8_rows_expand_as_the_bf16_rows_of_their_values(P, H):
+    """Codes times power-of-two scales are bf16 numbers, and both caches take the
+    same products in the same order: bit for bit the same keys and values, however
+    often and whatever runs beside.  (Rows handed to the other SM's products
+    before they are all there would differ.)"""
+    kv, bt, _, _ = cache_and_rows(P, True, 31)
+    scales = torch.exp2(kv[..., 512:516].float() - 127)
+    lat = (kv[..., :512].view(torch.float8_e4m3fn).float().unflatten(-1, (4, 128)) * scales[..., None]).flatten(-2)
+    same = torch.cat([lat.bfloat16(), kv[..., 528:].contiguous().view(torch.bfloat16)], -1)
+    assert torch.equal(same[..., :512].float(), lat)
+    w_uk, w_uv = rand((H, 512, 128), 1) * 512 ** -0.5, rand((H, 512, 128), 2) * 512 ** -0.5
+    want = m.prefix_expand(same, bt, P, w_uk, w_uv)
+    side, noise = torch.cuda.Stream(), torch.empty(1 << 26, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(20):
+        if i % 2:
+            with torch.cuda.stream(side):
+                noise.add_(1)
+        status = status_word()
+        got = m.prefix_expand(kv, bt, P, w_uk, w_uv, status=status)
+        assert int(status) == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+    torch.cuda.synchronize()
+
+
 def test_keys_that_are_not_finite_are_reported():
     kv, bt, lat, pe = cache_and_rows(200, False, 4)
     w_uk, w_uv = rand((2, 512, 128), 1), rand((2, 512, 128), 2)

@@ -130,17 +130,23 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
 
   if (threadIdx.x == 0) {
-    for (uint32_t i = kFp8 ? kSlots : 0; i < kNumBars; ++i) mbar_init(bar0 + 8u * i, 1);
+    // each once: to initialise a barrier that is one already is undefined
+    for (uint32_t s = 0; s < kSlots; ++s) {
+      mbar_init(a_full(s), kFp8 ? kConverters / 2 + 1 : 1);  // FP8: rank 0's group, and rank 1's relay
+      mbar_init(a_empty(s), 1);
+      mbar_init(raw_full(s), 1);
+      mbar_init(widened(s), kConverters / 2);
+    }
+    for (uint32_t k = 0; k < kStages; ++k) {
+      mbar_init(w_full(k), 1);
+      mbar_init(w_empty(k), 1);
+    }
     for (uint32_t s = 0; s < 2; ++s) {
       mbar_init(acc_full(s), 2);    // both issuers
       mbar_init(acc_empty(s), 16);  // the drain warps of both CTAs
+      mbar_init(turn(s), 1);
     }
     mbar_init(bar_drain, 2);  // both issuers
-    if (kFp8)
-      for (uint32_t s = 0; s < kSlots; ++s) {
-        mbar_init(a_full(s), kConverters / 2 + 1);  // rank 0's group, and rank 1's relay
-        mbar_init(widened(s), kConverters / 2);
-      }
     *abort_flag = 0u;
     fence_mbar_init();
   }

@@ -432,6 +432,51 @@ def test_suffix_joined_in_place():
     assert out is so and lse is sl and torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("how", ["plain", "fp32", "in place"])
+@pytest.mark.parametrize("T,H,P", [(1, 1, 20000), (7, 1, 4097), (3, 5, 1400), (70, 16, 3001), (100, 5, 900), (256, 3, 30000),
+                                   (700, 1, 5000), (300, 3, 1000), (2500, 2, 3000), (129, 100, 3000)])
+def test_heads_cut_in_pieces_with_a_suffix_and_partly_visible(T, H, P, how):
+    """Calls whose heads are split over SMs (few and many pieces, rows of both
+    kernels, ranges that end one head and begin another): pieces that a token
+    sees nothing of, the suffix's share, and its rows written over."""
+    assert m.mla_prefix_attend_workspace_size(T, H, P) > 0  # split
+    x = inputs(T, H, P, seed=T + H)
+    vis = torch.randint(0, P + 1, (T,), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(P))
+    edges = torch.tensor([P - 1, 1, 0, P, 129, 128, -1, P // 2], device="cuda", dtype=torch.int32)
+    n = min(T, len(edges))
+    vis[T - n:] = edges[:n]
+    so, sl = rand((T, H, 128), 6), math.log(P) - 2 + 3 * rand((T, H), 7, torch.float32)
+    if T > 1:
+        sl[::3] = -math.inf
+        so[::3] = float("nan")
+    sl[T // 2, H - 1] = 90.0
+    kw = dict(out=so.clone(), lse=sl.clone()) if how == "in place" else dict(out_fp32=how == "fp32")
+    suffix = (kw["out"], kw["lse"]) if how == "in place" else (so, sl)
+    status = status_word()
+    out, lse = m.prefix_attend(*x, SCALE, visible=vis, suffix_out=suffix[0], suffix_lse=suffix[1], status=status, **kw)
+    assert int(status) == 0
+    rng = np.random.default_rng(P)
+    tokens = np.unique(np.r_[0, T // 2, T - n + rng.permutation(n)[:5], rng.integers(0, T, 3)])
+    heads = np.unique(np.r_[0, H - 1, rng.integers(0, H, 2)])
+    assert_attended(out, lse, *x, visible=vis, suffix=(so, sl), tokens=tokens, heads=heads)
+    # every element against the plain form in 32 bits, a head at a time
+    for h in range(H):
+        s = (x[0][:, h].float() @ x[2][h].float().t() + x[1][:, h].float() @ x[3].float().t()) * SCALE
+        s.masked_fill_(torch.arange(P, device="cuda")[None] >= vis[:, None], -math.inf)
+        own = torch.logsumexp(s, -1)
+        total = torch.logaddexp(own, sl[:, h])
+        base = total.masked_fill(total == -math.inf, 0)
+        ref = torch.exp(s - base[:, None]) @ x[4][h].float()
+        share = torch.exp(sl[:, h] - base)[:, None]
+        ref += torch.where(share > 0, share * so[:, h].float(), 0)  # a row that counts and is not a number stays so
+        fin = torch.isfinite(total)
+        assert torch.equal(fin, torch.isfinite(lse[:, h])) and not out[~fin, h].any()
+        assert float((lse[fin, h] - total[fin]).abs().max()) <= 1e-3
+        nan, got = ref.isnan(), out[:, h].float()
+        tol = 4e-3 + (2.0 ** -8 * ref.abs() if how != "fp32" else 0)
+        assert torch.equal(nan, got.isnan()) and bool((((got - ref).abs() <= tol) | nan).all())
+
+
 @pytest.mark.parametrize("T", [4, 200])
 def test_fewer_rows_than_held_and_what_lies_behind_them(T):
     """Rows behind prefix_len may hold anything."""

@@ -72,7 +72,8 @@ size_t mla_prefix_attend_workspace_size(int num_tokens, int num_heads, int prefi
  *   k_nope, v, head_rows, k_pe, prefix_len, num_heads: as mla_prefix_expand
  *                wrote them.  Every value of the prefix must be finite: a
  *                value row that is not reaches every token of the call that
- *                sees any row.
+ *                sees any row.  (Scores of rows that a token does not see may
+ *                overflow.)
  *   visible      int32 [num_tokens] or NULL: token t sees the prefix's first
  *                visible[t] rows (clamped to 0 .. prefix_len): requests that
  *                share only part of it, and padded tokens (0).  NULL: all.

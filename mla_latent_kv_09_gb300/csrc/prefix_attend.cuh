@@ -100,15 +100,29 @@ __device__ __forceinline__ void mask32(uint32_t (&x)[32], int limit) {
     if (k >= limit) x[k] = 0xff800000u;
 }
 
+// The largest of three, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The largest score, NaN if one is no number.
 __device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
   float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
 #pragma unroll
   for (int k = 2; k < 30; k += 4) {
-    a = fmaxf(fmaxf(a, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
-    b = fmaxf(fmaxf(b, __uint_as_float(x[k + 2])), __uint_as_float(x[k + 3]));
+    a = max3_nan(a, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+    b = max3_nan(b, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
   }
-  return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
+  return max3_nan(max3_nan(a, b, __uint_as_float(x[30])), __uint_as_float(x[31]), -INFINITY);
 }
+
+// Whether a row that sees none of these keys has a score among them whose
+// weight 2^(score * scale - inf) would not be zero: +inf, or no number (finite
+// keys may overflow, and a padded token's query may hold anything).  Without
+// `visible` only rows behind the prefix are hidden, which read as zeros.
+__device__ __forceinline__ bool hidden_overflow(int limit, float top) { return limit <= 0 && !(top < INFINITY); }
 
 // Weights 2^(x * scale - base) to 16 columns of tensor memory in fp16, and
 // their sums: of the fp32 values, and of the fp16 ones that the value product

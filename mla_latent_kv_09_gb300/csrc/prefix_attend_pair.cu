@@ -276,7 +276,8 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
         // which is read twice: held across the step, it would push the thread
         // over its registers, into local memory.
         const int limit = seen - key0 - 32 * hf;      // keys of this tile the row sees
-        // only rows that end in this tile need masks (a row that sees none of it gets zeros below)
+        // only rows that end in this tile need masks (a row that sees none of it
+        // gets zeros below, unless its scores overflow)
         const bool ragged = __any_sync(0xffffffffu, limit > 0 && limit < 96);
         uint32_t x[32];
         float top;
@@ -289,8 +290,11 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
             mask32(x, limit);
             mask32(y, limit - 64);
           }
-          top = limit <= 0 ? -INFINITY : fmaxf(max32(x), max32(y));
+          top = max3_nan(max32(x), max32(y), -INFINITY);
         }
+        const bool overflow = p.visible && __any_sync(0xffffffffu, hidden_overflow(limit, top));
+        if (overflow) mask32(x, limit);
+        if (limit <= 0) top = -INFINITY;
         float* xmax = xmax2 + ((q >> 1) & 1u) * 2 * kTile;
         xmax[hf * kTile] = top;
         ok = named_bar_all(pair_bar, 64, ok);         // votes: a wait that ran out in one warp ends both
@@ -330,7 +334,7 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
           if (c == 1) {
             tmem_ld32(ts + 64u + 32u * hf, x);
             tmem_wait_ld();
-            if (ragged) mask32(x, limit - 64);
+            if (ragged || overflow) mask32(x, limit - 64);
           }
           weights32(x, p.scale_log2, base, ts + 32u * c + 16u * hf, total, used);
           tmem_wait_st();
@@ -356,7 +360,6 @@ mla_prefix_attend_pair_kernel(const __grid_constant__ AttendParams p, const __gr
       // maximum.  All softmax warps vote, so that a wait that ran out in one
       // ends them all.
       float* mine = xchg + (g * 2 + hf) * 3 * kTile;
-      if (seen <= sg.k0 * kTile) total = used = 0.f;  // sees none of the segment: so too if its scores are no numbers
       mine[0] = m;
       mine[kTile] = total;
       mine[2 * kTile] = used;

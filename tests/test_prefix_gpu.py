@@ -422,6 +422,23 @@ def test_queries_of_padded_tokens_may_hold_anything(T, P):
             assert torch.equal(got, out) and torch.equal(got_lse, lse)
 
 
+@pytest.mark.parametrize("big", [3e38, -3e38, "both"])
+@pytest.mark.parametrize("T,H,P", [(6, 2, 700), (128, 1, 600), (150, 3, 1000), (300, 2, 4000)])
+def test_hidden_keys_whose_scores_overflow(T, H, P, big):
+    """Keys that no token sees may be any finite numbers: their scores, infinite
+    or no numbers in fp32, reach no result."""
+    x = inputs(T, H, P, seed=11)
+    vis = torch.randint(0, 301, (T,), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(3))
+    vis[:4] = torch.tensor([300, 0, 1, 256], device="cuda", dtype=torch.int32)
+    want, want_lse = m.prefix_attend(*x, SCALE, visible=vis, out_fp32=True)
+    assert_attended(want, want_lse, *x, visible=vis, tokens=np.arange(6))
+    x[2][:, 300:] = 3e38 * torch.sign(x[2][:, 300:]) if big == "both" else big
+    x[3][300:] = 3e38 if big == "both" else big
+    assert bool(x[2].isfinite().all())
+    out, lse = m.prefix_attend(*x, SCALE, visible=vis, out_fp32=True)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_suffix_joined_in_place():
     T, H, P = 20, 3, 333
     x = inputs(T, H, P)

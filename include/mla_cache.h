@@ -16,8 +16,10 @@
  *     (a, b) -> scale * (a cos - b sin, a sin + b cos)
  *
  * The pair is (2i, 2i + 1) (interleaved, the default) or (i, i + R / 2)
- * (MLA_FLAG_ROPE_HALF).  Scaling for long contexts is in inv_freq and
- * scale, which the caller computes once (linear interpolation, YaRN, ...).
+ * (MLA_FLAG_ROPE_HALF).  Scaling for long contexts is in inv_freq, which the
+ * caller computes once (linear interpolation, YaRN, ...).  A factor that YaRN
+ * puts on queries and keys may be `scale` only where every dim of a head turns;
+ * with 64 of 192 it belongs, squared, into the attention's softmax_scale.
  * Frequencies are radians per position in fp64; the angle is reduced modulo
  * one turn in 64-bit fixed point, so that it is as exact at position 2^31 - 1
  * as at 0.

@@ -13,8 +13,8 @@ kernels); this package is its Python face:
     the attention (query through W_UK, output through W_UV);
   * `indexer_scores` / `topk_indices`, the sparse-attention indexer that
     produces the top-k lists the sparse decode consumes;
-  * `rope` / `rope_frequencies` and `cache_append`, which turn the RoPE dims
-    and put tokens into the paged latent cache;
+  * `rope` / `rope_frequencies` / `softmax_scale` and `cache_append`, which
+    turn the RoPE dims and put tokens into the paged latent cache;
   * `prefix_expand` / `prefix_attend`, attention for a batch that shares a
     long prefix: its keys and values expanded once, attended to by all.
 
@@ -295,15 +295,21 @@ def _elsewhere(first, stream, name: str):
 def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.0, yarn: float = 1.0,
                      original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
     """Frequencies of a rotation of `rope_dim` dims, for `rope` and
-    `cache_append`: (fp64 [rope_dim / 2] radians per position, the factor on
-    the turned dims).
+    `cache_append`: (fp64 [rope_dim / 2] radians per position, YaRN's factor).
 
     Pair i turns by base^(-2i / rope_dim) a position.  For contexts longer
     than the `original_len` a model was trained on: `linear` divides every
     frequency (position interpolation); `yarn` is YaRN's stretch: pairs of
     fewer than beta_slow turns over original_len are slowed down by it, pairs
     of more than beta_fast turns are kept, those between are blended linearly
-    over the pair's index, and the factor is 0.1 ln(yarn) + 1.
+    over the pair's index, and the factor is 0.1 ln(yarn) + 1 (else 1).
+
+    The factor belongs on the whole query and the whole key, squared on their
+    score.  Heads of which every dim turns may have it as `rope`'s and
+    `cache_append`'s scale.  Heads of which only a part turns (MLA: 64 of 192)
+    must not, or it would weigh the turned part of a score against the rest:
+    there the rotations keep their scale of 1, and the attention takes
+    `softmax_scale(head_dim, factor)`.
     """
     import math
 
@@ -324,6 +330,15 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, *, linear: float = 1.
         inv = inv / yarn * slow + inv * (1 - slow)
         factor = 0.1 * math.log(yarn) + 1.0
     return inv.to(device), factor
+
+
+def softmax_scale(head_dim: int = 192, factor: float = 1.0) -> float:
+    """The attention's softmax scale, factor^2 / sqrt(head_dim): `head_dim` dims
+    of a query and a key before absorption (MLA: 128 + 64), `factor` as
+    `rope_frequencies` returns it."""
+    if head_dim < 1 or not 0 < factor < float("inf"):
+        raise ValueError("softmax_scale: head_dim >= 1, factor > 0 and finite")
+    return factor * factor * head_dim ** -0.5
 
 
 def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse: bool = False, scale: float = 1.0,

@@ -600,6 +600,27 @@ def test_attention_refusals():
 
 # ---------------------------------------------------------------- all of them together
 
+def test_a_context_stretched_by_yarn():
+    """Queries and keys turned with YaRN's frequencies, its factor in the softmax
+    scale: the scores of queries and keys multiplied by it as a whole, in fp64 on
+    the rows as they are held."""
+    T, H, P = 4, 3, 200
+    inv, factor = m.rope_frequencies(64, yarn=40.0)
+    ints = lambda a: torch.tensor(a, device="cuda", dtype=torch.int32)  # noqa: E731
+    cache, table = torch.zeros((4, 64, 576), dtype=torch.bfloat16, device="cuda"), ints([2, 0, 3, 1])
+    x, q = rand((P, 576), 1), rand((T, H, 192), 2)
+    m.cache_append(x[:, :512], x[:, 512:], cache, table[None], ints(np.arange(P)), inv_freq=inv)
+    m.rope(q, ints(np.arange(P, P + T)), inv, offset=128, out=q)
+    w_uk, w_uv = rand((H, 512, 128), 3) * 512 ** -0.5, rand((H, 512, 128), 4) * 512 ** -0.5
+    k_nope, k_pe, v = m.prefix_expand(cache, table, P, w_uk, w_uv)
+    out, lse = m.prefix_attend(q[..., :128], q[..., 128:], k_nope, k_pe, v, m.softmax_scale(192, factor), out_fp32=True)
+    a = [f64(t) for t in (q[..., :128], q[..., 128:], k_nope, k_pe, v)]
+    whole = [factor * t for t in a[:4]] + a[4:]
+    ref, ref_lse = oracle.prefix_attend(*whole, 192 ** -0.5)
+    bo, bl = oracle.attend_error_bound(*whole, 192 ** -0.5, ref)
+    assert (np.abs(f64(out) - ref) <= bo).all() and (np.abs(f64(lse) - ref_lse) <= bl).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_a_decode_step_over_a_shared_prefix(fp8):
     """Prefix tokens appended to the cache and expanded once; then a step of B

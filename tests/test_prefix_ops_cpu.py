@@ -128,6 +128,27 @@ def test_yarn_keeps_fast_pairs_and_slows_slow_ones():
     assert (np.diff(ratio) <= 1e-15).all() and (ratio >= 1 / 40 - 1e-15).all()
 
 
+def test_yarn_factor_of_heads_that_turn_in_part():
+    """YaRN multiplies whole queries and keys by its factor.  Of 192 dims 64 turn:
+    the scale on the softmax gives these scores, one on the turned dims others."""
+    rng = np.random.default_rng(3)
+    f, factor = m.rope_frequencies(64, yarn=40.0, device="cpu")
+    q, k = rng.standard_normal((2, 5, 192))
+    pos_q, pos_k = rng.integers(0, 100000, (2, 5))
+    turn = lambda x, p, scale=1.0: oracle.rope(x[:, None], p, f.numpy(), offset=128, scale=scale)[:, 0]  # noqa: E731
+    want = (factor * turn(q, pos_q)) @ (factor * turn(k, pos_k)).T / math.sqrt(192)
+    got = m.softmax_scale(192, factor) * turn(q, pos_q) @ turn(k, pos_k).T
+    assert np.allclose(got, want, rtol=1e-12, atol=0)
+    assert not np.allclose(m.softmax_scale() * turn(q, pos_q, factor) @ turn(k, pos_k, factor).T, want, rtol=1e-2)
+    assert m.softmax_scale() == 192 ** -0.5 and m.softmax_scale(128) == 128 ** -0.5
+
+
+@pytest.mark.parametrize("a", [(0,), (-1,), (192, 0.0), (192, math.nan), (192, math.inf)])
+def test_softmax_scale_refuses(a):
+    with pytest.raises(ValueError):
+        m.softmax_scale(*a)
+
+
 @pytest.mark.parametrize("kw", [dict(rope_dim=63), dict(rope_dim=0), dict(base=1.0), dict(linear=0.5), dict(yarn=0.0),
                                 dict(original_len=0), dict(beta_fast=1.0, beta_slow=2.0), dict(beta_slow=0.0)])
 def test_frequencies_refuse(kw):

@@ -20,9 +20,10 @@
  * caller computes once (linear interpolation, YaRN, ...).  A factor that YaRN
  * puts on queries and keys may be `scale` only where every dim of a head turns;
  * with 64 of 192 it belongs, squared, into the attention's softmax_scale.
- * Frequencies are radians per position in fp64; the angle is reduced modulo
- * one turn in 64-bit fixed point, so that it is as exact at position 2^31 - 1
- * as at 0.
+ * Frequencies are radians per position in fp64, of magnitudes below 2^52; the
+ * angle is reduced modulo one turn in 64-bit fixed point, so that it is as exact
+ * at position 2^31 - 1 as at 0 (off by 2^-32 turns at most, before its cosine
+ * and sine are taken in fp32).
  *
  * Conventions: as for mla_decode.h (device pointers, asynchronous on
  * `stream`, no allocation, no host synchronisation, graph-capturable,
@@ -54,7 +55,7 @@ enum {
  *                turned, the others copied
  *   rope_offset  multiple of 8
  *   rope_dim     multiple of 16, at most MLA_MAX_ROPE_DIM
- *   inv_freq     fp64 [rope_dim / 2], radians per position, finite, 8-byte
+ *   inv_freq     fp64 [rope_dim / 2], radians per position, below 2^52, 8-byte
  *                aligned
  *   scale        factor on the turned dims (finite)
  *   flags        MLA_FLAG_ROPE_HALF, MLA_FLAG_ROPE_INVERSE
@@ -74,7 +75,7 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
  *   norm_weight  bf16 [512] or NULL.  With it the stored latent is
  *                latent * norm_weight / sqrt(mean(latent^2) + eps)
  *   eps          >= 0, used with norm_weight only
- *   inv_freq     fp64 [32], finite, or NULL (k_pe is stored as it is)
+ *   inv_freq     fp64 [32], below 2^52, or NULL (k_pe is stored as it is)
  *   rope_scale   factor on the turned dims (with inv_freq only)
  *   positions    int32 [num_tokens]: token t's position in its request's
  *                sequence, which is also its angle's; a negative position

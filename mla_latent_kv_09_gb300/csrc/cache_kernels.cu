@@ -5,17 +5,20 @@
 // operations each, so HBM bounds the long calls and launch latency the short
 // ones.  Measured: rotation of 8192 tokens x 128 heads x 192 dims 117.6 us (805
 // MB at 6.85 TB/s, a copy's rate; half layout 122), 1332 x 64 x 128 in the half
-// layout 7.2 us where the rows lie in L2, 9.6 from the HBM (44 MB), 64 x 128 x 64
-// 2.0 us; append of 8192 tokens 5.4 us (19 MB), of 64 tokens 2.5 us.
+// layout 6.9 us where the rows lie in L2, 9.6 from the HBM (44 MB), 64 x 128 x 64
+// 2.0 us; append of 8192 tokens 4.6 us (19 MB), of 64 tokens 2.2 us.
 //
 // Angles.  Pair i at position p turns by p * f_i radians.  In fp32 that loses
 // the angle at far positions (at p = 2^20 one ulp is 1/16 radian), and fp64
 // is slow on this chip.  A rotation only needs the angle modulo one turn, and
 // p is whole: with F = f_i / 2 pi as a 64-bit fixed-point fraction of a turn,
 // p * F mod 2^64 IS the angle modulo one turn, exact in F's last bit, in one
-// integer product.  F takes one fp64 product per (token, pair); its error,
-// 2^-53 of F, is a 2^-34 turn at p = 2^20.  The top 32 bits as a signed
-// fraction in [-1/2, 1/2) go through sincospif.
+// integer product.  F comes in whole numbers too, as f_i's 53-bit mantissa times
+// the 128 bits of 1 / 2 pi that its exponent picks: off by less than 2 2^-64
+// turns, so the angle by 2^-32 turns at most, whatever the frequency (an fp64
+// product f_i * (1 / 2 pi) is off by 2^-53 of itself: 2e-5 radians for f = 100
+// at p = 2^31).  The top 32 bits as a signed fraction in [-1/2, 1/2) go through
+// sincospif.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -37,9 +40,21 @@ constexpr int kFp8Row = MLA_FP8_ROW_BYTES;
 constexpr int kAppendWarps = 4;
 
 __device__ __forceinline__ float2 turn(double f, int pos, bool inverse, float scale) {
-  double t = f * 0.15915494309189533577;  // turns per position: f / (2 pi)
-  t -= floor(t);                          // positions are whole: whole turns drop out
-  const unsigned long long fix = __double2ull_rn(t * 18446744073709551616.0);
+  // f = m 2^(e - 1075), so turns a position times 2^64, modulo 2^64 (positions are
+  // whole: whole turns drop out), are m times (1 / 2 pi) 2^(e - 1011): its 64 bits
+  // ahead of the point and the 64 behind it, from the first 128 bits of 1 / 2 pi.
+  constexpr unsigned long long kTurn0 = 0x28be60db9391054aull, kTurn1 = 0x7f09d5f47d4d3770ull;
+  const long long bits = __double_as_longlong(f);
+  const int e = static_cast<int>(bits >> 52) & 2047;
+  const unsigned long long m = (bits & 0xfffffffffffffll) | (e != 0 ? 0x10000000000000ll : 0ll);
+  const int up = min(e - 1011, 63);  // (frequencies of 2^52 and more turn by no angle in particular)
+  unsigned long long ahead = 0, behind = up > -64 ? kTurn0 >> (-up & 63) : 0;
+  if (up > 0) {
+    ahead = kTurn0 >> (64 - up);
+    behind = kTurn0 << up | kTurn1 >> (64 - up);
+  }
+  unsigned long long fix = m * ahead + __umul64hi(m, behind);
+  if (bits < 0) fix = 0 - fix;
   const unsigned long long a = fix * static_cast<unsigned long long>(static_cast<long long>(pos));
   const float half_turns = static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
   float s, c;

@@ -11,6 +11,8 @@ it, before the rounding to bf16 (2^-8) or E4M3 (2^-4, or half of the smallest
 step, 2^-10, in units of the group's scale).
 """
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -96,6 +98,54 @@ def test_frequencies_of_whole_turns_and_above():
     inv = torch.tensor([2 * np.pi, 7.0, 0.0, 1e-9, -0.5, 3.5, 100.0, 0.25], dtype=torch.float64, device="cuda")
     x, pos = rand((9, 3, 16), 4), torch.arange(9, device="cuda", dtype=torch.int32)
     assert_rope(m.rope(x, pos, inv), x, pos, inv, 0, False, False, 1.0)
+
+
+def angles(inv, pos):
+    """pos * inv modulo one turn in radians, from 400 bits of pi (Machin's formula)."""
+    one = 1 << 432
+
+    def atan_inverse(x):
+        total = term = one // x
+        n = 1
+        while term:
+            term //= x * x
+            n += 2
+            total += term // n * (-1 if n % 4 == 3 else 1)
+        return total
+
+    pi = Fraction(4 * (4 * atan_inverse(5) - atan_inverse(239)), one)
+    assert float(pi) == np.pi
+    turn = lambda f, p: (Fraction(f) * int(p) / (2 * pi)) % 1  # noqa: E731
+    return np.array([[2 * np.pi * float(turn(float(f), p)) for f in inv] for p in pos])
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_every_frequency_keeps_its_angle_at_far_positions(half):
+    """Frequencies of more than a radian at far positions: p f in fp64 would be
+    off by 2^-53 of it, up to a whole turn here, so the angles come from whole
+    numbers; the bound is the other tests'."""
+    inv = np.array([1.0, 7.0, 100.0, 2 * np.pi, -7.0, 1e-9, 12345.678, 2.0 ** 40 + 0.5, -(2.0 ** 51), 0.0, -1e-300, 5e-324,
+                    3.5, -0.001, 4.0e15, 0.5])
+    pos = np.array([2 ** 31 - 1, -2 ** 31, -1, 1, 123456789, 1 << 30, 0, -987654321])
+    x = rand((len(pos), 2, 32), 41)
+    got = f64(m.rope(x, torch.tensor(pos, dtype=torch.int32, device="cuda"), torch.tensor(inv, device="cuda"), half=half))
+
+    def check(got, x, a):
+        n = a.shape[-1]
+        part = lambda t: (t[..., :n], t[..., n:]) if half else (t[..., 0::2], t[..., 1::2])  # noqa: E731
+        u, v = part(x)
+        mass = np.abs(u) + np.abs(v)
+        for y, ref in zip(part(got), (u * np.cos(a) - v * np.sin(a), u * np.sin(a) + v * np.cos(a))):
+            assert (np.abs(y - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * mass).all()
+
+    check(got, f64(x), angles(inv, pos)[:, None])
+    # the append's rows too
+    pe, inv32, at = rand((4, 64), 42), np.r_[inv, inv], np.array([5, 100000, 12345678, 64 * 300000 - 1])
+    bt, cache = torch.arange(300000, device="cuda", dtype=torch.int32)[None] % 4, pool(4, False, 43)
+    m.cache_append(rand((4, 512), 44), pe, cache, bt, torch.tensor(at, dtype=torch.int32, device="cuda"),
+                   request_ids=torch.zeros(4, dtype=torch.int32, device="cuda"), inv_freq=torch.tensor(inv32, device="cuda"),
+                   half=half)
+    check(f64(cache)[at // 64 % 4, at % 64, 512:], f64(pe), angles(inv32, at))
 
 
 @pytest.mark.parametrize("half", [False, True])

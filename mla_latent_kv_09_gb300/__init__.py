@@ -265,11 +265,12 @@ def topk_indices(scores, cache_lens, topk: int, *, causal: bool = False, max_len
 
 def _tensor(t, name: str, dtype, shape, device, contiguous: bool = True):
     """Checks a tensor argument: its type, shape and device, and that it is
-    contiguous, or with contiguous=False that its last dim is.  (Called for
-    every tensor of a call that may be shorter than ten of these checks: it
-    does little, and words are found only for a failure.)"""
+    contiguous, or with contiguous=False that its last dim is (whose stride says
+    nothing if it is one).  (Called for every tensor of a call that may be
+    shorter than ten of these checks: it does little, and words are found only
+    for a failure.)"""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not (
-            t.is_contiguous() if contiguous else t.stride(-1) == 1):
+            t.is_contiguous() if contiguous else t.stride(-1) == 1 or t.shape[-1] == 1):
         raise ValueError(f"{name}: expected {dtype} {list(shape)} on GPU {device}, "
                          f"{'contiguous' if contiguous else 'unit stride in the last dim'}; got {t.dtype} "
                          f"{list(t.shape)} on {t.device}, strides {list(t.stride())}")

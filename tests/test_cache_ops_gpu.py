@@ -375,6 +375,22 @@ def test_a_slice_of_a_wider_block_table():
         assert int(status) == m.MLA_ERR_BAD_TABLE and torch.equal(a, before)
 
 
+def test_a_block_table_of_one_column_may_have_any_stride():
+    """The stride of a dim of one says nothing: a row turned into a column."""
+    x = rand((3, 576), 1)
+    ints = lambda *a: torch.tensor(a, device="cuda", dtype=torch.int32)  # noqa: E731
+    column = ints([3, 1, 2]).t()
+    assert column.shape == (3, 1) and column.stride() == (1, 3)
+    spaced = ints([3, 0, 0], [1, 0, 0], [2, 0, 0])[:, :1]
+    want = pool(4, False, 5)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.cache_append(x[:, :512], x[:, 512:], want, ints([3], [1], [2]), ints(0, 5, 63), status=status)
+    for bt in (column, spaced):
+        got = pool(4, False, 5)
+        m.cache_append(x[:, :512], x[:, 512:], got, bt, ints(0, 5, 63), status=status)
+        assert torch.equal(got, want) and int(status) == 0
+
+
 def test_fp8_groups_of_zeros_tiny_huge_and_not_finite_values():
     x = rand((8, 576), 3).float()
     x[0, :128] = 0

@@ -637,14 +637,15 @@ __global__ void __launch_bounds__(128) mla_prefix_empty_kernel(const __grid_cons
   grid_dependency_wait();
   const long long at = static_cast<long long>(blockIdx.x) * 128 + threadIdx.x;
   const long long row = at / (kHeadDim / 8);
-  if (row >= static_cast<long long>(p.num_tokens) * p.num_heads) return;
+  const bool real = row < static_cast<long long>(p.num_tokens) * p.num_heads;
   const int col = static_cast<int>(at % (kHeadDim / 8)) * 8;
-  const float other2 = p.suffix_lse ? p.suffix_lse[row] * kLog2e : -INFINITY;
+  const float other = real && p.suffix_lse ? p.suffix_lse[row] : -INFINITY;
   const float zero[8] = {};
-  write8(p, row, col, zero, join(-INFINITY, other2));
-  // 16 threads of one warp share the row: the one that writes its LSE does so after all have read it
-  __syncwarp(__activemask());
-  if (col == 0) p.lse[row] = p.suffix_lse ? p.suffix_lse[row] : -INFINITY;
+  if (real) write8(p, row, col, zero, join(-INFINITY, other * kLog2e));
+  // 16 threads of one warp share the row: the one that writes its LSE, which may
+  // be the suffix's, does so after all have read it
+  __syncwarp();
+  if (real && col == 0) p.lse[row] = other;
 }
 
 // ============================================================ host side

@@ -494,6 +494,19 @@ def test_heads_cut_in_pieces_with_a_suffix_and_partly_visible(T, H, P, how):
         assert torch.equal(nan, got.isnan()) and bool((((got - ref).abs() <= tol) | nan).all())
 
 
+@pytest.mark.parametrize("T,H", [(1, 1), (20, 3), (333, 7)])
+def test_no_prefix_in_place(T, H):
+    """The suffix's result, written over itself."""
+    x = inputs(T, H, 5)
+    so, sl = rand((T, H, 128), 6), rand((T, H), 7, torch.float32)
+    sl[::2] = -math.inf
+    so[::2] = float("nan")
+    want, want_lse = torch.where(torch.isfinite(sl)[..., None], so, 0), sl.clone()
+    for _ in range(3):
+        out, lse = m.prefix_attend(*x, SCALE, prefix_len=0, suffix_out=so, suffix_lse=sl, out=so, lse=sl)
+        assert out is so and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 @pytest.mark.parametrize("T", [4, 200])
 def test_fewer_rows_than_held_and_what_lies_behind_them(T):
     """Rows behind prefix_len may hold anything."""

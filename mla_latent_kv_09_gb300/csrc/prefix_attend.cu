@@ -428,6 +428,7 @@ mla_prefix_attend_kernel(const __grid_constant__ AttendParams p, const __grid_co
 #pragma unroll 1
       for (uint32_t c = c0; c < c0 + 32u; c += 16u) {
         uint32_t a[16], b[16];
+        __syncwarp();  // lanes without a row have gone round sooner; the loads are the whole warp's
         tmem_ld16(to + c, a);
         if (second) tmem_ld16(to + 128u + c, b);
         tmem_wait_ld();

@@ -95,11 +95,11 @@ int mla_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, const
  *                that token is skipped.  Never cleared by the call.
  * Every other row of the cache is left as it was.  No two tokens may name the
  * same row (which of them it then holds is not defined, and it may mix them).
- * The latent is normed in fp32 and rounded once, to bf16 or to E4M3.  An FP8
- * group of 128 dims takes the smallest power-of-two scale that brings its
- * largest finite magnitude to at most 448 (scale 1 for a group of zeros, and
- * no scale below 2^-127); dims that are not finite become NaN codes; the
- * row's 12 unused bytes are written as zeros. */
+ * The latent is normed in fp32 (its squares may leave fp32's range) and rounded
+ * once, to bf16 or to E4M3.  An FP8 group of 128 dims takes the smallest
+ * power-of-two scale that brings its largest finite magnitude to at most 448
+ * (scale 1 for a group of zeros, and no scale below 2^-127); dims that are not
+ * finite become NaN codes; the row's 12 unused bytes are written as zeros. */
 int mla_cache_append(const void* latent, int64_t latent_stride, const void* k_pe, int64_t k_pe_stride,
                      const void* norm_weight, float eps, const double* inv_freq, float rope_scale,
                      const int32_t* positions, const int32_t* request_ids, int num_tokens,

@@ -6,7 +6,7 @@
 // ones.  Measured: rotation of 8192 tokens x 128 heads x 192 dims 117.6 us (805
 // MB at 6.85 TB/s, a copy's rate; half layout 122), 1332 x 64 x 128 in the half
 // layout 6.9 us where the rows lie in L2, 9.6 from the HBM (44 MB), 64 x 128 x 64
-// 2.0 us; append of 8192 tokens 4.6 us (19 MB), of 64 tokens 2.2 us.
+// 2.0 us; append of 8192 tokens 4.7 us (19 MB), of 64 tokens 2.2 us.
 //
 // Angles.  Pair i at position p turns by p * f_i radians.  In fp32 that loses
 // the angle at far positions (at p = 2^20 one ulp is 1/16 radian), and fp64
@@ -253,12 +253,27 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
     }
   }
   if (p.weight) {
-    float ss = 0.f;
+    auto squares = [&x] {
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = 1.0f / sqrtf(ss * (1.0f / kLatent) + p.eps);
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      return ss;
+    };
+    float mean = squares() * (1.0f / kLatent), eps = p.eps;
+    // Squares beyond fp32's range, at either end, where eps does not outweigh
+    // them: again with the latent times a power of two, which the norm drops
+    // (2^-70 keeps the sum of 512 squares finite; 2^100 brings the least bf16
+    // number, 2^-133, to where its square is a normal one).
+    if (!(mean + eps < INFINITY) || mean + eps < 1e-30f) {
+      const float by = mean < 1.f ? 0x1p100f : 0x1p-70f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= by;
+      mean = squares() * (1.0f / kLatent);
+      eps = eps * by * by;
+    }
+    const float r = 1.0f / sqrtf(mean + eps);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint4 wv = *reinterpret_cast<const uint4*>(p.weight + 256 * i + 8 * lane);

@@ -411,6 +411,23 @@ def test_fp8_groups_of_zeros_tiny_huge_and_not_finite_values():
     assert_rows(cache[0, :8], lat, pe, x[:, 512:], False, True)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_latents_whose_squares_leave_the_range_of_fp32(fp8, eps):
+    """Normed, they are numbers of order one all the same (or, below sqrt(eps),
+    small ones)."""
+    x = rand((8, 576), 51).float()
+    x[:, :512] *= torch.tensor([1e18, 3e19, 1e30, 1e37, 1e-17, 1e-25, 1e-38, 1.0], device="cuda")[:, None]
+    x = x.to(torch.bfloat16)
+    w = (1 + 0.2 * rand((512,), 52).float()).to(torch.bfloat16)
+    cache, pos = pool(1, fp8, 4), torch.arange(8, device="cuda", dtype=torch.int32)
+    m.cache_append(x[:, :512], x[:, 512:], cache, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), pos, norm_weight=w,
+                   eps=eps)
+    lat, pe = oracle.appended_rows(f64(x[:, :512]), f64(x[:, 512:]), pos.cpu().numpy(), f64(w), eps)
+    rows = slice(None) if eps == 0 else [0, 1, 2, 3, 4, 5, 7]  # 1e-38 / sqrt(eps): below bf16's normal numbers' precision
+    assert_rows(cache[0, :8][rows], lat[rows], pe[rows], x[rows, 512:], False, fp8)
+
+
 def test_appended_rows_are_what_the_decode_reads():
     """Append a request's tokens, then decode over them: bf16 and FP8 rows."""
     L = 150

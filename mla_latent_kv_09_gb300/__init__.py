@@ -347,7 +347,7 @@ def rope(x, positions, inv_freq, *, offset: int = 0, half: bool = False, inverse
     """Rotary positions over part of each head.
 
     x [T, H, D] bf16 (tokens and heads may be strided), positions [T] int32,
-    inv_freq [R / 2] fp64 (see `rope_frequencies`): dims [offset, offset + R)
+    inv_freq [R / 2] fp64 (see `rope_frequencies`; below 2^52): dims [offset, offset + R)
     of row (t, h) are turned by positions[t] * inv_freq and multiplied by
     `scale`, the others copied.  Pairs are (2i, 2i + 1), or (i, i + R / 2)
     with half=True; inverse=True turns back (the gradient of the rotation, and
@@ -405,7 +405,8 @@ def cache_append(latent, k_pe, kv_cache, block_table, positions, *, request_ids=
     `rope` does, with `half` and `rope_scale`).  No two tokens may name the
     same row.  `status` (int32 device tensor, one element) receives
     MLA_ERR_BAD_TABLE if a token's request, position or page is out of range;
-    that token is skipped.  Returns kv_cache.
+    that token is skipped (without a `status` nobody learns of it).  Returns
+    kv_cache.
     """
     import torch
     dev = latent.get_device()
@@ -452,9 +453,10 @@ def prefix_expand(kv_cache, block_table, prefix_len: int, w_uk, w_uv, *, out=Non
     [H, 512, 128] bf16 (as for `absorb_q` / `absorb_o`).  Returns (k_nope
     [H, R, 128] bf16, k_pe [R, 64] bf16, v [H, R, 128] fp16), by default new
     with R = prefix_len; `out` may hold them with any R >= prefix_len, whose
-    further rows are left as they are.  `status` receives MLA_ERR_BAD_TABLE for
-    a page outside the pool and MLA_ERR_VALUE_RANGE for a key or value that is
-    not finite once rounded.
+    further rows are left as they are.  `status` (int32 device tensor, one
+    element; without it nobody learns of these) receives MLA_ERR_BAD_TABLE for a
+    page outside the pool and MLA_ERR_VALUE_RANGE for a key or value that is not
+    finite once rounded.
     """
     import torch
     dev = kv_cache.get_device()
@@ -498,16 +500,18 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
     """Attention of T query tokens over one shared, expanded prefix.
 
     q_nope [T, H, 128], q_pe [T, H, 64] bf16 with one row stride (slices of a
-    [T, H, 192] projection output; q_pe already turned); k_nope [H, R, 128],
-    k_pe [R, 64], v [H, R, 128] as `prefix_expand` returns them, of which the
-    first prefix_len (default R) rows count; every value of them finite.
+    [T, H, 192] projection output q, turned by rope(q, ..., offset=128, out=q));
+    k_nope [H, R, 128], k_pe [R, 64], v [H, R, 128] as `prefix_expand` returns
+    them, of which the first prefix_len (default R) rows count; every value of
+    them finite.
     visible [T] int32: token t sees the first visible[t] rows only (padded
     tokens: 0).  suffix_out [T, H, 128] bf16 and suffix_lse [T, H] fp32: what
     each (token, head) attended to elsewhere (`decode_step`'s output through
     `absorb_o`, and its LSE); the result is then the attention over both.
     Returns (out [T, H, 128] bf16 or fp32, lse [T, H] fp32); out and lse may
     be suffix_out and suffix_lse themselves.  `workspace` (uint8,
-    mla_prefix_attend_workspace_size bytes) is allocated if not given.
+    mla_prefix_attend_workspace_size bytes) is allocated if not given; `status`
+    receives MLA_ERR_TIMEOUT if a device wait runs out.
     """
     import torch
     dev = q_nope.get_device()

@@ -4,8 +4,8 @@
 // Both are streams: every element is read once and written once, a few
 // operations each, so HBM bounds the long calls and launch latency the short
 // ones.  Measured: rotation of 8192 tokens x 128 heads x 192 dims 117.6 us (805
-// MB at 6.85 TB/s, a copy's rate; half layout 122), 1332 x 64 x 128 in the half
-// layout 6.9 us where the rows lie in L2, 9.6 from the HBM (44 MB), 64 x 128 x 64
+// MB at 6.85 TB/s, a copy's rate; half layout 121), 1332 x 64 x 128 in the half
+// layout 6.9 us where the rows lie in L2, 9.3 from the HBM (44 MB), 64 x 128 x 64
 // 2.0 us; append of 8192 tokens 4.7 us (19 MB), of 64 tokens 2.2 us.
 //
 // Angles.  Pair i at position p turns by p * f_i radians.  In fp32 that loses
@@ -83,7 +83,7 @@ struct RopeParams {
 
 // One CTA: one token, its heads in turns of per_turn * kRopeItems, or several
 // tokens of few heads (8192 tokens x 1 head x 64 dims 22 us with a CTA each,
-// 4.8 so).  A unit is 8 contiguous dims: 4 interleaved pairs, or 8 copied dims; a warp's units are
+// 4.0 so).  A unit is 8 contiguous dims: 4 interleaved pairs, or 8 copied dims; a warp's units are
 // neighbours in memory.  A thread keeps one unit for all its heads: its cosines
 // and sines stay in registers, and nothing is divided in the loop.  In the half
 // layout a unit's 8 dims need their 8 partners: there the two threads of a unit

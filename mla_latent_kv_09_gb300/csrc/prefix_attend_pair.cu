@@ -30,10 +30,10 @@
 // before is done.  Each thread keeps its own sums, against the maximum it last
 // saw.
 //
-// Measured, whole calls: 256 tokens x 16384 rows x 128 heads 238 us (4.5 TB/s,
-// 1.2 PFLOP/s; 245 to 252 with scores that move the maximum late, 276 of them for
-// seconds on end, at the 1.7 GHz that the power limit leaves), 2048 x 4096 x 16 59
-// us (1.46 PFLOP/s).  A key tile takes a pair about 1,950 cycles, of which
+// Measured, whole calls: 256 tokens x 16384 rows x 128 heads 226 us (4.8 TB/s,
+// 1.5 PFLOP/s; 246 to 252 with scores that move the maximum late, 281 of them for
+// seconds on end, at the 1.7 GHz that the power limit leaves), 2048 x 4096 x 16 58
+// us (1.48 PFLOP/s).  A key tile takes a pair about 1,950 cycles, of which
 // the products are 1,550 (an MMA with A in shared memory takes 83 cycles, with
 // A in tensor memory 69, of the 64 that M = 256 N = 128 K = 16 would need); the
 // rest are waits along the chain scores -> softmax -> value product.  Two row

@@ -17,7 +17,7 @@
 // line, head by head, cut into equal ranges, one per pair.
 //
 // Measured: 8192 rows x 128 heads 157 to 163 us (1.7 PFLOP/s, 3.35 TB/s written;
-// called for seconds on end 182 to 187, as the power limit, 1,378 W, then holds
+// called for seconds on end 182 to 194, as the power limit, 1,378 W, then holds
 // the clock at 1.5 GHz).  Without its stores the kernel takes 133 us, with half
 // of its products 156: the results' way out (shuffles and stores share the data
 // path that the MMAs read their operands on) and the products get in each
@@ -42,7 +42,7 @@
 // bits and a power of two), by every pair for every head, so that a prefix needs
 // one launch and no workspace.  Against a kernel that widens the prefix once, in
 // a workspace, for the bf16 product: 100 rows x 16 heads 8.4 / 9.0 us, 1000 x 16
-// 10.4 / 10.9 (and 9 us less of the host's time), 4000 x 64 65 / 52.3, 8192 x 128
+// 10.2 / 10.9 (and 9 us less of the host's time), 4000 x 64 65 / 52.3, 8192 x 128
 // 238 / 165: there the widening (890 cycles a chunk) and the way to the other
 // SM's issuers hold up the products' 690.  Not kept (measured while rank 1's
 // converters released to their own CTA only, which orders nothing for an issuer

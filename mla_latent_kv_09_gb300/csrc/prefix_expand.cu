@@ -16,10 +16,11 @@
 // drained under the next one's products.  (row tile, head) items form one
 // line, head by head, cut into equal ranges, one per pair.
 //
-// Measured: 8192 rows x 128 heads 157 to 163 us (1.7 PFLOP/s, 3.35 TB/s written;
-// called for seconds on end 182 to 194, as the power limit, 1,378 W, then holds
-// the clock at 1.5 GHz).  Without its stores the kernel takes 133 us, with half
-// of its products 156: the results' way out (shuffles and stores share the data
+// Measured: 8192 rows x 128 heads 166 us (1.66 PFLOP/s, 3.25 TB/s written; called
+// for seconds on end 187 to 194, as the power limit, 1,378 W, then holds the clock
+// at 1.5 GHz).  The rest was measured with two issuing warps, 157 to 163 us.
+// Without its stores the kernel took 133 us, with half of its products 156: the
+// results' way out (shuffles and stores share the data
 // path that the MMAs read their operands on) and the products get in each
 // other's way.  Streaming stores, 64 bytes a row over four lanes, are the best of
 // those tried: not streaming 165 to 170, 128 bytes over eight lanes 161, 32-byte
@@ -29,14 +30,15 @@
 // memory); keys and values as two N = 128 products that share A (184).
 //
 //   warp 0     TMA: latents and weights
-//   warps 1, 11  MMA issue (rank 0, for both CTAs), in turns; with an FP8 cache
-//              rank 1's pass its converters' arrivals on to them
+//   warp 1     MMA issue (rank 0, for both CTAs)
 //   warps 2-9  drain: tensor memory -> bf16 / fp16 -> global memory, 64 columns
 //              at a time; keys and values by four warps each
 //   warp 10    copies the RoPE dims and checks the block table
 //
 //   warps 12-19  (FP8 cache only) widen the latents: TMA brings a chunk's codes
 //              into the upper half of its slot, bf16 replaces them
+//   warps 1, 11  of rank 1 (FP8 cache only) pass its converters' arrivals on to
+//              rank 0's warp 1
 //
 // FP8 rows are widened on their way into shared memory (exactly: 4 significant
 // bits and a power of two), by every pair for every head, so that a prefix needs
@@ -44,7 +46,7 @@
 // a workspace, for the bf16 product: 100 rows x 16 heads 8.4 / 9.0 us, 1000 x 16
 // 10.2 / 10.9 (and 9 us less of the host's time), 4000 x 64 65 / 52.3, 8192 x 128
 // 238 / 165: there the widening (890 cycles a chunk) and the way to the other
-// SM's issuers hold up the products' 690.  Not kept (measured while rank 1's
+// SM's issuer hold up the products' 690.  Not kept (measured while rank 1's
 // converters released to their own CTA only, which orders nothing for an issuer
 // in the other; 205 us so): four warps 274 us, six or three warps with a chunk
 // each 277 and 375, the next chunk's codes read ahead 322, integer widening 219.
@@ -74,14 +76,16 @@ constexpr int kSlots = 6;
 constexpr int kOffW = 0;
 constexpr int kOffRing = kStages * kChunk;                // 128 KiB
 constexpr int kOffBar = kOffRing + kSlots * kChunk;       // 224 KiB
-constexpr int kNumBars = 4 * kSlots + 2 * kStages + 4 + 3;
+constexpr int kNumBars = 4 * kSlots + 2 * kStages + 4 + 1;
 constexpr int kSlack = 1024;                 // re-aligned to 1024 B (128-byte swizzle atoms)
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
 static_assert(kSmem <= 232448, "shared memory");
-constexpr int kThreads = 384;
-constexpr int kConverters = 8;               // further warps, FP8 cache only: two groups of four
+constexpr int kThreads = 352;
+constexpr int kRelayWarp = 11;               // further warps, FP8 cache only: the relay of odd chunks,
+constexpr int kConverterWarp = 12;           // and two groups of four
+constexpr int kConverters = 8;
 static_assert(kSlots % 2 == 0, "a slot's chunks are one group's");
-constexpr int kThreadsFp8 = kThreads + 32 * kConverters;
+constexpr int kThreadsFp8 = 32 * (kConverterWarp + kConverters);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = idesc_bf16(256, 256, 1);
 
@@ -124,7 +128,6 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
   auto acc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 2 + s); };
   auto raw_full = [&](uint32_t s) { return bar0 + 8u * (2 * kSlots + 2 * kStages + 4 + s); };  // codes (FP8 cache)
   auto widened = [&](uint32_t s) { return bar0 + 8u * (3 * kSlots + 2 * kStages + 4 + s); };  // bf16 (FP8 cache, rank 1)
-  auto turn = [&](uint32_t issuer) { return bar0 + 8u * (kNumBars - 3 + issuer); };
   const uint32_t bar_drain = bar0 + 8u * (kNumBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
@@ -142,11 +145,10 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       mbar_init(w_empty(k), 1);
     }
     for (uint32_t s = 0; s < 2; ++s) {
-      mbar_init(acc_full(s), 2);    // both issuers
+      mbar_init(acc_full(s), 1);
       mbar_init(acc_empty(s), 16);  // the drain warps of both CTAs
-      mbar_init(turn(s), 1);
     }
-    mbar_init(bar_drain, 2);  // both issuers
+    mbar_init(bar_drain, 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -223,70 +225,63 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == 11) {
-    const uint32_t me = warp == 1 ? 0u : 1u;
-    if (rank == 0) {
-      // Two warps issue, stages of 64 latent dims (512 cycles of products) in
-      // turns, all into the tile's accumulator: between its four MMAs and its
-      // next ones a warp commits, gives the turn away and waits for its next
-      // chunk, 300 cycles in which the tensor core, which queues one or two
-      // MMAs, would run dry (one issuer: 5,700 cycles a tile).  The whole warp
-      // runs, one lane issues (uniform operands).
-      const uint32_t leader = lane == 0 ? 1u : 0u;
-      const uint64_t wd = smem_desc(sbase + kOffW, kChunk / 2, 1024u);   // MN-major: 64-column halves kChunk / 2 apart
-      const uint64_t ad = smem_desc(sbase + kOffRing, 16u, 1024u);
-      uint32_t heads = 0, turns = 0, chunk = me;
-      int m = m0;
-      bool ok = true;
-      for (int i = 0; ok && i < n; ++i) {
-        const uint32_t buf = i & 1, d = tmem + 256u * buf;
-        const bool new_head = i == 0 || m == 0, last = m == tiles - 1;
+  } else if (warp == 1 && rank == 0) {
+    // One thread issues all products, in the order of their sum.  Two warps with
+    // a stage each in turns fill the gaps in which a commit and a wait let the
+    // tensor core run dry (8192 x 128 in 160 us instead of 166), but a token that
+    // passes between them does not keep their MMAs in order: once in a thousand
+    // calls a value's last bit differed.  The whole warp runs, one lane issues
+    // (uniform operands).  Commits or waits between a stage's MMAs: 171 to 185.
+    const uint32_t leader = lane == 0 ? 1u : 0u;
+    const uint64_t wd = smem_desc(sbase + kOffW, kChunk / 2, 1024u);   // MN-major: 64-column halves kChunk / 2 apart
+    const uint64_t ad = smem_desc(sbase + kOffRing, 16u, 1024u);
+    uint32_t heads = 0, chunk = 0;
+    int m = m0;
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+      const uint32_t buf = i & 1, d = tmem + 256u * buf;
+      const bool new_head = i == 0 || m == 0, last = m == tiles - 1;
+      if (i >= 2) ok = warp_wait_uniform<true>(acc_empty(buf), ((i >> 1) - 1) & 1, ctl);
 #pragma unroll
-        for (uint32_t e = 0; e < kStages / 2; ++e) {
-          const uint32_t k = 2 * e + me, s = chunk % kSlots;
-          if (k == 0 && i >= 2) ok = warp_wait_uniform<true>(acc_empty(buf), ((i >> 1) - 1) & 1, ctl);
-          if (new_head) ok = ok && warp_wait_uniform<true>(w_full(k), heads & 1, ctl);
-          ok = ok && warp_wait_uniform<true>(a_full(s), (chunk / kSlots) & 1, ctl);
-          chunk += 2;
-          if (k != 0 || i != 0) ok = ok && warp_wait_uniform(turn(me), turns++ & 1, ctl);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_pair_ss_if(leader, d, ad + static_cast<uint64_t>((s * kChunk + 32 * kk) >> 4),
-                            wd + static_cast<uint64_t>((k * kChunk + 2048 * kk) >> 4), kIdesc,
-                            (k | kk) != 0 ? 1u : 0u);
-          tc_fence_before();
-          if (leader) mbar_arrive_relaxed(turn(me ^ 1u));
-          umma_commit_pair_if(leader, a_empty(s), 3);
-          if (last) umma_commit_pair_if(leader, w_empty(k), 3);
-        }
+      for (uint32_t k = 0; k < kStages; ++k, ++chunk) {
+        const uint32_t s = chunk % kSlots;
+        if (new_head) ok = ok && warp_wait_uniform<true>(w_full(k), heads & 1, ctl);
+        ok = ok && warp_wait_uniform<true>(a_full(s), (chunk / kSlots) & 1, ctl);
         if (!ok) break;
-        umma_commit_pair_if(leader, acc_full(buf), 3);  // both issuers' products
-        if (new_head) ++heads;
-        m = last ? 0 : m + 1;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_pair_ss_if(leader, d, ad + static_cast<uint64_t>((s * kChunk + 32 * kk) >> 4),
+                          wd + static_cast<uint64_t>((k * kChunk + 2048 * kk) >> 4), kIdesc,
+                          (k | kk) != 0 ? 1u : 0u);
+        umma_commit_pair_if(leader, a_empty(s), 3);
+        if (last) umma_commit_pair_if(leader, w_empty(k), 3);
       }
-      umma_commit_pair_if(leader, bar_drain, 1);  // arrives once every MMA issued above has completed
-      drain_bar(bar_drain, 0u);
-      __syncwarp();
-    } else if (kFp8) {
-      // Rank 1's issuers have nothing to issue: they relay its converters'
-      // arrivals to rank 0, whose MMAs read this CTA's rows too.  The converters
-      // release to their own CTA; a thread without stores of its own, which has
-      // acquired their rows, releases to the cluster.  That is slow beside the
-      // drain's stores (8192 x 128: 236 us; a third relay 232, but then no warp
-      // is left for rank 1's RoPE rows; the converters releasing to the cluster
-      // themselves 337).
-      if (lane == 0) {
-        const uint32_t ra = mapa(a_full(0), 0), chunks = static_cast<uint32_t>(n) * kStages;
-        for (uint32_t chunk = me; chunk < chunks; chunk += 2) {
-          const uint32_t s = chunk % kSlots;
-          if (!wait(widened(s), (chunk / kSlots) & 1, ctl)) break;
-          mbar_arrive_remote(ra + 8u * s);
-        }
-      }
-      __syncwarp();
+      if (!ok) break;
+      umma_commit_pair_if(leader, acc_full(buf), 3);
+      if (new_head) ++heads;
+      m = last ? 0 : m + 1;
     }
+    umma_commit_pair_if(leader, bar_drain, 1);  // arrives once every MMA issued above has completed
+    drain_bar(bar_drain, 0u);
+    __syncwarp();
+  } else if (warp == 1 || warp == kRelayWarp) {
+    // Rank 1 has nothing to issue.  With an FP8 cache two of its warps relay its
+    // converters' arrivals to rank 0, whose MMAs read this CTA's rows too.  The
+    // converters release to their own CTA; a thread without stores of its own,
+    // which has acquired their rows, releases to the cluster.  That is slow beside
+    // the drain's stores (a third relay gains 2 %, but then no warp is left for
+    // rank 1's RoPE rows; the converters releasing to the cluster themselves take
+    // 8192 x 128 from 236 us to 337).
+    if (kFp8 && rank == 1 && lane == 0) {
+      const uint32_t ra = mapa(a_full(0), 0), chunks = static_cast<uint32_t>(n) * kStages;
+      for (uint32_t chunk = warp == 1 ? 0u : 1u; chunk < chunks; chunk += 2) {
+        const uint32_t s = chunk % kSlots;
+        if (!wait(widened(s), (chunk / kSlots) & 1, ctl)) break;
+        mbar_arrive_remote(ra + 8u * s);
+      }
+    }
+    __syncwarp();
   } else if (warp < 10) {
     const int q = warp & 3;  // tensor-memory lanes 32 q .. +31: those rows of the tile
     const bool keys = warp < 6;
@@ -345,14 +340,14 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
         ++h;
       }
     }
-  } else if (kFp8 && warp >= kThreads / 32) {
+  } else if (kFp8 && warp >= kConverterWarp) {
     // Latents from FP8 rows: a chunk's codes (8 KiB) land in the upper half of
     // its slot, each thread of four warps takes 4 x 16 of them (4 lanes a row, 8
     // rows of the warp's 32 at a time), and when all have, bf16 replaces them.
     // That is 1,180 cycles a chunk, most of them latency beside the MMAs' reads
     // of shared memory; two groups of warps, each with every second chunk
     // (always of the same slots, so that it sees all their phases), hide it.
-    const uint32_t g = static_cast<uint32_t>(warp - kThreads / 32) >> 2;
+    const uint32_t g = static_cast<uint32_t>(warp - kConverterWarp) >> 2;
     const int w = warp & 3, sub = lane >> 2, u = lane & 3;
     const uint32_t done = rank == 0 ? a_full(0) : widened(0);
     const uint32_t in = sbase + kOffRing + kChunk / 2 + static_cast<uint32_t>(32 * w) * 64u + static_cast<uint32_t>(lane) * 16u;

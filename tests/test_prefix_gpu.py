@@ -195,6 +195,22 @@ def test_fp8_rows_expand_as_the_bf16_rows_of_their_values(P, H):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_expansion_repeats_bit_for_bit(fp8):
+    """Products are summed in one order, whatever the timing."""
+    P, H = 1394, 128
+    kv, bt, _, _ = cache_and_rows(P, fp8, 33)
+    w_uk, w_uv = rand((H, 512, 128), 1) * 512 ** -0.5, rand((H, 512, 128), 2) * 512 ** -0.5
+    want = m.prefix_expand(kv, bt, P, w_uk, w_uv)
+    out = tuple(torch.empty_like(t) for t in want)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(2000):
+        m.prefix_expand(kv, bt, P, w_uk, w_uv, out=out)
+        for x, y in zip(out, want):
+            differ += (x.view(torch.int16) != y.view(torch.int16)).any()
+    assert int(differ) == 0
+
+
 def test_keys_that_are_not_finite_are_reported():
     kv, bt, lat, pe = cache_and_rows(200, False, 4)
     w_uk, w_uv = rand((2, 512, 128), 1), rand((2, 512, 128), 2)

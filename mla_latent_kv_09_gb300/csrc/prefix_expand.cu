@@ -16,8 +16,8 @@
 // drained under the next one's products.  (row tile, head) items form one
 // line, head by head, cut into equal ranges, one per pair.
 //
-// Measured: 8192 rows x 128 heads 166 us (1.66 PFLOP/s, 3.25 TB/s written; called
-// for seconds on end 187 to 194, as the power limit, 1,378 W, then holds the clock
+// Measured: 8192 rows x 128 heads 163 to 167 us (1.67 PFLOP/s, 3.25 TB/s written;
+// called for seconds on end 187 to 194, as the power limit, 1,378 W, then holds the clock
 // at 1.5 GHz).  The rest was measured with two issuing warps, 157 to 163 us.
 // Without its stores the kernel took 133 us, with half of its products 156: the
 // results' way out (shuffles and stores share the data
@@ -228,7 +228,7 @@ mla_prefix_expand_kernel(const __grid_constant__ ExpandParams p, const __grid_co
   } else if (warp == 1 && rank == 0) {
     // One thread issues all products, in the order of their sum.  Two warps with
     // a stage each in turns fill the gaps in which a commit and a wait let the
-    // tensor core run dry (8192 x 128 in 160 us instead of 166), but a token that
+    // tensor core run dry (8192 x 128 in 160 us instead of 165), but a token that
     // passes between them does not keep their MMAs in order: once in a thousand
     // calls a value's last bit differed.  The whole warp runs, one lane issues
     // (uniform operands).  Commits or waits between a stage's MMAs: 171 to 185.

@@ -247,6 +247,36 @@ def test_rows_and_pages_beyond_32_bit_offsets():
                         heads=np.array([0, H - 1]))
 
 
+@pytest.mark.parametrize("P", [130, 0])
+def test_more_query_rows_than_32_bit_offsets_reach(P):
+    """More than 2^31 elements between the first and the last token's rows."""
+    T, H = 140000, 128
+    q = torch.empty((T, H, 192), dtype=torch.bfloat16, device="cuda").fill_(0.5)
+    q[:2], q[-3:] = rand((2, H, 192), 1), rand((3, H, 192), 2)
+    k, pe, v = rand((H, P, 128), 3), rand((P, 64), 4), rand((H, P, 128), 5, torch.float16)
+    so, sl = torch.zeros((T, H, 128), dtype=torch.bfloat16, device="cuda"), torch.full((T, H), -math.inf, device="cuda")
+    so[-3:], sl[-3:] = rand((3, H, 128), 6), rand((3, H), 7, torch.float32)
+    ends = lambda t: torch.cat([t[:2], t[-3:]])  # noqa: E731
+    suffix = ends(so), ends(sl)
+    status = status_word()
+    out, lse = m.prefix_attend(q[..., :128], q[..., 128:], k, pe, v, SCALE, suffix_out=so, suffix_lse=sl, out=so, lse=sl,
+                               status=status)
+    assert int(status) == 0
+    some = ends(q)
+    assert_attended(ends(out), ends(lse), some[..., :128], some[..., 128:], k, pe, v, suffix=suffix, heads=np.array([0, 64, 127]))
+    # the tokens between have one query: each within the bound of its result (heads
+    # are cut at other places from row block to row block, so not bit for bit)
+    a = [f64(t) for t in (q[2:3, :, :128], q[2:3, :, 128:], k, pe, v)]
+    ref, ref_lse = oracle.prefix_attend(*a, SCALE)
+    bo, bl = oracle.attend_error_bound(*a, SCALE, ref)
+    ref, bo, bl = [torch.tensor(t, device="cuda") for t in (ref, bo + 2.0 ** -8 * np.abs(ref) * 1.01, bl + 2.0 ** -21)]
+    ref_lse = torch.tensor(ref_lse, device="cuda")
+    for t in range(2, T - 3, 10000):
+        part = slice(t, min(t + 10000, T - 3))
+        assert bool(((out[part].double() - ref).abs() <= bo).all())
+        assert bool(((lse[part].double() - ref_lse).abs() <= bl).all()) if P else bool((lse[part] == -math.inf).all())
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_expansion_captured_replayed_and_beside_another(fp8):
     """A replay reads the cache as it is then; two calls at once on two streams

@@ -16,7 +16,12 @@ kernels); this package is its Python face:
   * `rope` / `rope_frequencies` / `softmax_scale` and `cache_append`, which
     turn the RoPE dims and put tokens into the paged latent cache;
   * `prefix_expand` / `prefix_attend`, attention for a batch that shares a
-    long prefix: its keys and values expanded once, attended to by all.
+    long prefix: its keys and values expanded once, attended to by all;
+  * `chunk_attend`, attention of chunks of new tokens (any number a request)
+    over the paged cache;
+  * `attention_weights` / `evict_select` / `cache_compact`, which shrink a
+    cache by what was attended to: the weight every row received, the rows
+    that stay, and their move to pages of their own.
 
 PyTorch is used only to allocate device memory and to name streams.
 """
@@ -46,7 +51,13 @@ from ._binding import (  # noqa: F401
     load,
     mla_absorb_o,
     mla_absorb_q,
+    mla_attention_weights,
+    mla_attention_weights_workspace_size,
     mla_cache_append,
+    mla_cache_compact,
+    mla_chunk_attend,
+    mla_chunk_attend_workspace_size,
+    mla_evict_select,
     mla_indexer_scores,
     mla_prefix_attend,
     mla_prefix_attend_workspace_size,
@@ -567,3 +578,251 @@ def prefix_attend(q_nope, q_pe, k_nope, k_pe, v, softmax_scale: float, *, prefix
                       suffix_out, suffix_lse, MLA_FLAG_OUT_FP32 if out_fp32 else 0, workspace,
                       0 if workspace is None else workspace.numel(), out, lse, status, stream)
     return out, lse
+
+
+def _request_args(q, kv_cache, block_table, cache_lens, token_starts, max_len, dev):
+    """The checks that `chunk_attend` and `attention_weights` share: tokens,
+    requests, the bound of their lengths, the table's row stride and the
+    cache's flag."""
+    import torch
+    T = q.shape[0]
+    _tensor(q, "q", torch.bfloat16, (T, NUM_HEADS, D_QK), dev)
+    flags = _cache_flags(kv_cache, dev)
+    B, width = block_table.shape
+    _tensor(block_table, "block_table", torch.int32, (B, width), dev, contiguous=False)
+    _tensor(cache_lens, "cache_lens", torch.int32, (B,), dev)
+    if token_starts is not None:
+        _tensor(token_starts, "token_starts", torch.int32, (B + 1,), dev)
+    elif B == 0 or T % B:
+        raise ValueError("token_starts: needed where the requests have different numbers of tokens")
+    if max_len is None:
+        max_len = width * PAGE
+    elif not 0 < max_len <= width * PAGE:
+        raise ValueError("max_len: outside the block table")
+    # (the stride of a dim of one says nothing)
+    bt_stride = block_table.stride(0) if B > 1 else width
+    if bt_stride < width:
+        raise ValueError("block_table: its rows overlap")
+    return T, B, max_len, bt_stride, flags
+
+
+def chunk_attend(q, kv_cache, block_table, cache_lens, softmax_scale: float, *, token_starts=None, causal: bool = True,
+                 max_len: int | None = None, out_fp32: bool = False, out=None, lse=None, workspace=None, status=None,
+                 stream=None):
+    """Attention of chunks of new tokens over the paged latent cache: the
+    decode step's, for any number of tokens a request.
+
+    q [T, 128, 576] bf16 (as `absorb_q` returns it), the requests' tokens one
+    after the other; kv_cache and block_table [B, W] int32 (rows may be
+    strided) as for `cache_append`, which has put the new tokens' own rows into
+    the cache; cache_lens [B] int32 counts them.  token_starts [B + 1] int32:
+    request b's tokens are token_starts[b] .. token_starts[b + 1] - 1, and
+    tokens of no request are left as they were; None: B equal runs.  causal:
+    token i of request b's n sees its first cache_lens[b] - n + i + 1 rows,
+    else all.  max_len bounds every cache_lens[b] (default 64 W; an FP8 cache
+    needs B * max_len * 1152 bytes of workspace).  Returns (out [T, 128, 512]
+    bf16 or fp32, lse [T, 128] fp32); a token that sees nothing gets 0 and
+    -inf.  Values have to stay below 65504 in magnitude; rows that no token
+    sees may hold anything.
+
+    The cost of a (token, row) is that of the absorbed form.  Chunks of more
+    than some 200 tokens of one request cost less by `prefix_expand` of its
+    whole cache and `prefix_attend` with `visible` counts.
+
+    `workspace` (uint8, mla_chunk_attend_workspace_size bytes) is allocated if
+    not given; `status` (int32 device tensor, one element; without it nobody
+    learns of these) receives MLA_ERR_BAD_TABLE for a length, start or page out
+    of range and MLA_ERR_TIMEOUT if a device wait runs out.
+    """
+    import torch
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(q, stream, "chunk_attend"):
+            return chunk_attend(q, kv_cache, block_table, cache_lens, softmax_scale, token_starts=token_starts,
+                                causal=causal, max_len=max_len, out_fp32=out_fp32, out=out, lse=lse,
+                                workspace=workspace, status=status)
+    T, B, max_len, bt_stride, flags = _request_args(q, kv_cache, block_table, cache_lens, token_starts, max_len, dev)
+    flags |= (MLA_FLAG_CAUSAL if causal else 0) | (MLA_FLAG_OUT_FP32 if out_fp32 else 0)
+    if out is None:
+        out = torch.empty((T, NUM_HEADS, D_V), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=dev)
+    else:
+        _tensor(out, "out", torch.float32 if out_fp32 else torch.bfloat16, (T, NUM_HEADS, D_V), dev)
+    if lse is None:
+        lse = torch.empty((T, NUM_HEADS), dtype=torch.float32, device=dev)
+    else:
+        _tensor(lse, "lse", torch.float32, (T, NUM_HEADS), dev)
+    if T == 0:
+        return out, lse
+    if workspace is None:
+        need = mla_chunk_attend_workspace_size(T, B, max_len, flags)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+    else:
+        _tensor(status, "status", torch.int32, status.shape, dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    mla_chunk_attend(q, kv_cache, kv_cache.shape[0], block_table, bt_stride, cache_lens, max_len, token_starts, B, T,
+                     NUM_HEADS, softmax_scale, flags, workspace, workspace.numel(), out, lse, status, stream)
+    return out, lse
+
+
+def attention_weights(q, lse, kv_cache, block_table, cache_lens, softmax_scale: float, weights=None, *,
+                      token_starts=None, causal: bool = True, decay: float = 1.0, max_len: int | None = None, out=None,
+                      workspace=None, status=None, stream=None):
+    """The attention weight that every cached row received, summed over heads
+    and tokens and added to what it had:
+
+        out[b, j] = decay * weights[b, j] + sum_t sum_h exp(s[t, h, j] - lse[t, h])
+
+    over request b's tokens that see row j (s: the scores of `chunk_attend` or
+    `decode_step`, whose q, reshaped to [T, 128, 576], and lse [T, 128] fp32
+    these are).  weights [B, >= max_len] fp32 (rows may be strided), or None
+    for none so far; `out` (default: weights itself, or a new tensor of zeros)
+    is returned, left as it was behind each request's rows and in requests
+    without tokens.  The other arguments are `chunk_attend`'s.  Equal calls
+    give equal bits.
+    """
+    import torch
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(q, stream, "attention_weights"):
+            return attention_weights(q, lse, kv_cache, block_table, cache_lens, softmax_scale, weights,
+                                     token_starts=token_starts, causal=causal, decay=decay, max_len=max_len, out=out,
+                                     workspace=workspace, status=status)
+    if max_len is None and (out if out is not None else weights) is not None:
+        max_len = min((out if out is not None else weights).shape[1], block_table.shape[1] * PAGE)
+    T, B, max_len, bt_stride, flags = _request_args(q, kv_cache, block_table, cache_lens, token_starts, max_len, dev)
+    flags |= MLA_FLAG_CAUSAL if causal else 0
+    _tensor(lse, "lse", torch.float32, (T, NUM_HEADS), dev)
+    if out is None:
+        out = torch.zeros((B, max_len), dtype=torch.float32, device=dev) if weights is None else weights
+    for name, t in (("weights", weights), ("out", out)):
+        if t is not None:
+            _tensor(t, name, torch.float32, (B, t.shape[1]), dev, contiguous=False)
+            if t.shape[1] < max_len or (B > 1 and t.stride(0) < max_len):
+                raise ValueError(f"{name}: its rows are shorter than max_len, or overlap")
+    if weights is None:
+        decay = 0.0
+    if T == 0:
+        return out
+    if workspace is None:
+        need = mla_attention_weights_workspace_size(T, B, max_len, flags)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _tensor(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+    else:
+        _tensor(status, "status", torch.int32, status.shape, dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    mla_attention_weights(q, lse, kv_cache, kv_cache.shape[0], block_table, bt_stride, cache_lens, max_len, token_starts,
+                          B, T, NUM_HEADS, softmax_scale, decay, weights,
+                          0 if weights is None else weights.stride(0) if B > 1 else max_len, flags, workspace,
+                          workspace.numel(), out, out.stride(0) if B > 1 else max_len, status, stream)
+    return out
+
+
+def evict_select(weights, cache_lens, keep: int, *, sinks: int = 0, recent: int = 0, out=None, status=None, stream=None):
+    """Which `keep` rows of each request stay.
+
+    weights [B, L] fp32 (rows may be strided; see `attention_weights`),
+    cache_lens [B] int32.  The first `sinks` and the last `recent` rows stay,
+    and of the others those of the largest weight, the first of equal ones
+    (NaN counts as -inf); requests of up to `keep` rows keep all.  Returns
+    (kept [B, keep] int32: increasing positions, then -1; new_lens [B] int32;
+    new_weights [B, L] fp32: the kept rows' weights in their new places, then
+    zeros), by default new; `out` may hold them, new_weights with any width of
+    at least min(keep, L), or None in its place, and not in the memory of
+    `weights`.  `status` receives MLA_ERR_BAD_TABLE for a length out of range
+    (it counts as 0 or L).
+    """
+    import torch
+    dev = weights.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(weights, stream, "evict_select"):
+            return evict_select(weights, cache_lens, keep, sinks=sinks, recent=recent, out=out, status=status)
+    B, L = weights.shape
+    _tensor(weights, "weights", torch.float32, (B, L), dev, contiguous=False)
+    _tensor(cache_lens, "cache_lens", torch.int32, (B,), dev)
+    if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep:
+        raise ValueError("keep: at least 1, and at least the sinks and the recent rows")
+    if out is None:
+        out = (torch.empty((B, keep), dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev),
+               torch.empty((B, L), dtype=torch.float32, device=dev))
+    kept, new_lens, new = out
+    _tensor(kept, "kept", torch.int32, (B, keep), dev)
+    _tensor(new_lens, "new_lens", torch.int32, (B,), dev)
+    if new is not None:
+        _tensor(new, "new_weights", torch.float32, (B, new.shape[1]), dev, contiguous=False)
+        if new.shape[1] < min(keep, L) or (B > 1 and new.stride(0) < new.shape[1]):
+            raise ValueError("new_weights: its rows are too short, or overlap")
+    if B > 1 and weights.stride(0) < L:
+        raise ValueError("weights: its rows overlap")
+    if B == 0 or L == 0:
+        new_lens.zero_()
+        kept.fill_(-1)
+        if new is not None:
+            new.zero_()
+        return out
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+    else:
+        _tensor(status, "status", torch.int32, status.shape, dev)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    mla_evict_select(weights, weights.stride(0) if B > 1 else L, cache_lens, B, L, keep, sinks, recent, kept, new_lens,
+                     new, 0 if new is None else new.stride(0) if B > 1 else new.shape[1],
+                     0 if new is None else new.shape[1], status, stream)
+    return out
+
+
+def cache_compact(cache, block_table, kept, lens, out_table, *, status=None, stream=None):
+    """Copies the kept rows of a paged cache to the pages of another table.
+
+    cache: a latent cache ([num_pages, 64, 576] bf16 or [num_pages, 64, 656]
+    uint8) or the indexer's keys ([num_pages, 64, 128] bf16); row kept[b, i] of
+    request b (its page in block_table [B, W] int32) becomes row i of out_table
+    [B, W'] int32, for i < lens[b]; kept [B, K] and lens [B] int32 as
+    `evict_select` returns them.  The tables' and kept's rows may be strided.
+    No page of out_table may hold a row that is kept, of this request or
+    another; pages that only block_table names can be freed afterwards.  The
+    rows' position dims stay turned by the positions that they were appended
+    at: tokens appended later go to the places behind lens[b] (`cache_append`'s
+    positions), with their position dims turned before (`rope`, and no
+    inv_freq there).  Returns cache.  `status` receives MLA_ERR_BAD_TABLE for a
+    length or page out of range and MLA_ERR_BAD_INDEX for a row outside its
+    request's table; these rows are skipped.
+    """
+    import torch
+    dev = cache.get_device()
+    if stream is not None or dev < 0 or dev != torch._C._cuda_getDevice():
+        with _elsewhere(cache, stream, "cache_compact"):
+            return cache_compact(cache, block_table, kept, lens, out_table, status=status)
+    if cache.dtype == torch.bfloat16 and cache.shape[-1] == 128:
+        _tensor(cache, "cache", torch.bfloat16, (cache.shape[0], PAGE, 128), dev)
+        row_bytes = 256
+    else:
+        row_bytes = 656 if _cache_flags(cache, dev) else 2 * D_QK
+    B, width = block_table.shape
+    K, out_width = kept.shape[1], out_table.shape[1]
+    _tensor(block_table, "block_table", torch.int32, (B, width), dev, contiguous=False)
+    _tensor(out_table, "out_table", torch.int32, (B, out_width), dev, contiguous=False)
+    _tensor(kept, "kept", torch.int32, (B, K), dev, contiguous=False)
+    _tensor(lens, "lens", torch.int32, (B,), dev)
+    if out_table.data_ptr() == block_table.data_ptr() and B:
+        raise ValueError("out_table: the rows cannot stay in their own pages")
+    if B > 1 and (block_table.stride(0) < width or out_table.stride(0) < out_width or kept.stride(0) < K):
+        raise ValueError("block_table, out_table, kept: rows overlap")
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+    else:
+        _tensor(status, "status", torch.int32, status.shape, dev)
+    if B == 0 or K == 0:
+        return cache
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    # (the stride of a dim of one says nothing)
+    mla_cache_compact(cache, cache.shape[0], row_bytes, block_table, block_table.stride(0) if B > 1 else width, width,
+                      kept, kept.stride(0) if B > 1 else K, K, lens, B, out_table,
+                      out_table.stride(0) if B > 1 else out_width, out_width, status, stream)
+    return cache

@@ -1,4 +1,4 @@
-"""ctypes binding of libmla_decode.so: the C ABI of include/mla_decode.h.
+"""ctypes binding of libmla_decode.so: the C ABI of the headers in include/.
 
 Argument marshalling only.  Functions keep the C names and take either raw
 integers (device pointers, sizes) or torch tensors, whose data pointers are
@@ -64,6 +64,16 @@ SIGNATURES = {
     "mla_prefix_attend_workspace_size": (_c_size, [_c_int, _c_int, _c_int, ctypes.POINTER(_c_int)]),
     "mla_prefix_attend": (_c_int, [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _c_int, _vp, _c_int, _c_int, _f32, _vp, _vp,
                                    _uint, _vp, _c_size, _vp, _vp, _vp, _vp]),
+    "mla_chunk_attend_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _uint, ctypes.POINTER(_c_int)]),
+    "mla_chunk_attend": (_c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _f32, _uint, _vp,
+                                  _c_size, _vp, _vp, _vp, _vp]),
+    "mla_attention_weights_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _uint, ctypes.POINTER(_c_int)]),
+    "mla_attention_weights": (_c_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _f32,
+                                       _f32, _vp, _i64, _uint, _vp, _c_size, _vp, _i64, _vp, _vp]),
+    "mla_evict_select": (_c_int, [_vp, _i64, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _i64, _c_int,
+                                  _vp, _vp]),
+    "mla_cache_compact": (_c_int, [_vp, _i64, _c_int, _vp, _i64, _c_int, _vp, _i64, _c_int, _vp, _c_int, _vp, _i64,
+                                   _c_int, _vp, _vp]),
 }
 
 _lib = None
@@ -271,3 +281,52 @@ def mla_prefix_attend(q_nope, q_pe, q_stride: int, k_nope, v, head_rows: int, k_
         _ptr(q_nope), _ptr(q_pe), q_stride, _ptr(k_nope), _ptr(v), head_rows, _ptr(k_pe), prefix_len, _ptr(visible),
         num_tokens, num_heads, softmax_scale, _ptr(suffix_out), _ptr(suffix_lse), flags, _ptr(workspace), ws_bytes,
         _ptr(out), _ptr(lse), _ptr(status), _stream(stream)))
+
+
+def mla_chunk_attend_workspace_size(num_tokens: int, num_requests: int, max_len: int, flags: int) -> int:
+    err = ctypes.c_int(0)
+    n = load().mla_chunk_attend_workspace_size(num_tokens, num_requests, max_len, flags, ctypes.byref(err))
+    _check("mla_chunk_attend_workspace_size", err.value)
+    return n
+
+
+def mla_chunk_attend(q, kv_cache, num_pages: int, block_table, bt_stride: int, cache_lens, max_len: int, token_starts,
+                     num_requests: int, num_tokens: int, num_heads: int, softmax_scale: float, flags: int, workspace,
+                     ws_bytes: int, out, lse, status, stream=None) -> None:
+    _check("mla_chunk_attend", load().mla_chunk_attend(
+        _ptr(q), _ptr(kv_cache), num_pages, _ptr(block_table), bt_stride, _ptr(cache_lens), max_len, _ptr(token_starts),
+        num_requests, num_tokens, num_heads, softmax_scale, flags, _ptr(workspace), ws_bytes, _ptr(out), _ptr(lse),
+        _ptr(status), _stream(stream)))
+
+
+def mla_attention_weights_workspace_size(num_tokens: int, num_requests: int, max_len: int, flags: int) -> int:
+    err = ctypes.c_int(0)
+    n = load().mla_attention_weights_workspace_size(num_tokens, num_requests, max_len, flags, ctypes.byref(err))
+    _check("mla_attention_weights_workspace_size", err.value)
+    return n
+
+
+def mla_attention_weights(q, lse, kv_cache, num_pages: int, block_table, bt_stride: int, cache_lens, max_len: int,
+                          token_starts, num_requests: int, num_tokens: int, num_heads: int, softmax_scale: float,
+                          decay: float, weights, weights_stride: int, flags: int, workspace, ws_bytes: int, out,
+                          out_stride: int, status, stream=None) -> None:
+    _check("mla_attention_weights", load().mla_attention_weights(
+        _ptr(q), _ptr(lse), _ptr(kv_cache), num_pages, _ptr(block_table), bt_stride, _ptr(cache_lens), max_len,
+        _ptr(token_starts), num_requests, num_tokens, num_heads, softmax_scale, decay, _ptr(weights), weights_stride,
+        flags, _ptr(workspace), ws_bytes, _ptr(out), out_stride, _ptr(status), _stream(stream)))
+
+
+def mla_evict_select(weights, weights_stride: int, cache_lens, num_requests: int, max_len: int, keep: int, sinks: int,
+                     recent: int, kept, new_lens, new_weights, new_weights_stride: int, new_width: int, status,
+                     stream=None) -> None:
+    _check("mla_evict_select", load().mla_evict_select(
+        _ptr(weights), weights_stride, _ptr(cache_lens), num_requests, max_len, keep, sinks, recent, _ptr(kept),
+        _ptr(new_lens), _ptr(new_weights), new_weights_stride, new_width, _ptr(status), _stream(stream)))
+
+
+def mla_cache_compact(cache, num_pages: int, row_bytes: int, block_table, bt_stride: int, bt_width: int, kept,
+                      kept_stride: int, kept_width: int, lens, num_requests: int, out_table, out_stride: int,
+                      out_width: int, status, stream=None) -> None:
+    _check("mla_cache_compact", load().mla_cache_compact(
+        _ptr(cache), num_pages, row_bytes, _ptr(block_table), bt_stride, bt_width, _ptr(kept), kept_stride, kept_width,
+        _ptr(lens), num_requests, _ptr(out_table), out_stride, out_width, _ptr(status), _stream(stream)))

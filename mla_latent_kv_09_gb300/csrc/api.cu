@@ -10,16 +10,20 @@
 #include <vector>
 
 #include "common.cuh"
+#include "mla_chunk.h"
 #include "mla_decode.h"
 #include "plan.cuh"
 
 namespace mla {
-__global__ void mla_plan_kernel(const int* lens, int B, int topk, int tile_rows, int U, int* hdr,
-                                int* unit_meta, int* req_meta, int slots_cap);
+cudaError_t plan_launch(const int* lens, int B, int topk, int tile_rows, int U, int* hdr, int* unit_meta, int* req_meta,
+                        int slots_cap, const ChunkPairs* chunk, cudaStream_t stream);
+cudaError_t combine_launch(const int* hdr, const int* req_meta, const float* part_lse, const uint16_t* part_o,
+                           int part_bf16, int s_q, int out_fp32, void* out, float* lse, int n_bt, const ChunkPairs* chunk,
+                           const int* table, long long bt_stride, long long num_pages, cudaStream_t stream);
+__global__ void mla_widen_kernel(const uint8_t* kv, long long num_pages, const int* table, long long bt_stride,
+                                 const int* lens, int max_len, int requests, int pages, uint16_t* wide,
+                                 int* wide_table, int* status);
 __global__ void mla_wait_timeout_kernel(int* status);
-__global__ void mla_combine_kernel(const int* hdr, const int* req_meta, const float* part_lse,
-                                   const uint16_t* part_o, int part_bf16, int s_q, int out_fp32, void* out,
-                                   float* lse, int n_bt);
 __global__ void mla_validate_kernel(const int* lens, const int* bt, long long bt_stride,
                                     long long num_pages, int B, int s_q, const int* topk_idx, int topk,
                                     const uint16_t* kv, int check_range, int* status);
@@ -201,6 +205,63 @@ int encode_out_2d(CUtensorMap* m, void* base, uint64_t rows, bool fp32) {
   return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
 }
 
+int launched(cudaError_t e) {
+  if (e == cudaSuccess) return MLA_OK;
+  cudaGetLastError();
+  return MLA_ERR_CUDA;
+}
+
+int launch_plan(char* ws, const WsLayout& L, const int* lens, int batch, int topk, int tile_rows, int units,
+                const ChunkPairs* chunk, mla_stream_t stream) {
+  return launched(plan_launch(lens, batch, topk, tile_rows, units, reinterpret_cast<int*>(ws + L.hdr),
+                              reinterpret_cast<int*>(ws + L.units), reinterpret_cast<int*>(ws + L.reqs), L.slots, chunk,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+int launch_combine(const char* ws, const WsLayout& L, int batch, int s_q, unsigned flags, void* out, float* lse,
+                   const ChunkPairs* chunk, const int* table, int64_t bt_stride, int64_t num_pages,
+                   mla_stream_t stream) {
+  return launched(combine_launch(reinterpret_cast<const int*>(ws + L.hdr), reinterpret_cast<const int*>(ws + L.reqs),
+                                 reinterpret_cast<const float*>(ws + L.part_lse),
+                                 reinterpret_cast<const uint16_t*>(ws + L.part_o), (flags & MLA_FLAG_BF16_PV) ? 1 : 0, s_q,
+                                 (flags & MLA_FLAG_OUT_FP32) ? 1 : 0, out, lse, batch * s_q, chunk, table, bt_stride,
+                                 num_pages, static_cast<cudaStream_t>(stream)));
+}
+
+// Chunk attention's workspace: the decode step's for its pairs, the pairs, and
+// for an FP8 cache the widened rows behind an identity table.
+struct ChunkLayout {
+  int slots, units, pages;  // pages: of a request's widened rows
+  WsLayout step;
+  size_t pairs, lens, table, wide, total;
+};
+int chunk_layout(int num_tokens, int num_requests, int max_len, unsigned flags, ChunkLayout* c) {
+  if (num_tokens < 0 || num_requests < 1 || max_len < 1) return MLA_ERR_INVALID_ARG;
+  c->slots = static_cast<int>((static_cast<int64_t>(num_tokens) + num_requests) / 2);
+  // rows of q are numbered, and the plan adds tiles, in 32 bits
+  if ((static_cast<int64_t>(num_tokens) + 1) * kHeads > INT32_MAX || max_len > (1 << 30) ||
+      c->slots * (static_cast<int64_t>(max_len) / 128 + 1 + kPlanC0) > INT32_MAX / 2)
+    return MLA_ERR_UNSUPPORTED;
+  const int rc = resolve_units(2, 0, &c->units);
+  if (rc != MLA_OK) return rc;
+  c->step = ws_layout(c->slots, 2, c->units);
+  size_t off = c->step.total;
+  c->pairs = off;
+  off += align256(static_cast<size_t>(c->slots) * sizeof(int4));
+  c->lens = off;
+  off += align256(static_cast<size_t>(c->slots) * sizeof(int));
+  c->pages = (max_len + kPage - 1) / kPage;
+  c->table = c->wide = off;
+  if (flags & MLA_FLAG_KV_FP8) {
+    if (static_cast<int64_t>(num_requests) * c->pages > INT32_MAX / kPage - 1) return MLA_ERR_UNSUPPORTED;
+    off += align256(static_cast<size_t>(num_requests) * c->pages * sizeof(int));
+    c->wide = off;
+    off += static_cast<size_t>(num_requests) * c->pages * kPage * kDqk * 2;
+  }
+  c->total = off;
+  return MLA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -241,12 +302,7 @@ int mla_decode_plan(const int32_t* cache_lens, int batch, int s_q, int topk, int
   const WsLayout L = ws_layout(batch, s_q, U);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  // up to 128 requests (every decode batch the bench times) one 128-thread
-  // CTA: its block scans meet at fewer warps (~1 us off each call)
-  mla_plan_kernel<<<1, batch <= 128 ? 128 : 1024, 0, static_cast<cudaStream_t>(stream)>>>(
-      cache_lens, batch, topk, plan_tile_rows(s_q, topk), U, reinterpret_cast<int*>(ws + L.hdr),
-      reinterpret_cast<int*>(ws + L.units), reinterpret_cast<int*>(ws + L.reqs), L.slots);
-  return last_cuda_error();
+  return launch_plan(ws, L, cache_lens, batch, topk, plan_tile_rows(s_q, topk), U, nullptr, stream);
 }
 
 int mla_decode_plan_host(const int32_t* lens, int batch, int s_q, int topk, int num_units, int32_t* unit_meta,
@@ -422,30 +478,102 @@ int mla_combine(void* workspace, size_t ws_bytes, int batch, int s_q, int num_he
   const WsLayout L = ws_layout(batch, s_q, U);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   const char* ws = static_cast<const char*>(workspace);
-  // a programmatic dependent of the decode kernel: scheduled while the decode
-  // kernel's last units finish, it waits for that grid before reading
-  cudaLaunchConfig_t cfg = {};
-  // at most one wave: 76 x 16 blocks of 256 threads (8 per SM on 152 SMs),
-  // each block taking every 76th (request, token) row
-  cfg.gridDim = dim3(batch * s_q < 76 ? batch * s_q : 76, kHeads / 8, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, mla_combine_kernel, reinterpret_cast<const int*>(ws + L.hdr),
-                         reinterpret_cast<const int*>(ws + L.reqs),
-                         reinterpret_cast<const float*>(ws + L.part_lse),
-                         reinterpret_cast<const uint16_t*>(ws + L.part_o), (flags & MLA_FLAG_BF16_PV) ? 1 : 0, s_q,
-                         (flags & MLA_FLAG_OUT_FP32) ? 1 : 0, out, lse, batch * s_q);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return MLA_ERR_CUDA;
+  return launch_combine(ws, L, batch, s_q, flags, out, lse, nullptr, nullptr, 0, 0, stream);
+}
+
+size_t mla_chunk_attend_workspace_size(int num_tokens, int num_requests, int max_len, unsigned flags, int* err) {
+  ChunkLayout c;
+  const int rc = (flags & ~static_cast<unsigned>(MLA_FLAG_CAUSAL | MLA_FLAG_OUT_FP32 | MLA_FLAG_KV_FP8))
+                     ? static_cast<int>(MLA_ERR_INVALID_ARG)
+                     : chunk_layout(num_tokens, num_requests, max_len, flags, &c);
+  if (err) *err = rc;
+  return rc == MLA_OK ? c.total : 0;
+}
+
+int mla_chunk_attend(const void* q, const void* kv_cache, int64_t num_pages, const int32_t* block_table,
+                     int64_t bt_stride, const int32_t* cache_lens, int max_len, const int32_t* token_starts,
+                     int num_requests, int num_tokens, int num_heads, float softmax_scale, unsigned flags,
+                     void* workspace, size_t ws_bytes, void* out, float* lse, int* status, mla_stream_t stream) {
+  if (!status || !aligned(status, 4) || (token_starts && !aligned(token_starts, 4))) return MLA_ERR_INVALID_ARG;
+  if (flags & ~static_cast<unsigned>(MLA_FLAG_CAUSAL | MLA_FLAG_OUT_FP32 | MLA_FLAG_KV_FP8)) return MLA_ERR_INVALID_ARG;
+  int rc = check_decode_args(q, kv_cache, num_pages, block_table, bt_stride, cache_lens, num_requests, 1, num_heads,
+                             softmax_scale, nullptr, 0, flags, out, lse);
+  if (rc != MLA_OK) return rc;
+  if (num_tokens < 0 || max_len < 1 || (!token_starts && num_tokens % num_requests)) return MLA_ERR_INVALID_ARG;
+  if (num_requests > 1 && bt_stride < (static_cast<int64_t>(max_len) + kPage - 1) / kPage) return MLA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != MLA_OK) return rc;
+  ChunkLayout c;
+  if ((rc = chunk_layout(num_tokens, num_requests, max_len, flags, &c)) != MLA_OK) return rc;
+  if (ws_bytes < c.total) return MLA_ERR_WORKSPACE;
+  if (num_tokens == 0) return MLA_OK;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool fp8 = (flags & MLA_FLAG_KV_FP8) != 0;
+  const WsLayout& L = c.step;
+
+  ChunkPairs pairs;
+  pairs.starts = token_starts;
+  pairs.lens = cache_lens;
+  pairs.requests = num_requests;
+  pairs.tokens = num_tokens;
+  pairs.causal = (flags & MLA_FLAG_CAUSAL) ? 1 : 0;
+  pairs.max_len = max_len;
+  pairs.pairs = reinterpret_cast<int4*>(ws + c.pairs);
+  pairs.pair_lens = reinterpret_cast<int*>(ws + c.lens);
+  pairs.status = status;
+
+  const uint16_t* kv = static_cast<const uint16_t*>(kv_cache);
+  const int* table = block_table;
+  int64_t stride = bt_stride, pages = num_pages;
+  if (fp8) {
+    kv = reinterpret_cast<const uint16_t*>(ws + c.wide);
+    table = reinterpret_cast<const int*>(ws + c.table);
+    stride = c.pages;
+    pages = static_cast<int64_t>(num_requests) * c.pages;
+    const int blocks = (c.pages + 1) / 2;  // 8 warps, 16 rows each
+    mla_widen_kernel<<<dim3(blocks < 4096 ? blocks : 4096, num_requests < 65535 ? num_requests : 65535), 256, 0, s>>>(
+        static_cast<const uint8_t*>(kv_cache), num_pages, block_table, bt_stride, cache_lens, max_len, num_requests,
+        c.pages, reinterpret_cast<uint16_t*>(ws + c.wide), reinterpret_cast<int*>(ws + c.table), status);
+    if ((rc = last_cuda_error()) != MLA_OK) return rc;
   }
-  return MLA_OK;
+  if ((rc = launch_plan(ws, L, pairs.pair_lens, c.slots, 0, 128, c.units, &pairs, stream)) != MLA_OK) return rc;
+
+  DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = kv;
+  p.block_table = table;
+  // rows are inside the table by max_len; a single request's stride says nothing
+  p.bt_stride = stride > c.pages ? stride : c.pages;
+  p.cache_lens = pairs.pair_lens;
+  p.pairs = pairs.pairs;
+  p.batch = c.slots;
+  p.s_q = 2;
+  p.causal = pairs.causal;
+  p.num_pages = pages;
+  p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  p.out = out;
+  p.lse = lse;
+  p.out_fp32 = (flags & MLA_FLAG_OUT_FP32) ? 1 : 0;
+  p.num_units = c.units;
+  p.ws_hdr = reinterpret_cast<int*>(ws + L.hdr);
+  p.unit_meta = reinterpret_cast<const int*>(ws + L.units);
+  p.req_meta = reinterpret_cast<const int*>(ws + L.reqs);
+  p.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
+  p.part_o = reinterpret_cast<uint16_t*>(ws + L.part_o);
+
+  CUtensorMap tm_q, tm_k3, tm_v2, tm_out, tm_part;
+  const uint64_t rows = static_cast<uint64_t>(pages) * kPage, q_rows = static_cast<uint64_t>(num_tokens) * kHeads;
+  if ((rc = encode_2d(&tm_q, q, q_rows, kPage)) != MLA_OK) return rc;
+  if ((rc = encode_kv_3d(&tm_k3, kv, rows, 3)) != MLA_OK) return rc;
+  if ((rc = encode_kv_3d(&tm_v2, kv, rows, 2)) != MLA_OK) return rc;
+  if ((rc = encode_out_2d(&tm_out, out, q_rows, p.out_fp32 != 0)) != MLA_OK) return rc;
+  if ((rc = encode_out_2d(&tm_part, p.part_o, static_cast<uint64_t>(L.slots) * 2 * kHeads, false)) != MLA_OK) return rc;
+  if ((rc = launched(mtp_launch(false, c.units, s, p, tm_q, tm_k3, tm_v2, tm_out, tm_part))) != MLA_OK) return rc;
+  return launch_combine(ws, L, c.slots, 2, flags, out, lse, &pairs, fp8 ? nullptr : block_table, bt_stride, num_pages,
+                        stream);
 }
 
 int mla_selftest_wait_timeout(void* workspace, size_t ws_bytes, mla_stream_t stream) {

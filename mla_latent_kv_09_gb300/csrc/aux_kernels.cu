@@ -40,15 +40,55 @@ __device__ int block_inclusive_scan(int v, int* s_warp, int& total) {
   return res;
 }
 
+// First token of request b (b = requests: one past the last), kept inside [0, tokens].
+__device__ __forceinline__ int chunk_start(const ChunkPairs& c, int b) {
+  if (!c.starts) return b * (c.tokens / c.requests);
+  return min(max(__ldg(c.starts + b), 0), c.tokens);
+}
+
+// The token pair of a slot (see ChunkPairs); returns the rows that its last token sees.
+__device__ int chunk_pair(const ChunkPairs& c, int slot) {
+  int lo = 0, hi = c.requests - 1;
+  while (lo < hi) {  // the last request whose pairs begin at or before the slot
+    const int mid = (lo + hi + 1) >> 1;
+    if ((chunk_start(c, mid) + mid) / 2 <= slot)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int first = chunk_start(c, lo), end = chunk_start(c, lo + 1);
+  const int at = first + 2 * (slot - (first + lo) / 2);
+  const int count = at < first || at >= end ? 0 : min(2, end - at);
+  int len = 0;
+  if (count > 0) {
+    const int L = c.lens[lo];
+    if (L < 0 || L > c.max_len) atomicCAS(c.status, 0, static_cast<int>(kStBadTable));
+    const int all = min(max(L, 0), c.max_len);
+    len = c.causal ? max(all - (end - at - count), 0) : all;
+  }
+  if (c.starts && slot < c.requests) {  // (as many slots as half of the requests at least: two starts each)
+    for (int b = 2 * slot; b <= min(2 * slot + 1, c.requests - 1); ++b) {
+      const int s0 = c.starts[b], s1 = c.starts[b + 1];
+      if (s0 < 0 || s1 < s0 || s1 > c.tokens) atomicCAS(c.status, 0, static_cast<int>(kStBadTable));
+    }
+  }
+  c.pairs[slot] = make_int4(at, lo, count, 0);
+  c.pair_lens[slot] = len;
+  return len;
+}
+
 // One CTA (128 threads up to 128 requests, else 1024).  Step 1: tiles and
 // cost prefix per request.
 // Step 2: split count and first partial slot per request.  Step 3: the
 // (request, tile) range of every unit, by binary search over the cost
 // prefixes (kept in shared memory when they fit: the searches are chains of
-// dependent reads).  Also resets the status word.
+// dependent reads).  Also resets the status word.  kPairs: the requests are
+// the slots of `chunk`, whose pairs are found on the way.
+template <bool kPairs>
 __global__ void __launch_bounds__(1024) mla_plan_kernel(const int* __restrict__ lens, int B, int topk,
                                                         int tile_rows, int U, int* hdr, int* unit_meta,
-                                                        int* req_meta, int slots_cap) {
+                                                        int* req_meta, int slots_cap,
+                                                        const __grid_constant__ ChunkPairs chunk) {
   __shared__ int s_warp[32];
   __shared__ int s_prefix[kPlanSmemReqs];  // exclusive cost prefix per request
   __shared__ int s_tiles[kPlanSmemReqs];   // tiles per request
@@ -60,7 +100,7 @@ __global__ void __launch_bounds__(1024) mla_plan_kernel(const int* __restrict__ 
   int carry = 0, tot = 0;
   for (int base = 0; base < B; base += blockDim.x) {
     const int b = base + threadIdx.x;
-    const int n = b < B ? plan_tiles(max(lens[b], 0), topk, tile_rows) : 0;
+    const int n = b < B ? plan_tiles(kPairs ? chunk_pair(chunk, b) : max(lens[b], 0), topk, tile_rows) : 0;
     const int c = plan_cost(n);
     const int incl = block_inclusive_scan(c, s_warp, tot);
     if (b < B) {
@@ -108,27 +148,115 @@ __global__ void __launch_bounds__(1024) mla_plan_kernel(const int* __restrict__ 
   }
 }
 
+// `chunk`: null for a decode step.  Up to 128 requests (every decode batch the
+// bench times) one 128-thread CTA: its block scans meet at fewer warps (~1 us
+// off each call).
+cudaError_t plan_launch(const int* lens, int B, int topk, int tile_rows, int U, int* hdr, int* unit_meta, int* req_meta,
+                        int slots_cap, const ChunkPairs* chunk, cudaStream_t stream) {
+  const int threads = B <= 128 ? 128 : 1024;
+  if (chunk)
+    mla_plan_kernel<true><<<1, threads, 0, stream>>>(lens, B, topk, tile_rows, U, hdr, unit_meta, req_meta, slots_cap,
+                                                     *chunk);
+  else
+    mla_plan_kernel<false><<<1, threads, 0, stream>>>(lens, B, topk, tile_rows, U, hdr, unit_meta, req_meta, slots_cap,
+                                                      ChunkPairs{});
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ FP8 rows, widened once
+// Chunk attention over an FP8 cache: the rows of a request in order, as bf16
+// rows behind an identity table (row j of request b in page b * pages + j / 64),
+// a warp a row.
+// An E4M3 code has 4 significant bits and the scale is a power of two, so bf16
+// holds every value exactly (within its range).  A chunk's
+// kernel reads every row once for each two of its tokens, so that one more
+// pass over the rows (656 bytes in, 1,152 out) is little beside it.
+__global__ void __launch_bounds__(256) mla_widen_kernel(const uint8_t* __restrict__ kv, long long num_pages,
+                                                        const int* __restrict__ table, long long bt_stride,
+                                                        const int* __restrict__ lens, int max_len, int requests,
+                                                        int pages, uint16_t* __restrict__ wide,
+                                                        int* __restrict__ wide_table, int* status) {
+  const int lane = threadIdx.x & 31;
+  for (int b = blockIdx.y; b < requests; b += gridDim.y) {
+    const int len = min(max(lens[b], 0), max_len);
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < pages; i += gridDim.x * blockDim.x)
+      wide_table[static_cast<long long>(b) * pages + i] = b * pages + i;
+    for (int j = blockIdx.x * 8 + (threadIdx.x >> 5); j < len; j += gridDim.x * 8) {
+      const int page = table[b * bt_stride + j / kPage];
+      uint4* dst = reinterpret_cast<uint4*>(wide + (static_cast<long long>(b) * pages * kPage + j) * kDqk);
+      uint4 w[2] = {}, pe = {};
+      if (page >= 0 && page < num_pages) {
+        const uint8_t* row = kv + (static_cast<long long>(page) * kPage + j % kPage) * 656;
+        const uint4 codes = __ldg(reinterpret_cast<const uint4*>(row) + lane);  // codes 16 lane ..: group lane / 8
+        const uint32_t e = __ldg(row + 512 + (lane >> 3));
+        if (lane < 8) pe = __ldg(reinterpret_cast<const uint4*>(row + 528) + lane);
+        // 2^(e - 127); e = 0 is a subnormal, and 255 no number
+        const float scale = __uint_as_float(e == 255 ? 0x7fffffffu : e ? e << 23 : 0x00400000u);
+        const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+        uint32_t* out = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t two = (c[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+          uint32_t h;
+          asm("{\n .reg .b16 c;\n cvt.u16.u32 c, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}" : "=r"(h) : "r"(two));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          out[i] = pack_bf16x2(f.x * scale, f.y * scale);
+        }
+      } else if (lane == 0) {
+        atomicCAS(status, 0, static_cast<int>(kStBadTable));
+      }
+      dst[2 * lane] = w[0];
+      dst[2 * lane + 1] = w[1];
+      if (lane < 8) dst[64 + lane] = pe;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ combine
 // Grid (min(B * s_q, 76), 128 / 8), one wave of 256-thread blocks on 152
 // SMs: block x takes (request, token) rows x, x + gridDim.x, ..; warp w of
 // a block merges head blockIdx.y * 8 + w.
 // Requests with one split were finished by the decode kernel; requests with
-// no tiles get O = 0, LSE = -inf.
+// no tiles get O = 0, LSE = -inf.  kPairs: (request, token) rows are those of
+// the chunk's pairs, and the pages of the requests are checked on the way
+// (table null: they were checked before).
+template <bool kPairs>
 __global__ void __launch_bounds__(256) mla_combine_kernel(const int* __restrict__ hdr,
                                                           const int* __restrict__ req_meta,
                                                           const float* __restrict__ part_lse,
                                                           const uint16_t* __restrict__ part_o, int part_bf16,
-                                                          int s_q, int out_fp32, void* out, float* lse, int n_bt) {
+                                                          int s_q, int out_fp32, void* out, float* lse, int n_bt,
+                                                          const __grid_constant__ ChunkPairs chunk,
+                                                          const int* __restrict__ table, long long bt_stride,
+                                                          long long num_pages) {
   grid_launch_dependents();  // a kernel launched after this one may set up (it waits for this grid)
   grid_dependency_wait();    // the decode kernel has finished (programmatic dependent launch)
-  if (hdr[kHdrStatus] != 0) return;  // a failed check or wait: the step's outputs stay unwritten
+  if (hdr[kHdrStatus] != 0) {  // a failed check or wait: the step's outputs stay unwritten
+    if (kPairs && threadIdx.x == 0) atomicCAS(chunk.status, 0, hdr[kHdrStatus]);
+    return;
+  }
+  if (kPairs && table && blockIdx.y == 0) {
+    for (int b = blockIdx.x; b < chunk.requests; b += gridDim.x) {
+      const int pages = (min(max(chunk.lens[b], 0), chunk.max_len) + kPage - 1) / kPage;
+      for (int i = threadIdx.x; i < pages; i += blockDim.x) {
+        const int page = table[b * bt_stride + i];
+        if (page < 0 || page >= num_pages) atomicCAS(chunk.status, 0, static_cast<int>(kStBadTable));
+      }
+    }
+  }
   for (int bt = blockIdx.x; bt < n_bt; bt += gridDim.x) {
     const int b = bt / s_q, t = bt - b * s_q;
     const int ns = req_meta[4 * b + 1];
     if (ns == 1) continue;
+    long long row_bt = bt;
+    if (kPairs) {
+      const int4 pair = chunk.pairs[b];
+      if (t >= pair.z) continue;
+      row_bt = pair.x + t;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y * 8 + warp;
-    const long long orow = (static_cast<long long>(bt) * kHeads + h) * kDv;
+    const long long orow = (row_bt * kHeads + h) * kDv;
     float acc[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[k] = 0.f;
@@ -140,10 +268,12 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(const int* __restrict_
       const int slot0 = req_meta[4 * b + 2];
       auto lse_of = [&](int s) { return part_lse[(static_cast<long long>(slot0 + s) * s_q + t) * kHeads + h]; };
       const float lse_l = lane < ns ? lse_of(lane) : -INFINITY;
+      // (a chunk's token whose scores are no numbers gets none as its result)
+      auto larger = [](float x, float y) { return kPairs ? max3_nan(x, y, -INFINITY) : fmaxf(x, y); };
       float m = lse_l;
-      for (int s = lane + 32; s < ns; s += 32) m = fmaxf(m, lse_of(s));
+      for (int s = lane + 32; s < ns; s += 32) m = larger(m, lse_of(s));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 16; o > 0; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (m != -INFINITY) {
         float sum = lane < ns ? expf(lse_l - m) : 0.f;
         for (int s = lane + 32; s < ns; s += 32) sum += expf(lse_of(s) - m);
@@ -223,8 +353,29 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(const int* __restrict_
         dst[32 * k] = make_uint2(lo, hi);
       }
     }
-    if (lane == 0) lse[static_cast<long long>(bt) * kHeads + h] = LSE;
+    if (lane == 0) lse[row_bt * kHeads + h] = LSE;
   }
+}
+
+// A programmatic dependent of the decode kernel: scheduled while the decode
+// kernel's last units finish, it waits for that grid before reading.  At most
+// one wave: 76 x 16 blocks of 256 threads (8 per SM on 152 SMs), each block
+// taking every 76th (request, token) row.
+cudaError_t combine_launch(const int* hdr, const int* req_meta, const float* part_lse, const uint16_t* part_o,
+                           int part_bf16, int s_q, int out_fp32, void* out, float* lse, int n_bt, const ChunkPairs* chunk,
+                           const int* table, long long bt_stride, long long num_pages, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_bt < 76 ? n_bt : 76, kHeads / 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk ? mla_combine_kernel<true> : mla_combine_kernel<false>, hdr, req_meta, part_lse,
+                            part_o, part_bf16, s_q, out_fp32, out, lse, n_bt, chunk ? *chunk : ChunkPairs{}, table,
+                            bt_stride, num_pages);
 }
 
 // ------------------------------------------------------------------ validate

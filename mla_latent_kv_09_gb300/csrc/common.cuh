@@ -73,6 +73,22 @@ struct DecodeParams {
   float* part_lse;            // [slots, s_q, 128]
   uint16_t* part_o;           // [slots, s_q, 128, 512], fp16 (bf16 when part_bf16)
   int part_bf16;              // partial rows in bf16 (MLA_FLAG_BF16_PV) instead of fp16
+  const int4* pairs;          // chunk attention: the token pair behind each request of the plan (see ChunkPairs)
+};
+
+// Chunk attention runs the two-token kernel on pairs of a request's tokens:
+// every pair is a request of the plan.  Request b's pairs begin at slot
+// (starts[b] + b) / 2: the next request's first slot is then at least ceil(n_b
+// / 2) further on, so that a slot's request is found by a search over `starts`
+// and no prefix sum over pair counts is needed; (tokens + requests) / 2 slots
+// hold them all, at most one of a request empty.
+struct ChunkPairs {
+  const int* starts;  // [requests + 1], or null: equal runs
+  const int* lens;    // [requests]
+  int requests, tokens, causal, max_len;
+  int4* pairs;        // per slot {first token, request, tokens (0, 1 or 2), 0}
+  int* pair_lens;     // per slot: rows that its last token sees (at least 0)
+  int* status;
 };
 
 }  // namespace mla

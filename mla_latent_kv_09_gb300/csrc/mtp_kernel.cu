@@ -80,6 +80,15 @@ __device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
+// Eight bf16, zero in the place of infinities and NaN.
+__device__ __forceinline__ uint4 numbers_only(uint4 v) {
+  auto two = [](uint32_t w) {
+    const uint32_t lo = (w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu;
+    return lo | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+  };
+  return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+}
+
 constexpr int kTileRows = 2 * kPage;              // 128 cached rows per tile
 constexpr int kPageChunk = kPage * 128;           // 8 KiB: 64 rows x 64 dims (bf16), 128B-swizzled
 constexpr int kKSlots = 21;                       // score ranks: chunk slots (2 1/3 tiles)
@@ -213,7 +222,23 @@ __host__ __device__ constexpr uint32_t p_message_bytes(bool last) {
   return static_cast<uint32_t>(kPSlot + kHeads * 4 + (last ? kHeads * 4 : 0));
 }
 
-template <bool kBf16PV>
+// The two query tokens behind a request of the plan: their first row of q and
+// out, the request whose pages they read, and how many there are.
+struct TokenPair {
+  int first, req, count;
+};
+template <bool kPairs>
+__device__ __forceinline__ TokenPair token_pair(const DecodeParams& p, int b) {
+  if (!kPairs) return {2 * b, b, 2};
+  const int4 v = p.pairs[b];
+  return {v.x, v.y, v.z};
+}
+
+// The same instance serves decode steps and chunks (kPairs): there a request of
+// the plan is a pair of a request's tokens, the last of an odd number without
+// its second one.  The first one's query then stands in for it, and what comes
+// of it is not written.
+template <bool kBf16PV, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 1)
 mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k3, const __grid_constant__ CUtensorMap tm_v2,
@@ -423,7 +448,9 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     if (to_part && sg.slot >= 2 * U) return;  // the plan never uses more than 2 * (U - 1) slots
     const bool f32 = !to_part && p.out_fp32;  // partials are 16-bit (fp16, or bf16 with kBf16PV)
     const CUtensorMap* tm = to_part ? &tm_part : &tm_out;
-    const long long orow = to_part ? static_cast<long long>(sg.slot) * 2 + tok : static_cast<long long>(sg.b) * 2 + tok;
+    const TokenPair pair = token_pair<kPairs>(p, sg.b);
+    if (kPairs && !to_part && static_cast<int>(tok) >= pair.count) return;
+    const long long orow = to_part ? static_cast<long long>(sg.slot) * 2 + tok : static_cast<long long>(pair.first) + tok;
     const int y = static_cast<int>(orow * kHeads) + 32 * (w & 3);
     const int x0 = 128 * (w >> 2);
     const uint32_t ul = static_cast<uint32_t>(lane);
@@ -496,14 +523,17 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     float* xmax = reinterpret_cast<float*>(smem + kOffXchg);                   // [2 parity][4 cg][128]
     float* xsum = reinterpret_cast<float*>(smem + kOffXchg + 8 * kHeads * 4);  // [2 sum][4 cg][128]
     const int qbar = 1 + q4;
+    // a chunk's token whose scores are no numbers gets none as its result
+    auto larger = [](float x, float y) { return kPairs ? max3_nan(x, y, -__int_as_float(0x7f800000)) : fmaxf(x, y); };
     SegIter it(p, unit);
     Seg sg;
     uint32_t g = 0;
     bool ok = true, stop = false;  // ok: this warp's waits so far; stop: the quarter leaves
     while (!stop && it.next(sg)) {
       const int L = max(p.cache_lens[sg.b], 0);
-      const int vis = p.causal ? L - 1 + static_cast<int>(tok) : L;
-      const long long bt_row = static_cast<long long>(sg.b) * 2 + tok;
+      const TokenPair pair = token_pair<kPairs>(p, sg.b);
+      const int vis = p.causal ? min(L, L + 1 - pair.count + static_cast<int>(tok)) : L;
+      const long long bt_row = static_cast<long long>(pair.first) + tok;
       // zr: sum of the 16-bit weights the value product uses; it normalises O,
       // so O is a convex combination of value rows and a weight's rounding
       // error acts on (v_j - O) instead of v_j.  zx: sum of the fp32 weights,
@@ -539,18 +569,18 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
         {
           float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-          for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
-          xmax[(sb * 4 + cg) * kHeads + row] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int c = 0; c < 32; ++c) m4[c & 3] = larger(m4[c & 3], s[c]);
+          xmax[(sb * 4 + cg) * kHeads + row] = larger(larger(m4[0], m4[1]), larger(m4[2], m4[3]));
         }
         if (!named_bar_all(qbar, 128, ok)) {
           stop = true;
           break;
         }
         const float* xm = xmax + sb * 4 * kHeads + row;
-        const float mt = fmaxf(fmaxf(xm[0], xm[kHeads]), fmaxf(xm[2 * kHeads], xm[3 * kHeads])) * p.scale_log2;
+        const float mt = larger(larger(xm[0], xm[kHeads]), larger(xm[2 * kHeads], xm[3 * kHeads])) * p.scale_log2;
 
         float alpha = 1.f;
-        if (mt > m_used + kRescaleLog2) {
+        if (kPairs ? !(mt <= m_used + kRescaleLog2) : mt > m_used + kRescaleLog2) {
           alpha = (m_used == NEG_INF) ? 0.f : ex2_approx(m_used - mt);
           m_used = mt;
           zr *= alpha;
@@ -594,10 +624,11 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           if (lead) {
             const float zrt = (zr + xsum[kHeads + row]) + (xsum[2 * kHeads + row] + xsum[3 * kHeads + row]);
             const float zxt = (zx + xsum[5 * kHeads + row]) + (xsum[6 * kHeads + row] + xsum[7 * kHeads + row]);
-            fin_out[row] = zrt > 0.f ? 1.f / zrt : 0.f;  // O_final = O_acc / zr
-            const float lse = zxt > 0.f ? (m_used + log2f(zxt)) * 0.69314718055994531f : NEG_INF;
+            const bool some = kPairs ? zxt != 0.f : zxt > 0.f;  // (not: sees nothing)
+            fin_out[row] = (kPairs ? zrt != 0.f : zrt > 0.f) ? 1.f / zrt : 0.f;  // O_final = O_acc / zr
+            const float lse = some ? (m_used + log2f(zxt)) * 0.69314718055994531f : NEG_INF;
             if (sg.slot < 0) {
-              p.lse[bt_row * kHeads + row] = lse;
+              if (!kPairs || static_cast<int>(tok) < pair.count) p.lse[bt_row * kHeads + row] = lse;
             } else if (sg.slot < 2 * U) {  // the plan never uses more than 2 * (U - 1) slots
               p.part_lse[(static_cast<long long>(sg.slot) * 2 + tok) * kHeads + row] = lse;
             }
@@ -798,7 +829,8 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
       };
       while (ok && it.next(sg)) {
         const int L = max(p.cache_lens[sg.b], 0);
-        const int qy = (sg.b * 2 + static_cast<int>(tok)) * kHeads;
+        const TokenPair pair = token_pair<kPairs>(p, sg.b);
+        const int qy = (pair.first + min(static_cast<int>(tok), pair.count - 1)) * kHeads;
         for (uint32_t npad = q_pads(u); npad > 0 && ok; --npad) {  // pads
           if (!(ok = claim(0))) break;
           ++u;
@@ -820,7 +852,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           for (int h = 0; h < 2; ++h)
             tma_load_2d_pair(sbase + kOffQr + h * kPageChunk, &tm_q, 8 * kChunk, qy + h * kPage, rQRF);
         }
-        const int* bt_row = p.block_table + static_cast<long long>(sg.b) * p.bt_stride;
+        const int* bt_row = p.block_table + static_cast<long long>(pair.req) * p.bt_stride;
         const int npages = (L + kPage - 1) / kPage;
         for (int jb = sg.t0; jb < sg.t1 && ok; jb += 32) {
           const int cnt = min(32, sg.t1 - jb);
@@ -865,11 +897,12 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
         SegIter it0(p, unit);
         Seg s0;
         if (it0.next(s0)) {
-          const long long qrow = (static_cast<long long>(s0.b) * 2 + tok) * kHeads;
+          const TokenPair pair = token_pair<kPairs>(p, s0.b);
+          const long long qrow = (static_cast<long long>(pair.first) + min(static_cast<int>(tok), pair.count - 1)) * kHeads;
           for (int h = 0; h < 2; ++h) bulk_prefetch_l2(p.q + (qrow + h * kPage) * kDqk, kPage * kDqk * 2);
           const int nl = max(p.cache_lens[s0.b], 0);
           const int np = (nl + kPage - 1) / kPage;
-          const int* row = p.block_table + static_cast<long long>(s0.b) * p.bt_stride;
+          const int* row = p.block_table + static_cast<long long>(pair.req) * p.bt_stride;
           for (int t = s0.t0; t < s0.t1 && t < s0.t0 + 2; ++t) {
             const int pi = 2 * t + static_cast<int>(tok);
             if (pi >= np || pi >= p.bt_stride) break;
@@ -883,7 +916,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
       Ring<kVSlots> rv;
       while (kBf16PV && ok && it.next(sg)) {
         const int L = max(p.cache_lens[sg.b], 0);
-        const int* bt_row = p.block_table + static_cast<long long>(sg.b) * p.bt_stride;
+        const int* bt_row = p.block_table + static_cast<long long>(token_pair<kPairs>(p, sg.b).req) * p.bt_stride;
         const int npages = (L + kPage - 1) / kPage;
         for (int jb = sg.t0; jb < sg.t1 && ok; jb += 32) {
           const int cnt = min(32, sg.t1 - jb);
@@ -953,6 +986,10 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     // put an L2 round trip (the entry does not stay in the small L1 that the
     // value stream passes through) in front of every page.
     const int* bt_row = nullptr;
+    // the row that only the second token of a chunk's pair sees: its weight for
+    // the first is zero, and what is no number there (the second's result is
+    // none either, by its score) must not reach the first's, so it counts as zero
+    int hidden = -1;
     int L = 0, ids_base = 0, ids_cur = -1, ids_next = -1;
     auto fetch_ids = [&](int base) {
       const int pi = base + lane;
@@ -978,6 +1015,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
       for (int i = 0; i < kRowsPerThread; ++i) {
         const int r = lw + 12 * i;
         dst[i] = (page >= 0 && r < kPage && r < rows) ? ld_global_nc_v4(src + r * kDqk) : make_uint4(0u, 0u, 0u, 0u);
+        if (kPairs && pi * kPage + r == hidden) dst[i] = numbers_only(dst[i]);
       }
     };
     const uint32_t rVR = mapa(bar(kVR), 2);
@@ -991,7 +1029,9 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     bool wok = true;
     while (it.next(sg)) {
       L = max(p.cache_lens[sg.b], 0);
-      bt_row = p.block_table + static_cast<long long>(sg.b) * p.bt_stride;
+      const TokenPair pair = token_pair<kPairs>(p, sg.b);
+      bt_row = p.block_table + static_cast<long long>(pair.req) * p.bt_stride;
+      hidden = kPairs && p.causal && pair.count == 2 ? L - 1 : -1;
       const int p0 = 2 * sg.t0, np = 2 * (sg.t1 - sg.t0);  // this segment's pages: p0 .. p0 + np - 1
       ids_base = p0;
       ids_cur = fetch_ids(p0);
@@ -1129,11 +1169,12 @@ void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int num_
 
 // ------------------------------------------------------------------ host side
 cudaError_t mtp_set_attrs() {
-  cudaError_t e = cudaFuncSetAttribute(mtp::mla_decode_mtp_kernel<false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, mtp::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(mtp::mla_decode_mtp_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              mtp::kSmemBytes);
+  for (auto* kernel : {mtp::mla_decode_mtp_kernel<false, false>, mtp::mla_decode_mtp_kernel<true, false>,
+                       mtp::mla_decode_mtp_kernel<false, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mtp::kSmemBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // Co-resident 4-CTA clusters of the two-token kernel on the current device.
@@ -1141,7 +1182,7 @@ cudaError_t mtp_max_clusters(int* n, int num_clusters_hint) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   mtp::cluster_config<false>(cfg, attr, num_clusters_hint, nullptr, false);
-  return cudaOccupancyMaxActiveClusters(n, mtp::mla_decode_mtp_kernel<false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(n, mtp::mla_decode_mtp_kernel<false, false>, &cfg);
 }
 
 cudaError_t mtp_launch(bool bf16_pv, int num_clusters, cudaStream_t stream, const DecodeParams& p,
@@ -1150,9 +1191,9 @@ cudaError_t mtp_launch(bool bf16_pv, int num_clusters, cudaStream_t stream, cons
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   mtp::cluster_config<false>(cfg, attr, num_clusters, stream, true);
-  return bf16_pv
-      ? cudaLaunchKernelEx(&cfg, mtp::mla_decode_mtp_kernel<true>, p, tm_q, tm_k3, tm_v2, tm_out, tm_part)
-      : cudaLaunchKernelEx(&cfg, mtp::mla_decode_mtp_kernel<false>, p, tm_q, tm_k3, tm_v2, tm_out, tm_part);
+  auto* kernel = p.pairs ? mtp::mla_decode_mtp_kernel<false, true>
+                 : bf16_pv ? mtp::mla_decode_mtp_kernel<true, false> : mtp::mla_decode_mtp_kernel<false, false>;
+  return cudaLaunchKernelEx(&cfg, kernel, p, tm_q, tm_k3, tm_v2, tm_out, tm_part);
 }
 
 }  // namespace mla

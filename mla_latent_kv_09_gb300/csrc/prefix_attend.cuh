@@ -100,13 +100,6 @@ __device__ __forceinline__ void mask32(uint32_t (&x)[32], int limit) {
     if (k >= limit) x[k] = 0xff800000u;
 }
 
-// The largest of three, NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // The largest score, NaN if one is no number.
 __device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
   float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);

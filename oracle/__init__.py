@@ -26,3 +26,4 @@ from .indexer_oracle import indexer_scores, indexer_topk, topk_select, topk_sele
 from .fp8_oracle import e4m3_to_f64, fp8_rows_to_f64, mla_decode_fp8, ue8m0_to_f64  # noqa: F401,E402
 from .cache_oracle import (append_places, appended_rows, group_scales, rms_norm, rope, rotate)  # noqa: F401,E402
 from .prefix_oracle import attend_error_bound, join, prefix_attend, prefix_expand  # noqa: F401,E402
+from .evict_oracle import (attention_weights, chunk_attend, chunk_error_bound, chunk_visible, evict_select)  # noqa: F401,E402

@@ -32,7 +32,7 @@ size_t mla_attention_weights_workspace_size(int num_tokens, int num_requests, in
  *   q, kv_cache, num_pages, block_table, bt_stride, cache_lens, max_len,
  *   token_starts, num_requests, num_tokens, num_heads, softmax_scale: as for
  *                 mla_chunk_attend
- *   lse           fp32 [num_tokens, 128]: of the attention these are the
+ *   lse           fp32 [num_tokens, 128], 16-B aligned: of the attention these are the
  *                 weights of (which may have seen more than this cache); -inf:
  *                 the head attended to nothing
  *   weights, out  fp32 rows of max_len at a stride of weights_stride and

@@ -1,107 +1,679 @@
 // weights_kernel.cu — the attention weight that every cached row received, with
 // its C ABI (include/mla_evict.h).
+//
+// w[j] = sum over the tokens that see row j, and over 128 heads, of
+// exp(q . row_j * scale - lse): the scores are products of rows and heads with
+// K = 576, and what comes of them is one number a row.  So rows are the MMA's M
+// and a token's heads its N: every thread of the epilogue holds a row's scores
+// with 64 heads, and the sum over heads needs no other lane.
+//
+// A pair of SMs takes tiles of 256 rows (four pages) and runs a token's 128
+// heads over each: M256 N128 tcgen05 operations over the pair, each CTA holding
+// half of the rows and half of the heads.  Rows stay in shared memory for all
+// tokens of their request and a token's query for all tiles until the next
+// token's comes: one step a request (decode) streams rows past a resident query,
+// bound by HBM; many tokens (an observation window) stream queries past resident
+// rows, bound by the tensor cores.  Both operands lie in four groups of 64-dim
+// chunks, each given back as soon as its last product is done, so that the next
+// one's load runs behind the other groups' products.
+//
+// A step's K is cut into two accumulators, chunks 0-4 and 5-8, that eight
+// warps add in fp32 (four lane quarters, two halves of the heads).  A tensor core
+// truncates when it accumulates, so that a score comes out too small by about
+// half a step for each of its K / 16 additions, and the sum over heads and tokens
+// does not average that away: 32 tokens x 16384 rows were off by 1.5e-6 with one
+// accumulator, 7e-7 with two.  And each accumulator has a thread of its own to
+// issue its products: one thread alone issues more slowly than they execute (32 x
+// 16384 75 us against 55).
+//
+// Work: the (tile, token) steps of all requests lie on a line that is cut into
+// equal ranges, one a pair.  A range that begins inside a tile's tokens writes
+// that tile's part to the workspace, and a second kernel adds the parts in the
+// line's order: no atomics, equal calls give equal bits.
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
-#include "kernel_common.cuh"
 #include "mla_evict.h"
+#include "prefix_common.cuh"
 
 namespace mla {
 namespace {
 
+using namespace prefix;
+
+constexpr int kRows = 128;                    // of a CTA's half of a tile
+constexpr int kTileRows = 2 * kRows;
+constexpr int kKChunk = kRows * 128;          // 16 KiB: 128 rows x 64 dims
+constexpr int kQChunk = 64 * 128;             // 8 KiB: 64 heads x 64 dims
+constexpr int kFirst = 5;                     // chunks of the first accumulator
+// Chunks lie in groups that land and are given back together (a commit a chunk
+// made 32 x 16384 107 us instead of 55).
+constexpr int kGroups = 4;
+__host__ __device__ constexpr int group_begin(int g) { return g < 2 ? 3 * g : 2 * g + 1; }  // 0, 3, 5, 7, 9
+static_assert(group_begin(kGroups) == kNumChunks && group_begin(kGroups / 2) == kFirst, "groups end where the accumulators do");
+constexpr int kUnits = 76;                    // SM pairs
+constexpr int kOffQ = kNumChunks * kKChunk;
+constexpr int kOffLse = kOffQ + kNumChunks * kQChunk;      // float[8 warps][64]
+constexpr int kOffHalf = kOffLse + 8 * 64 * 4;             // float[2][128]: the other half's sums
+constexpr int kOffWalk = kOffHalf + 2 * kRows * 4;         // where this unit's range begins
+constexpr int kOffBar = kOffWalk + 64;
+enum Bar {
+  kKF = 0,                    // [4] rank 0: a group of the rows landed in both CTAs
+  kKE = kKF + kGroups,        // [4] its last product is done
+  kQF = kKE + kGroups,        // [4] rank 0: a group of the query landed in both CTAs
+  kQE = kQF + kGroups,        // [4] its last product is done
+  kAF = kQE + kGroups,        // [2] both accumulators of a step complete
+  kAE = kAF + 2,              // [2] rank 0: ... and read by the sixteen warps of both CTAs
+  kWide = kAE + 2,            // [4] rank 1, FP8 rows: widened (for the relay)
+  kDrain = kWide + kGroups,   // [2] per issuer
+  kNumBars = kDrain + 2
+};
+constexpr int kSlack = 1024;
+constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr int kEpiWarp = 4;                   // eight warps (a multiple of four: lane quarters)
+constexpr int kFillWarp = 12;                 // eight further warps, FP8 rows only
+constexpr int kThreads = 32 * 12, kThreadsFp8 = 32 * 20;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdesc = idesc_bf16(256, 128, 0);
+constexpr float kLog2e = 1.4426950408889634f;
+
 struct WeightsParams {
-  const uint16_t* q;
-  const float* lse;
   const uint8_t* kv;
   long long num_pages;
+  const float* lse;
   const int* table;
   long long bt_stride;
   const int* lens;
   int max_len;
   const int* starts;
-  int requests, tokens, causal, fp8;
+  int requests, tokens, causal;
   float scale_log2, decay;
   const float* weights;
   long long w_stride;
   float* out;
   long long out_stride;
+  int4* begins;  // [kUnits] {request, tile, first token in it, 0}; request -1: no work
+  float* parts;  // [kUnits][kTileRows]
   int* status;
 };
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ int start_of(const WeightsParams& p, int b) {
   if (!p.starts) return b * (p.tokens / p.requests);
   return min(max(__ldg(p.starts + b), 0), p.tokens);
 }
+__device__ __forceinline__ int len_of(const WeightsParams& p, int b) {
+  return min(max(__ldg(p.lens + b), 0), p.max_len);
+}
 
-// A warp a row: its dims in registers, a dot product with every head of every
-// token that sees it.
-__global__ void __launch_bounds__(256) mla_attention_weights_kernel(const __grid_constant__ WeightsParams p) {
-  const int lane = threadIdx.x & 31;
-  for (int b = blockIdx.y; b < p.requests; b += gridDim.y) {
-    const int given = p.lens[b], len = min(max(given, 0), p.max_len);
-    const int first = start_of(p, b), n = start_of(p, b + 1) - first;
-    if (blockIdx.x == 0 && threadIdx.x == 0 &&
-        (given != len || (p.starts && (p.starts[b] < 0 || p.starts[b + 1] < p.starts[b] || p.starts[b + 1] > p.tokens))))
-      atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
-    if (n <= 0) continue;
-    for (int j = blockIdx.x * 8 + (threadIdx.x >> 5); j < len; j += gridDim.x * 8) {
-      const int page = p.table[b * p.bt_stride + j / kPage];
-      float k[18] = {};
-      if (page >= 0 && page < p.num_pages) {
-        const long long at = static_cast<long long>(page) * kPage + j % kPage;
-#pragma unroll
-        for (int i = 0; i < 18; ++i) {
-          const int d = 32 * i + lane;
-          if (!p.fp8 || d >= 512) {
-            const uint16_t* row = reinterpret_cast<const uint16_t*>(p.kv + at * (p.fp8 ? 656 : 1152)) + (p.fp8 ? -248 : 0);
-            k[i] = __uint_as_float(static_cast<uint32_t>(row[d]) << 16);
-          } else {
-            const uint8_t* row = p.kv + at * 656;
-            const uint32_t c = row[d], e = row[512 + d / 128];
-            const uint32_t m = c & 0x7fu;
-            float v = m == 0x7fu ? __int_as_float(0x7fffffff) : __uint_as_float(m << 20) * 0x1p120f;
-            v *= __uint_as_float(e == 255 ? 0x7fffffffu : e ? e << 23 : 0x00400000u);
-            k[i] = c & 0x80u ? -v : v;
-          }
-        }
-      } else if (lane == 0) {
-        atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
-      }
-      float sum = 0.f;
-      for (int t = p.causal ? max(0, j - (len - n)) : 0; t < n; ++t) {
-        for (int h = 0; h < kHeads; ++h) {
-          const long long qh = static_cast<long long>(first + t) * kHeads + h;
-          float s = 0.f;
-#pragma unroll
-          for (int i = 0; i < 18; ++i)
-            s = fmaf(k[i], __uint_as_float(static_cast<uint32_t>(p.q[qh * kDqk + 32 * i + lane]) << 16), s);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          const float lse = p.lse[qh];
-          if (lse != -INFINITY) sum += exp2f(fmaf(s, p.scale_log2, -lse * kLog2e));
-        }
-      }
-      if (lane == 0) {
-        const float old = p.decay != 0.f ? p.decay * p.weights[b * p.w_stride + j] : 0.f;
-        p.out[b * p.out_stride + j] = old + sum;
-      }
+// A unit's visits to tiles, in the line's order.
+struct Visit {
+  int b, tile, t0, t1;    // tokens [t0, t1) of the request
+  int first, n, len;      // the request's first token, its tokens and rows
+  int pos;                // t0 or the first token that sees a row of the tile
+};
+__device__ __forceinline__ int limit(const Visit& v, int t, int causal) {  // rows that token t sees
+  return causal ? max(0, v.len - v.n + t + 1) : v.len;
+}
+struct Walk {
+  const WeightsParams& p;
+  int b, tile, tok;
+  long long left;
+  int first, n, len;
+  __device__ Walk(const WeightsParams& params, const int* begin) : p(params) {
+    b = begin[0];
+    tile = begin[1];
+    tok = begin[2];
+    left = static_cast<long long>(static_cast<uint32_t>(begin[4])) | static_cast<long long>(begin[5]) << 32;
+    if (left > 0) request();
+  }
+  __device__ void request() {
+    first = start_of(p, b);
+    n = start_of(p, b + 1) - first;
+    len = len_of(p, b);
+  }
+  __device__ bool next(Visit& v) {
+    if (left <= 0) return false;
+    while (n <= 0 || tile * kTileRows >= len) {  // (`left` says that there is a further request)
+      if (++b >= p.requests) return false;
+      tile = 0;
+      request();
     }
+    v.b = b;
+    v.tile = tile;
+    v.t0 = tok;
+    v.t1 = left < n - tok ? tok + static_cast<int>(left) : n;
+    v.first = first;
+    v.n = n;
+    v.len = len;
+    v.pos = p.causal ? max(tok, tile * kTileRows - (len - n)) : tok;
+    left -= v.t1 - tok;
+    tok = v.t1;
+    if (tok == n) {
+      tok = 0;
+      ++tile;
+    }
+    return true;
+  }
+  // the next visit with a token that sees some of the tile
+  __device__ bool next_live(Visit& v) {
+    while (next(v))
+      if (v.pos < v.t1) return true;
+    return false;
+  }
+};
+
+// Where the range of every unit begins: a CTA finds its own, over all threads.
+template <int kThreadCount>
+__device__ void find_begin(const WeightsParams& p, int unit, int* begin) {
+  __shared__ long long s_warp[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto steps_of = [&](int b) -> long long {
+    if (b >= p.requests) return 0;
+    const int n = start_of(p, b + 1) - start_of(p, b);
+    return n <= 0 ? 0 : static_cast<long long>((len_of(p, b) + kTileRows - 1) / kTileRows) * n;
+  };
+  if (threadIdx.x == 0) {
+    begin[0] = -1;
+    begin[1] = begin[2] = begin[4] = begin[5] = 0;
+  }
+  const long long mine = steps_of(threadIdx.x);  // (of the first kThreadCount requests)
+  long long total = 0;
+  for (int b = threadIdx.x + kThreadCount; b < p.requests; b += kThreadCount) total += steps_of(b);
+  total += mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) s_warp[warp] = total;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < kThreadCount / 32; ++w) total += s_warp[w];
+  const long long s0 = total * unit / kUnits, s1 = total * (unit + 1) / kUnits;
+  long long carry = 0;
+  for (int base = 0; base < p.requests; base += kThreadCount) {
+    const int b = base + threadIdx.x;
+    const long long own = base == 0 ? mine : steps_of(b);
+    long long upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    __syncthreads();  // s_warp has been read
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    long long chunk = 0;
+    for (int w = 0; w < kThreadCount / 32; ++w) {
+      if (w == warp) upto += carry + chunk;
+      chunk += s_warp[w];
+    }
+    if (s1 > s0 && upto - own <= s0 && s0 < upto) {
+      const int n = start_of(p, b + 1) - start_of(p, b);
+      const long long at = s0 - (upto - own), left = s1 - s0;
+      begin[0] = b;
+      begin[1] = static_cast<int>(at / n);
+      begin[2] = static_cast<int>(at % n);
+      begin[4] = static_cast<int>(static_cast<uint32_t>(left));
+      begin[5] = static_cast<int>(left >> 32);
+    }
+    carry += chunk;
   }
 }
 
-bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// The pool's page of place i of request b; pages outside the pool are reported and read as zeros.
+__device__ __forceinline__ int page_of(const WeightsParams& p, const Visit& v, int i) {
+  if (i * kPage >= v.len) return -1;
+  const int page = __ldg(p.table + v.b * p.bt_stride + i);
+  if (page >= 0 && page < p.num_pages) return page;
+  atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
+  return -1;
+}
 
+// Two E4M3 codes in the upper bytes of a word's halves (the rest zero) as bf16
+// times 2^-120: sign, then exponent and mantissa four bits lower.
+__device__ __forceinline__ uint32_t place2(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 8 codes with the scale 2^(e - 127) as 8 bf16: exact (powers of two) while
+// they are in bf16's range.  NaN codes (S.1111.111) and scales of 2^8 and more
+// (whose 2^(e - 7) bf16 does not hold) are rare, and their way is not inlined:
+// the fill warps' loop has to stay in the instruction cache.
+__device__ __noinline__ uint4 widen8_rare(uint32_t a, uint32_t b, uint32_t e) {
+  const uint32_t s = e == 255 ? 0x7fffu : e ? e << 7 : 0x0040u;
+  const uint32_t c[2] = {a, b};
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = __byte_perm(c[k >> 1], 0u, k & 1 ? 0x3424 : 0x1404);
+    const bool lo = (w & 0x7f00u) == 0x7f00u, hi = (w & 0x7f000000u) == 0x7f000000u;
+    o[k] = mul_bf16x2(mul_bf16x2(place2(w), 0x7b807b80u), s | s << 16) | (lo ? 0x7fffu : 0u) | (hi ? 0x7fff0000u : 0u);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t e) {
+  const uint32_t nan = (((a & 0x7f7f7f7fu) + 0x01010101u) | ((b & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+  if (nan != 0 || e > 134) return widen8_rare(a, b, e);
+  const uint32_t f = (e + 120) << 7, f2 = f | f << 16;  // 2^(e - 7)
+  return make_uint4(mul_bf16x2(place2(__byte_perm(a, 0u, 0x1404)), f2), mul_bf16x2(place2(__byte_perm(a, 0u, 0x3424)), f2),
+                    mul_bf16x2(place2(__byte_perm(b, 0u, 0x1404)), f2), mul_bf16x2(place2(__byte_perm(b, 0u, 0x3424)), f2));
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1) __cluster_dims__(2, 1, 1)
+mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap tm_q,
+                             const __grid_constant__ CUtensorMap tm_k) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t mis = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + mis;
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = static_cast<int>(uniform(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const uint32_t rank = uniform(cluster_ctarank());
+  const int unit = blockIdx.x >> 1;
+  int* begin = reinterpret_cast<int*>(smem + kOffWalk);
+  auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + kNumBars * 8);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffBar + kNumBars * 8 + 4);
+
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < kGroups; ++g) {
+      mbar_init(bar(kKF + g), kFp8 ? 9 : 1);  // FP8: rank 0's fill warps and rank 1's relay
+      mbar_init(bar(kKE + g), 1);
+      mbar_init(bar(kQF + g), 1);
+      mbar_init(bar(kQE + g), 1);
+      mbar_init(bar(kWide + g), 8);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar(kAF + a), 2);  // both issuers
+      mbar_init(bar(kAE + a), 16);
+      mbar_init(bar(kDrain + a), 1);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  find_begin<kFp8 ? kThreadsFp8 : kThreads>(p, unit, begin);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any remote operation
+  tc_fence_after();
+  const uint32_t tmem = uniform(*tmem_slot);
+  Ctl ctl;
+  ctl.abort = abort_flag;
+  ctl.n_remote = 1;
+  ctl.abort_remote[0] = mapa(smem_u32(const_cast<uint32_t*>(abort_flag)), rank ^ 1u);
+  ctl.status = p.status;
+
+  if (threadIdx.x == 0 && rank == 0) {
+    p.begins[unit] = make_int4(begin[0], begin[1], begin[2], 0);
+    for (int b = unit; b < p.requests; b += kUnits) {
+      const int L = p.lens[b];
+      bool bad = L < 0 || L > p.max_len;
+      if (p.starts) bad = bad || p.starts[b] < 0 || p.starts[b + 1] < p.starts[b] || p.starts[b + 1] > p.tokens;
+      if (bad) atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
+    }
+  }
+
+  // The producers' and issuers' warps walk whole, one lane issues.  Every copy
+  // completes on rank 0's barriers, which rank 0 arms with the bytes of both CTAs.
+  auto landing_time = [&]() {  // after a failed wait: copies in flight land before the CTA goes away
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kDrainNs / 8) {
+    }
+  };
+  if (warp == 0 && !kFp8) {
+    // ================================================= rows, by TMA
+    const uint32_t rk = mapa(bar(kKF), 0);
+    if (lane == 0) tma_prefetch_desc(&tm_k);
+    Walk walk(p, begin);
+    Visit v;
+    bool ok = true;
+    for (uint32_t nk = 0; ok && walk.next_live(v); ++nk) {
+      int y[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        int page = -1;
+        if (lane == 0) page = page_of(p, v, v.tile * 4 + static_cast<int>(rank) * 2 + e);
+        page = __shfl_sync(0xffffffffu, page, 0);
+        y[e] = (page >= 0 ? page : static_cast<int>(p.num_pages)) * kPage;
+      }
+      for (int g = 0; g < kGroups; ++g) {
+        if (nk > 0 && !(ok = warp_wait_uniform<true>(bar(kKE + g), (nk - 1) & 1, ctl))) break;
+        if (lane == 0) {
+          const int c0 = group_begin(g), c1 = group_begin(g + 1);
+          if (rank == 0) mbar_arrive_expect_tx_relaxed(bar(kKF + g), (c1 - c0) * 2 * kKChunk);
+          for (int c = c0; c < c1; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              tma_load_2d_pair(sbase + c * kKChunk + e * (kKChunk / 2), &tm_k, 64 * c, y[e], rk + 8u * g);
+        }
+      }
+    }
+    if (!ok && lane == 0) landing_time();
+    __syncwarp();
+  } else if (warp == 2) {
+    // ================================================= queries, by TMA
+    const uint32_t rq = mapa(bar(kQF), 0);
+    if (lane == 0) tma_prefetch_desc(&tm_q);
+    Walk walk(p, begin);
+    Visit v;
+    uint32_t nq = 0;
+    int last_q = -1;
+    bool ok = true;
+    while (ok && walk.next_live(v)) {
+      for (int t = v.pos; ok && t < v.t1; ++t) {
+        if (v.first + t == last_q) continue;
+        last_q = v.first + t;
+        for (int g = 0; g < kGroups; ++g) {
+          if (nq > 0 && !(ok = warp_wait_uniform<true>(bar(kQE + g), (nq - 1) & 1, ctl))) break;
+          if (lane == 0) {
+            const int c0 = group_begin(g), c1 = group_begin(g + 1);
+            if (rank == 0) mbar_arrive_expect_tx_relaxed(bar(kQF + g), (c1 - c0) * 2 * kQChunk);
+            for (int c = c0; c < c1; ++c)
+              tma_load_2d_pair(sbase + kOffQ + c * kQChunk, &tm_q, 64 * c, last_q * kHeads + static_cast<int>(rank) * 64,
+                               rq + 8u * g);
+          }
+        }
+        ++nq;
+      }
+    }
+    if (!ok && lane == 0) landing_time();
+    __syncwarp();
+  } else if ((warp == 1 || warp == 3) && rank == 0) {
+    // ================================================= MMA issue: warp 1 the first accumulator, warp 3 the second
+    const uint32_t leader = lane == 0 ? 1u : 0u;
+    const int which = warp >> 1;
+    const uint64_t kd = smem_desc(sbase, 16u, 1024u), qd = smem_desc(sbase + kOffQ, 16u, 1024u);
+    Walk walk(p, begin);
+    Visit v, after;
+    uint32_t nk = 0, nq = 0, step = 0;
+    int last_q = -1;
+    bool ok = true, more = walk.next_live(v);
+    auto issue = [&](auto first, auto end) {  // groups [first, end) of every step
+      while (ok && more) {
+        more = walk.next_live(after);
+        for (int t = v.pos; ok && t < v.t1; ++t, ++step) {
+          const bool new_k = t == v.pos, new_q = v.first + t != last_q, last = t == v.t1 - 1;
+          const bool q_goes = !last || (more && after.first + after.pos != v.first + t);
+          const uint32_t buf = step & 1, d = tmem + 256u * buf + kHeads * which;
+          if (step >= 2) ok = warp_wait_uniform<true>(bar(kAE + buf), ((step >> 1) - 1) & 1, ctl);
+          if (new_q) ++nq;
+          last_q = v.first + t;
+#pragma unroll
+          for (int g = first; g < end; ++g) {
+            if (new_k) ok = ok && warp_wait_uniform<true>(bar(kKF + g), nk & 1, ctl);
+            if (new_q) ok = ok && warp_wait_uniform<true>(bar(kQF + g), (nq - 1) & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = group_begin(g); c < group_begin(g + 1); ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_pair_ss_if(leader, d, kd + static_cast<uint64_t>((c * kKChunk + 32 * kk) >> 4),
+                                qd + static_cast<uint64_t>((c * kQChunk + 32 * kk) >> 4), kIdesc,
+                                (c != 0 && c != kFirst) || kk > 0 ? 1u : 0u);
+            if (last) umma_commit_pair_if(leader, bar(kKE + g), 3);
+            if (q_goes) umma_commit_pair_if(leader, bar(kQE + g), 3);
+          }
+          if (!ok) break;
+          umma_commit_pair_if(leader, bar(kAF + buf), 3);
+        }
+        ++nk;
+        v = after;
+      }
+    };
+    if (which == 0)
+      issue(std::integral_constant<int, 0>(), std::integral_constant<int, kGroups / 2>());
+    else
+      issue(std::integral_constant<int, kGroups / 2>(), std::integral_constant<int, kGroups>());
+    umma_commit_pair_if(leader, bar(kDrain + which), 1);  // arrives once every MMA issued above has completed
+    drain_bar(bar(kDrain + which), 0u);
+    __syncwarp();
+  } else if (warp == 1 || warp == 3) {
+    // Rank 1 has nothing to issue.  With an FP8 cache these threads relay its fill
+    // warps' arrivals to rank 0, whose MMAs read this CTA's rows too: the warps
+    // release to their own CTA, a thread without stores of its own to the cluster
+    // (a release to the cluster by each of them waits for its earlier stores).
+    if (kFp8 && lane == 0) {
+      const uint32_t rk = mapa(bar(kKF), 0);
+      const int first = warp == 1 ? 0 : kGroups / 2, end = warp == 1 ? kGroups / 2 : kGroups;
+      Walk walk(p, begin);
+      Visit v;
+      bool ok = true;
+      for (uint32_t nk = 0; ok && walk.next_live(v); ++nk)
+        for (int g = first; ok && g < end; ++g)
+          if ((ok = wait(bar(kWide + g), nk & 1, ctl))) mbar_arrive_remote(rk + 8u * g);
+    }
+    __syncwarp();
+  } else if (warp >= kEpiWarp && warp < kEpiWarp + 8) {
+    // ================================================= sums over heads and tokens
+    // Warp (quarter, half): rows 32 quarter .. of the CTA's 128, one a lane, heads 64 half .. +63.
+    const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
+    const int r = 32 * quarter + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 64u * half;
+    const uint32_t s_lse = sbase + kOffLse + 256u * (warp - kEpiWarp);  // this warp's own
+    float2* my_lse = reinterpret_cast<float2*>(smem + kOffLse + 256 * (warp - kEpiWarp)) + lane;
+    float* s_half = reinterpret_cast<float*>(smem + kOffHalf);
+    const uint32_t racc = mapa(bar(kAE), 0);
+    Walk walk(p, begin);
+    Visit v;
+    uint32_t step = 0;
+    for (uint32_t visit = 0; walk.next(v); ++visit) {
+      const int pos = v.tile * kTileRows + static_cast<int>(rank) * kRows + r;
+      float old = 0.f;
+      if (half == 0 && v.t0 == 0 && pos < v.len && p.decay != 0.f)
+        old = p.decay * p.weights[v.b * p.w_stride + pos];
+      float sum = 0.f;
+      bool ok = true;
+      const float2* lse = reinterpret_cast<const float2*>(p.lse + static_cast<long long>(v.first) * kHeads + 64 * half) + lane;
+      float2 l2 = v.pos < v.t1 ? __ldg(lse + static_cast<long long>(v.pos) * (kHeads / 2)) : make_float2(0.f, 0.f);
+      for (int t = v.pos; t < v.t1; ++t, ++step) {
+        const uint32_t buf = step & 1;
+        // a head without a result (-inf) weighs nothing: 2^(s - inf)
+        auto log2_of = [](float x) { return x == -INFINITY ? -INFINITY : -x * kLog2e; };
+        *my_lse = make_float2(log2_of(l2.x), log2_of(l2.y));
+        if (t + 1 < v.t1) l2 = __ldg(lse + static_cast<long long>(t + 1) * (kHeads / 2));
+        __syncwarp();
+        ok = warp_wait_uniform<true>(bar(kAF + buf), (step >> 1) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        float e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[2][32];
+          tmem_ld32(tl + 256u * buf + 32u * h, x[0]);
+          tmem_ld32(tl + 256u * buf + kHeads + 32u * h, x[1]);
+          tmem_wait_ld();
+          if (h == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(racc + 8u * buf);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 l = ld_shared_v4f(s_lse + 128u * h + 4u * c);
+            const float bias[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              e[i] += ex2_approx(fmaf(__uint_as_float(x[0][c + i]) + __uint_as_float(x[1][c + i]), p.scale_log2, bias[i]));
+          }
+        }
+        __syncwarp();  // the warp's lse has been read
+        if (pos < limit(v, t, p.causal)) sum += (e[0] + e[1]) + (e[2] + e[3]);  // hidden rows may hold anything
+      }
+      // the two halves of the heads meet; the buffer of the visit before the last is free again
+      if (half == 1) s_half[(visit & 1) * kRows + r] = sum;
+      if (!named_bar_all(1 + quarter, 64, ok)) break;
+      if (half == 0) {
+        sum += s_half[(visit & 1) * kRows + r];
+        if (v.t0 != 0)
+          p.parts[unit * kTileRows + static_cast<int>(rank) * kRows + r] = sum;
+        else if (pos < v.len)
+          p.out[v.b * p.out_stride + pos] = old + sum;
+      }
+    }
+  } else if (kFp8 && warp >= kFillWarp) {
+    // ================================================= FP8 rows: read, widened and stored as the TMA would
+    // Warp w has rows 16 w .. +15 (all of one page).  In turns of 64 bytes a row,
+    // eight of codes (a chunk each) and two of position dims (half a chunk), four
+    // lanes read a row and eight rows lie side by side: a lane has a 16-byte unit
+    // of two rows.  Three turns' loads are in flight while one is widened, and the
+    // rows of the visits after that are asked into L2.  The loop is rolled (the
+    // loads move through registers): unrolled, the warps waited for instructions
+    // (64 x 8192 196 us).
+    const int w = warp - kFillWarp;
+    constexpr int kAhead = 3;   // visits whose rows are asked into L2 (the one at work among them)
+    constexpr int kTurns = 10;
+    Walk walk(p, begin), ahead(p, begin);
+    Visit v;
+    uint32_t nk = 0;
+    bool ok = true, more = walk.next_live(v);
+    const int row0 = lane >> 2, unit16 = lane & 3;
+    // the lane's two rows of a visit (null: a page that is not there reads as zeros)
+    auto rows_of = [&](const Visit& s) -> const uint8_t* {
+      const int page = page_of(p, s, s.tile * 4 + static_cast<int>(rank) * 2 + (w >> 2));
+      return page < 0 ? nullptr
+                      : p.kv + (static_cast<long long>(page) * kPage + 16 * (w & 3) + row0) * MLA_FP8_ROW_BYTES;
+    };
+    auto ask = [&]() {
+      Visit far;
+      if (!ahead.next_live(far)) return;
+      const uint8_t* src = rows_of(far);
+      if (src && lane == 0) bulk_prefetch_l2(src, 16 * MLA_FP8_ROW_BYTES);
+    };
+    struct Turn {
+      uint4 a, b;
+    };
+    auto load = [&](const uint8_t* rows, int j) {
+      Turn t = {};
+      if (rows) {
+        const uint8_t* src = rows + 64 * j + (j < 8 ? 0 : 16) + 16 * unit16;
+        t.a = ld_global_nc_v4(src);
+        t.b = ld_global_nc_v4(src + 8 * MLA_FP8_ROW_BYTES);
+      }
+      return t;
+    };
+    auto scales_of = [&](const uint8_t* rows) {
+      return rows ? make_uint2(__ldg(reinterpret_cast<const uint32_t*>(rows + 512)),
+                               __ldg(reinterpret_cast<const uint32_t*>(rows + 8 * MLA_FP8_ROW_BYTES + 512)))
+                  : make_uint2(0u, 0u);
+    };
+    const uint32_t to = sbase + (16 * w + row0) * 128, sw = row0;  // (row & 7, for both of the rows)
+    const uint8_t* rows = more ? rows_of(v) : nullptr;
+    uint2 scales = scales_of(rows);
+    Turn t0 = load(rows, 0), t1 = load(rows, 1), t2 = load(rows, 2);
+    for (int i = 0; i < kAhead; ++i) ask();
+    while (ok && more) {
+      more = walk.next_live(v);
+      const uint8_t* next = more ? rows_of(v) : nullptr;
+      const uint2 next_scales = scales_of(next);
+      ask();
+#pragma unroll 1
+      for (int j = 0; j < kTurns; ++j) {
+        const int g = j < 3 ? 0 : j < 5 ? 1 : j < 7 ? 2 : 3;  // (turns 8 and 9 are chunk 8)
+        if (nk > 0 && ((1u << j) & 0xa9u)) ok = warp_wait_uniform<true>(bar(kKE + g), (nk - 1) & 1, ctl);
+        if (!ok) break;
+        if (j < 8) {
+          const uint32_t dst = to + j * kKChunk, at0 = ((2u * unit16) ^ sw) << 4, at1 = ((2u * unit16 + 1u) ^ sw) << 4;
+          const uint32_t e0 = (scales.x >> (8 * (j >> 1))) & 255u, e1 = (scales.y >> (8 * (j >> 1))) & 255u;
+          const uint4 o0 = widen8(t0.a.x, t0.a.y, e0), o1 = widen8(t0.a.z, t0.a.w, e0);
+          st_shared_v4(dst + at0, o0.x, o0.y, o0.z, o0.w);
+          st_shared_v4(dst + at1, o1.x, o1.y, o1.z, o1.w);
+          const uint4 o2 = widen8(t0.b.x, t0.b.y, e1), o3 = widen8(t0.b.z, t0.b.w, e1);
+          st_shared_v4(dst + 1024u + at0, o2.x, o2.y, o2.z, o2.w);
+          st_shared_v4(dst + 1024u + at1, o3.x, o3.y, o3.z, o3.w);
+        } else {
+          const uint32_t dst = to + 8 * kKChunk + (((unit16 + 4u * (j - 8)) ^ sw) << 4);
+          st_shared_v4(dst, t0.a.x, t0.a.y, t0.a.z, t0.a.w);
+          st_shared_v4(dst + 1024u, t0.b.x, t0.b.y, t0.b.z, t0.b.w);
+        }
+        t0 = t1;
+        t1 = t2;
+        t2 = j + 3 < kTurns ? load(rows, j + 3) : load(next, j + 3 - kTurns);
+        if ((1u << j) & 0x254u) {  // the group's last turn
+          fence_proxy_async_smem();  // generic writes, read next by the tensor core
+          __syncwarp();
+          if (lane == 0) mbar_arrive(rank == 0 ? bar(kKF + g) : bar(kWide + g));
+        }
+      }
+      scales = next_scales;
+      rows = next;
+      ++nk;
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA touches another's shared memory after this
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// Adds the parts of tiles that several units share, in the line's order: block u
+// does so for the tile in whose tokens unit u begins, if no unit before it does.
+__global__ void __launch_bounds__(kTileRows) mla_attention_weights_join_kernel(const __grid_constant__ WeightsParams p) {
+  const int u = blockIdx.x;
+  const int4 mine = p.begins[u];
+  if (mine.x < 0 || mine.z == 0) return;
+  auto same = [&](const int4& o) { return o.x == mine.x && o.y == mine.y && o.z > 0; };
+  for (int v = u - 1; v >= 0; --v) {
+    const int4 o = p.begins[v];
+    if (o.x < 0) continue;
+    if (same(o)) return;
+    break;
+  }
+  const int pos = mine.y * kTileRows + static_cast<int>(threadIdx.x);
+  if (pos >= len_of(p, mine.x)) return;
+  float* out = p.out + mine.x * p.out_stride + pos;
+  float sum = *out + p.parts[u * kTileRows + threadIdx.x];
+  for (int v = u + 1; v < kUnits; ++v) {
+    const int4 o = p.begins[v];
+    if (o.x < 0) continue;
+    if (!same(o)) break;
+    sum += p.parts[v * kTileRows + threadIdx.x];
+  }
+  *out = sum;
+}
+
+// Device check and kernel attributes, once per device.
 int weights_device_ready() {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_DEVICE;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  return major == 10 && minor == 3 ? MLA_OK : MLA_ERR_DEVICE;
+  static std::once_flag once[64];
+  static int state[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_DEVICE;
+  std::call_once(once[dev], [dev] {
+    int major = 0, minor = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (major != 10 || minor != 3) {
+      state[dev] = MLA_ERR_DEVICE;
+      return;
+    }
+    state[dev] = MLA_OK;
+    for (auto* kernel : {mla_attention_weights_kernel<false>, mla_attention_weights_kernel<true>})
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        state[dev] = MLA_ERR_CUDA;
+    cudaGetLastError();
+  });
+  return state[dev];
+}
+
+// Rows of 576 dims as boxes of 64 dims x 64 rows.
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows) {
+  const cuuint64_t size[2] = {kDqk, rows}, strides[1] = {kDqk * 2};
+  const cuuint32_t box[2] = {64, 64};
+  return encode(m, false, 2, base, size, strides, box);
 }
 
 int check_sizes(int num_tokens, int num_requests, int max_len, unsigned flags) {
@@ -110,6 +682,9 @@ int check_sizes(int num_tokens, int num_requests, int max_len, unsigned flags) {
   if ((static_cast<int64_t>(num_tokens) + 1) * kHeads > INT32_MAX || max_len > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
+
+constexpr size_t kBeginBytes = (kUnits * sizeof(int4) + 255) / 256 * 256;
+constexpr size_t kWorkspace = kBeginBytes + kUnits * kTileRows * sizeof(float);
 
 }  // namespace
 }  // namespace mla
@@ -121,7 +696,7 @@ extern "C" {
 size_t mla_attention_weights_workspace_size(int num_tokens, int num_requests, int max_len, unsigned flags, int* err) {
   const int rc = check_sizes(num_tokens, num_requests, max_len, flags);
   if (err) *err = rc;
-  return rc == MLA_OK ? 256 : 0;
+  return rc == MLA_OK ? kWorkspace : 0;
 }
 
 int mla_attention_weights(const void* q, const float* lse, const void* kv_cache, int64_t num_pages,
@@ -131,7 +706,7 @@ int mla_attention_weights(const void* q, const float* lse, const void* kv_cache,
                           unsigned flags, void* workspace, size_t ws_bytes, float* out, int64_t out_stride,
                           int* status, mla_stream_t stream) {
   if (!q || !lse || !kv_cache || !block_table || !cache_lens || !out || !status || !workspace) return MLA_ERR_INVALID_ARG;
-  if (!al(q, 16) || !al(kv_cache, 16) || !al(lse, 4) || !al(block_table, 4) || !al(cache_lens, 4) || !al(token_starts, 4) ||
+  if (!al(q, 16) || !al(kv_cache, 16) || !al(lse, 16) || !al(block_table, 4) || !al(cache_lens, 4) || !al(token_starts, 4) ||
       !al(weights, 4) || !al(out, 4) || !al(status, 4) || !al(workspace, 256))
     return MLA_ERR_INVALID_ARG;
   if (num_heads != kHeads) return MLA_ERR_UNSUPPORTED;
@@ -145,15 +720,14 @@ int mla_attention_weights(const void* q, const float* lse, const void* kv_cache,
     return MLA_ERR_INVALID_ARG;
   if (out == weights && num_requests > 1 && out_stride != weights_stride) return MLA_ERR_INVALID_ARG;
   if (num_pages > (INT32_MAX / kPage) - 1) return MLA_ERR_UNSUPPORTED;
-  if (ws_bytes < mla_attention_weights_workspace_size(num_tokens, num_requests, max_len, flags, nullptr))
-    return MLA_ERR_WORKSPACE;
+  if (ws_bytes < kWorkspace) return MLA_ERR_WORKSPACE;
   if ((rc = weights_device_ready()) != MLA_OK) return rc;
   if (num_tokens == 0) return MLA_OK;
+  const bool fp8 = (flags & MLA_FLAG_KV_FP8) != 0;
   WeightsParams p;
-  p.q = static_cast<const uint16_t*>(q);
-  p.lse = lse;
   p.kv = static_cast<const uint8_t*>(kv_cache);
   p.num_pages = num_pages;
+  p.lse = lse;
   p.table = block_table;
   p.bt_stride = bt_stride;
   p.lens = cache_lens;
@@ -162,17 +736,27 @@ int mla_attention_weights(const void* q, const float* lse, const void* kv_cache,
   p.requests = num_requests;
   p.tokens = num_tokens;
   p.causal = (flags & MLA_FLAG_CAUSAL) ? 1 : 0;
-  p.fp8 = (flags & MLA_FLAG_KV_FP8) ? 1 : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   p.decay = decay;
   p.weights = weights;
   p.w_stride = weights_stride;
   p.out = out;
   p.out_stride = out_stride;
+  p.begins = static_cast<int4*>(workspace);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kBeginBytes);
   p.status = status;
-  const int x = (max_len + 7) / 8;
-  mla_attention_weights_kernel<<<dim3(x < 4096 ? x : 4096, num_requests < 65535 ? num_requests : 65535), 256, 0,
-                                 static_cast<cudaStream_t>(stream)>>>(p);
+  CUtensorMap tm_q, tm_k;
+  if (!encode_rows(&tm_q, q, static_cast<uint64_t>(num_tokens) * kHeads)) return MLA_ERR_CUDA;
+  // (an FP8 cache's rows do not come by TMA)
+  if (!encode_rows(&tm_k, fp8 ? q : kv_cache, fp8 ? kHeads : static_cast<uint64_t>(num_pages) * kPage)) return MLA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (fp8)
+    mla_attention_weights_kernel<true><<<2 * kUnits, kThreadsFp8, kSmem, s>>>(p, tm_q, tm_k);
+  else
+    mla_attention_weights_kernel<false><<<2 * kUnits, kThreads, kSmem, s>>>(p, tm_q, tm_k);
+  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  if (!token_starts && num_tokens == num_requests) return MLA_OK;  // one step a tile: no tile is shared
+  mla_attention_weights_join_kernel<<<kUnits, kTileRows, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

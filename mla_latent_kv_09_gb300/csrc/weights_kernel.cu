@@ -68,7 +68,8 @@ enum Bar {
   kQE = kQF + kGroups,        // [4] its last product is done
   kAF = kQE + kGroups,        // [2] both accumulators of a step complete
   kAE = kAF + 2,              // [2] rank 0: ... and read by the sixteen warps of both CTAs
-  kWide = kAE + 2,            // [4] rank 1, FP8 rows: widened (for the relay)
+  kRaw = kAE + 2,             // [4] FP8 rows: a group's codes landed in this CTA
+  kWide = kRaw + kGroups,     // [4] rank 1, FP8 rows: widened (for the relay)
   kDrain = kWide + kGroups,   // [2] per issuer
   kNumBars = kDrain + 2
 };
@@ -77,6 +78,7 @@ constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + kSlack;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr int kEpiWarp = 4;                   // eight warps (a multiple of four: lane quarters)
 constexpr int kFillWarp = 12;                 // eight further warps, FP8 rows only
+constexpr int kPeAt = 264;                    // an FP8 row's position dims, in bf16 elements
 constexpr int kThreads = 32 * 12, kThreadsFp8 = 32 * 20;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = idesc_bf16(256, 128, 0);
@@ -267,7 +269,7 @@ __device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t e) {
 template <bool kFp8>
 __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1) __cluster_dims__(2, 1, 1)
 mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap tm_q,
-                             const __grid_constant__ CUtensorMap tm_k) {
+                             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_pe) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t mis = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + mis;
@@ -286,6 +288,7 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
       mbar_init(bar(kKE + g), 1);
       mbar_init(bar(kQF + g), 1);
       mbar_init(bar(kQE + g), 1);
+      mbar_init(bar(kRaw + g), 1);
       mbar_init(bar(kWide + g), 8);
     }
     for (int a = 0; a < 2; ++a) {
@@ -329,10 +332,15 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     while (globaltimer_ns() - t0 < kDrainNs / 8) {
     }
   };
-  if (warp == 0 && !kFp8) {
+  if (warp == 0) {
     // ================================================= rows, by TMA
+    // FP8: a chunk's codes go to the second half of its slot (row r at 64 r), for
+    // this CTA's fill warps to widen in place; the position dims to theirs at once.
     const uint32_t rk = mapa(bar(kKF), 0);
-    if (lane == 0) tma_prefetch_desc(&tm_k);
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      if (kFp8) tma_prefetch_desc(&tm_pe);
+    }
     Walk walk(p, begin);
     Visit v;
     bool ok = true;
@@ -349,6 +357,17 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
         if (nk > 0 && !(ok = warp_wait_uniform<true>(bar(kKE + g), (nk - 1) & 1, ctl))) break;
         if (lane == 0) {
           const int c0 = group_begin(g), c1 = group_begin(g + 1);
+          if (kFp8) {
+            mbar_arrive_expect_tx_relaxed(bar(kRaw + g), (c1 - c0) * (kKChunk / 2) + (c1 == kNumChunks ? kKChunk / 2 : 0));
+            for (int c = c0; c < c1; ++c)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (c < 8)
+                  tma_load_2d(sbase + c * kKChunk + kKChunk / 2 + e * (kKChunk / 4), &tm_k, 64 * c, y[e], bar(kRaw + g));
+                else
+                  tma_load_2d(sbase + c * kKChunk + e * (kKChunk / 2), &tm_pe, kPeAt, y[e], bar(kRaw + g));
+            continue;
+          }
           if (rank == 0) mbar_arrive_expect_tx_relaxed(bar(kKF + g), (c1 - c0) * 2 * kKChunk);
           for (int c = c0; c < c1; ++c)
 #pragma unroll
@@ -521,91 +540,64 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
       }
     }
   } else if (kFp8 && warp >= kFillWarp) {
-    // ================================================= FP8 rows: read, widened and stored as the TMA would
-    // Warp w has rows 16 w .. +15 (all of one page).  In turns of 64 bytes a row,
-    // eight of codes (a chunk each) and two of position dims (half a chunk), four
-    // lanes read a row and eight rows lie side by side: a lane has a 16-byte unit
-    // of two rows.  Three turns' loads are in flight while one is widened, and the
-    // rows of the visits after that are asked into L2.  The loop is rolled (the
-    // loads move through registers): unrolled, the warps waited for instructions
-    // (64 x 8192 196 us).
+    // ================================================= FP8 rows: codes widened in place
+    // Warp w has rows 16 w .. +15 (all of one page): four lanes a row, eight rows
+    // side by side, a 16-byte unit of a chunk's codes of two rows a lane.  A
+    // group's codes are in the eight warps' registers before the first of them
+    // writes over codes.  (Rows read from global memory by these warps, three
+    // turns of loads in flight: 64 x 8192 245 us, bound by their latency; the TMA
+    // holds a whole tile in flight.)
     const int w = warp - kFillWarp;
-    constexpr int kAhead = 3;   // visits whose rows are asked into L2 (the one at work among them)
-    constexpr int kTurns = 10;
-    Walk walk(p, begin), ahead(p, begin);
+    Walk walk(p, begin);
     Visit v;
     uint32_t nk = 0;
     bool ok = true, more = walk.next_live(v);
     const int row0 = lane >> 2, unit16 = lane & 3;
-    // the lane's two rows of a visit (null: a page that is not there reads as zeros)
-    auto rows_of = [&](const Visit& s) -> const uint8_t* {
+    // the scale bytes of the lane's two rows of a visit
+    auto scales_of = [&](const Visit& s) {
       const int page = page_of(p, s, s.tile * 4 + static_cast<int>(rank) * 2 + (w >> 2));
-      return page < 0 ? nullptr
-                      : p.kv + (static_cast<long long>(page) * kPage + 16 * (w & 3) + row0) * MLA_FP8_ROW_BYTES;
-    };
-    auto ask = [&]() {
-      Visit far;
-      if (!ahead.next_live(far)) return;
-      const uint8_t* src = rows_of(far);
-      if (src && lane == 0) bulk_prefetch_l2(src, 16 * MLA_FP8_ROW_BYTES);
-    };
-    struct Turn {
-      uint4 a, b;
-    };
-    auto load = [&](const uint8_t* rows, int j) {
-      Turn t = {};
-      if (rows) {
-        const uint8_t* src = rows + 64 * j + (j < 8 ? 0 : 16) + 16 * unit16;
-        t.a = ld_global_nc_v4(src);
-        t.b = ld_global_nc_v4(src + 8 * MLA_FP8_ROW_BYTES);
-      }
-      return t;
-    };
-    auto scales_of = [&](const uint8_t* rows) {
-      return rows ? make_uint2(__ldg(reinterpret_cast<const uint32_t*>(rows + 512)),
-                               __ldg(reinterpret_cast<const uint32_t*>(rows + 8 * MLA_FP8_ROW_BYTES + 512)))
-                  : make_uint2(0u, 0u);
+      if (page < 0) return make_uint2(0u, 0u);
+      const uint8_t* row = p.kv + (static_cast<long long>(page) * kPage + 16 * (w & 3) + row0) * MLA_FP8_ROW_BYTES + 512;
+      return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row)),
+                        __ldg(reinterpret_cast<const uint32_t*>(row + 8 * MLA_FP8_ROW_BYTES)));
     };
     const uint32_t to = sbase + (16 * w + row0) * 128, sw = row0;  // (row & 7, for both of the rows)
-    const uint8_t* rows = more ? rows_of(v) : nullptr;
-    uint2 scales = scales_of(rows);
-    Turn t0 = load(rows, 0), t1 = load(rows, 1), t2 = load(rows, 2);
-    for (int i = 0; i < kAhead; ++i) ask();
+    const uint32_t at0 = ((2u * unit16) ^ sw) << 4, at1 = ((2u * unit16 + 1u) ^ sw) << 4;
+    const uint32_t from = sbase + kKChunk / 2 + (16 * w + row0) * 64 + 16 * unit16;
+    uint2 scales = more ? scales_of(v) : make_uint2(0u, 0u);
     while (ok && more) {
       more = walk.next_live(v);
-      const uint8_t* next = more ? rows_of(v) : nullptr;
-      const uint2 next_scales = scales_of(next);
-      ask();
+      const uint2 next_scales = more ? scales_of(v) : make_uint2(0u, 0u);
 #pragma unroll 1
-      for (int j = 0; j < kTurns; ++j) {
-        const int g = j < 3 ? 0 : j < 5 ? 1 : j < 7 ? 2 : 3;  // (turns 8 and 9 are chunk 8)
-        if (nk > 0 && ((1u << j) & 0xa9u)) ok = warp_wait_uniform<true>(bar(kKE + g), (nk - 1) & 1, ctl);
-        if (!ok) break;
-        if (j < 8) {
-          const uint32_t dst = to + j * kKChunk, at0 = ((2u * unit16) ^ sw) << 4, at1 = ((2u * unit16 + 1u) ^ sw) << 4;
-          const uint32_t e0 = (scales.x >> (8 * (j >> 1))) & 255u, e1 = (scales.y >> (8 * (j >> 1))) & 255u;
-          const uint4 o0 = widen8(t0.a.x, t0.a.y, e0), o1 = widen8(t0.a.z, t0.a.w, e0);
-          st_shared_v4(dst + at0, o0.x, o0.y, o0.z, o0.w);
-          st_shared_v4(dst + at1, o1.x, o1.y, o1.z, o1.w);
-          const uint4 o2 = widen8(t0.b.x, t0.b.y, e1), o3 = widen8(t0.b.z, t0.b.w, e1);
-          st_shared_v4(dst + 1024u + at0, o2.x, o2.y, o2.z, o2.w);
-          st_shared_v4(dst + 1024u + at1, o3.x, o3.y, o3.z, o3.w);
-        } else {
-          const uint32_t dst = to + 8 * kKChunk + (((unit16 + 4u * (j - 8)) ^ sw) << 4);
-          st_shared_v4(dst, t0.a.x, t0.a.y, t0.a.z, t0.a.w);
-          st_shared_v4(dst + 1024u, t0.b.x, t0.b.y, t0.b.z, t0.b.w);
-        }
-        t0 = t1;
-        t1 = t2;
-        t2 = j + 3 < kTurns ? load(rows, j + 3) : load(next, j + 3 - kTurns);
-        if ((1u << j) & 0x254u) {  // the group's last turn
-          fence_proxy_async_smem();  // generic writes, read next by the tensor core
-          __syncwarp();
-          if (lane == 0) mbar_arrive(rank == 0 ? bar(kKF + g) : bar(kWide + g));
-        }
+      for (int g = 0; g < kGroups; ++g) {
+        const int c0 = group_begin(g), c1 = min(group_begin(g + 1), 8);
+        ok = warp_wait_uniform(bar(kRaw + g), nk & 1, ctl);
+        uint4 a[3], b[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (ok && c0 + i < c1) {
+            a[i] = ld_shared_v4u(from + (c0 + i) * kKChunk);
+            b[i] = ld_shared_v4u(from + (c0 + i) * kKChunk + 512u);
+          }
+        if (!(ok = named_bar_all(5, 256, ok))) break;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (c0 + i < c1) {
+            const int c = c0 + i;
+            const uint32_t dst = to + c * kKChunk;
+            const uint32_t e0 = (scales.x >> (8 * (c >> 1))) & 255u, e1 = (scales.y >> (8 * (c >> 1))) & 255u;
+            const uint4 o0 = widen8(a[i].x, a[i].y, e0), o1 = widen8(a[i].z, a[i].w, e0);
+            st_shared_v4(dst + at0, o0.x, o0.y, o0.z, o0.w);
+            st_shared_v4(dst + at1, o1.x, o1.y, o1.z, o1.w);
+            const uint4 o2 = widen8(b[i].x, b[i].y, e1), o3 = widen8(b[i].z, b[i].w, e1);
+            st_shared_v4(dst + 1024u + at0, o2.x, o2.y, o2.z, o2.w);
+            st_shared_v4(dst + 1024u + at1, o3.x, o3.y, o3.z, o3.w);
+          }
+        fence_proxy_async_smem();  // generic writes, read next by the tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rank == 0 ? bar(kKF + g) : bar(kWide + g));
       }
       scales = next_scales;
-      rows = next;
       ++nk;
     }
     __syncwarp();
@@ -667,6 +659,22 @@ int weights_device_ready() {
     cudaGetLastError();
   });
   return state[dev];
+}
+
+// The codes of an FP8 cache's rows as boxes of 64 x 64 rows, as they are.
+bool encode_codes(CUtensorMap* m, const void* base, uint64_t rows) {
+  EncodeTiledFn fn = encode_tiled();
+  const cuuint64_t size[2] = {512, rows}, strides[1] = {MLA_FP8_ROW_BYTES};
+  const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), size, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Their position dims as boxes of 64 dims x 64 rows.
+bool encode_position(CUtensorMap* m, const void* base, uint64_t rows) {
+  const cuuint64_t size[2] = {MLA_FP8_ROW_BYTES / 2, rows}, strides[1] = {MLA_FP8_ROW_BYTES};
+  const cuuint32_t box[2] = {64, 64};
+  return encode(m, false, 2, base, size, strides, box);
 }
 
 // Rows of 576 dims as boxes of 64 dims x 64 rows.
@@ -745,15 +753,17 @@ int mla_attention_weights(const void* q, const float* lse, const void* kv_cache,
   p.begins = static_cast<int4*>(workspace);
   p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kBeginBytes);
   p.status = status;
-  CUtensorMap tm_q, tm_k;
+  CUtensorMap tm_q, tm_k, tm_pe = {};
+  const uint64_t rows = static_cast<uint64_t>(num_pages) * kPage;
   if (!encode_rows(&tm_q, q, static_cast<uint64_t>(num_tokens) * kHeads)) return MLA_ERR_CUDA;
-  // (an FP8 cache's rows do not come by TMA)
-  if (!encode_rows(&tm_k, fp8 ? q : kv_cache, fp8 ? kHeads : static_cast<uint64_t>(num_pages) * kPage)) return MLA_ERR_CUDA;
+  if (fp8 ? !encode_codes(&tm_k, kv_cache, rows) || !encode_position(&tm_pe, kv_cache, rows)
+          : !encode_rows(&tm_k, kv_cache, rows))
+    return MLA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (fp8)
-    mla_attention_weights_kernel<true><<<2 * kUnits, kThreadsFp8, kSmem, s>>>(p, tm_q, tm_k);
+    mla_attention_weights_kernel<true><<<2 * kUnits, kThreadsFp8, kSmem, s>>>(p, tm_q, tm_k, tm_pe);
   else
-    mla_attention_weights_kernel<false><<<2 * kUnits, kThreads, kSmem, s>>>(p, tm_q, tm_k);
+    mla_attention_weights_kernel<false><<<2 * kUnits, kThreads, kSmem, s>>>(p, tm_q, tm_k, tm_pe);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   if (!token_starts && num_tokens == num_requests) return MLA_OK;  // one step a tile: no tile is shared
   mla_attention_weights_join_kernel<<<kUnits, kTileRows, 0, s>>>(p);

@@ -12,23 +12,29 @@ namespace mla {
 namespace {
 
 // ------------------------------------------------------------------ select
-// A cluster of CTAs per request, a slice of its rows each, which stays in
-// shared memory where it fits.  Weights map to order-preserving 32-bit keys;
-// three histogram passes over the cluster (11, 11, 10 bits) find the key T of
-// the last row to keep among those that are not protected, and how many of the
-// keys equal to T to keep; an ordered pass (ballots within a warp's run of
+// A cluster of CTAs per request, a slice of its rows each, which stays in shared
+// memory where it fits.  Weights map to order-preserving 32-bit keys; histogram
+// passes over the cluster (11, 11, 10 bits) find the key of the last row to keep
+// among those that are not protected, and how many of the keys equal to it to
+// keep.  They end as soon as a bin is taken whole, which saves the third one
+// wherever few keys share 22 bits.  An ordered pass (ballots within a group of 32
 // rows, prefix sums over warps and CTAs) then writes the kept rows in order.
+// Bound by latency: a load, two or three passes of three meetings each, the
+// ordered pass.  Loops are rolled: with the weights in registers and everything
+// unrolled, fetching the instructions took longer than running them (one request
+// of 8192 rows 15 us on one CTA).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kSelRows = 49152;  // rows of a slice that shared memory holds; the rest is read again in every pass
+constexpr int kMaxCluster = 16;  // (more than 8 as a permission asks)
+constexpr int kSelRows = 4096;   // of a CTA, before the request gets further ones
+constexpr int kRoomRows = 49152;  // of a slice that shared memory holds; others are read again in every pass
 
 struct SelectParams {
   const float* weights;
   long long stride;
   const int* lens;
   int max_len, keep, sinks, recent, cluster;
-  int smem_rows;  // of a slice, in dynamic shared memory
+  int room;  // rows of a slice in dynamic shared memory (a multiple of 32)
   int* kept;
   int* new_lens;
   float* new_weights;
@@ -37,7 +43,8 @@ struct SelectParams {
   int* status;
 };
 
-// Larger weight -> larger key; the two zeros are one key, NaN is -inf's.
+// Larger weight -> larger key, none of them 0 or kProtected; the two zeros are one key, NaN is -inf's.
+constexpr uint32_t kProtected = 0xffffffffu, kZero = 0x80000000u, kLowest = 0x007fffffu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) w = -__int_as_float(0x7f800000);
   const uint32_t u = __float_as_uint(w + 0.f);
@@ -50,37 +57,33 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   return v;
 }
 
-// Inclusive scan over a block of one value per thread (warp sums in s[32]); the caller syncs before s is used again.
-__device__ __forceinline__ int block_scan(int v, int* s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ int warp_scan(int v) {  // inclusive
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int n = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += n;
   }
-  if (lane == 31) s[warp] = v;
-  __syncthreads();
-  int before = lane < warp ? s[lane] : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  return v + before;
+  return v;
 }
 
 __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ float s_rows[];
-  __shared__ int s_hist[2][2048];  // this CTA's counts, by pass parity
-  __shared__ int s_sum[kSelWarps], s_found[2], s_count[2], s_warp[2][kSelWarps];
+  extern __shared__ uint32_t s_keys[];
+  __shared__ int s_hist[3][2048];  // this CTA's counts, per pass
+  __shared__ int s_coarse[3][64];  // ... of 32 bins together
+  __shared__ int s_found[3], s_count[2], s_warp[2][kSelWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
   const int given = p.lens[b];
   const int len = min(max(given, 0), p.max_len);
+  const float* row = p.weights + b * p.stride;
+  int* kept = p.kept + static_cast<long long>(b) * p.keep;
+  float* out = p.new_weights ? p.new_weights + b * p.new_stride : nullptr;
+
   if (tid == 0 && rank == 0) {
     if (given != len) atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
     p.new_lens[b] = min(len, p.keep);
   }
-  const float* row = p.weights + b * p.stride;
-  int* kept = p.kept + static_cast<long long>(b) * p.keep;
-  float* out = p.new_weights ? p.new_weights + b * p.new_stride : nullptr;
   const int all = rank * kSelThreads + tid, step = p.cluster * kSelThreads;
   const int stay = min(len, p.keep);
   for (int i = stay + all; i < p.keep; i += step) kept[i] = -1;
@@ -93,75 +96,90 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __g
     }
     return;
   }
+  // this CTA's slice, in groups of 32 rows; a run of them per warp
+  const int slice = ((len + p.cluster - 1) / p.cluster + 31) / 32, j0 = min(rank * slice * 32, len);
+  const int n = min(slice * 32, len - j0), per = (slice + kSelWarps - 1) / kSelWarps;
+  // of the slice, rows [free0, free1) are not protected
+  const int free0 = max(p.sinks - j0, 0), free1 = min(len - p.recent - j0, n);
+  auto key_of = [&](int i, float x) { return i < free0 || i >= free1 ? kProtected : weight_key(x); };
+#pragma unroll 4
+  for (int i = tid; i < min(n, p.room); i += kSelThreads) s_keys[i] = key_of(i, __ldg(row + j0 + i));
+  for (int i = tid; i < 3 * 2048; i += kSelThreads) s_hist[0][i] = 0;
+  __syncthreads();
+  const int i0 = min(32 * warp * per, n), i1 = min(32 * (warp + 1) * per, n);  // this warp's rows of the slice
 
-  // slices are multiples of 32 rows, so that a warp's ballots do not straddle them
-  const int slice = ((len + p.cluster - 1) / p.cluster + 31) / 32 * 32;
-  const int j0 = min(rank * slice, len), n = min(slice, len - j0);
-  for (int i = tid; i < min(n, p.smem_rows); i += kSelThreads) s_rows[i] = row[j0 + i];
-  auto weight = [&](int i) { return i < p.smem_rows ? s_rows[i] : __ldg(row + j0 + i); };
-  const int old_end = len - p.recent;
-  auto fixed = [&](int i) { return j0 + i < p.sinks || j0 + i >= old_end; };
+  // f(row of the slice, its key) for every lane's row of every group of the warp (0 for rows from i1 on)
+  auto each = [&](auto f) {
+#pragma unroll 2
+    for (int i = i0 + lane; i - lane < min(i1, p.room); i += 32) f(i, i < i1 ? s_keys[i] : 0u);
+#pragma unroll 1
+    for (int i = max(i0, p.room) + lane; i - lane < i1; i += 32) f(i, i < i1 ? key_of(i, __ldg(row + j0 + i)) : 0u);
+  };
 
   // ---- the key of the last row to keep
   uint32_t prefix = 0, mask = 0;
   int left = p.keep - p.sinks - p.recent;  // rows still to be taken among the keys that match the prefix
+  const bool some = left > 0;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    int* hist = s_hist[pass & 1];
+  for (int pass = 0; some && pass < 3; ++pass) {
+    int* hist = s_hist[pass];
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-    for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+    each([&](int, uint32_t key) {
+      if (key - 1u < kProtected - 1u && ((key ^ prefix) & mask) == 0) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+    });
     __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t key = weight_key(weight(i));
-      if ((key & mask) == prefix && !fixed(i)) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+    for (int i = warp; i < bins / 32; i += kSelWarps) {
+      const int sum = __reduce_add_sync(0xffffffffu, hist[32 * i + lane]);
+      if (lane == 0) s_coarse[pass][i] = sum;
     }
     if (p.cluster > 1)
       cluster_sync();
     else
       __syncthreads();
-    // bins from the largest down, two a thread
-    int c[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int bin = bins - 1 - (2 * tid + e);
-      if (bin < 0) continue;
-      if (p.cluster == 1)
-        c[e] = hist[bin];
-      else
-        for (int r = 0; r < p.cluster; ++r) c[e] += ld_cluster(&hist[bin], r);
-    }
-    const int upto = block_scan(c[0] + c[1], s_sum), before = upto - c[0] - c[1];
-    if (before < left && left <= upto) {
+    // One warp looks for the bin, from the largest down: among 64 sums of 32 bins
+    // (two a lane), then among those 32.  Every bin of every CTA read by every
+    // CTA cost 2,500 cycles a pass with eight of them.
+    if (warp == 0) {
+      int c[2] = {0, 0};
+      const int top = bins / 32 - 1 - 2 * lane;
+      if (top > 0)
+        for (int r = 0; r < p.cluster; ++r) {
+          c[0] += ld_cluster(&s_coarse[pass][top], r);
+          c[1] += ld_cluster(&s_coarse[pass][top - 1], r);
+        }
+      int upto = warp_scan(c[0] + c[1]), before = upto - c[0] - c[1];
       const int e = left <= before + c[0] ? 0 : 1;
-      s_found[0] = bins - 1 - (2 * tid + e);
-      s_found[1] = before + (e ? c[0] : 0);
+      const uint32_t here = __ballot_sync(0xffffffffu, before < left && left <= upto);
+      const int from = __ffs(here) - 1;  // (one lane: `left` is between 1 and the number of keys)
+      const int block = __shfl_sync(0xffffffffu, top - e, from);
+      const int above = __shfl_sync(0xffffffffu, before + (e ? c[0] : 0), from);
+      const int bin = 32 * block + 31 - lane;
+      int mine = 0;
+      for (int r = 0; r < p.cluster; ++r) mine += ld_cluster(&hist[bin], r);
+      upto = above + warp_scan(mine);
+      if (upto - mine < left && left <= upto) {
+        s_found[0] = bin;
+        s_found[1] = upto - mine;
+        s_found[2] = mine;
+      }
     }
     __syncthreads();
-    if (left > 0) {  // (left = 0: no bin was found, and none is needed)
-      prefix |= static_cast<uint32_t>(s_found[0]) << shift;
-      mask |= static_cast<uint32_t>(bins - 1) << shift;
-      left -= s_found[1];
-    }
-    __syncthreads();
+    prefix |= static_cast<uint32_t>(s_found[0]) << shift;
+    mask |= static_cast<uint32_t>(bins - 1) << shift;
+    left -= s_found[1];
+    if (left == s_found[2]) break;  // (the next pass writes s_found behind two more meetings)
   }
-  const bool some = p.keep > p.sinks + p.recent;
-  // 2: stays, 1: stays if there is room for it, 0: goes
-  auto grade = [&](int i) {
-    if (i >= n) return 0;
-    if (fixed(i)) return 2;
-    const uint32_t key = weight_key(weight(i));
-    return !some || key < prefix ? 0 : key > prefix ? 2 : 1;
-  };
+  if (!some) {  // the protected ones only
+    prefix = kProtected - 1u;
+    mask = kProtected;
+  }
 
-  // ---- the kept rows in order: a run of 32-row groups per warp
-  const int groups = (n + 31) / 32, per = (groups + kSelWarps - 1) / kSelWarps;
-  const int g0 = min(warp * per, groups), g1 = min(g0 + per, groups);
+  // ---- the kept rows in order
   int sure = 0, maybe = 0;
-  for (int g = g0; g < g1; ++g) {
-    const int a = grade(32 * g + lane);
-    sure += __popc(__ballot_sync(0xffffffffu, a == 2));
-    maybe += __popc(__ballot_sync(0xffffffffu, a == 1));
-  }
+  each([&](int, uint32_t key) {
+    sure += __popc(__ballot_sync(0xffffffffu, (key & mask) > prefix));
+    maybe += __popc(__ballot_sync(0xffffffffu, (key & mask) == prefix));
+  });
   if (lane == 0) {
     s_warp[0][warp] = sure;
     s_warp[1][warp] = maybe;
@@ -188,27 +206,33 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __g
     }
   }
   const uint32_t lower = (1u << lane) - 1u;
-  for (int g = g0; g < g1; ++g) {
-    const int i = 32 * g + lane, a = grade(i);
-    const uint32_t s = __ballot_sync(0xffffffffu, a == 2), m = __ballot_sync(0xffffffffu, a == 1);
+  each([&](int i, uint32_t key) {
+    const bool stays = (key & mask) > prefix, may = (key & mask) == prefix;
+    const uint32_t s = __ballot_sync(0xffffffffu, stays), m = __ballot_sync(0xffffffffu, may);
     const int maybe_at = maybe_before + __popc(m & lower);
-    const int place = sure_before + __popc(s & lower) + min(maybe_at, left);
-    if (a == 2 || (a == 1 && maybe_at < left)) {
+    if (stays || (may && maybe_at < left)) {
+      const int place = sure_before + __popc(s & lower) + min(maybe_at, left);
       kept[place] = j0 + i;
-      if (out) out[place] = weight(i);
+      // a key says what the weight was, but for zeros' signs, NaN and protected rows
+      if (out)
+        out[place] = key == kZero || key == kLowest || key == kProtected ? __ldg(row + j0 + i)
+                     : __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
     }
     sure_before += __popc(s);
     maybe_before += __popc(m);
-  }
+  });
   if (p.cluster > 1) cluster_sync();  // no CTA's counts go away while another reads them
 }
 
 // ------------------------------------------------------------------ compact
 // A CTA moves kMoveRows rows of a request: where they lie and where they go is
-// looked up once, then every thread copies 16-byte units, kMoveDepth of them in
-// flight.  HBM-bound: a row is read once and written once.
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;
+// looked up once, then every thread copies 16-byte units, all of its loads in
+// flight together.  HBM-bound: a row is read once and written once.  Small CTAs,
+// so that one's lookups run beside others' copies, and streaming loads and stores:
+// 64 requests x 4096 of up to 8192 rows (553 MB) 84.7 us, 6.5 TB/s, near a device
+// copy's rate; 110 us with 256 threads and 32 rows a CTA, 104.5 without streaming.
+constexpr int kMoveThreads = 128;
+constexpr int kMoveRows = 16;
 
 struct MoveParams {
   uint4* cache;
@@ -262,12 +286,12 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_compact_kernel(const _
 #pragma unroll
       for (int k = 0; k < kDepth; ++k) {
         const int at = k * kMoveThreads + threadIdx.x, r = at / kUnits;
-        if (at < kItems && s_src[r] >= 0) v[k] = p.cache[s_src[r] + at % kUnits];
+        if (at < kItems && s_src[r] >= 0) v[k] = ld_global_nc_v4(p.cache + s_src[r] + at % kUnits);
       }
 #pragma unroll
       for (int k = 0; k < kDepth; ++k) {
         const int at = k * kMoveThreads + threadIdx.x, r = at / kUnits;
-        if (at < kItems && s_src[r] >= 0) p.cache[s_dst[r] + at % kUnits] = v[k];
+        if (at < kItems && s_src[r] >= 0) __stcs(p.cache + s_dst[r] + at % kUnits, v[k]);
       }
       __syncthreads();
     }
@@ -291,7 +315,9 @@ int evict_device_ready() {
       return;
     }
     state[dev] = cudaFuncSetAttribute(mla_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      kSelRows * 4) == cudaSuccess
+                                      kRoomRows * 4) == cudaSuccess &&
+                         cudaFuncSetAttribute(mla_evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                              1) == cudaSuccess
                      ? MLA_OK
                      : MLA_ERR_CUDA;
     cudaGetLastError();
@@ -333,9 +359,9 @@ int mla_evict_select(const float* weights, int64_t weights_stride, const int32_t
   p.sinks = sinks;
   p.recent = recent;
   p.cluster = 1;
-  while (p.cluster < kMaxCluster && static_cast<int64_t>(p.cluster) * 4096 < max_len) p.cluster *= 2;
-  const int slice = ((max_len + p.cluster - 1) / p.cluster + 31) / 32 * 32;
-  p.smem_rows = slice < kSelRows ? slice : kSelRows;
+  while (p.cluster < kMaxCluster && static_cast<int64_t>(p.cluster) * kSelRows < max_len) p.cluster *= 2;
+  const int rows = ((max_len + p.cluster - 1) / p.cluster + 31) / 32 * 32;
+  p.room = rows < kRoomRows ? rows : kRoomRows;
   p.kept = kept;
   p.new_lens = new_lens;
   p.new_weights = new_weights;
@@ -345,7 +371,7 @@ int mla_evict_select(const float* weights, int64_t weights_stride, const int32_t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_requests) * p.cluster);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_rows) * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.room) * 4;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -133,7 +133,8 @@ def test_a_peaked_softmax():
 
 
 def test_equal_runs_are_the_decode_step():
-    """Two tokens a request: the decode step's own kernel, so its very bits."""
+    """Two tokens a request: the decode step's kernel, and (where no score beats
+    the first tile's largest by 2^8, as here) its very bits."""
     lens = [130, 64, 700]
     cache, table, rows = paged(lens, False, 10)
     q = rand((6, 128, 576), 11)

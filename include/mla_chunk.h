@@ -57,7 +57,8 @@ size_t mla_chunk_attend_workspace_size(int num_tokens, int num_requests, int max
  *   workspace     mla_chunk_attend_workspace_size bytes, 256-B aligned; a call
  *                 needs nothing of what an earlier one left there, and two
  *                 calls that may overlap need one each
- *   out           [num_tokens, 128, 512], bf16 (or fp32 with OUT_FP32)
+ *   out           [num_tokens, 128, 512], bf16 (or fp32 with OUT_FP32); must
+ *                 not overlap q
  *   lse           fp32 [num_tokens, 128], natural log
  *   status        device int, set (from 0, never cleared) to
  *                 MLA_ERR_BAD_TABLE if a length, a page (its rows read as

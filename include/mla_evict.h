@@ -36,8 +36,8 @@ size_t mla_attention_weights_workspace_size(int num_tokens, int num_requests, in
  *                 weights of (which may have seen more than this cache); -inf:
  *                 the head attended to nothing
  *   weights, out  fp32 rows of max_len at a stride of weights_stride and
- *                 out_stride; out may be weights itself.  weights may be NULL
- *                 where decay is 0
+ *                 out_stride; out may be weights itself, and must not overlap
+ *                 it otherwise.  weights may be NULL where decay is 0
  *   flags         MLA_FLAG_CAUSAL, MLA_FLAG_KV_FP8
  *   workspace     mla_attention_weights_workspace_size bytes, 256-B aligned;
  *                 two calls that may overlap need one each

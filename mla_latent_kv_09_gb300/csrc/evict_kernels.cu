@@ -5,11 +5,14 @@
 #include <cstdint>
 #include <mutex>
 
-#include "kernel_common.cuh"
 #include "mla_evict.h"
+#include "prefix_common.cuh"
 
 namespace mla {
 namespace {
+
+using prefix::al;
+using prefix::share;
 
 // ------------------------------------------------------------------ select
 // A cluster of CTAs per request, a slice of its rows each, which stays in shared
@@ -298,8 +301,6 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_compact_kernel(const _
   }
 }
 
-bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 // Device check and the selection's shared memory, once per device.
 int evict_device_ready() {
   static std::once_flag once[64];
@@ -337,7 +338,7 @@ int mla_evict_select(const float* weights, int64_t weights_stride, const int32_t
                      float* new_weights, int64_t new_weights_stride, int new_width, int* status,
                      mla_stream_t stream) {
   if (!weights || !cache_lens || !kept || !new_lens || !status || !al(weights, 4) || !al(cache_lens, 4) || !al(kept, 4) ||
-      !al(new_lens, 4) || !al(status, 4) || !al(new_weights, 4) || weights == new_weights)
+      !al(new_lens, 4) || !al(status, 4) || !al(new_weights, 4))
     return MLA_ERR_INVALID_ARG;
   if (num_requests < 0 || max_len < 1 || keep < 1 || sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks)
     return MLA_ERR_INVALID_ARG;
@@ -347,6 +348,8 @@ int mla_evict_select(const float* weights, int64_t weights_stride, const int32_t
   // rows are numbered in 32 bits, beyond the end by a grid's step
   if (max_len > (1 << 30) || keep > (1 << 30) || new_width > (1 << 30) || num_requests > INT32_MAX / kMaxCluster)
     return MLA_ERR_UNSUPPORTED;
+  if (share(weights, weights_stride, max_len, new_weights, new_weights_stride, new_width, num_requests))
+    return MLA_ERR_INVALID_ARG;
   const int rc = evict_device_ready();
   if (rc != MLA_OK) return rc;
   if (num_requests == 0) return MLA_OK;

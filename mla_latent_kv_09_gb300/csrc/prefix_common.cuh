@@ -198,6 +198,19 @@ int launch_dependent(void (*kernel)(A...), dim3 grid, dim3 block, int smem, int 
   return MLA_OK;
 }
 
+// Whether [rows][width] floats at a, and [rows][other_width] at b, share memory (rows at their strides; the strides of
+// one row say nothing).
+inline bool share(const float* a, int64_t a_stride, int64_t width, const float* b, int64_t b_stride, int64_t other_width,
+                  int64_t rows) {
+  if (!a || !b || width <= 0 || other_width <= 0 || rows <= 0) return false;
+  const int64_t d = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / static_cast<int64_t>(sizeof(float));
+  const int64_t a_all = (rows - 1) * a_stride + width, b_all = (rows - 1) * b_stride + other_width;
+  if (d >= a_all || -d >= b_all) return false;
+  if (rows == 1 || a_stride != b_stride) return true;
+  const int64_t at = (d % a_stride + a_stride) % a_stride;  // columns beside each other in rows of one stride
+  return at < width || at + other_width > a_stride;
+}
+
 inline bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace prefix

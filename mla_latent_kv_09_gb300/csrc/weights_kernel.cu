@@ -726,7 +726,9 @@ int mla_attention_weights(const void* q, const float* lse, const void* kv_cache,
   if (num_requests > 1 && (bt_stride < (static_cast<int64_t>(max_len) + kPage - 1) / kPage || out_stride < max_len ||
                            (decay != 0.f && weights_stride < max_len)))
     return MLA_ERR_INVALID_ARG;
-  if (out == weights && num_requests > 1 && out_stride != weights_stride) return MLA_ERR_INVALID_ARG;
+  if (decay != 0.f && (out != weights || (num_requests > 1 && out_stride != weights_stride)) &&
+      share(out, out_stride, max_len, weights, weights_stride, max_len, num_requests))
+    return MLA_ERR_INVALID_ARG;
   if (num_pages > (INT32_MAX / kPage) - 1) return MLA_ERR_UNSUPPORTED;
   if (ws_bytes < kWorkspace) return MLA_ERR_WORKSPACE;
   if ((rc = weights_device_ready()) != MLA_OK) return rc;

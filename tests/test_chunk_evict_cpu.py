@@ -65,6 +65,13 @@ def test_weights_check_their_arguments(lib):
            (13, math.nan), (13, math.inf), (15, 199), (16, 2), (16, 4), (20, 199), (20, 256)], m.MLA_ERR_INVALID_ARG)
     check(lib.mla_attention_weights, WEIGHTS, [(11, 16), (3, 1 << 40), (10, 1 << 24)], m.MLA_ERR_UNSUPPORTED)
     check(lib.mla_attention_weights, WEIGHTS, [(18, 0)], m.MLA_ERR_WORKSPACE)
+    for w, wst, out, ost, fits in [(OK, 200, OK + 400, 200, False), (OK, 200, OK, 256, False), (OK, 200, OK + 2396, 200, False),
+                                   (OK, 400, OK + 800, 400, True), (OK, 400, OK + 796, 400, False), (OK, 200, OK, 200, True),
+                                   (OK + 2400, 200, OK, 200, True), (OK + 2396, 200, OK, 200, False)]:
+        a = list(WEIGHTS)
+        a[14], a[15], a[19], a[20] = w, wst, out, ost
+        a[18] = 0  # (what passes the other checks fails for its workspace)
+        assert lib.mla_attention_weights(*a) == (m.MLA_ERR_WORKSPACE if fits else m.MLA_ERR_INVALID_ARG), (w, wst, out, ost)
 
 
 #         w   st   lens B  L    keep si re kept lens new     nst  nw   status stream
@@ -77,6 +84,10 @@ def test_select_checks_its_arguments(lib):
            (10, OK + 2), (13, OK + 2), (10, OK), (1, 99), (3, -1), (4, 0), (5, 0), (5, 11), (6, -1), (6, 41), (7, -1),
            (7, 37), (7, 2 ** 31 - 1), (11, 99), (12, 39)], m.MLA_ERR_INVALID_ARG)
     check(lib.mla_evict_select, SELECT, [(3, 1 << 29)], m.MLA_ERR_UNSUPPORTED)
+    for new, nst in [(OK + 4, 100), (OK + 1196, 100), (OK - 1196, 100), (OK + 200, 250)]:  # into the weights
+        a = list(SELECT)
+        a[10], a[11] = new, nst
+        assert lib.mla_evict_select(*a) == m.MLA_ERR_INVALID_ARG
 
 
 #          cache pages row  bt  st w kept kst kw lens B  out_table ost ow status stream

@@ -124,12 +124,43 @@ def test_many_tokens_of_a_long_request(fp8):
     assert_chunk(out, lse, q, rows, [0, 150, 211], tokens=[0, 1, 2, 77, 78, 148, 149, 150, 180, 209, 210])
 
 
+def test_more_pairs_than_the_plan_keeps_in_shared_memory():
+    """8,400 tokens of 3 requests, one of them most."""
+    lens, counts = [70, 300, 200], [8301, 1, 98]
+    cache, table, rows = paged(lens, False, 31)
+    starts = starts_of(counts)
+    q = rand((starts[-1], 128, 576), 32)
+    out, lse = attend(q, cache, table, ints(lens), SCALE, token_starts=ints(starts), causal=False)
+    assert_chunk(out, lse, q, rows, starts, False, tokens=[0, 1, 4095, 4096, 8191, 8192, 8193, 8299, 8300, 8301, 8302, 8398, 8399])
+    # equal queries, equal results, wherever in the line they are
+    q[:8301] = q[5]
+    out, lse = attend(q, cache, table, ints(lens), SCALE, token_starts=ints(starts), causal=False, out_fp32=True)
+    bo, bl = oracle.chunk_error_bound(f64(q[5:6]), rows[:1], [0, 1], SCALE,
+                                      oracle.chunk_attend(f64(q[5:6]), rows[:1], [0, 1], SCALE, False)[0], False)
+    assert (f64((out[:8301] - out[5]).abs().amax(0)) <= 2 * bo[0]).all() and (f64((lse[:8301] - lse[5]).abs().amax(0)) <= 2 * bl[0]).all()
+
+
 def test_a_peaked_softmax():
     lens, counts = [900, 333], [7, 20]
     cache, table, rows = paged(lens, False, 8, spread=8.0)
     q = rand((27, 128, 576), 9)
     out, lse = attend(q, cache, table, ints(lens), SCALE, token_starts=ints([0, 7, 27]), out_fp32=True)
     assert_chunk(out, lse, q, rows, [0, 7, 27])
+
+
+@pytest.mark.parametrize("growth", [1.5, 4.0])
+def test_scores_that_grow_along_the_cache(growth):
+    """Every tile's largest score beats the last one's, up to what fp16 weights would not hold unscaled."""
+    lens = [1500]
+    cache, table, rows = paged(lens, False, 33)
+    q = rand((5, 128, 576), 34)
+    j = torch.arange(1500, device="cuda")
+    place = table[0].long()[j // 64] * 64 + j % 64
+    flat = cache.view(-1, 576)
+    flat[place] = (flat[place].float() * (1 + growth * j[:, None] / 128)).bfloat16()
+    rows = [f64(flat[place])]
+    out, lse = attend(q, cache, table, ints(lens), SCALE, out_fp32=True)
+    assert_chunk(out, lse, q, rows, [0, 5])
 
 
 def test_equal_runs_are_the_decode_step():

@@ -94,6 +94,34 @@ def test_heads_that_attended_to_nothing_and_wider_sums():
     assert_weights(out, torch.zeros_like(out), 1.0, q, lse, rows, starts)
 
 
+def test_weights_over_fp8_rows_of_every_scale():
+    """Scales from 2^-27 to 2^33, NaN codes and scales among rows that are seen: only theirs are no numbers."""
+    lens = [300]
+    cache, table, _ = paged(lens, True, 33)
+    g = torch.Generator(device="cuda").manual_seed(34)
+    scale = torch.randint(100, 161, (4,), generator=g, device="cuda")
+    scale[0], scale[1] = 100, 160
+    cache[..., 512:516] = scale.to(torch.uint8)
+    flat = cache.view(-1, 656)
+    j = torch.arange(300, device="cuda")
+    place = table[0].long()[j // 64] * 64 + j % 64
+    flat[place[7], 100] = 0x7f
+    flat[place[200], 511] = 0xff
+    flat[place[290], 513] = 255
+    rows = [oracle.fp8_rows_to_f64(flat[place].cpu().numpy())]
+    # queries that undo the scales, so that all four groups count
+    q = rand((3, 128, 576), 35).float()
+    q[..., :512] *= torch.exp2(121.0 - scale).repeat_interleave(128)
+    q = q.bfloat16()
+    seen = [np.nan_to_num(rows[0], nan=0.0)]
+    lse = torch.tensor(oracle.chunk_attend(f64(q), seen, [0, 3], SCALE)[1], device="cuda").float()
+    got = m.attention_weights(q, lse, cache, table, ints(lens), SCALE)
+    bad = np.isnan(rows[0]).any(1)
+    assert bad.sum() == 3 and np.array_equal(np.isnan(f64(got)[0, :300]), bad)
+    ref, bound = oracle.attention_weights(f64(q), f64(lse), seen, [0, 3], SCALE)
+    assert (np.abs(f64(got)[0, :300] - ref[0])[~bad] <= bound[0][~bad]).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_hidden_rows_reach_no_weight(fp8):
     lens, starts = [70, 200], [0, 5, 12]
@@ -319,7 +347,7 @@ def test_rows_without_a_place_are_skipped_and_reported():
 def test_refusals():
     cache, table, _ = paged([130, 70], False, 29)
     q, lens, lse = rand((4, 128, 576), 30), ints([130, 70]), torch.zeros((4, 128), device="cuda")
-    w = torch.zeros((2, 192), device="cuda")
+    w, w3 = torch.zeros((2, 192), device="cuda"), torch.zeros((3, 192), device="cuda")
     for kw in (dict(out=w[:, :100]), dict(max_len=193), dict(out=w.double()), dict(token_starts=ints([0, 4]))):
         with pytest.raises(ValueError):
             m.attention_weights(q, lse, cache, table, lens, SCALE, w[:, :100] if "out" not in kw and "max_len" in kw else w,
@@ -331,6 +359,8 @@ def test_refusals():
     for kw in (dict(keep=0), dict(keep=5, sinks=3, recent=3), dict(keep=5, sinks=-1), dict(keep=5, recent=-1)):
         with pytest.raises(ValueError):
             m.evict_select(w, lens, **kw)
+    with pytest.raises(m.MlaError):  # over the weights, a row further on
+        m.attention_weights(q, lse, cache, table, lens, SCALE, w3[:2], out=w3[1:])
     with pytest.raises(m.MlaError):  # into the weights themselves
         m.evict_select(w, lens, 8, out=(torch.empty((2, 8), dtype=torch.int32, device="cuda"), ints([0, 0]), w))
     kept = torch.zeros((2, 8), dtype=torch.int32, device="cuda")

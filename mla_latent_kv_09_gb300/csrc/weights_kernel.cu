@@ -303,6 +303,8 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_pair();
   }
+  grid_launch_dependents();  // (the join waits for this grid)
+  grid_dependency_wait();
   find_begin<kFp8 ? kThreadsFp8 : kThreads>(p, unit, begin);
   tc_fence_before();
   __syncthreads();
@@ -615,6 +617,7 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
 // Adds the parts of tiles that several units share, in the line's order: block u
 // does so for the tile in whose tokens unit u begins, if no unit before it does.
 __global__ void __launch_bounds__(kTileRows) mla_attention_weights_join_kernel(const __grid_constant__ WeightsParams p) {
+  grid_dependency_wait();
   const int u = blockIdx.x;
   const int4 mine = p.begins[u];
   if (mine.x < 0 || mine.z == 0) return;
@@ -761,15 +764,13 @@ int mla_attention_weights(const void* q, const float* lse, const void* kv_cache,
   if (fp8 ? !encode_codes(&tm_k, kv_cache, rows) || !encode_position(&tm_pe, kv_cache, rows)
           : !encode_rows(&tm_k, kv_cache, rows))
     return MLA_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (fp8)
-    mla_attention_weights_kernel<true><<<2 * kUnits, kThreadsFp8, kSmem, s>>>(p, tm_q, tm_k, tm_pe);
-  else
-    mla_attention_weights_kernel<false><<<2 * kUnits, kThreads, kSmem, s>>>(p, tm_q, tm_k, tm_pe);
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  rc = fp8 ? launch_dependent(mla_attention_weights_kernel<true>, dim3(2 * kUnits), dim3(kThreadsFp8), kSmem, 1, stream, p,
+                              tm_q, tm_k, tm_pe)
+           : launch_dependent(mla_attention_weights_kernel<false>, dim3(2 * kUnits), dim3(kThreads), kSmem, 1, stream, p,
+                              tm_q, tm_k, tm_pe);
+  if (rc != MLA_OK) return rc;
   if (!token_starts && num_tokens == num_requests) return MLA_OK;  // one step a tile: no tile is shared
-  mla_attention_weights_join_kernel<<<kUnits, kTileRows, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return launch_dependent(mla_attention_weights_join_kernel, dim3(kUnits), dim3(kTileRows), 0, 1, stream, p);
 }
 
 }  // extern "C"

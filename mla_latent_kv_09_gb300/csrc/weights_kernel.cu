@@ -485,23 +485,33 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     float* s_half = reinterpret_cast<float*>(smem + kOffHalf);
     const uint32_t racc = mapa(bar(kAE), 0);
     Walk walk(p, begin);
-    Visit v;
+    Visit v, after;
     uint32_t step = 0;
-    for (uint32_t visit = 0; walk.next(v); ++visit) {
-      const int pos = v.tile * kTileRows + static_cast<int>(rank) * kRows + r;
-      float old = 0.f;
-      if (half == 0 && v.t0 == 0 && pos < v.len && p.decay != 0.f)
-        old = p.decay * p.weights[v.b * p.w_stride + pos];
+    // a visit's older weight and its first token's lse are asked for a visit ahead
+    float old = 0.f, next_old = 0.f;
+    float2 l2 = make_float2(0.f, 0.f), next_l2 = l2;
+    auto lse_of = [&](const Visit& s, int t) {
+      return reinterpret_cast<const float2*>(p.lse + static_cast<long long>(s.first + t) * kHeads + 64 * half) + lane;
+    };
+    auto row_of = [&](const Visit& s) { return s.tile * kTileRows + static_cast<int>(rank) * kRows + r; };
+    auto ask = [&](const Visit& s, float& o, float2& l) {
+      if (half == 0 && s.t0 == 0 && row_of(s) < s.len && p.decay != 0.f) o = p.weights[s.b * p.w_stride + row_of(s)];
+      if (s.pos < s.t1) l = __ldg(lse_of(s, s.pos));
+    };
+    bool more = walk.next(v);
+    if (more) ask(v, old, l2);
+    for (uint32_t visit = 0; more; ++visit) {
+      more = walk.next(after);
+      if (more) ask(after, next_old, next_l2);
+      const int pos = row_of(v);
       float sum = 0.f;
       bool ok = true;
-      const float2* lse = reinterpret_cast<const float2*>(p.lse + static_cast<long long>(v.first) * kHeads + 64 * half) + lane;
-      float2 l2 = v.pos < v.t1 ? __ldg(lse + static_cast<long long>(v.pos) * (kHeads / 2)) : make_float2(0.f, 0.f);
       for (int t = v.pos; t < v.t1; ++t, ++step) {
         const uint32_t buf = step & 1;
         // a head without a result (-inf) weighs nothing: 2^(s - inf)
         auto log2_of = [](float x) { return x == -INFINITY ? -INFINITY : -x * kLog2e; };
         *my_lse = make_float2(log2_of(l2.x), log2_of(l2.y));
-        if (t + 1 < v.t1) l2 = __ldg(lse + static_cast<long long>(t + 1) * (kHeads / 2));
+        if (t + 1 < v.t1) l2 = __ldg(lse_of(v, t + 1));
         __syncwarp();
         ok = warp_wait_uniform<true>(bar(kAF + buf), (step >> 1) & 1, ctl);
         if (!ok) break;
@@ -538,8 +548,11 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
         if (v.t0 != 0)
           p.parts[unit * kTileRows + static_cast<int>(rank) * kRows + r] = sum;
         else if (pos < v.len)
-          p.out[v.b * p.out_stride + pos] = old + sum;
+          p.out[v.b * p.out_stride + pos] = (p.decay != 0.f ? p.decay * old : 0.f) + sum;
       }
+      v = after;
+      old = next_old;
+      l2 = next_l2;
     }
   } else if (kFp8 && warp >= kFillWarp) {
     // ================================================= FP8 rows: codes widened in place

@@ -71,15 +71,6 @@
 namespace mla {
 namespace mtp {
 
-// Arrive on an mbarrier of the value pair's rank 2 with release at CTA scope:
-// the arriving warp's shared-memory stores are performed before the arrive
-// lands.  The tensor core of the pair reads them from this CTA's shared memory
-// only after rank 2 has seen the arrival.  (Release at cluster scope costs
-// each arriving warp about a thousand cycles under load.)
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t remote_bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
-}
-
 // Eight bf16, zero in the place of infinities and NaN.
 __device__ __forceinline__ uint4 numbers_only(uint4 v) {
   auto two = [](uint32_t w) {

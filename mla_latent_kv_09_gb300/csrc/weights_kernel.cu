@@ -17,7 +17,7 @@
 // chunks, each given back as soon as its last product is done, so that the next
 // one's load runs behind the other groups' products.
 //
-// A step's K is cut into two accumulators, chunks 0-4 and 5-8, that eight
+// A step's K is cut into two accumulators, chunks 0-4 and 5-8 (FP8 0-3 and 4-8), that eight
 // warps add in fp32 (four lane quarters, two halves of the heads).  A tensor core
 // truncates when it accumulates, so that a score comes out too small by about
 // half a step for each of its K / 16 additions, and the sum over heads and tokens
@@ -49,12 +49,15 @@ constexpr int kRows = 128;                    // of a CTA's half of a tile
 constexpr int kTileRows = 2 * kRows;
 constexpr int kKChunk = kRows * 128;          // 16 KiB: 128 rows x 64 dims
 constexpr int kQChunk = 64 * 128;             // 8 KiB: 64 heads x 64 dims
-constexpr int kFirst = 5;                     // chunks of the first accumulator
 // Chunks lie in groups that land and are given back together (a commit a chunk
-// made 32 x 16384 107 us instead of 55).
+// made 32 x 16384 107 us instead of 55).  An FP8 cache's codes come two chunks at
+// a time; bf16 rows with these groups: 64 x 2 x 8192 143 us against 131.
 constexpr int kGroups = 4;
-__host__ __device__ constexpr int group_begin(int g) { return g < 2 ? 3 * g : 2 * g + 1; }  // 0, 3, 5, 7, 9
-static_assert(group_begin(kGroups) == kNumChunks && group_begin(kGroups / 2) == kFirst, "groups end where the accumulators do");
+template <bool kFp8>
+__host__ __device__ constexpr int group_begin(int g) {  // 0, 3, 5, 7, 9; FP8 0, 2, 4, 6, 9
+  return kFp8 ? (g < 4 ? 2 * g : 9) : (g < 2 ? 3 * g : 2 * g + 1);
+}
+static_assert(group_begin<false>(kGroups) == kNumChunks && group_begin<true>(kGroups) == kNumChunks, "all chunks");
 constexpr int kUnits = 76;                    // SM pairs
 constexpr int kOffQ = kNumChunks * kKChunk;
 constexpr int kOffLse = kOffQ + kNumChunks * kQChunk;      // float[8 warps][64]
@@ -69,8 +72,7 @@ enum Bar {
   kAF = kQE + kGroups,        // [2] both accumulators of a step complete
   kAE = kAF + 2,              // [2] rank 0: ... and read by the sixteen warps of both CTAs
   kRaw = kAE + 2,             // [4] FP8 rows: a group's codes landed in this CTA
-  kWide = kRaw + kGroups,     // [4] rank 1, FP8 rows: widened (for the relay)
-  kDrain = kWide + kGroups,   // [2] per issuer
+  kDrain = kRaw + kGroups,    // [2] per issuer
   kNumBars = kDrain + 2
 };
 constexpr int kSlack = 1024;
@@ -114,12 +116,15 @@ __device__ __forceinline__ int len_of(const WeightsParams& p, int b) {
 
 // A unit's visits to tiles, in the line's order.
 struct Visit {
-  int b, tile, t0, t1;    // tokens [t0, t1) of the request
+  int b, tile, t0, t1;    // steps [t0, t1) of the tile
   int first, n, len;      // the request's first token, its tokens and rows
-  int pos;                // t0 or the first token that sees a row of the tile
+  // Those of its steps whose token sees a row of the tile: how many, the first
+  // one's token of the batch, and the way on.  Tokens take their turns over odd
+  // tiles backwards, so that a tile begins with the query that the last one ended with.
+  int steps, q0, way;
 };
-__device__ __forceinline__ int limit(const Visit& v, int t, int causal) {  // rows that token t sees
-  return causal ? max(0, v.len - v.n + t + 1) : v.len;
+__device__ __forceinline__ int limit(const Visit& v, int q, int causal) {  // rows that token q of the batch sees
+  return causal ? max(0, v.len - v.n + q - v.first + 1) : v.len;
 }
 struct Walk {
   const WeightsParams& p;
@@ -152,7 +157,11 @@ struct Walk {
     v.first = first;
     v.n = n;
     v.len = len;
-    v.pos = p.causal ? max(tok, tile * kTileRows - (len - n)) : tok;
+    const int blind = p.causal ? max(0, tile * kTileRows - (len - n)) : 0;  // tokens that see nothing of it
+    const int s0 = tile & 1 ? v.t0 : max(v.t0, blind);
+    v.steps = (tile & 1 ? min(v.t1, n - blind) : v.t1) - s0;
+    v.q0 = first + (tile & 1 ? n - 1 - s0 : s0);
+    v.way = tile & 1 ? -1 : 1;
     left -= v.t1 - tok;
     tok = v.t1;
     if (tok == n) {
@@ -164,7 +173,7 @@ struct Walk {
   // the next visit with a token that sees some of the tile
   __device__ bool next_live(Visit& v) {
     while (next(v))
-      if (v.pos < v.t1) return true;
+      if (v.steps > 0) return true;
     return false;
   }
 };
@@ -225,45 +234,50 @@ __device__ void find_begin(const WeightsParams& p, int unit, int* begin) {
   }
 }
 
-// The pool's page of place i of request b; pages outside the pool are reported and read as zeros.
-__device__ __forceinline__ int page_of(const WeightsParams& p, const Visit& v, int i) {
+// Place i of a visit's block table, asked for ahead, and the pool's page that it
+// names; pages outside the pool are reported and read as zeros.
+__device__ __forceinline__ int ask_page(const WeightsParams& p, const Visit& v, int i) {
+  return i * kPage < v.len ? __ldg(p.table + v.b * p.bt_stride + i) : 0;
+}
+__device__ __forceinline__ int page_of(const WeightsParams& p, const Visit& v, int i, int page) {
   if (i * kPage >= v.len) return -1;
-  const int page = __ldg(p.table + v.b * p.bt_stride + i);
   if (page >= 0 && page < p.num_pages) return page;
   atomicCAS(p.status, 0, static_cast<int>(kStBadTable));
   return -1;
 }
 
-// Two E4M3 codes in the upper bytes of a word's halves (the rest zero) as bf16
-// times 2^-120: sign, then exponent and mantissa four bits lower.
-__device__ __forceinline__ uint32_t place2(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
+// Two neighbouring E4M3 codes of a word as bf16 times 2^-120: a code beside its
+// sign's copies (prmt makes both), four bits higher, without the copies between
+// sign and exponent.
+template <int kHigh>
+__device__ __forceinline__ uint32_t place2(uint32_t codes) {
+  uint32_t w;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(w) : "r"(codes), "n"(kHigh ? 0xB3A2 : 0x9180));
+  return (w << 4) & 0x87f087f0u;
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 8 codes with the scale 2^(e - 127) as 8 bf16: exact (powers of two) while
-// they are in bf16's range.  NaN codes (S.1111.111) and scales of 2^8 and more
-// (whose 2^(e - 7) bf16 does not hold) are rare, and their way is not inlined:
-// the fill warps' loop has to stay in the instruction cache.
-__device__ __noinline__ uint4 widen8_rare(uint32_t a, uint32_t b, uint32_t e) {
+// 8 codes as bf16 times `factor` * 2^-120 (two copies of 2^(e - 7) for a scale of
+// 2^(e - 127)): exact (powers of two) while they are in bf16's range.
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t factor) {
+  return make_uint4(mul_bf16x2(place2<0>(a), factor), mul_bf16x2(place2<1>(a), factor), mul_bf16x2(place2<0>(b), factor),
+                    mul_bf16x2(place2<1>(b), factor));
+}
+// The same for any code and scale byte: NaN codes (S.1111.111), and scales of 2^8
+// and more, whose 2^(e - 7) bf16 does not hold.
+__device__ __noinline__ uint4 widen8_any(uint32_t a, uint32_t b, uint32_t e) {
   const uint32_t s = e == 255 ? 0x7fffu : e ? e << 7 : 0x0040u;
-  const uint32_t c[2] = {a, b};
+  const uint32_t w[4] = {place2<0>(a), place2<1>(a), place2<0>(b), place2<1>(b)};
   uint32_t o[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t w = __byte_perm(c[k >> 1], 0u, k & 1 ? 0x3424 : 0x1404);
-    const bool lo = (w & 0x7f00u) == 0x7f00u, hi = (w & 0x7f000000u) == 0x7f000000u;
-    o[k] = mul_bf16x2(mul_bf16x2(place2(w), 0x7b807b80u), s | s << 16) | (lo ? 0x7fffu : 0u) | (hi ? 0x7fff0000u : 0u);
+    const bool lo = (w[k] & 0x7f0u) == 0x7f0u, hi = (w[k] & 0x7f00000u) == 0x7f00000u;
+    o[k] = mul_bf16x2(mul_bf16x2(w[k], 0x7b807b80u), s | s << 16) | (lo ? 0x7fffu : 0u) | (hi ? 0x7fff0000u : 0u);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
-}
-__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t e) {
-  const uint32_t nan = (((a & 0x7f7f7f7fu) + 0x01010101u) | ((b & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
-  if (nan != 0 || e > 134) return widen8_rare(a, b, e);
-  const uint32_t f = (e + 120) << 7, f2 = f | f << 16;  // 2^(e - 7)
-  return make_uint4(mul_bf16x2(place2(__byte_perm(a, 0u, 0x1404)), f2), mul_bf16x2(place2(__byte_perm(a, 0u, 0x3424)), f2),
-                    mul_bf16x2(place2(__byte_perm(b, 0u, 0x1404)), f2), mul_bf16x2(place2(__byte_perm(b, 0u, 0x3424)), f2));
 }
 
 template <bool kFp8>
@@ -284,12 +298,11 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
 
   if (threadIdx.x == 0) {
     for (int g = 0; g < kGroups; ++g) {
-      mbar_init(bar(kKF + g), kFp8 ? 9 : 1);  // FP8: rank 0's fill warps and rank 1's relay
+      mbar_init(bar(kKF + g), kFp8 ? 16 : 1);  // FP8: both CTAs' fill warps
       mbar_init(bar(kKE + g), 1);
       mbar_init(bar(kQF + g), 1);
       mbar_init(bar(kQE + g), 1);
       mbar_init(bar(kRaw + g), 1);
-      mbar_init(bar(kWide + g), 8);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar(kAF + a), 2);  // both issuers
@@ -336,38 +349,42 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
   };
   if (warp == 0) {
     // ================================================= rows, by TMA
-    // FP8: a chunk's codes go to the second half of its slot (row r at 64 r), for
-    // this CTA's fill warps to widen in place; the position dims to theirs at once.
+    // FP8: the codes of a group's two chunks go to the second one's slot, for this
+    // CTA's fill warps to widen in place; the position dims to theirs at once.
     const uint32_t rk = mapa(bar(kKF), 0);
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       if (kFp8) tma_prefetch_desc(&tm_pe);
     }
     Walk walk(p, begin);
-    Visit v;
-    bool ok = true;
-    for (uint32_t nk = 0; ok && walk.next_live(v); ++nk) {
+    Visit v, after;
+    // (a lane a page, a visit ahead)
+    auto place = [&](const Visit& s) { return s.tile * 4 + static_cast<int>(rank) * 2 + (lane & 1); };
+    bool ok = true, more = walk.next_live(v);
+    int asked = more ? ask_page(p, v, place(v)) : 0;
+    for (uint32_t nk = 0; ok && more; ++nk) {
+      const int page = page_of(p, v, place(v), asked);
+      if ((more = walk.next_live(after))) asked = ask_page(p, after, place(after));
+      v = after;
       int y[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        int page = -1;
-        if (lane == 0) page = page_of(p, v, v.tile * 4 + static_cast<int>(rank) * 2 + e);
-        page = __shfl_sync(0xffffffffu, page, 0);
-        y[e] = (page >= 0 ? page : static_cast<int>(p.num_pages)) * kPage;
+        const int mine = __shfl_sync(0xffffffffu, page, e);
+        y[e] = (mine >= 0 ? mine : static_cast<int>(p.num_pages)) * kPage;
       }
-      for (int g = 0; g < kGroups; ++g) {
+      for (int i = 0; i < kGroups; ++i) {
+        const int g = (i & 1) << 1 | i >> 1;
         if (nk > 0 && !(ok = warp_wait_uniform<true>(bar(kKE + g), (nk - 1) & 1, ctl))) break;
         if (lane == 0) {
-          const int c0 = group_begin(g), c1 = group_begin(g + 1);
+          const int c0 = group_begin<kFp8>(g), c1 = group_begin<kFp8>(g + 1);
           if (kFp8) {
-            mbar_arrive_expect_tx_relaxed(bar(kRaw + g), (c1 - c0) * (kKChunk / 2) + (c1 == kNumChunks ? kKChunk / 2 : 0));
-            for (int c = c0; c < c1; ++c)
+            mbar_arrive_expect_tx_relaxed(bar(kRaw + g), (c1 - c0 - 1) * kKChunk);
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (c < 8)
-                  tma_load_2d(sbase + c * kKChunk + kKChunk / 2 + e * (kKChunk / 4), &tm_k, 64 * c, y[e], bar(kRaw + g));
-                else
-                  tma_load_2d(sbase + c * kKChunk + e * (kKChunk / 2), &tm_pe, kPeAt, y[e], bar(kRaw + g));
+            for (int e = 0; e < 2; ++e) {
+              tma_load_2d(sbase + (c0 + 1) * kKChunk + e * (kKChunk / 2), &tm_k, 64 * c0, y[e], bar(kRaw + g));
+              if (c1 == kNumChunks)
+                tma_load_2d(sbase + 8 * kKChunk + e * (kKChunk / 2), &tm_pe, kPeAt, y[e], bar(kRaw + g));
+            }
             continue;
           }
           if (rank == 0) mbar_arrive_expect_tx_relaxed(bar(kKF + g), (c1 - c0) * 2 * kKChunk);
@@ -390,13 +407,14 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     int last_q = -1;
     bool ok = true;
     while (ok && walk.next_live(v)) {
-      for (int t = v.pos; ok && t < v.t1; ++t) {
-        if (v.first + t == last_q) continue;
-        last_q = v.first + t;
-        for (int g = 0; g < kGroups; ++g) {
+      for (int i = v.steps, q = v.q0; ok && i > 0; --i, q += v.way) {
+        if (q == last_q) continue;
+        last_q = q;
+        for (int j = 0; j < kGroups; ++j) {
+          const int g = (j & 1) << 1 | j >> 1;
           if (nq > 0 && !(ok = warp_wait_uniform<true>(bar(kQE + g), (nq - 1) & 1, ctl))) break;
           if (lane == 0) {
-            const int c0 = group_begin(g), c1 = group_begin(g + 1);
+            const int c0 = group_begin<kFp8>(g), c1 = group_begin<kFp8>(g + 1);
             if (rank == 0) mbar_arrive_expect_tx_relaxed(bar(kQF + g), (c1 - c0) * 2 * kQChunk);
             for (int c = c0; c < c1; ++c)
               tma_load_2d_pair(sbase + kOffQ + c * kQChunk, &tm_q, 64 * c, last_q * kHeads + static_cast<int>(rank) * 64,
@@ -421,13 +439,15 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     auto issue = [&](auto first, auto end) {  // groups [first, end) of every step
       while (ok && more) {
         more = walk.next_live(after);
-        for (int t = v.pos; ok && t < v.t1; ++t, ++step) {
-          const bool new_k = t == v.pos, new_q = v.first + t != last_q, last = t == v.t1 - 1;
-          const bool q_goes = !last || (more && after.first + after.pos != v.first + t);
+        const int steps = uniform(v.steps), way = uniform(v.way), then = uniform(more ? after.q0 : -1);
+        int q = uniform(v.q0);
+        for (int i = steps; ok && i > 0; --i, q += way, ++step) {
+          const bool new_k = i == steps, new_q = q != last_q, last = i == 1;
+          const bool q_goes = !last || (then >= 0 && then != q);
           const uint32_t buf = step & 1, d = tmem + 256u * buf + kHeads * which;
           if (step >= 2) ok = warp_wait_uniform<true>(bar(kAE + buf), ((step >> 1) - 1) & 1, ctl);
           if (new_q) ++nq;
-          last_q = v.first + t;
+          last_q = q;
 #pragma unroll
           for (int g = first; g < end; ++g) {
             if (new_k) ok = ok && warp_wait_uniform<true>(bar(kKF + g), nk & 1, ctl);
@@ -435,12 +455,12 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int c = group_begin(g); c < group_begin(g + 1); ++c)
+            for (int c = group_begin<kFp8>(g); c < group_begin<kFp8>(g + 1); ++c)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma_pair_ss_if(leader, d, kd + static_cast<uint64_t>((c * kKChunk + 32 * kk) >> 4),
                                 qd + static_cast<uint64_t>((c * kQChunk + 32 * kk) >> 4), kIdesc,
-                                (c != 0 && c != kFirst) || kk > 0 ? 1u : 0u);
+                                (c != 0 && c != group_begin<kFp8>(kGroups / 2)) || kk > 0 ? 1u : 0u);
             if (last) umma_commit_pair_if(leader, bar(kKE + g), 3);
             if (q_goes) umma_commit_pair_if(leader, bar(kQE + g), 3);
           }
@@ -458,22 +478,6 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     umma_commit_pair_if(leader, bar(kDrain + which), 1);  // arrives once every MMA issued above has completed
     drain_bar(bar(kDrain + which), 0u);
     __syncwarp();
-  } else if (warp == 1 || warp == 3) {
-    // Rank 1 has nothing to issue.  With an FP8 cache these threads relay its fill
-    // warps' arrivals to rank 0, whose MMAs read this CTA's rows too: the warps
-    // release to their own CTA, a thread without stores of its own to the cluster
-    // (a release to the cluster by each of them waits for its earlier stores).
-    if (kFp8 && lane == 0) {
-      const uint32_t rk = mapa(bar(kKF), 0);
-      const int first = warp == 1 ? 0 : kGroups / 2, end = warp == 1 ? kGroups / 2 : kGroups;
-      Walk walk(p, begin);
-      Visit v;
-      bool ok = true;
-      for (uint32_t nk = 0; ok && walk.next_live(v); ++nk)
-        for (int g = first; ok && g < end; ++g)
-          if ((ok = wait(bar(kWide + g), nk & 1, ctl))) mbar_arrive_remote(rk + 8u * g);
-    }
-    __syncwarp();
   } else if (warp >= kEpiWarp && warp < kEpiWarp + 8) {
     // ================================================= sums over heads and tokens
     // Warp (quarter, half): rows 32 quarter .. of the CTA's 128, one a lane, heads 64 half .. +63.
@@ -490,13 +494,13 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     // a visit's older weight and its first token's lse are asked for a visit ahead
     float old = 0.f, next_old = 0.f;
     float2 l2 = make_float2(0.f, 0.f), next_l2 = l2;
-    auto lse_of = [&](const Visit& s, int t) {
-      return reinterpret_cast<const float2*>(p.lse + static_cast<long long>(s.first + t) * kHeads + 64 * half) + lane;
+    auto lse_of = [&](int q) {
+      return reinterpret_cast<const float2*>(p.lse + static_cast<long long>(q) * kHeads + 64 * half) + lane;
     };
     auto row_of = [&](const Visit& s) { return s.tile * kTileRows + static_cast<int>(rank) * kRows + r; };
     auto ask = [&](const Visit& s, float& o, float2& l) {
       if (half == 0 && s.t0 == 0 && row_of(s) < s.len && p.decay != 0.f) o = p.weights[s.b * p.w_stride + row_of(s)];
-      if (s.pos < s.t1) l = __ldg(lse_of(s, s.pos));
+      if (s.steps > 0) l = __ldg(lse_of(s.q0));
     };
     bool more = walk.next(v);
     if (more) ask(v, old, l2);
@@ -506,31 +510,37 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
       const int pos = row_of(v);
       float sum = 0.f;
       bool ok = true;
-      for (int t = v.pos; t < v.t1; ++t, ++step) {
+      for (int i = v.steps, q = v.q0; i > 0; --i, q += v.way, ++step) {
         const uint32_t buf = step & 1;
         // a head without a result (-inf) weighs nothing: 2^(s - inf)
         auto log2_of = [](float x) { return x == -INFINITY ? -INFINITY : -x * kLog2e; };
         *my_lse = make_float2(log2_of(l2.x), log2_of(l2.y));
-        if (t + 1 < v.t1) l2 = __ldg(lse_of(v, t + 1));
+        if (i > 1) l2 = __ldg(lse_of(q + v.way));
         __syncwarp();
         ok = warp_wait_uniform<true>(bar(kAF + buf), (step >> 1) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
         float e[4] = {0.f, 0.f, 0.f, 0.f};
+        constexpr int kCols = kFp8 ? 16 : 32;  // (registers: 20 warps have 96 a thread)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[2][32];
-          tmem_ld32(tl + 256u * buf + 32u * h, x[0]);
-          tmem_ld32(tl + 256u * buf + kHeads + 32u * h, x[1]);
+        for (int h = 0; h < 64 / kCols; ++h) {
+          uint32_t x[2][kCols];
+          for (int a = 0; a < 2; ++a) {
+            const uint32_t at = tl + 256u * buf + kHeads * a + kCols * h;
+            if constexpr (kFp8)
+              tmem_ld16(at, x[a]);
+            else
+              tmem_ld32(at, x[a]);
+          }
           tmem_wait_ld();
-          if (h == 1) {
+          if (h == 64 / kCols - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_relaxed(racc + 8u * buf);
           }
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 l = ld_shared_v4f(s_lse + 128u * h + 4u * c);
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 l = ld_shared_v4f(s_lse + 4u * (kCols * h + c));
             const float bias[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -538,7 +548,7 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
           }
         }
         __syncwarp();  // the warp's lse has been read
-        if (pos < limit(v, t, p.causal)) sum += (e[0] + e[1]) + (e[2] + e[3]);  // hidden rows may hold anything
+        if (pos < limit(v, q, p.causal)) sum += (e[0] + e[1]) + (e[2] + e[3]);  // hidden rows may hold anything
       }
       // the two halves of the heads meet; the buffer of the visit before the last is free again
       if (half == 1) s_half[(visit & 1) * kRows + r] = sum;
@@ -556,61 +566,82 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     }
   } else if (kFp8 && warp >= kFillWarp) {
     // ================================================= FP8 rows: codes widened in place
-    // Warp w has rows 16 w .. +15 (all of one page): four lanes a row, eight rows
-    // side by side, a 16-byte unit of a chunk's codes of two rows a lane.  A
-    // group's codes are in the eight warps' registers before the first of them
-    // writes over codes.  (Rows read from global memory by these warps, three
-    // turns of loads in flight: 64 x 8192 245 us, bound by their latency; the TMA
-    // holds a whole tile in flight.)
+    // Warp w has rows 16 w .. +15 (all of one page).  A row's codes of two chunks
+    // lie in the 128 bytes that its second chunk's dims take, so that a warp that
+    // holds its rows' codes waits for no other before it writes.  Four lanes a row
+    // take 16 bytes each: odd rows the other chunk's first, so that eight lanes
+    // meet all banks, reading and writing.  (Boxes of one chunk's codes, 64 bytes a
+    // row: 33 x 2 x 2560 42.7 us, 64 x 1 x 8192 128; rows read from global memory
+    // by these warps, three turns of loads in flight: 64 x 2 x 8192 245, bound by
+    // their latency, where the TMA holds a whole tile in flight.)
     const int w = warp - kFillWarp;
+    const uint32_t filled = mapa(bar(kKF), 0);
     Walk walk(p, begin);
     Visit v;
     uint32_t nk = 0;
-    bool ok = true, more = walk.next_live(v);
     const int row0 = lane >> 2, unit16 = lane & 3;
+    auto place = [&](const Visit& s) { return s.tile * 4 + static_cast<int>(rank) * 2 + (w >> 2); };
     // the scale bytes of the lane's two rows of a visit
-    auto scales_of = [&](const Visit& s) {
-      const int page = page_of(p, s, s.tile * 4 + static_cast<int>(rank) * 2 + (w >> 2));
+    auto scales_of = [&](const Visit& s, int asked) {
+      const int page = page_of(p, s, place(s), asked);
       if (page < 0) return make_uint2(0u, 0u);
       const uint8_t* row = p.kv + (static_cast<long long>(page) * kPage + 16 * (w & 3) + row0) * MLA_FP8_ROW_BYTES + 512;
       return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row)),
                         __ldg(reinterpret_cast<const uint32_t*>(row + 8 * MLA_FP8_ROW_BYTES)));
     };
-    const uint32_t to = sbase + (16 * w + row0) * 128, sw = row0;  // (row & 7, for both of the rows)
+    // scales are asked for a visit ahead, pages two
+    bool ok = true, more = walk.next_live(v);
+    uint2 scales = more ? scales_of(v, ask_page(p, v, place(v))) : make_uint2(0u, 0u);
+    bool next = more && walk.next_live(v);
+    int asked = next ? ask_page(p, v, place(v)) : 0;
+    const uint32_t rows = sbase + (16 * w + row0) * 128, sw = row0;  // (row & 7, for both of the rows)
     const uint32_t at0 = ((2u * unit16) ^ sw) << 4, at1 = ((2u * unit16 + 1u) ^ sw) << 4;
-    const uint32_t from = sbase + kKChunk / 2 + (16 * w + row0) * 64 + 16 * unit16;
-    uint2 scales = more ? scales_of(v) : make_uint2(0u, 0u);
     while (ok && more) {
-      more = walk.next_live(v);
-      const uint2 next_scales = more ? scales_of(v) : make_uint2(0u, 0u);
+      const uint2 next_scales = next ? scales_of(v, asked) : make_uint2(0u, 0u);
+      more = next;
+      if (next && (next = walk.next_live(v))) asked = ask_page(p, v, place(v));
+      // no byte above 134
+      const bool small = __vcmpgtu4(scales.x, 0x86868686u) == 0 && __vcmpgtu4(scales.y, 0x86868686u) == 0;
 #pragma unroll 1
-      for (int g = 0; g < kGroups; ++g) {
-        const int c0 = group_begin(g), c1 = min(group_begin(g + 1), 8);
-        ok = warp_wait_uniform(bar(kRaw + g), nk & 1, ctl);
-        uint4 a[3], b[3];
+      for (int i = 0; i < kGroups; ++i) {
+        const int g = (i & 1) << 1 | i >> 1;
+        if (!(ok = warp_wait_uniform(bar(kRaw + g), nk & 1, ctl))) break;
+        const uint32_t pair = rows + 2 * g * kKChunk;
+        uint4 x[2][2];
+        uint32_t nan = 0;
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (ok && c0 + i < c1) {
-            a[i] = ld_shared_v4u(from + (c0 + i) * kKChunk);
-            b[i] = ld_shared_v4u(from + (c0 + i) * kKChunk + 512u);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint4 v4 = x[t][r] = ld_shared_v4u(pair + kKChunk + 1024u * r + 64u * (t ^ (row0 & 1)) + 16u * unit16);
+            nan |= ((v4.x & 0x7f7f7f7fu) + 0x01010101u) | ((v4.y & 0x7f7f7f7fu) + 0x01010101u) |
+                   ((v4.z & 0x7f7f7f7fu) + 0x01010101u) | ((v4.w & 0x7f7f7f7fu) + 0x01010101u);
           }
-        if (!(ok = named_bar_all(5, 256, ok))) break;
+        __syncwarp();  // the warp holds its codes, and writes over them
+        // (one question for a whole group: asked for every 8 codes, it took as long as they)
+        const bool plain = (nan & 0x80808080u) == 0 && small;
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (c0 + i < c1) {
-            const int c = c0 + i;
-            const uint32_t dst = to + c * kKChunk;
-            const uint32_t e0 = (scales.x >> (8 * (c >> 1))) & 255u, e1 = (scales.y >> (8 * (c >> 1))) & 255u;
-            const uint4 o0 = widen8(a[i].x, a[i].y, e0), o1 = widen8(a[i].z, a[i].w, e0);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t dst = pair + kKChunk * (t ^ (row0 & 1)) + 1024u * r;
+            const uint32_t e = ((r ? scales.y : scales.x) >> (8 * g)) & 255u;
+            const uint4 v4 = x[t][r];
+            uint4 o0, o1;
+            if (plain) {
+              const uint32_t f = (e + 120) << 7, factor = f | f << 16;
+              o0 = widen8(v4.x, v4.y, factor);
+              o1 = widen8(v4.z, v4.w, factor);
+            } else {
+              o0 = widen8_any(v4.x, v4.y, e);
+              o1 = widen8_any(v4.z, v4.w, e);
+            }
             st_shared_v4(dst + at0, o0.x, o0.y, o0.z, o0.w);
             st_shared_v4(dst + at1, o1.x, o1.y, o1.z, o1.w);
-            const uint4 o2 = widen8(b[i].x, b[i].y, e1), o3 = widen8(b[i].z, b[i].w, e1);
-            st_shared_v4(dst + 1024u + at0, o2.x, o2.y, o2.z, o2.w);
-            st_shared_v4(dst + 1024u + at1, o3.x, o3.y, o3.z, o3.w);
           }
         fence_proxy_async_smem();  // generic writes, read next by the tensor core
         __syncwarp();
-        if (lane == 0) mbar_arrive(rank == 0 ? bar(kKF + g) : bar(kWide + g));
+        if (lane == 0) mbar_arrive_remote_cta(filled + 8u * g);
       }
       scales = next_scales;
       ++nk;
@@ -677,11 +708,11 @@ int weights_device_ready() {
   return state[dev];
 }
 
-// The codes of an FP8 cache's rows as boxes of 64 x 64 rows, as they are.
+// The codes of an FP8 cache's rows as boxes of two chunks x 64 rows, as they are.
 bool encode_codes(CUtensorMap* m, const void* base, uint64_t rows) {
   EncodeTiledFn fn = encode_tiled();
   const cuuint64_t size[2] = {512, rows}, strides[1] = {MLA_FP8_ROW_BYTES};
-  const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {128, 64}, one[2] = {1, 1};
   return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), size, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

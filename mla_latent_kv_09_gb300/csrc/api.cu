@@ -421,12 +421,9 @@ int mla_decode(const void* q, const void* kv_cache, int64_t num_pages, const int
   p.part_o = reinterpret_cast<uint16_t*>(ws + L.part_o);
   p.part_bf16 = (flags & MLA_FLAG_BF16_PV) ? 1 : 0;
 
-  // the two-token kernel moves Q through its 8 KiB chunk slots: 64-row boxes
   const bool fp8 = (flags & MLA_FLAG_KV_FP8) != 0;
   CUtensorMap tm_q, tm_kv, tm_rope;
-  if ((rc = encode_2d(&tm_q, q, static_cast<uint64_t>(batch) * s_q * kHeads, pair_path ? kPage : kHeads)) !=
-      MLA_OK)
-    return rc;
+  if ((rc = encode_2d(&tm_q, q, static_cast<uint64_t>(batch) * s_q * kHeads, kHeads)) != MLA_OK) return rc;
   if (fp8) {
     if ((rc = encode_fp8_kv(&tm_kv, &tm_rope, kv_cache, static_cast<uint64_t>(num_pages) * kPage)) != MLA_OK)
       return rc;
@@ -566,7 +563,7 @@ int mla_chunk_attend(const void* q, const void* kv_cache, int64_t num_pages, con
 
   CUtensorMap tm_q, tm_k3, tm_v2, tm_out, tm_part;
   const uint64_t rows = static_cast<uint64_t>(pages) * kPage, q_rows = static_cast<uint64_t>(num_tokens) * kHeads;
-  if ((rc = encode_2d(&tm_q, q, q_rows, kPage)) != MLA_OK) return rc;
+  if ((rc = encode_2d(&tm_q, q, q_rows, kHeads)) != MLA_OK) return rc;
   if ((rc = encode_kv_3d(&tm_k3, kv, rows, 3)) != MLA_OK) return rc;
   if ((rc = encode_kv_3d(&tm_v2, kv, rows, 2)) != MLA_OK) return rc;
   if ((rc = encode_out_2d(&tm_out, out, q_rows, p.out_fp32 != 0)) != MLA_OK) return rc;

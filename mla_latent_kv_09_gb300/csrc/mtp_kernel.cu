@@ -29,7 +29,17 @@
 //     (the B columns it holds in the pair) through a ring of page slots, and
 //     rank 2 issues O += P V (M = 256, N = 2 x 256, K = 128).  At the end of
 //     a segment all sixteen warps write O (scaled by 1 / z) with tensor
-//     stores, staged in the P slot the last tile used.
+//     stores, staged in the P slot the last tile used.  The next segment's
+//     value products start once every warp has read its share of O.
+//
+// Between two segments the value products pause for some 4.5 us: Q (288 KiB a
+// pair) takes the ring's place of the last tile's rows, and O leaves tensor
+// memory.  What is there already when they may go on: Q in L2 (asked for a
+// segment ahead), the first chunks of the first tile behind Q in the ring, the
+// first tile's value pages in their slots.  (Value pages loaded after the
+// epilogue, Q a load a slot, O handed over by one thread of each rank after all
+// stores: 13 requests of 47 tokens x 2048 rows 343 us instead of 321, 612 tokens
+// x 4096 495 / 480; decode of 64 x 2 tokens with up to 8192 rows 132.5 / 130.)
 // P and V are fp16 by default (11 significant bits on the softmax weights;
 // values must stay below 65504 in magnitude): the value ranks' conversion
 // warps read each page's value dims from global memory (an L2 hit behind the
@@ -87,8 +97,6 @@ constexpr int kKGroup = 3;                        // chunk slots per landing / f
 constexpr int kKGroups = kKSlots / kKGroup;
 constexpr int kVPage = 4 * kPageChunk;            // 32 KiB: one page, this rank's 256 value dims
 constexpr int kVSlots = 4;                        // value ranks: page slots (two tiles)
-constexpr int kVDepth = 1;                        // fp16 variant: pages of value loads in flight per thread
-                                                  // beyond the one being stored (2 measured no faster)
 // P tile, 128 heads x 128 keys of 16-bit weights, as a K-major 128B-swizzled
 // operand whose 8-row groups hold both 64-key halves side by side: byte
 // (row / 8) * 2048 + half * 1024 + (row % 8) * 128 + swizzled 16-B piece.  A
@@ -162,15 +170,16 @@ enum Bar {
   kPR = 58,       // [2] rank 2: O rescaled and P landed in both value ranks
   kPD = 60,       // [2] value ranks: PV of a tile of that parity finished (commit from rank 2)
   kOF = 62,       // value ranks: a segment's last PV finished (commit from rank 2)
-  kOE = 63,       // rank 2: both value ranks' epilogues read O
+  kOE = 63,       // rank 2: both value ranks' epilogues read O (one arrival per warp)
   kMmaDone = 64,  // teardown
   kPsFull = 65,   // score ranks: the local P copy is written (one arrival per softmax warp)
   kPsFree = 66,   // score ranks: the bulk copy has read the local P copy
   kMmaDone2 = 67, // teardown (second issuer)
   kHand = 68,     // [2] rank 0: score-MMA issue token (tile parity): the issuer of tile g may start
                   //     once the issuer of tile g - 1 has issued two thirds of its MMAs
-  kEpiD = 70,     // value ranks: the conversion warps' share of a segment epilogue is written
-  kNumBars = 71
+  kEpiD = 70,     // [2] value ranks: the rescale warps' shares of a segment's epilogue are written (by the
+                  //     segment's parity: these warps may be at the next one's before the others ask)
+  kNumBars = 72
 };
 static_assert(kNumBars * 8 + 16 <= kBarBytes, "barrier block");
 static_assert(kKGroups <= kKE - kKF && kKGroups <= kQRF - kKE, "slot-group barriers");
@@ -296,11 +305,11 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     }
     mbar_init(bar(kQF), 2);
     mbar_init(bar(kOF), 1);
-    mbar_init(bar(kOE), 2);
+    mbar_init(bar(kOE), 32);
     mbar_init(bar(kMmaDone), 1);
     mbar_init(bar(kPsFull), kSoftmaxWarps);
     mbar_init(bar(kPsFree), 1);
-    mbar_init(bar(kEpiD), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(kEpiD + i), 4);
     misc[1] = 0u;
     fence_mbar_init();
   }
@@ -380,7 +389,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
         tc_fence_after();
       }
       u = u_t;
-      if (!(ok = wait_bar<true>(bar(kQRF), nseg & 1u, ctl))) break;
+      bool rope_here = false;  // (Q's RoPE part lands while the segment's first products run)
       const uint64_t qr0 = smem_desc(sbase + kOffQr, 16u, 1024u);
       for (int j = sg.t0; j < sg.t1 && ok; ++j, ++g, u += kNumChunks) {
         const uint32_t sb = g & 1u, ph = (g >> 1) & 1u;
@@ -401,6 +410,11 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           const uint32_t uc = u + c;
           const uint32_t G = uc / kKGroup;
           if (c == 6) mbar_arrive_relaxed(bar(kHand + sb));  // the other issuer may start its tile
+          if (c == 8 && !rope_here) {
+            if (!(ok = wait_bar<true>(bar(kQRF), nseg & 1u, ctl))) break;
+            tc_fence_after();
+            rope_here = true;
+          }
           if (c > 0 && c % kKGroup == 0) {  // the next slot group (the first was waited for above)
             if (!next_ready && !(ok = wait_bar<true>(kf0 + 8u * (G % kKGroups), (G / kKGroups) & 1u, ctl))) break;
             tc_fence_after();
@@ -443,13 +457,22 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
   // finished with it, and the score rank refills it only after the epilogue)
   // and written by tensor stores, so both the shared-memory writes and the
   // global writes are full-width.
+  const uint32_t rOE = mapa(bar(kOE), 2);
   auto epilogue_share = [&](int w, float fin, const Seg& sg, uint32_t pb) {
     const bool to_part = sg.slot >= 0;
-    if (to_part && sg.slot >= 2 * U) return;  // the plan never uses more than 2 * (U - 1) slots
+    auto o_read = [&]() {  // (tcgen05.wait::ld has completed this warp's loads)
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(rOE);
+    };
     const bool f32 = !to_part && p.out_fp32;  // partials are 16-bit (fp16, or bf16 with kBf16PV)
     const CUtensorMap* tm = to_part ? &tm_part : &tm_out;
     const TokenPair pair = token_pair<kPairs>(p, sg.b);
-    if (kPairs && !to_part && static_cast<int>(tok) >= pair.count) return;
+    // (the plan never uses more than 2 * (U - 1) slots)
+    if (to_part ? sg.slot >= 2 * U : kPairs && static_cast<int>(tok) >= pair.count) {
+      o_read();
+      return;
+    }
     const long long orow = to_part ? static_cast<long long>(sg.slot) * 2 + tok : static_cast<long long>(pair.first) + tok;
     const int y = static_cast<int>(orow * kHeads) + 32 * (w & 3);
     const int x0 = 128 * (w >> 2);
@@ -467,12 +490,14 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
         uint32_t r[16];
         tmem_ld16(taddr + static_cast<uint32_t>(16 * i), r);
         tmem_wait_ld();
+        if (i == nbox - 1) o_read();
 #pragma unroll
         for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(r[c]) * fin);
       } else {
         uint32_t r[32];
         tmem_ld32(taddr + static_cast<uint32_t>(32 * i), r);
         tmem_wait_ld();
+        if (i == nbox - 1) o_read();
         if (to_part && !kBf16PV) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -500,6 +525,15 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     }
     if (lane == 0) bulk_wait_read();
     __syncwarp();
+  };
+
+  // The twelve warps' shares are done: with the other four's, P slot `pb` is free
+  // for the score rank that ships this rank's P (the stores have read what it
+  // overwrites).
+  auto free_staging = [&](uint32_t pb, uint32_t nseg) {
+    if (!warp_wait(bar(kEpiD + (nseg & 1u)), (nseg >> 1) & 1u, ctl)) return false;
+    if (lane == 0) mbar_arrive_remote_cta(mapa(bar(kPFree), tok) + 8u * pb);
+    return true;
   };
 
   if (halt) {
@@ -685,8 +719,6 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     const volatile float* alpha_s = reinterpret_cast<const volatile float*>(smem + kOffAlpha);
     const volatile float* fin_s = reinterpret_cast<const volatile float*>(smem + kOffFin);
     const uint32_t rPR = mapa(bar(kPR), 2);
-    const uint32_t rOE = mapa(bar(kOE), 2);
-    const uint32_t rPFree = mapa(bar(kPFree), tok);  // the score rank that ships this rank's P
     SegIter it(p, unit);
     Seg sg;
     uint32_t g = 0, nseg = 0;
@@ -742,16 +774,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           }
           tc_fence_after();
           epilogue_share(warp, fin, sg, pb);
-          ok = warp_wait(bar(kEpiD), nseg & 1u, ctl);  // the other twelve warps' shares
-          tc_fence_before();
-          if (!named_bar_all(5, 128, ok)) {
-            stop = true;
-            break;
-          }
-          if (row == 0) {
-            mbar_arrive_remote_relaxed(rOE);       // O read (tcgen05.wait::ld completed in all 16 warps)
-            mbar_arrive_remote(rPFree + 8u * pb);  // the staging (this P slot) is free again
-          }
+          if (lane == 0) mbar_arrive(bar(kEpiD + (nseg & 1u)));
         }
       }
       ++nseg;
@@ -821,45 +844,43 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
       const uint32_t rKF = mapa(bar(kKF), 0);
       const uint32_t rQRF = mapa(bar(kQRF), 0);
       uint32_t u = 0, nseg = 0;
-      // claim the next slot: wait for its group to be free at the group's
-      // first use, add its bytes (both ranks) to the group's landing barrier,
-      // and arrive once at the group's last use.  Relaxed forms: the
-      // producer writes none of the data, and release semantics make each
-      // barrier operation wait for the thread's earlier memory operations.
-      auto claim = [&](uint32_t bytes) -> bool {
-        const uint32_t sl = u % kKSlots, grp = sl / kKGroup;
-        if (sl % kKGroup == 0 && !warp_wait(bar(kKE + grp), ((u / kKSlots) & 1u) ^ 1u, ctl)) return false;
-        if (lane == 0 && tok == 0) {
-          if (sl % kKGroup == kKGroup - 1) mbar_arrive_expect_tx_relaxed(bar(kKF + grp), 2u * bytes);
-          else if (bytes) mbar_expect_tx_relaxed(bar(kKF + grp), 2u * bytes);
-        }
-        return true;
+      SegIter ahead(p, unit);  // one segment further
+      Seg then;
+      ahead.next(then);
+      // The next use's slot group: free (asked at the group's first use) and, with the
+      // group's last use, armed.  Relaxed forms: the producer writes none of the
+      // data, and release semantics make each barrier operation wait for the
+      // thread's earlier memory operations.
+      auto group = [&](uint32_t use) { return (use % kKSlots) / kKGroup; };
+      auto claim = [&](uint32_t use) {
+        return use % kKGroup != 0 || warp_wait(bar(kKE + group(use)), ((use / kKSlots) & 1u) ^ 1u, ctl);
       };
       while (ok && it.next(sg)) {
         const int L = max(p.cache_lens[sg.b], 0);
         const TokenPair pair = token_pair<kPairs>(p, sg.b);
         const int qy = (pair.first + min(static_cast<int>(tok), pair.count - 1)) * kHeads;
-        for (uint32_t npad = q_pads(u); npad > 0 && ok; --npad) {  // pads
-          if (!(ok = claim(0))) break;
-          ++u;
+        for (uint32_t npad = q_pads(u); npad > 0 && ok; --npad, ++u) {  // pads
+          if (!(ok = claim(u))) break;
+          if (u % kKGroup == kKGroup - 1 && lane == 0 && tok == 0) mbar_arrive_relaxed(bar(kKF + group(u)));
         }
-        for (int i = 0; i < 8 && ok; ++i) {
-          for (int h = 0; h < 2; ++h) {
-            if (!(ok = claim(kPageChunk))) break;
-            if (lane == 0)
-              tma_load_2d_pair(kslot(u % kKSlots), &tm_q, i * kChunk, qy + h * kPage,
-                               rKF + 8u * ((u % kKSlots) / kKGroup));
-            ++u;
+        // Q, a chunk (two uses, side by side) a load: its bytes count for its second
+        // half's group, which the copy into tensor memory waits for with the first's.
+        // (With a load a use the ring made room faster than they were issued.)
+        for (int i = 0; i < 8 && ok; ++i, u += 2) {
+          if (!(ok = claim(u) && claim(u + 1))) break;
+          if (lane == 0) {
+            const uint32_t ga = group(u), gb = group(u + 1);
+            if (tok == 0) {
+              if (ga != gb) mbar_arrive_relaxed(bar(kKF + ga));
+              if (u % kKGroup == 1)
+                mbar_arrive_expect_tx_relaxed(bar(kKF + gb), 2u * kQChunk);
+              else
+                mbar_expect_tx_relaxed(bar(kKF + gb), 2u * kQChunk);
+            }
+            tma_load_2d_pair(kslot(u % kKSlots), &tm_q, i * kChunk, qy, rKF + 8u * gb);
           }
         }
         if (!ok) break;
-        // RoPE part of Q (not in the ring) once the previous segment's score MMAs are done with it
-        if (nseg >= 1 && !(ok = warp_wait(bar(kQFree), (nseg - 1u) & 1u, ctl))) break;
-        if (lane == 0) {
-          if (tok == 0) mbar_arrive_expect_tx_relaxed(bar(kQRF), 2u * kQChunk);
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d_pair(sbase + kOffQr + h * kPageChunk, &tm_q, 8 * kChunk, qy + h * kPage, rQRF);
-        }
         const int* bt_row = p.block_table + static_cast<long long>(pair.req) * p.bt_stride;
         const int npages = (L + kPage - 1) / kPage;
         for (int jb = sg.t0; jb < sg.t1 && ok; jb += 32) {
@@ -873,6 +894,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           for (int jj = 0; jj < cnt && ok; ++jj) {
             const int page = __shfl_sync(0xffffffffu, my_page, jj);
             const int y = page >= 0 ? page * kPage : static_cast<int>(p.num_pages) * kPage;
+            const bool first = jb + jj == sg.t0;
             // a tile is three whole slot groups: one 3-chunk load per group
             for (int c = 0; c < kNumChunks; c += kKGroup) {
               const uint32_t sl = u % kKSlots, grp = sl / kKGroup;
@@ -882,7 +904,24 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
                 tma_load_3d_pair(kslot(sl), &tm_k3, 0, y, c, rKF + 8u * grp);
               }
               u += kKGroup;
+              // RoPE part of Q (not in the ring) once the previous segment's score MMAs are
+              // done with it, behind the chunks of the first tile that the ring has room for
+              if (first && c == 0) {
+                if (nseg >= 1 && !(ok = warp_wait(bar(kQFree), (nseg - 1u) & 1u, ctl))) break;
+                if (lane == 0) {
+                  if (tok == 0) mbar_arrive_expect_tx_relaxed(bar(kQRF), 2u * kQChunk);
+                  tma_load_2d_pair(sbase + kOffQr, &tm_q, 8 * kChunk, qy, rQRF);
+                }
+              }
             }
+            // the next segment's Q on its way to L2: the ring takes it in the few tiles
+            // before its turn, which HBM is too far away for
+            if (first && ok && ahead.next(then) && lane == 0) {
+              const TokenPair next = token_pair<kPairs>(p, then.b);
+              const long long row = (static_cast<long long>(next.first) + min(static_cast<int>(tok), next.count - 1)) * kHeads;
+              for (int h = 0; h < 2; ++h) bulk_prefetch_l2(p.q + (row + h * kPage) * kDqk, kPage * kDqk * 2);
+            }
+            __syncwarp();
           }
         }
         ++nseg;
@@ -985,9 +1024,9 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     const uint32_t spc = static_cast<uint32_t>(kp & 7);
     constexpr int kRowsPerThread = (kPage + 11) / 12;  // 6: rows lw + 12 i
     const volatile float* fin_s = reinterpret_cast<const volatile float*>(smem + kOffFin);
-    // kVDepth pages of loads in flight per thread (registers), so that a
-    // page's load latency spans several pages' turns
-    uint4 v[kVDepth][kRowsPerThread];
+    // one page of loads in flight per thread (registers) beyond the one being
+    // stored (two measured no faster)
+    uint4 v[kRowsPerThread];
     // Page ids of the segment, 32 at a time and one batch ahead: lane j holds
     // the pool page of page ids_base + j (-1 past the cache end or outside the
     // pool).  Reading the block-table entry next to each page's loads would
@@ -1028,66 +1067,77 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     };
     const uint32_t rVR = mapa(bar(kVR), 2);
     SegIter it(p, unit);
-    Seg sg;
+    Seg sg{};
     Ring<kVSlots> rv;
     uint32_t g = 0, nseg = 0;
     // this warp's waits so far; the twelve warps vote at each segment's
     // epilogue barrier, so a warp whose wait failed skips the rest of the
     // segment's pages and they all leave there together
     bool wok = true;
-    while (it.next(sg)) {
+    // The first tile of a segment is stored before the epilogue of the last one,
+    // whose value products run meanwhile: its loads (block table, then rows) and
+    // its conversion are then not between the two segments' products.
+    int p0 = 0, np = 0, q = 0;  // the segment's pages p0 .. p0 + np - 1, the next one to store
+    auto begin_segment = [&]() {
       L = max(p.cache_lens[sg.b], 0);
       const TokenPair pair = token_pair<kPairs>(p, sg.b);
       bt_row = p.block_table + static_cast<long long>(pair.req) * p.bt_stride;
       hidden = kPairs && p.causal && pair.count == 2 ? L - 1 : -1;
-      const int p0 = 2 * sg.t0, np = 2 * (sg.t1 - sg.t0);  // this segment's pages: p0 .. p0 + np - 1
+      p0 = 2 * sg.t0;
+      np = 2 * (sg.t1 - sg.t0);
+      q = 0;
       ids_base = p0;
       ids_cur = fetch_ids(p0);
       ids_next = fetch_ids(p0 + 32);
+      if (wok) load_page(v, p0);
+    };
+    Seg done{};            // the segment before, while its epilogue is due
+    bool due = false, more = it.next(sg);
+    if (more) begin_segment();
+    while (more || due) {
+      const int until = !more ? 0 : due ? 2 : np;
+      for (; q < until; ++q) {
+        wok = wok && warp_wait(bar(kVE + rv.idx), rv.phase ^ 1u, ctl);  // PV is done with the slot
+        if (wok) {
+          const uint32_t stg = vslot(rv.idx) + scol;
 #pragma unroll
-      for (int d = 0; d < kVDepth; ++d)
-        if (wok && d < np) load_page(v[d], p0 + d);
-      for (int q0 = 0; q0 < np; q0 += kVDepth) {
-#pragma unroll
-        for (int d = 0; d < kVDepth; ++d) {
-          const int q = q0 + d;
-          if (q >= np) break;
-          wok = wok && warp_wait(bar(kVE + rv.idx), rv.phase ^ 1u, ctl);  // PV is done with the slot
-          if (wok) {
-            const uint32_t stg = vslot(rv.idx) + scol;
-#pragma unroll
-            for (int i = 0; i < kRowsPerThread; ++i) {
-              const int r = lw + 12 * i;
-              if (r < kPage)
-                st_shared_v4(stg + static_cast<uint32_t>(r) * 128u + ((spc ^ static_cast<uint32_t>(r & 7)) << 4),
-                             bf16x2_to_f16x2(v[d][i].x), bf16x2_to_f16x2(v[d][i].y),
-                             bf16x2_to_f16x2(v[d][i].z), bf16x2_to_f16x2(v[d][i].w));
-            }
-            fence_proxy_async_smem();  // generic writes, read next by the tensor core
-            __syncwarp();
-            // Each warp announces its own rows to rank 2 (release, cumulative
-            // over the warp's stores), before its loads of the next page.  One
-            // announcer per rank after a group barrier put that barrier and
-            // the announcer's release on every page's path.
-            if (lane == 0) mbar_arrive_remote_cta(rVR + 8u * rv.idx);
+          for (int i = 0; i < kRowsPerThread; ++i) {
+            const int r = lw + 12 * i;
+            if (r < kPage)
+              st_shared_v4(stg + static_cast<uint32_t>(r) * 128u + ((spc ^ static_cast<uint32_t>(r & 7)) << 4),
+                           bf16x2_to_f16x2(v[i].x), bf16x2_to_f16x2(v[i].y), bf16x2_to_f16x2(v[i].z),
+                           bf16x2_to_f16x2(v[i].w));
           }
-          rv.advance();
-          // the segment's page kVDepth ahead goes into the buffer just stored
-          if (wok && q + kVDepth < np) load_page(v[d], p0 + q + kVDepth);
+          fence_proxy_async_smem();  // generic writes, read next by the tensor core
+          __syncwarp();
+          // Each warp announces its own rows to rank 2 (release, cumulative
+          // over the warp's stores), before its loads of the next page.  One
+          // announcer per rank after a group barrier put that barrier and
+          // the announcer's release on every page's path.
+          if (lane == 0) mbar_arrive_remote_cta(rVR + 8u * rv.idx);
         }
+        rv.advance();
+        // the segment's next page goes into the buffer just stored
+        if (wok && q + 1 < np) load_page(v, p0 + q + 1);
       }
-      g += static_cast<uint32_t>(sg.t1 - sg.t0);
+      if (!due) {  // all pages of a segment are stored
+        g += static_cast<uint32_t>(sg.t1 - sg.t0);
+        done = sg;
+        due = true;
+        if ((more = it.next(sg))) begin_segment();
+        continue;
+      }
       {  // ---- this group's share of the segment epilogue
         const uint32_t pb = (g - 1u) & 1u;  // the segment's last tile
         // O complete; the last P message (with the final scales) landed
         bool ok = wok && warp_wait(bar(kOF), nseg & 1u, ctl) && warp_wait(bar(kPM + pb), ((g - 1u) >> 1) & 1u, ctl);
         if (!named_bar_all(6, kConvThreads, ok)) break;
         tc_fence_after();
-        epilogue_share(warp, fin_s[pb * kHeads + 32 * (warp & 3) + lane], sg, pb);
-        tc_fence_before();
+        epilogue_share(warp, fin_s[pb * kHeads + 32 * (warp & 3) + lane], done, pb);
         named_bar_sync(6, kConvThreads);
-        if (ptid == 0) mbar_arrive(bar(kEpiD));
+        if (warp == 4) wok = free_staging(pb, nseg) && wok;
       }
+      due = false;
       ++nseg;
     }
     if (lane == 0) bulk_wait_all();  // the output stores have completed
@@ -1133,9 +1183,8 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           }
           tc_fence_after();
           epilogue_share(warp, fin_s[pb * kHeads + 32 * (warp & 3) + lane], sg, pb);
-          tc_fence_before();
           named_bar_sync(6, kConvThreads);
-          if (ptid == 0) mbar_arrive(bar(kEpiD));
+          if (warp == 4) free_staging(pb, nseg);
         }
       }
       ++nseg;

@@ -81,6 +81,15 @@
 namespace mla {
 namespace mtp {
 
+// Arrive on an mbarrier of the value pair's rank 2 with release at CTA scope:
+// the arriving warp's shared-memory stores are performed before the arrive
+// lands.  The tensor core of the pair reads them from this CTA's shared memory
+// only after rank 2 has seen the arrival.  (Release at cluster scope costs
+// each arriving warp about a thousand cycles under load.)
+__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+}
+
 // Eight bf16, zero in the place of infinities and NaN.
 __device__ __forceinline__ uint4 numbers_only(uint4 v) {
   auto two = [](uint32_t w) {
@@ -177,8 +186,8 @@ enum Bar {
   kMmaDone2 = 67, // teardown (second issuer)
   kHand = 68,     // [2] rank 0: score-MMA issue token (tile parity): the issuer of tile g may start
                   //     once the issuer of tile g - 1 has issued two thirds of its MMAs
-  kEpiD = 70,     // [2] value ranks: the rescale warps' shares of a segment's epilogue are written (by the
-                  //     segment's parity: these warps may be at the next one's before the others ask)
+  kEpiD = 70,     // [2] value ranks: a segment's epilogue is written (one arrival per warp), by the segment's
+                  //     parity: the rescale warps may be at the next one's before this one's is passed on
   kNumBars = 72
 };
 static_assert(kNumBars * 8 + 16 <= kBarBytes, "barrier block");
@@ -309,7 +318,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     mbar_init(bar(kMmaDone), 1);
     mbar_init(bar(kPsFull), kSoftmaxWarps);
     mbar_init(bar(kPsFree), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(kEpiD + i), 4);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(kEpiD + i), 16);
     misc[1] = 0u;
     fence_mbar_init();
   }
@@ -525,15 +534,6 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
     }
     if (lane == 0) bulk_wait_read();
     __syncwarp();
-  };
-
-  // The twelve warps' shares are done: with the other four's, P slot `pb` is free
-  // for the score rank that ships this rank's P (the stores have read what it
-  // overwrites).
-  auto free_staging = [&](uint32_t pb, uint32_t nseg) {
-    if (!warp_wait(bar(kEpiD + (nseg & 1u)), (nseg >> 1) & 1u, ctl)) return false;
-    if (lane == 0) mbar_arrive_remote_cta(mapa(bar(kPFree), tok) + 8u * pb);
-    return true;
   };
 
   if (halt) {
@@ -774,7 +774,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           }
           tc_fence_after();
           epilogue_share(warp, fin, sg, pb);
-          if (lane == 0) mbar_arrive(bar(kEpiD + (nseg & 1u)));
+          if (lane == 0) mbar_arrive(bar(kEpiD + (nseg & 1u)));  // this warp's stores have read the staging
         }
       }
       ++nseg;
@@ -826,6 +826,20 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
       }
       umma_commit_pair(bar(kMmaDone), 1u << 2);
       drain_bar(bar(kMmaDone), 0);
+    } else if (lane == 0 && !score_rank && warp == kMma2Warp) {
+      // A segment's epilogue is written: the P slot that staged it is free for the
+      // score rank that ships this rank's P.  (A thread of its own: the release to
+      // the cluster took a microsecond of the rescale warps' way to the next tile.)
+      const uint32_t rPFree = mapa(bar(kPFree), tok);
+      SegIter it(p, unit);
+      Seg sg;
+      uint32_t g = 0, nseg = 0;
+      while (it.next(sg)) {
+        g += static_cast<uint32_t>(sg.t1 - sg.t0);
+        if (!wait_bar<false>(bar(kEpiD + (nseg & 1u)), (nseg >> 1) & 1u, ctl)) break;
+        mbar_arrive_remote(rPFree + 8u * ((g - 1u) & 1u));
+        ++nseg;
+      }
     }
     __syncwarp();
   } else if (warp == kTmaWarp) {
@@ -1134,8 +1148,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
         if (!named_bar_all(6, kConvThreads, ok)) break;
         tc_fence_after();
         epilogue_share(warp, fin_s[pb * kHeads + 32 * (warp & 3) + lane], done, pb);
-        named_bar_sync(6, kConvThreads);
-        if (warp == 4) wok = free_staging(pb, nseg) && wok;
+        if (lane == 0) mbar_arrive(bar(kEpiD + (nseg & 1u)));
       }
       due = false;
       ++nseg;
@@ -1183,8 +1196,7 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
           }
           tc_fence_after();
           epilogue_share(warp, fin_s[pb * kHeads + 32 * (warp & 3) + lane], sg, pb);
-          named_bar_sync(6, kConvThreads);
-          if (warp == 4) free_staging(pb, nseg);
+          if (lane == 0) mbar_arrive(bar(kEpiD + (nseg & 1u)));
         }
       }
       ++nseg;

@@ -66,15 +66,6 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t remote_bar) 
                ::"r"(remote_bar) : "memory");
 }
 
-// The same with release at CTA scope, for shared memory that this CTA writes and
-// the tensor core of its pair reads from this CTA's shared memory once the peer
-// has seen the arrival: the arriving warp's stores are performed before the
-// arrive lands.  (Release at cluster scope takes a thousand cycles and more
-// under load.)
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t remote_bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
-}
-
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

@@ -32,11 +32,11 @@
 // line's order: no atomics, equal calls give equal bits.
 //
 // FP8 rows come as codes by TMA and are widened in place by eight further warps, a
-// chain (codes 2 us, widening 0.8, products 0.9) that one tile in shared memory
-// lets run once a tile and so bounds one or two tokens a request: 64 x 8192 111
-// us (3.1 TB/s; bf16 100, 6.1 TB/s), 33 x 2 x 2560 38 (30), 64 x 2 x 8192 170
-// (129).  Many tokens: 32 x 16384 54 (53), 64 x 65536 337 (352: 1.75 PFLOP/s).
-// One row tile ahead in L2 did not shorten it.
+// chain (codes 2 us, widening 0.8, hand-over to the pair 0.5, products 0.6) that
+// one tile in shared memory lets run once a tile and so bounds one or two tokens
+// a request: 64 x 8192 114 us (3.0 TB/s; bf16 100, 6.1 TB/s), 33 x 2 x 2560 35
+// (29), 64 x 2 x 8192 161 (125).  Many tokens: 32 x 16384 55 (52), 64 x 65536 341
+// (343: 1.8 PFLOP/s).  The next tile's pages asked into L2 did not shorten it.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -83,7 +83,8 @@ enum Bar {
   kAF = kQE + kGroups,        // [2] both accumulators of a step complete
   kAE = kAF + 2,              // [2] rank 0: ... and read by the sixteen warps of both CTAs
   kRaw = kAE + 2,             // [4] FP8 rows: a group's codes landed in this CTA
-  kDrain = kRaw + kGroups,    // [2] per issuer
+  kWide = kRaw + kGroups,     // [4] rank 1, FP8 rows: widened (for the relay)
+  kDrain = kWide + kGroups,   // [2] per issuer
   kNumBars = kDrain + 2
 };
 constexpr int kSlack = 1024;
@@ -309,11 +310,12 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
 
   if (threadIdx.x == 0) {
     for (int g = 0; g < kGroups; ++g) {
-      mbar_init(bar(kKF + g), kFp8 ? 16 : 1);  // FP8: both CTAs' fill warps
+      mbar_init(bar(kKF + g), kFp8 ? 9 : 1);  // FP8: rank 0's fill warps and rank 1's relay
       mbar_init(bar(kKE + g), 1);
       mbar_init(bar(kQF + g), 1);
       mbar_init(bar(kQE + g), 1);
       mbar_init(bar(kRaw + g), 1);
+      mbar_init(bar(kWide + g), 8);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar(kAF + a), 2);  // both issuers
@@ -467,7 +469,9 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
             if (new_q) ok = ok && warp_wait_uniform<true>(bar(kQF + g), (nq - 1) & 1, ctl);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+            // (rolled: 20 warps of six kinds share the instruction cache; unrolled 64 tokens x
+            // 65536 FP8 392 us against 345, bf16 356 / 344)
+#pragma unroll 1
             for (int c = group_begin<kFp8>(g); c < group_begin<kFp8>(g + 1); ++c)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -490,6 +494,23 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
       issue(std::integral_constant<int, kGroups / 2>(), std::integral_constant<int, kGroups>());
     umma_commit_pair_if(leader, bar(kDrain + which), 1);  // arrives once every MMA issued above has completed
     drain_bar(bar(kDrain + which), 0u);
+    __syncwarp();
+  } else if (warp == 1 || warp == 3) {
+    // Rank 1 has nothing to issue.  With an FP8 cache these threads relay its fill
+    // warps' arrivals to rank 0, whose MMAs read this CTA's rows too: the warps
+    // release to their own CTA, a thread without stores of its own to the cluster
+    // (a release to the cluster by each of them waits for its earlier stores).
+    if (kFp8 && lane == 0) {
+      const uint32_t rk = mapa(bar(kKF), 0);
+      Walk walk(p, begin);
+      Visit v;
+      bool ok = true;
+      for (uint32_t nk = 0; ok && walk.next_live(v); ++nk)
+        for (int i = 0; ok && i < kGroups / 2; ++i) {
+          const int g = kGroups / 2 * (warp >> 1) + i;
+          if ((ok = wait(bar(kWide + g), nk & 1, ctl))) mbar_arrive_remote(rk + 8u * g);
+        }
+    }
     __syncwarp();
   } else if (warp >= kEpiWarp && warp < kEpiWarp + 8) {
     // ================================================= sums over heads and tokens
@@ -535,7 +556,7 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
         tc_fence_after();
         float e[4] = {0.f, 0.f, 0.f, 0.f};
         constexpr int kCols = kFp8 ? 16 : 32;  // (registers: 20 warps have 96 a thread)
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 64 / kCols; ++h) {
           uint32_t x[2][kCols];
           for (int a = 0; a < 2; ++a) {
@@ -588,7 +609,6 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
     // by these warps, three turns of loads in flight: 64 x 2 x 8192 245, bound by
     // their latency, where the TMA holds a whole tile in flight.)
     const int w = warp - kFillWarp;
-    const uint32_t filled = mapa(bar(kKF), 0);
     Walk walk(p, begin);
     Visit v;
     uint32_t nk = 0;
@@ -654,7 +674,7 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
           }
         fence_proxy_async_smem();  // generic writes, read next by the tensor core
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_cta(filled + 8u * g);
+        if (lane == 0) mbar_arrive(bar((rank == 0 ? kKF : kWide) + g));
       }
       scales = next_scales;
       ++nk;

@@ -34,7 +34,8 @@ size_t mla_attention_weights_workspace_size(int num_tokens, int num_requests, in
  *                 mla_chunk_attend
  *   lse           fp32 [num_tokens, 128], 16-B aligned: of the attention these are the
  *                 weights of (which may have seen more than this cache); -inf:
- *                 the head attended to nothing
+ *                 the head attended to nothing and adds nothing, whatever q
+ *                 holds there
  *   weights, out  fp32 rows of max_len at a stride of weights_stride and
  *                 out_stride; out may be weights itself, and must not overlap
  *                 it otherwise.  weights may be NULL where decay is 0

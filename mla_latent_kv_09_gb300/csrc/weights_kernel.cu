@@ -546,8 +546,10 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
       bool ok = true;
       for (int i = v.steps, q = v.q0; i > 0; --i, q += v.way, ++step) {
         const uint32_t buf = step & 1;
-        // a head without a result (-inf) weighs nothing: 2^(s - inf)
+        // a head without a result (-inf) weighs nothing: 2^(s - inf), and where there are
+        // such heads their scores, which may be no numbers, are left out
         auto log2_of = [](float x) { return x == -INFINITY ? -INFINITY : -x * kLog2e; };
+        const bool empty = __any_sync(0xffffffffu, l2.x == -INFINITY || l2.y == -INFINITY);
         *my_lse = make_float2(log2_of(l2.x), log2_of(l2.y));
         if (i > 1) l2 = __ldg(lse_of(q + v.way));
         __syncwarp();
@@ -572,14 +574,23 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_relaxed(racc + 8u * buf);
           }
+          auto add = [&](auto some) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 l = ld_shared_v4f(s_lse + 4u * (kCols * h + c));
-            const float bias[4] = {l.x, l.y, l.z, l.w};
+            for (int c = 0; c < kCols; c += 4) {
+              const float4 l = ld_shared_v4f(s_lse + 4u * (kCols * h + c));
+              const float bias[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              e[i] += ex2_approx(fmaf(__uint_as_float(x[0][c + i]) + __uint_as_float(x[1][c + i]), p.scale_log2, bias[i]));
-          }
+              for (int i = 0; i < 4; ++i) {
+                const float w =
+                    ex2_approx(fmaf(__uint_as_float(x[0][c + i]) + __uint_as_float(x[1][c + i]), p.scale_log2, bias[i]));
+                e[i] += some && bias[i] == -INFINITY ? 0.f : w;
+              }
+            }
+          };
+          if (empty)
+            add(std::true_type());
+          else
+            add(std::false_type());
         }
         __syncwarp();  // the warp's lse has been read
         if (pos < limit(v, q, p.causal)) sum += (e[0] + e[1]) + (e[2] + e[3]);  // hidden rows may hold anything

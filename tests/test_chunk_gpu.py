@@ -140,6 +140,19 @@ def test_more_pairs_than_the_plan_keeps_in_shared_memory():
     assert (f64((out[:8301] - out[5]).abs().amax(0)) <= 2 * bo[0]).all() and (f64((lse[:8301] - lse[5]).abs().amax(0)) <= 2 * bl[0]).all()
 
 
+@pytest.mark.parametrize("out_fp32", [False, True])
+def test_many_short_requests_one_after_the_other(out_fp32):
+    """Segments of one tile and two, several to a unit, pairs and single tokens in turn."""
+    counts = [1 + (i * 7) % 3 for i in range(300)]
+    lens = [max(n, 1 + (i * 37) % 200) for i, n in enumerate(counts)]
+    starts = starts_of(counts)
+    cache, table, rows = paged(lens, False, 61)
+    q = rand((starts[-1], 128, 576), 62)
+    for _ in range(3):
+        out, lse = attend(q, cache, table, ints(lens), SCALE, token_starts=ints(starts), out_fp32=out_fp32)
+        assert_chunk(out, lse, q, rows, starts)
+
+
 def test_a_peaked_softmax():
     lens, counts = [900, 333], [7, 20]
     cache, table, rows = paged(lens, False, 8, spread=8.0)

@@ -94,6 +94,29 @@ def test_heads_that_attended_to_nothing_and_wider_sums():
     assert_weights(out, torch.zeros_like(out), 1.0, q, lse, rows, starts)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_heads_without_a_result_add_nothing_whatever_their_query(fp8):
+    """Padded tokens (all heads) and single heads: lse = -inf, queries NaN or
+    infinite.  The others' weights are those of zeros in their place, bit for bit."""
+    lens, starts = [700, 300], [0, 3, 5]
+    cache, table, _ = paged(lens, fp8, 77)
+    q = rand((5, 128, 576), 78)
+    args = (cache, table, ints(lens), SCALE)
+    _, lse = m.chunk_attend(q, *args, token_starts=ints(starts))
+    none = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    none[1] = True
+    none[3, ::7] = True
+    none[4, 64:] = True
+    lse[none] = -float("inf")
+    q[none] = 0.0
+    want = m.attention_weights(q, lse, *args, token_starts=ints(starts))
+    q[1] = float("nan")
+    q[3, ::7] = float("inf")
+    q[4, 64:, 5] = -float("inf")
+    got = m.attention_weights(q, lse, *args, token_starts=ints(starts))
+    assert torch.equal(got, want) and bool((got[0, :697] > 0).all())
+
+
 def test_weights_over_fp8_rows_of_every_scale():
     """Scales from 2^-27 to 2^33, NaN codes and scales among rows that are seen: only theirs are no numbers."""
     lens = [300]
@@ -250,6 +273,60 @@ def test_a_long_choice(L):
         assert np.array_equal(new[b, :keep].cpu().numpy(), x[ref]) and not new[b, keep:].any()
 
 
+def test_a_choice_among_more_rows_than_shared_memory_holds():
+    L, keep = 1_000_003, 123_456
+    w = torch.exp(rand((1, L), 4, torch.float32)).bfloat16().float()
+    kept, new_lens, new = m.evict_select(w, ints([L]), keep, sinks=3, recent=70)
+    x = w[0].cpu().numpy()
+    inner = np.arange(3, L - 70)
+    order = inner[np.argsort(-x[inner], kind="stable")]
+    ref = np.sort(np.concatenate((np.arange(3), order[:keep - 73], np.arange(L - 70, L))))
+    assert int(new_lens) == keep and np.array_equal(kept[0].cpu().numpy(), ref)
+    assert np.array_equal(new[0, :keep].cpu().numpy(), x[ref]) and not new[0, keep:].any()
+
+
+def test_choice_and_move_captured_and_on_another_stream():
+    lens, keep = [300, 64, 700], 90
+    cache, table, rows = paged(lens, False, 50)
+    tables = table.shape[1]
+    pages = cache.shape[0]
+    both = torch.cat((cache, torch.zeros((6, 64, 576), dtype=cache.dtype, device="cuda")))
+    w = [rand((3, 64 * tables), s, torch.float32) for s in (51, 52)]
+    new_table = ints([[pages + 2 * b, pages + 2 * b + 1] for b in range(3)])
+    n = ints(lens)
+
+    def run(weights, to, **kw):
+        kept, new_lens, _ = m.evict_select(weights, n, keep, sinks=2, recent=5, **kw)
+        m.cache_compact(to, table, kept, new_lens, new_table, **kw)
+        return kept, new_lens
+
+    def check(weights, to, kept, new_lens):
+        for b, L in enumerate(lens):
+            ref = oracle.evict_select(weights[b].cpu().numpy(), L, keep, 2, 5)
+            assert int(new_lens[b]) == len(ref) and np.array_equal(kept[b, :len(ref)].cpu().numpy(), ref)
+            got = to[new_table[b].long()].reshape(-1, 576)[:len(ref)]
+            assert np.array_equal(f64(got), rows[b][ref])
+
+    held = w[0].clone()
+    run(held, both)  # (memory of the graph's outputs aside)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept, new_lens = run(held, both)
+    for i in (1, 0, 1):
+        held.copy_(w[i])
+        both[pages:].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        check(w[i], both, kept, new_lens)
+    side = torch.cuda.Stream()
+    both[pages:].zero_()
+    torch.cuda.synchronize()
+    kept, new_lens = run(w[0], both, stream=side)
+    torch.cuda.synchronize()
+    check(w[0], both, kept, new_lens)
+
+
 def test_choices_in_slices_and_without_weights():
     lens, keep = [300, 40], 100
     big = rand((2, 512), 40, torch.float32)
@@ -373,6 +450,28 @@ def test_refusals():
 
 
 # ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_beyond_32_bit_offsets(fp8):
+    """A pool of more than 2^32 bytes, its last pages in use."""
+    lens, starts = [300, 129], [0, 2, 5]
+    cache, table, rows = paged(lens, fp8, 90)
+    pages = 2 ** 32 // (64 * cache.shape[2] * cache.element_size()) + 100
+    pool = torch.empty((pages,) + cache.shape[1:], dtype=cache.dtype, device="cuda")
+    pool[pages - cache.shape[0]:] = cache
+    far = torch.where(table >= 0, table + (pages - cache.shape[0]), table)
+    q, s, n = rand((5, 128, 576), 91), ints(starts), ints(lens)
+    want = m.chunk_attend(q, cache, table, n, SCALE, token_starts=s)
+    got = m.chunk_attend(q, pool, far, n, SCALE, token_starts=s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    w = m.attention_weights(q, got[1], pool, far, n, SCALE, token_starts=s)
+    assert torch.equal(w, m.attention_weights(q, got[1], cache, table, n, SCALE, token_starts=s))
+    kept, new_lens, _ = m.evict_select(w, n, 100)
+    m.cache_compact(pool, far, kept, new_lens, ints([[5, 6], [7, 8]]))
+    for b in range(2):
+        old = pool[far[b, kept[b].long() // 64].long(), kept[b].long() % 64]
+        assert torch.equal(pool[5 + 2 * b:7 + 2 * b].reshape(128, -1)[:100].view(torch.uint8), old.view(torch.uint8))
+
 
 @pytest.mark.parametrize("fp8", [False, True])
 def test_a_prompt_in_chunks_whose_cache_shrinks(fp8):

@@ -626,7 +626,7 @@ def chunk_attend(q, kv_cache, block_table, cache_lens, softmax_scale: float, *, 
     sees may hold anything.
 
     The cost of a (token, row) is that of the absorbed form.  Chunks of more
-    than some 200 tokens of one request cost less by `prefix_expand` of its
+    than some 160 tokens of one request cost less by `prefix_expand` of its
     whole cache and `prefix_attend` with `visible` counts.
 
     `workspace` (uint8, mla_chunk_attend_workspace_size bytes) is allocated if

@@ -318,7 +318,7 @@ int mla_decode_plan_host(const int32_t* lens, int batch, int s_q, int topk, int 
     req_meta[4 * b + 3] = total;
     total += plan_cost(n);
   }
-  const int W = plan_width(total, num_units);
+  const int W = plan_width(total, num_units, kPlanMinTiles);
   int slots = 0;
   for (int b = 0; b < batch; ++b) {
     const int ns = plan_n_splits(req_meta[4 * b + 3], req_meta[4 * b + 0], W, num_units);

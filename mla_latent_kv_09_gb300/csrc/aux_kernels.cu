@@ -115,7 +115,9 @@ __global__ void __launch_bounds__(1024) mla_plan_kernel(const int* __restrict__ 
     carry += tot;
   }
   const int total = carry;
-  const int W = plan_width(total, U);
+  // (equal runs of two tokens are a decode step: its partition, and so its results' bits)
+  const bool step = !kPairs || (!chunk.starts && chunk.tokens == 2 * chunk.requests);
+  const int W = plan_width(total, U, step ? kPlanMinTiles : kPlanMinPairTiles);
   __syncthreads();
   carry = 0;
   for (int base = 0; base < B; base += blockDim.x) {

@@ -16,7 +16,7 @@
 
 namespace mla {
 cudaError_t plan_launch(const int* lens, int B, int topk, int tile_rows, int U, int* hdr, int* unit_meta, int* req_meta,
-                        int slots_cap, const ChunkPairs* chunk, cudaStream_t stream);
+                        int slots_cap, const ChunkPairs* chunk, bool beside, cudaStream_t stream);
 cudaError_t combine_launch(const int* hdr, const int* req_meta, const float* part_lse, const uint16_t* part_o,
                            int part_bf16, int s_q, int out_fp32, void* out, float* lse, int n_bt, const ChunkPairs* chunk,
                            const int* table, long long bt_stride, long long num_pages, cudaStream_t stream);
@@ -212,9 +212,9 @@ int launched(cudaError_t e) {
 }
 
 int launch_plan(char* ws, const WsLayout& L, const int* lens, int batch, int topk, int tile_rows, int units,
-                const ChunkPairs* chunk, mla_stream_t stream) {
+                const ChunkPairs* chunk, bool beside, mla_stream_t stream) {
   return launched(plan_launch(lens, batch, topk, tile_rows, units, reinterpret_cast<int*>(ws + L.hdr),
-                              reinterpret_cast<int*>(ws + L.units), reinterpret_cast<int*>(ws + L.reqs), L.slots, chunk,
+                              reinterpret_cast<int*>(ws + L.units), reinterpret_cast<int*>(ws + L.reqs), L.slots, chunk, beside,
                               static_cast<cudaStream_t>(stream)));
 }
 
@@ -302,7 +302,7 @@ int mla_decode_plan(const int32_t* cache_lens, int batch, int s_q, int topk, int
   const WsLayout L = ws_layout(batch, s_q, U);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  return launch_plan(ws, L, cache_lens, batch, topk, plan_tile_rows(s_q, topk), U, nullptr, stream);
+  return launch_plan(ws, L, cache_lens, batch, topk, plan_tile_rows(s_q, topk), U, nullptr, false, stream);
 }
 
 int mla_decode_plan_host(const int32_t* lens, int batch, int s_q, int topk, int num_units, int32_t* unit_meta,
@@ -529,13 +529,13 @@ int mla_chunk_attend(const void* q, const void* kv_cache, int64_t num_pages, con
     table = reinterpret_cast<const int*>(ws + c.table);
     stride = c.pages;
     pages = static_cast<int64_t>(num_requests) * c.pages;
-    const int blocks = (c.pages + 1) / 2;  // 8 warps, 16 rows each
+    const int blocks = c.pages;  // 8 warps, 8 rows each
     mla_widen_kernel<<<dim3(blocks < 4096 ? blocks : 4096, num_requests < 65535 ? num_requests : 65535), 256, 0, s>>>(
         static_cast<const uint8_t*>(kv_cache), num_pages, block_table, bt_stride, cache_lens, max_len, num_requests,
         c.pages, reinterpret_cast<uint16_t*>(ws + c.wide), reinterpret_cast<int*>(ws + c.table), status);
     if ((rc = last_cuda_error()) != MLA_OK) return rc;
   }
-  if ((rc = launch_plan(ws, L, pairs.pair_lens, c.slots, 0, 128, c.units, &pairs, stream)) != MLA_OK) return rc;
+  if ((rc = launch_plan(ws, L, pairs.pair_lens, c.slots, 0, 128, c.units, &pairs, fp8, stream)) != MLA_OK) return rc;
 
   DecodeParams p;
   std::memset(&p, 0, sizeof(p));

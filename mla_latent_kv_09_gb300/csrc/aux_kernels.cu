@@ -174,7 +174,7 @@ cudaError_t plan_launch(const int* lens, int B, int topk, int tile_rows, int U, 
 // Chunk attention over an FP8 cache: the rows of a request in order, as bf16
 // rows behind an identity table (row j of request b in page b * pages + j / 64),
 // four rows of a page a warp, their loads in flight together (one at a time: 7
-// requests of up to 8192 rows 19.9 us, the call 352).
+// requests of up to 8192 rows 19.9 us instead of 16.9).
 // An E4M3 code has 4 significant bits and the scale is a power of two, so bf16
 // holds every value exactly (within its range).  A chunk's
 // kernel reads every row once for each two of its tokens, so that one more

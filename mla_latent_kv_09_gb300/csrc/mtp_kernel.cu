@@ -149,14 +149,14 @@ constexpr int kShipWarp = 18;                    // score ranks: P shipper
 constexpr int kMma2Warp = 19;                    // rank 0: issues the score MMAs of odd tiles
 constexpr float kRescaleLog2 = 8.0f;
 // Chunks rescale O less often: a warp's rows move their reference together, when
-// one of them has a score that beats its own by 2^14 (weights stay below 2^16,
-// which fp16 holds), and then to 2^6 above the largest score they have seen.
+// one of them has a score that beats its own by 2^15.9 (weights stay below 65504,
+// fp16's largest), and then to 2^6 above the largest score they have seen.
 // Weights below 2^-8 of a row's largest may then be subnormal in fp16, off by
 // 2^-19 of the largest.  A rescale reads and writes 128 x 512 values, as long as
 // a tile's own products take: with rows of large magnitude (5 % of them 6 times
-// the others) 72 tokens x 4096 rows take 91 us instead of 105, x 32768 456
-// instead of 565.
-constexpr float kPairsRescaleLog2 = 14.0f, kPairsAheadLog2 = 6.0f;
+// the others) 72 tokens x 4096 rows take 87 us instead of 105, x 32768 441
+// instead of 565 (2^14: 89 and 445; 13 x 47 tokens x 2048 424 against 413).
+constexpr float kPairsRescaleLog2 = 15.9f, kPairsAheadLog2 = 6.0f;
 
 constexpr uint16_t kScoreMask = 0x3;  // ranks 0, 1
 constexpr uint16_t kValueMask = 0xC;  // ranks 2, 3

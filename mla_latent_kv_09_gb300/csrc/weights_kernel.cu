@@ -24,7 +24,7 @@
 // does not average that away: 32 tokens x 16384 rows were off by 1.5e-6 with one
 // accumulator, 7e-7 with two.  And each accumulator has a thread of its own to
 // issue its products: one thread alone issues more slowly than they execute (32 x
-// 16384 75 us against 55).
+// 16384 75 us against 55, before the steps below).
 //
 // Work: the (tile, token) steps of all requests lie on a line that is cut into
 // equal ranges, one a pair.  A range that begins inside a tile's tokens writes
@@ -57,7 +57,7 @@ constexpr int kTileRows = 2 * kRows;
 constexpr int kKChunk = kRows * 128;          // 16 KiB: 128 rows x 64 dims
 constexpr int kQChunk = 64 * 128;             // 8 KiB: 64 heads x 64 dims
 // Chunks lie in groups that land and are given back together (a commit a chunk
-// made 32 x 16384 107 us instead of 55).  An FP8 cache's codes come two chunks at
+// made 32 x 16384 107 us instead of the 55 of then).  An FP8 cache's codes come two chunks at
 // a time; bf16 rows with these groups: 64 x 2 x 8192 143 us against 131.
 constexpr int kGroups = 4;
 template <bool kFp8>

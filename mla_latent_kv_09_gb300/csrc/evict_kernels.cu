@@ -28,6 +28,7 @@ using prefix::share;
 // of 8192 rows 15 us on one CTA).
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+static_assert(kSelWarps == 32, "the ordered pass adds the warps' counts a lane each");
 constexpr int kMaxCluster = 16;  // (more than 8 as a permission asks)
 constexpr int kSelRows = 4096;   // of a CTA, before the request gets further ones
 constexpr int kRoomRows = 49152;  // of a slice that shared memory holds; others are read again in every pass
@@ -215,9 +216,10 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __g
     const int maybe_at = maybe_before + __popc(m & lower);
     if (stays || (may && maybe_at < left)) {
       const int place = sure_before + __popc(s & lower) + min(maybe_at, left);
-      kept[place] = j0 + i;
+      // (rows read again in every pass may change meanwhile, by a caller's mistake: not outside the list)
+      if (place < p.keep) kept[place] = j0 + i;
       // a key says what the weight was, but for zeros' signs, NaN and protected rows
-      if (out)
+      if (out && place < p.keep)
         out[place] = key == kZero || key == kLowest || key == kProtected ? __ldg(row + j0 + i)
                      : __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
     }

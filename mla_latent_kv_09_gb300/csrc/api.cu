@@ -16,13 +16,13 @@
 
 namespace mla {
 cudaError_t plan_launch(const int* lens, int B, int topk, int tile_rows, int U, int* hdr, int* unit_meta, int* req_meta,
-                        int slots_cap, const ChunkPairs* chunk, bool beside, cudaStream_t stream);
+                        int slots_cap, const ChunkPairs* chunk, cudaStream_t stream);
 cudaError_t combine_launch(const int* hdr, const int* req_meta, const float* part_lse, const uint16_t* part_o,
                            int part_bf16, int s_q, int out_fp32, void* out, float* lse, int n_bt, const ChunkPairs* chunk,
                            const int* table, long long bt_stride, long long num_pages, cudaStream_t stream);
-__global__ void mla_widen_kernel(const uint8_t* kv, long long num_pages, const int* table, long long bt_stride,
-                                 const int* lens, int max_len, int requests, int pages, uint16_t* wide,
-                                 int* wide_table, int* status);
+cudaError_t widen_launch(dim3 grid, const uint8_t* kv, long long num_pages, const int* table, long long bt_stride,
+                         const int* lens, int max_len, int requests, int pages, uint16_t* wide, int* wide_table,
+                         int* status, cudaStream_t stream);
 __global__ void mla_wait_timeout_kernel(int* status);
 __global__ void mla_validate_kernel(const int* lens, const int* bt, long long bt_stride,
                                     long long num_pages, int B, int s_q, const int* topk_idx, int topk,
@@ -212,9 +212,9 @@ int launched(cudaError_t e) {
 }
 
 int launch_plan(char* ws, const WsLayout& L, const int* lens, int batch, int topk, int tile_rows, int units,
-                const ChunkPairs* chunk, bool beside, mla_stream_t stream) {
+                const ChunkPairs* chunk, mla_stream_t stream) {
   return launched(plan_launch(lens, batch, topk, tile_rows, units, reinterpret_cast<int*>(ws + L.hdr),
-                              reinterpret_cast<int*>(ws + L.units), reinterpret_cast<int*>(ws + L.reqs), L.slots, chunk, beside,
+                              reinterpret_cast<int*>(ws + L.units), reinterpret_cast<int*>(ws + L.reqs), L.slots, chunk,
                               static_cast<cudaStream_t>(stream)));
 }
 
@@ -302,7 +302,7 @@ int mla_decode_plan(const int32_t* cache_lens, int batch, int s_q, int topk, int
   const WsLayout L = ws_layout(batch, s_q, U);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  return launch_plan(ws, L, cache_lens, batch, topk, plan_tile_rows(s_q, topk), U, nullptr, false, stream);
+  return launch_plan(ws, L, cache_lens, batch, topk, plan_tile_rows(s_q, topk), U, nullptr, stream);
 }
 
 int mla_decode_plan_host(const int32_t* lens, int batch, int s_q, int topk, int num_units, int32_t* unit_meta,
@@ -520,6 +520,7 @@ int mla_chunk_attend(const void* q, const void* kv_cache, int64_t num_pages, con
   pairs.pairs = reinterpret_cast<int4*>(ws + c.pairs);
   pairs.pair_lens = reinterpret_cast<int*>(ws + c.lens);
   pairs.status = status;
+  pairs.beside = fp8;
 
   const uint16_t* kv = static_cast<const uint16_t*>(kv_cache);
   const int* table = block_table;
@@ -530,12 +531,13 @@ int mla_chunk_attend(const void* q, const void* kv_cache, int64_t num_pages, con
     stride = c.pages;
     pages = static_cast<int64_t>(num_requests) * c.pages;
     const int blocks = c.pages;  // 8 warps, 8 rows each
-    mla_widen_kernel<<<dim3(blocks < 4096 ? blocks : 4096, num_requests < 65535 ? num_requests : 65535), 256, 0, s>>>(
-        static_cast<const uint8_t*>(kv_cache), num_pages, block_table, bt_stride, cache_lens, max_len, num_requests,
-        c.pages, reinterpret_cast<uint16_t*>(ws + c.wide), reinterpret_cast<int*>(ws + c.table), status);
-    if ((rc = last_cuda_error()) != MLA_OK) return rc;
+    if ((rc = launched(widen_launch(dim3(blocks < 4096 ? blocks : 4096, num_requests < 65535 ? num_requests : 65535),
+                                    static_cast<const uint8_t*>(kv_cache), num_pages, block_table, bt_stride, cache_lens,
+                                    max_len, num_requests, c.pages, reinterpret_cast<uint16_t*>(ws + c.wide),
+                                    reinterpret_cast<int*>(ws + c.table), status, s))) != MLA_OK)
+      return rc;
   }
-  if ((rc = launch_plan(ws, L, pairs.pair_lens, c.slots, 0, 128, c.units, &pairs, fp8, stream)) != MLA_OK) return rc;
+  if ((rc = launch_plan(ws, L, pairs.pair_lens, c.slots, 0, 128, c.units, &pairs, stream)) != MLA_OK) return rc;
 
   DecodeParams p;
   std::memset(&p, 0, sizeof(p));

@@ -89,6 +89,7 @@ struct ChunkPairs {
   int4* pairs;        // per slot {first token, request, tokens (0, 1 or 2), 0}
   int* pair_lens;     // per slot: rows that its last token sees (at least 0)
   int* status;
+  int beside;         // the plan runs beside the kernel before it (and waits for it at its end)
 };
 
 }  // namespace mla

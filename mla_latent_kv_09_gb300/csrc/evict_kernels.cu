@@ -12,6 +12,7 @@ namespace mla {
 namespace {
 
 using prefix::al;
+using prefix::launch_dependent;
 using prefix::share;
 
 // ------------------------------------------------------------------ select
@@ -25,7 +26,8 @@ using prefix::share;
 // Bound by latency: a load, two or three passes of three meetings each, the
 // ordered pass.  Loops are rolled: with the weights in registers and everything
 // unrolled, fetching the instructions took longer than running them (one request
-// of 8192 rows 15 us on one CTA).
+// of 8192 rows 15 us on one CTA).  A dependent launch: calls one after the other,
+// 64 x 8192 rows, 10.4 us each instead of 13.6.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 static_assert(kSelWarps == 32, "the ordered pass adds the warps' counts a lane each");
@@ -77,6 +79,8 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __g
   __shared__ int s_coarse[3][64];  // ... of 32 bins together
   __shared__ int s_found[3], s_count[2], s_warp[2][kSelWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int b = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
   const int given = p.lens[b];
   const int len = min(max(given, 0), p.max_len);
@@ -260,6 +264,8 @@ __global__ void __launch_bounds__(kMoveThreads) mla_cache_compact_kernel(const _
   __shared__ long long s_src[kMoveRows], s_dst[kMoveRows];
   constexpr int kItems = kMoveRows * kUnits;
   constexpr int kDepth = (kItems + kMoveThreads - 1) / kMoveThreads;
+  grid_launch_dependents();
+  grid_dependency_wait();
   for (int b = blockIdx.y; b < p.requests; b += gridDim.y) {
     const int given = p.lens[b];
     const int len = min(max(given, 0), p.kept_width);
@@ -373,23 +379,8 @@ int mla_evict_select(const float* weights, int64_t weights_stride, const int32_t
   p.new_stride = new_weights_stride;
   p.new_width = new_weights ? new_width : 0;
   p.status = status;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_requests) * p.cluster);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.room) * 4;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, mla_evict_select_kernel, p) != cudaSuccess) {
-    cudaGetLastError();
-    return MLA_ERR_CUDA;
-  }
-  return MLA_OK;
+  return launch_dependent(mla_evict_select_kernel, dim3(static_cast<unsigned>(num_requests) * p.cluster), dim3(kSelThreads),
+                          p.room * 4, p.cluster, stream, p);
 }
 
 int mla_cache_compact(void* cache, int64_t num_pages, int row_bytes, const int32_t* block_table, int64_t bt_stride,
@@ -424,15 +415,10 @@ int mla_cache_compact(void* cache, int64_t num_pages, int row_bytes, const int32
   p.status = status;
   const int x = (kept_width + kMoveRows - 1) / kMoveRows;
   const dim3 grid(x, num_requests < 65535 ? num_requests : 65535);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (row_bytes == 1152)
-    mla_cache_compact_kernel<72><<<grid, kMoveThreads, 0, s>>>(p);
-  else if (row_bytes == 256)
-    mla_cache_compact_kernel<16><<<grid, kMoveThreads, 0, s>>>(p);
-  else
-    mla_cache_compact_kernel<41><<<grid, kMoveThreads, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  return MLA_OK;
+  return launch_dependent(row_bytes == 1152 ? mla_cache_compact_kernel<72>
+                          : row_bytes == 256 ? mla_cache_compact_kernel<16>
+                                             : mla_cache_compact_kernel<41>,
+                          grid, dim3(kMoveThreads), 0, 1, stream, p);
 }
 
 }  // extern "C"

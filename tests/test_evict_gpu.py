@@ -515,3 +515,34 @@ def test_a_prompt_in_chunks_whose_cache_shrinks(fp8):
     bo, bl = oracle.chunk_error_bound(f64(step[:, 0]), chosen, [0, 1, 2], SCALE, ref)
     assert (np.abs(f64(o[:, 0]) - ref) <= bo + 2.0 ** -11 * np.abs(ref)).all()
     assert (np.abs(f64(l[:, 0]) - ref_lse) <= bl).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_calls_in_a_row_are_those_that_wait(fp8):
+    """The four calls, each on what the one before it leaves, launched one behind
+    the other without a wait: the bits of the same calls with a wait after each."""
+    lens, starts, keep = [500, 77, 1300], [0, 7, 8, 20], 200
+    cache, table, _ = paged(lens, fp8, 120)
+    pages, per = cache.shape[0], (keep + 63) // 64
+    pool = torch.cat((cache, torch.zeros((3 * per,) + cache.shape[1:], dtype=cache.dtype, device="cuda")))
+    free = ints([[pages + per * b + i for i in range(per)] for b in range(3)])
+    q, s, n = rand((20, 128, 576), 121), ints(starts), ints(lens)
+
+    def chain(wait):
+        got = list(m.chunk_attend(q, pool, table, n, SCALE, token_starts=s))
+        wait()
+        got.append(m.attention_weights(q, got[1], pool, table, n, SCALE, token_starts=s))
+        wait()
+        got += m.evict_select(got[2], n, keep, sinks=2, recent=9)
+        wait()
+        m.cache_compact(pool, table, got[3], got[4], free)
+        wait()
+        got += m.chunk_attend(q, pool, free, got[4], SCALE, token_starts=s, causal=False)
+        wait()
+        return got
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(20):
+        pool[pages:].zero_()
+        got = chain(lambda: None)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))

@@ -148,15 +148,18 @@ constexpr int kTmaWarp = 17;
 constexpr int kShipWarp = 18;                    // score ranks: P shipper
 constexpr int kMma2Warp = 19;                    // rank 0: issues the score MMAs of odd tiles
 constexpr float kRescaleLog2 = 8.0f;
-// Chunks rescale O less often: a warp's rows move their reference together, when
-// one of them has a score that beats its own by 2^15.9 (weights stay below 65504,
-// fp16's largest), and then to 2^6 above the largest score they have seen.
-// Weights below 2^-8 of a row's largest may then be subnormal in fp16, off by
-// 2^-19 of the largest.  A rescale reads and writes 128 x 512 values, as long as
-// a tile's own products take: with rows of large magnitude (5 % of them 6 times
-// the others) 72 tokens x 4096 rows take 87 us instead of 105, x 32768 441
-// instead of 565 (2^14: 89 and 445; 13 x 47 tokens x 2048 424 against 413).
-constexpr float kPairsRescaleLog2 = 15.9f, kPairsAheadLog2 = 6.0f;
+// Chunks rescale O less often: a warp's rows move their reference together, each to
+// the largest score that it has seen, when one of them has a score that beats its
+// own by 2^15.9 (weights stay below 65504, fp16's largest).  It is never above that
+// score: the largest weight is one or more, and fp16 loses no more than 2^-25 of it
+// in any other, whatever the warp's other rows do.  A rescale reads and writes 128 x
+// 512 values, as long as a tile's own products take.  With rows of large magnitude
+// (5 % of them 6 times the others) 72 tokens x 4096 rows take 94 us, x 32768 455, 13
+// x 47 tokens x 2048 439; with the decode step's rule, each row by itself at 2^8,
+// 105, 565 and 477.  (A reference 2^6 above the score takes 87, 441 and 414, but
+// loses up to 2^-19 of the largest weight in each: a long light remainder behind one
+// large score came out up to a third too light.)
+constexpr float kPairsRescaleLog2 = 15.9f;
 
 constexpr uint16_t kScoreMask = 0x3;  // ranks 0, 1
 constexpr uint16_t kValueMask = 0xC;  // ranks 2, 3
@@ -616,11 +619,10 @@ mla_decode_mtp_kernel(const __grid_constant__ DecodeParams p, const __grid_const
         float alpha = 1.f, m_new = mt;
         bool moves = mt > m_used + kRescaleLog2;
         if (kPairs) {  // (the quarter's four warps hold the same rows and decide alike)
-          m_seen = larger(m_seen, mt);
+          m_new = m_seen = larger(m_seen, mt);
           // (a row whose scores are no numbers moves alone, and moves no other)
           const bool together = __any_sync(0xffffffffu, mt > m_used + kPairsRescaleLog2);
-          m_new = m_used == NEG_INF ? m_seen : m_seen + kPairsAheadLog2;
-          moves = together ? !(m_new <= m_used) : m_seen != m_seen;
+          moves = together ? !(m_seen <= m_used) : m_seen != m_seen;
         }
         if (moves) {
           alpha = (m_used == NEG_INF) ? 0.f : ex2_approx(m_used - m_new);

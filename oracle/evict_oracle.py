@@ -49,9 +49,9 @@ def chunk_error_bound(q, rows, starts, scale: float, out, causal: bool = True):
 
     As for the expanded prefix (prefix_oracle.attend_error_bound): a relative
     error d_j on weight p_j moves the normalised sum by p_j d_j (v_j - out); a
-    weight's rounding is 2^-11 of it, or 2^-25 below fp16's normal range, where the
-    largest weight may be as small as 2^-6: 2^-19 of the largest.  A value below 2^-14 is off by 2^-25, a partial result by 2^-11 of
-    itself (at most sum p |v|)."""
+    weight's rounding is 2^-11 of it, or, below fp16's normal range, 2^-25 of a
+    weight of one, which the largest is not below.  A value below 2^-14 is off by
+    2^-25, a partial result by 2^-11 of itself (at most sum p |v|)."""
     q, scale = np.asarray(q, np.float64), float(np.float32(scale))  # (the calls take it in 32 bits)
     T, H = q.shape[:2]
     bo, bl = np.zeros((T, H, LATENT)), np.zeros((T, H))
@@ -73,7 +73,7 @@ def chunk_error_bound(q, rows, starts, scale: float, out, causal: bool = True):
             # sum_j p_j |v_j - out|, at most
             spread = np.minimum(mass + np.abs(out[t]), np.sqrt(np.maximum(p @ v ** 2 - out[t] ** 2, 0.0)))
             most = np.abs(v).max(0) + np.abs(out[t])
-            bo[t] = ((2.0 ** -11 + 2 * eta[:, None]) * spread * 1.01 + 2.0 ** -19 * (seen / z) * most + 2.0 ** -25
+            bo[t] = ((2.0 ** -11 + 2 * eta[:, None]) * spread * 1.01 + 2.0 ** -25 * (seen / z) * most + 2.0 ** -25
                      + (seen * 2.0 ** -23 + 2.0 ** -11 + 2.0 ** -20) * mass)
             bl[t] = eta + seen * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(m[:, 0]) + np.log(z[:, 0]))
     return bo, bl

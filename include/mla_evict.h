@@ -58,7 +58,8 @@ int mla_attention_weights(const void* q, const float* lse, const void* kv_cache,
  *   cache_lens    int32 [num_requests], <= max_len
  *   keep          >= 1; 0 <= sinks, 0 <= recent, sinks + recent <= keep
  *   kept          int32 [num_requests, keep]: increasing positions, then -1
- *   new_lens      int32 [num_requests]
+ *   new_lens      int32 [num_requests]; may be cache_lens itself, and must not
+ *                 overlap it otherwise
  *   new_weights   fp32 [num_requests, new_width] at a stride of
  *                 new_weights_stride, new_width >= min(keep, max_len): the
  *                 kept rows' weights, then zeros; or NULL.  Must not overlap

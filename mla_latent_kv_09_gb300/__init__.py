@@ -758,7 +758,7 @@ def evict_select(weights, cache_lens, keep: int, *, sinks: int = 0, recent: int 
     new_weights [B, L] fp32: the kept rows' weights in their new places, then
     zeros), by default new; `out` may hold them, new_weights with any width of
     at least min(keep, L), or None in its place, and not in the memory of
-    `weights`.  `status` receives MLA_ERR_BAD_TABLE for a length out of range
+    `weights`; new_lens may be cache_lens itself.  `status` receives MLA_ERR_BAD_TABLE for a length out of range
     (it counts as 0 or L).
     """
     import torch

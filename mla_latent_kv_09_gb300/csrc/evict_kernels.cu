@@ -84,6 +84,12 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const __g
   const int b = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
   const int given = p.lens[b];
   const int len = min(max(given, 0), p.max_len);
+  if (p.new_lens == p.lens) {  // written below: the whole cluster has read it
+    if (p.cluster > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
   const float* row = p.weights + b * p.stride;
   int* kept = p.kept + static_cast<long long>(b) * p.keep;
   float* out = p.new_weights ? p.new_weights + b * p.new_stride : nullptr;
@@ -356,6 +362,8 @@ int mla_evict_select(const float* weights, int64_t weights_stride, const int32_t
   // rows are numbered in 32 bits, beyond the end by a grid's step
   if (max_len > (1 << 30) || keep > (1 << 30) || new_width > (1 << 30) || num_requests > INT32_MAX / kMaxCluster)
     return MLA_ERR_UNSUPPORTED;
+  const int64_t apart = static_cast<int64_t>(reinterpret_cast<intptr_t>(new_lens) - reinterpret_cast<intptr_t>(cache_lens)) / 4;
+  if (apart != 0 && apart < num_requests && -apart < num_requests) return MLA_ERR_INVALID_ARG;  // another request's length
   if (share(weights, weights_stride, max_len, new_weights, new_weights_stride, new_width, num_requests))
     return MLA_ERR_INVALID_ARG;
   const int rc = evict_device_ready();

@@ -61,15 +61,15 @@ __device__ int chunk_pair(const ChunkPairs& c, int slot) {
   const int count = at < first || at >= end ? 0 : min(2, end - at);
   int len = 0;
   if (count > 0) {
-    const int L = c.lens[lo];
-    if (L < 0 || L > c.max_len) atomicCAS(c.status, 0, static_cast<int>(kStBadTable));
-    const int all = min(max(L, 0), c.max_len);
+    const int all = min(max(c.lens[lo], 0), c.max_len);
     len = c.causal ? max(all - (end - at - count), 0) : all;
   }
-  if (c.starts && slot < c.requests) {  // (as many slots as half of the requests at least: two starts each)
+  // every request is checked, those without tokens too (as many slots as half of the requests at least: two each)
+  if (slot < c.requests) {
     for (int b = 2 * slot; b <= min(2 * slot + 1, c.requests - 1); ++b) {
-      const int s0 = c.starts[b], s1 = c.starts[b + 1];
-      if (s0 < 0 || s1 < s0 || s1 > c.tokens) atomicCAS(c.status, 0, static_cast<int>(kStBadTable));
+      const int L = c.lens[b], s0 = c.starts ? c.starts[b] : 0, s1 = c.starts ? c.starts[b + 1] : 0;
+      if (L < 0 || L > c.max_len || s0 < 0 || s1 < s0 || s1 > c.tokens)
+        atomicCAS(c.status, 0, static_cast<int>(kStBadTable));
     }
   }
   c.pairs[slot] = make_int4(at, lo, count, 0);

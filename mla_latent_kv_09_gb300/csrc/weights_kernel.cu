@@ -704,6 +704,8 @@ mla_attention_weights_kernel(const __grid_constant__ WeightsParams p, const __gr
 
 // Adds the parts of tiles that several units share, in the line's order: block u
 // does so for the tile in whose tokens unit u begins, if no unit before it does.
+// The parts are added before they meet the older weight, which may be far larger
+// and would be rounded at each of them.
 __global__ void __launch_bounds__(kTileRows) mla_attention_weights_join_kernel(const __grid_constant__ WeightsParams p) {
   grid_dependency_wait();
   const int u = blockIdx.x;
@@ -718,15 +720,14 @@ __global__ void __launch_bounds__(kTileRows) mla_attention_weights_join_kernel(c
   }
   const int pos = mine.y * kTileRows + static_cast<int>(threadIdx.x);
   if (pos >= len_of(p, mine.x)) return;
-  float* out = p.out + mine.x * p.out_stride + pos;
-  float sum = *out + p.parts[u * kTileRows + threadIdx.x];
+  float sum = p.parts[u * kTileRows + threadIdx.x];
   for (int v = u + 1; v < kUnits; ++v) {
     const int4 o = p.begins[v];
     if (o.x < 0) continue;
     if (!same(o)) break;
     sum += p.parts[v * kTileRows + threadIdx.x];
   }
-  *out = sum;
+  p.out[mine.x * p.out_stride + pos] += sum;
 }
 
 // Device check and kernel attributes, once per device.

@@ -57,3 +57,22 @@ def test_weights_on_the_whole(requests, tokens, fp8):
     off = got.double() / ref - 1
     assert abs(float(off.mean())) <= 1.1e-6
     assert float(off.square().mean().sqrt()) <= 1.2e-6
+
+
+@pytest.mark.parametrize("L,tokens", [(200, 600), (700, 300), (256, 76), (1000, 1)])
+def test_older_weights_are_rounded_three_times_at_most(L, tokens):
+    """Large older weights, whose tile's tokens are cut into many ranges: times the
+    decay, plus the first range's sum, plus that of the others, a rounding each."""
+    cache, table = rand(((L + 63) // 64, 64, 576), 5), torch.arange((L + 63) // 64, dtype=torch.int32, device="cuda")[None]
+    q = rand((tokens, 128, 576), 6)
+    rows = cache.double().view(-1, 576)[:L]
+    scale = float(torch.tensor(SCALE, dtype=torch.float32))
+    s = scale * (q.double().view(-1, 576) @ rows.t())
+    lse = s.logsumexp(1).view(tokens, 128).float()
+    new = (s - lse.double().view(-1, 1)).exp().sum(0)
+    was = 1e5 * (1 + torch.rand((1, L), generator=torch.Generator(device="cuda").manual_seed(7), device="cuda"))
+    got = m.attention_weights(q, lse, cache, table, ints([L]), SCALE, was.clone(), causal=False, decay=0.75)
+    old = 0.75 * was[0].double()
+    # the new sum's own error: 2e-5 of it at most (the test above: 1e-6), next to nothing beside a rounding of the whole
+    allowed = 3 * 2.0 ** -24 * (old + new) * 1.001 + 2e-5 * new
+    assert float(((got[0].double() - (old + new)).abs() / allowed).max()) <= 1

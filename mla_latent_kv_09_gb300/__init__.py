@@ -758,8 +758,8 @@ def evict_select(weights, cache_lens, keep: int, *, sinks: int = 0, recent: int 
     new_weights [B, L] fp32: the kept rows' weights in their new places, then
     zeros), by default new; `out` may hold them, new_weights with any width of
     at least min(keep, L), or None in its place, and not in the memory of
-    `weights`; new_lens may be cache_lens itself.  `status` receives MLA_ERR_BAD_TABLE for a length out of range
-    (it counts as 0 or L).
+    `weights`; new_lens may be cache_lens itself.  `status` receives
+    MLA_ERR_BAD_TABLE for a length out of range (it counts as 0 or L).
     """
     import torch
     dev = weights.get_device()
@@ -783,7 +783,12 @@ def evict_select(weights, cache_lens, keep: int, *, sinks: int = 0, recent: int 
             raise ValueError("new_weights: its rows are too short, or overlap")
     if B > 1 and weights.stride(0) < L:
         raise ValueError("weights: its rows overlap")
+    if status is not None:
+        _tensor(status, "status", torch.int32, status.shape, dev)
     if B == 0 or L == 0:
+        if status is not None and B:  # (as the kernel would: the first error stays)
+            bad = (cache_lens != 0).any() & (status.view(-1)[0] == 0)
+            status.view(-1)[:1].masked_fill_(bad, MLA_ERR_BAD_TABLE)
         new_lens.zero_()
         kept.fill_(-1)
         if new is not None:
@@ -791,8 +796,6 @@ def evict_select(weights, cache_lens, keep: int, *, sinks: int = 0, recent: int 
         return out
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=dev)
-    else:
-        _tensor(status, "status", torch.int32, status.shape, dev)
     stream = torch._C._cuda_getCurrentRawStream(dev)
     mla_evict_select(weights, weights.stride(0) if B > 1 else L, cache_lens, B, L, keep, sinks, recent, kept, new_lens,
                      new, 0 if new is None else new.stride(0) if B > 1 else new.shape[1],

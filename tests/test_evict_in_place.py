@@ -64,3 +64,18 @@ def test_lengths_out_of_range_in_place():
     m.evict_select(w, held, 100, out=(kept, held, new), status=status)
     assert int(status) == m.MLA_ERR_BAD_TABLE and held.tolist() == [100, 0, 100, 20]
     assert torch.equal(kept, want[0]) and torch.equal(new, want[2])
+
+
+@pytest.mark.gpu
+def test_lengths_of_weights_without_columns():
+    """Nothing to choose from: lengths other than 0 are out of range there too."""
+    w = torch.zeros((3, 0), device="cuda")
+    for lens, before, after in (([0, 0, 0], 0, m.MLA_OK), ([0, 5, 0], 0, m.MLA_ERR_BAD_TABLE), ([0, 0, -1], 0, m.MLA_ERR_BAD_TABLE),
+                                ([0, 5, 0], m.MLA_ERR_BAD_INDEX, m.MLA_ERR_BAD_INDEX)):
+        status = torch.full((1,), before, dtype=torch.int32, device="cuda")
+        kept, new_lens, _ = m.evict_select(w, torch.tensor(lens, dtype=torch.int32, device="cuda"), 4, status=status)
+        assert int(status) == after and new_lens.tolist() == [0, 0, 0] and bool((kept == -1).all())
+    held = torch.tensor([0, 5, 0], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.evict_select(w, held, 4, out=(torch.empty((3, 4), dtype=torch.int32, device="cuda"), held, None), status=status)
+    assert int(status) == m.MLA_ERR_BAD_TABLE and held.tolist() == [0, 0, 0]

@@ -23,6 +23,16 @@
  * `visible` counts does with less (8192 rows, absorptions included: 128 tokens
  * 232 us against 271, 160 289 / 289, 256 428 / 298).
  *
+ * A request's odd token, and so a single one, costs what a pair does.  63
+ * requests of one token over 4096 rows take 129 us (mla_decode with s_q = 1:
+ * 114); beside 512 tokens of another request, in one call, 510 us (412 for those
+ * alone, so that two calls are no faster).
+ *
+ * An FP8 cache's rows are widened to bf16 before, those of every request up to
+ * its length, whatever the number of its tokens: 64 requests of 4 tokens over
+ * 8192 rows take 574 us (bf16 rows 420; mla_decode 1,113, whose steps read FP8
+ * rows once a token).
+ *
  * Conventions: as for mla_decode.h (device pointers, asynchronous on `stream`,
  * no allocation, no host synchronisation, graph-capturable).
  */
@@ -37,8 +47,10 @@ extern "C" {
 
 /* Bytes of workspace for a call of `num_tokens` tokens of `num_requests`
  * requests; `max_len` and `flags` as for the call (an FP8 cache's rows are
- * widened there once: num_requests * max_len rows of 1,152 bytes).  0 and *err
- * (may be NULL) on failure. */
+ * widened there once: num_requests * max_len rows of 1,152 bytes, 9.7 GB for 64
+ * requests of up to 131,072 rows: give the longest length there is, and split a
+ * batch over several calls where that is too much).  0 and *err (may be NULL) on
+ * failure. */
 size_t mla_chunk_attend_workspace_size(int num_tokens, int num_requests, int max_len, unsigned flags, int* err);
 
 /*
@@ -65,6 +77,7 @@ size_t mla_chunk_attend_workspace_size(int num_tokens, int num_requests, int max
  *                 MLA_ERR_BAD_TABLE if a length, a page (its rows read as
  *                 zeros) or a start is out of range, MLA_ERR_TIMEOUT if a
  *                 device wait ran out
+ * A call without tokens looks at nothing and leaves `status` as it was.
  * Values have to stay below 65504 in magnitude (the value product is fp16, as
  * in mla_decode); rows that no token of a call sees may hold anything.
  */

@@ -42,6 +42,8 @@ size_t mla_attention_weights_workspace_size(int num_tokens, int num_requests, in
  *   flags         MLA_FLAG_CAUSAL, MLA_FLAG_KV_FP8
  *   workspace     mla_attention_weights_workspace_size bytes, 256-B aligned;
  *                 two calls that may overlap need one each
+ * A call without tokens looks at nothing and leaves `status` and `out` as they
+ * were.
  */
 int mla_attention_weights(const void* q, const float* lse, const void* kv_cache, int64_t num_pages,
                           const int32_t* block_table, int64_t bt_stride, const int32_t* cache_lens, int max_len,

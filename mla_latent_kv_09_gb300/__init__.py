@@ -652,9 +652,11 @@ def chunk_attend(q, kv_cache, block_table, cache_lens, softmax_scale: float, *, 
     -inf.  Values have to stay below 65504 in magnitude; rows that no token
     sees may hold anything.
 
-    The cost of a (token, row) is that of the absorbed form.  Chunks of more
-    than some 160 tokens of one request cost less by `prefix_expand` of its
-    whole cache and `prefix_attend` with `visible` counts.
+    The cost of a (token, row) is that of the absorbed form, a request's odd or
+    single token counting as two; an FP8 cache's rows are widened first, up to
+    every request's length.  Chunks of more than some 160 tokens of one request
+    cost less by `prefix_expand` of its whole cache and `prefix_attend` with
+    `visible` counts, batches of one token a request by `decode_step`.
 
     `workspace` (uint8, mla_chunk_attend_workspace_size bytes) is allocated if
     not given; `status` (int32 device tensor, one element; without it nobody
